@@ -18,6 +18,10 @@ FMT = {"nvfp4": 0, "mxfp4": 1, "int4": 2}
 ACT = {"swigluoai": 0, "relu2": 1}
 ROUTE = {"topk_softmax": 0, "sigmoid_bias": 1}
 LAYOUT = {"interleaved": 0, "concat": 1}
+SCORE = {"softmax": 0, "sigmoid": 1}
+GROUP_SCORE = {"max": 0, "top2": 1}
+NORM = {"rms": 0, "layer": 1}
+KV_FMT = {"bf16": 0, "fp16": 1, "fp8": 2, "nvfp4": 3}
 STATUS_BYTES = 256
 
 #: symbols include/moe4.h declares
@@ -25,7 +29,9 @@ EXPORTS = ("moe_padded_rows", "moe_workspace_size", "moe_route_topk", "moe_align
            "moe_grouped_gemm1_act", "moe_grouped_gemm2_weighted", "moe_unpermute_reduce",
            "moe_forward", "moe_forward_host", "moe_read_status", "moe_clear_status", "moe_wait_selftest",
            "moe_status_string", "moe_last_launch_count", "moe_forward_static", "moe_forward_profile",
-           "moe_import_gptq_int4", "moe_import_modelopt_global_scale")
+           "moe_import_gptq_int4", "moe_import_modelopt_global_scale", "moe_route_grouped",
+           "moe_residual_norm", "moe_kv_record_bytes", "moe_kv_write", "moe_kv_read",
+           "moe_attn_workspace_size", "moe_attn_decode")
 
 
 class MoeError(RuntimeError):
@@ -42,6 +48,21 @@ class QWeight(ctypes.Structure):
 
 class Act(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("alpha", ctypes.c_float), ("limit", ctypes.c_float)]
+
+
+class Router(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("n_group", ctypes.c_int32), ("topk_group", ctypes.c_int32),
+                ("group_score", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class Norm(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("type", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("offset", ctypes.c_float), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+
+
+class KvCache(ctypes.Structure):
+    _fields_ = [("fmt", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("data", ctypes.c_void_p)]
 
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
@@ -71,6 +92,17 @@ _SIGS = {
     "moe_last_launch_count": (_i32, []),
     "moe_import_gptq_int4": (_i32, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp]),
     "moe_import_modelopt_global_scale": (_i32, [ctypes.c_float, _i32, _vp]),
+    "moe_route_grouped": (_i32, [_vp, _i32, _i64, _vp, _i32, _i32, _i32, ctypes.POINTER(Router), _vp, _vp, _vp,
+                                 _vp]),
+    "moe_residual_norm": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i32, _i32, _i32, _i32,
+                                 ctypes.POINTER(Norm), ctypes.c_float, _vp, _i64, ctypes.POINTER(Norm), _vp, _i64,
+                                 _vp]),
+    "moe_kv_record_bytes": (_i64, [_i32, _i32]),
+    "moe_kv_write": (_i32, [_vp, _vp, _i32, _i64, _i64, _i64, _i64, _vp, _i32, ctypes.POINTER(KvCache), _vp, _vp]),
+    "moe_kv_read": (_i32, [ctypes.POINTER(KvCache), _vp, _i32, _vp, _vp, _i32, _i64, _i64, _i64, _i64, _vp, _vp]),
+    "moe_attn_workspace_size": (_i32, [_i32, _i32, _i32, ctypes.POINTER(_sz)]),
+    "moe_attn_decode": (_i32, [_vp, _i32, _i64, _i64, ctypes.POINTER(KvCache), _vp, _i64, _i32, _vp, _i32, _i32,
+                               ctypes.c_float, _i32, _vp, _vp, _i64, _i64, _vp, _vp, _sz, _vp]),
 }
 
 _lib = None
@@ -288,3 +320,164 @@ def moe_import_modelopt_global_scale(weight_scale_2, E):
     _check(load().moe_import_modelopt_global_scale(float(weight_scale_2), E, _host_ptr(g)),
            "moe_import_modelopt_global_scale")
     return g
+
+
+# ------------------------------------------------ around the layer: routing with groups, norms, cache, attention
+_INVALID = 1
+
+
+def _dtype(t, where):
+    import torch
+    code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(t.dtype)
+    if code is None:
+        raise MoeError(_INVALID, f"{where}: {t.dtype}")
+    return code
+
+
+def _need(ok, where):
+    if not ok:
+        raise MoeError(_INVALID, where)
+
+
+def _is(t, name):
+    return str(t.dtype) == name
+
+
+def _plain(t, name, n):
+    """A contiguous tensor of n values of the dtype, or None."""
+    return t is None or (t.numel() == n and t.is_contiguous() and str(t.dtype) == name)
+
+
+def router(score="softmax", n_group=1, topk_group=1, group_score="max", renormalize=True, scale=1.0) -> Router:
+    return Router(SCORE[score] if isinstance(score, str) else int(score), int(n_group), int(topk_group),
+                  GROUP_SCORE[group_score] if isinstance(group_score, str) else int(group_score),
+                  int(bool(renormalize)), float(scale))
+
+
+def moe_route_grouped(logits, sel_bias, k, cfg, topk_ids, topk_weights, ws, stream=None):
+    """logits [T, E] bf16, fp16 or fp32 (rows may be apart), sel_bias fp32 [E] or None, cfg from router()."""
+    where = "moe_route_grouped"
+    T, E = logits.shape
+    _need(E == 0 or logits.stride(1) == 1 or E == 1, where)
+    _need(_plain(sel_bias, "torch.float32", E) and _plain(topk_ids, "torch.int32", T * k) and
+          _plain(topk_weights, "torch.float32", T * k), where)
+    _check(load().moe_route_grouped(_ptr(logits), _dtype(logits, where), logits.stride(0) if T > 1 else E,
+                                    _ptr(sel_bias), T, E, k, ctypes.byref(cfg), _ptr(topk_ids), _ptr(topk_weights),
+                                    _ptr(ws), _stream(stream)), where)
+
+
+def norm(kind="rms", weight=None, bias=None, eps=1e-5, offset=0.0) -> Norm:
+    """A norm's parameters; the caller keeps the tensors alive while the struct is in use."""
+    code = 2
+    for t in (weight, bias):
+        if t is not None:
+            code = _dtype(t, "norm")
+            _need(t.dim() == 1 and t.is_contiguous(), "norm")
+    _need(weight is None or bias is None or (weight.dtype == bias.dtype and weight.shape == bias.shape), "norm")
+    n = Norm(NORM[kind] if isinstance(kind, str) else int(kind), code, float(eps), float(offset),
+             None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr())
+    n.width = None if weight is None and bias is None else int((bias if weight is None else weight).shape[0])
+    return n
+
+
+def moe_residual_norm(z, residual, gate, post, alpha, h_out, pre, y_out, stream=None):
+    """h_out = residual + alpha * gate * post(z); y_out = pre(h_out). z, gate, y_out [T, H] of one type,
+    residual and h_out of it or fp32; gate [T, H], [T, 1] or [1, H]; post, pre from norm(). See the header
+    for which may be None."""
+    where = "moe_residual_norm"
+    base = z if z is not None else residual
+    _need(base is not None and base.dim() == 2, where)
+    T, H = base.shape
+    act = z if z is not None else (y_out if y_out is not None else residual)
+    res = residual if residual is not None else (h_out if h_out is not None else act)
+    for t, like in ((z, act), (y_out, act), (residual, res), (h_out, res)):
+        _need(t is None or (t.dtype == like.dtype and t.shape == base.shape and (H == 1 or t.stride(1) == 1)), where)
+    for n in (post, pre):
+        _need(n is None or getattr(n, "width", None) in (None, H), where)
+    gst = gsh = 0
+    if gate is not None:
+        _need(gate.dim() == 2 and gate.dtype == act.dtype, where)
+        gt, gh = gate.shape
+        _need(gt in (1, T) and gh in (1, H), where)
+        gst = gate.stride(0) if gt > 1 else 0
+        gsh = gate.stride(1) if gh > 1 else 0
+
+    def st(t):
+        return 0 if t is None else (t.stride(0) if T > 1 else (H + 7) // 8 * 8)
+    _check(load().moe_residual_norm(_ptr(z), st(z), _ptr(residual), st(residual), _ptr(gate), gst, gsh, T, H,
+                                    _dtype(act, where), _dtype(res, where),
+                                    None if post is None else ctypes.byref(post), float(alpha), _ptr(h_out), st(h_out),
+                                    None if pre is None else ctypes.byref(pre), _ptr(y_out), st(y_out),
+                                    _stream(stream)), where)
+
+
+def moe_kv_record_bytes(fmt, head_dim):
+    return int(load().moe_kv_record_bytes(KV_FMT[fmt] if isinstance(fmt, str) else int(fmt), head_dim))
+
+
+def kv_cache(data, fmt, head_dim) -> KvCache:
+    """KvCache view of a uint8 tensor [num_pages, kv_heads, page_size / 16, moe_kv_record_bytes(fmt, head_dim)];
+    the caller keeps the tensor alive while the struct is in use."""
+    code = KV_FMT[fmt] if isinstance(fmt, str) else int(fmt)
+    rec = moe_kv_record_bytes(code, head_dim)
+    _need(data.dim() == 4 and _is(data, "torch.uint8") and data.is_contiguous(), "kv_cache")
+    _need(rec == 0 or data.shape[3] == rec, "kv_cache")
+    return KvCache(code, int(data.shape[0]), int(data.shape[2]) * 16, int(data.shape[1]), int(head_dim),
+                   data.data_ptr())
+
+
+def _rows3(t, T, cache, where):
+    """Strides over tokens and heads of a [T, kv_heads, head_dim] tensor."""
+    _need(tuple(t.shape) == (T, cache.kv_heads, cache.head_dim) and t.stride(2) == 1, where)
+    return (t.stride(0) if T > 1 else cache.kv_heads * cache.head_dim,
+            t.stride(1) if cache.kv_heads > 1 else cache.head_dim)
+
+
+def moe_kv_write(k, v, slots, cache, ws, stream=None):
+    """k, v [T, kv_heads, head_dim] of one type (parts of a larger tensor are fine), slots int32 [T]."""
+    where = "moe_kv_write"
+    T = slots.numel()
+    _need(_plain(slots, "torch.int32", T) and k.dtype == v.dtype, where)
+    _check(load().moe_kv_write(_ptr(k), _ptr(v), _dtype(k, where), *_rows3(k, T, cache, where),
+                               *_rows3(v, T, cache, where), _ptr(slots), T, ctypes.byref(cache), _ptr(ws),
+                               _stream(stream)), where)
+
+
+def moe_kv_read(cache, slots, k_out, v_out, ws, stream=None):
+    """k_out, v_out [n, kv_heads, head_dim] of one type, either may be None; slots int32 [n]."""
+    where = "moe_kv_read"
+    n = slots.numel()
+    one = k_out if k_out is not None else v_out
+    _need(one is not None and _plain(slots, "torch.int32", n), where)
+    _need(k_out is None or v_out is None or k_out.dtype == v_out.dtype, where)
+    ks = (0, 0) if k_out is None else _rows3(k_out, n, cache, where)
+    vs = (0, 0) if v_out is None else _rows3(v_out, n, cache, where)
+    _check(load().moe_kv_read(ctypes.byref(cache), _ptr(slots), n, _ptr(k_out), _ptr(v_out), _dtype(one, where), *ks,
+                              *vs, _ptr(ws), _stream(stream)), where)
+
+
+def moe_attn_workspace_size(q_heads, kv_heads, head_dim):
+    n = ctypes.c_size_t(0)
+    _check(load().moe_attn_workspace_size(q_heads, kv_heads, head_dim, ctypes.byref(n)), "moe_attn_workspace_size")
+    return int(n.value)
+
+
+def moe_attn_decode(q, cache, block_table, seq_lens, out, ws, scale=None, window=0, sinks=None, lse=None, stream=None):
+    """q, out [B, q_heads, head_dim] bf16 or fp16, block_table int32 [B, pages], seq_lens int32 [B], sinks fp32
+    [q_heads], lse fp32 [B, q_heads]; scale None: head_dim ** -0.5."""
+    where = "moe_attn_decode"
+    B, heads, D = q.shape
+    _need(D == cache.head_dim and out.shape == q.shape and out.dtype == q.dtype, where)
+    _need(q.stride(2) == 1 and out.stride(2) == 1, where)
+    _need(block_table.dim() == 2 and block_table.shape[0] == B and _is(block_table, "torch.int32"), where)
+    pages = block_table.shape[1]
+    _need(pages <= 1 or block_table.stride(1) == 1, where)
+    _need(_plain(seq_lens, "torch.int32", B) and _plain(sinks, "torch.float32", heads) and
+          _plain(lse, "torch.float32", B * heads) and _is(ws, "torch.uint8"), where)
+
+    def st(t):
+        return (t.stride(0) if B > 1 else heads * D), (t.stride(1) if heads > 1 else D)
+    _check(load().moe_attn_decode(_ptr(q), _dtype(q, where), *st(q), ctypes.byref(cache), _ptr(block_table),
+                                  block_table.stride(0) if B > 1 else pages, pages, _ptr(seq_lens), B, heads,
+                                  D ** -0.5 if scale is None else float(scale), int(window), _ptr(sinks), _ptr(out),
+                                  *st(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)), where)

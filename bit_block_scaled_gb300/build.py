@@ -14,7 +14,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe4.so")
-SOURCES = ["api.cu", "route.cu", "align.cu", "gemm.cu", "unpermute.cu", "static_ws.cu", "convert.cu"]
+SOURCES = ["api.cu", "route.cu", "align.cu", "gemm.cu", "unpermute.cu", "static_ws.cu", "convert.cu",
+           "block_api.cu", "group_route.cu", "norm.cu", "kvcache.cu", "attn.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xptxas", "-warn-spills"]

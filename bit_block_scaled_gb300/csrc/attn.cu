@@ -1,0 +1,880 @@
+// Attention of one new token a sequence over the paged key-value cache.
+//
+//   out = sum_i p_i v_i / (sum_i p_i + sink),  p_i = exp(scale q.k_i - m)
+//
+// with the running maximum m and sum held per query head in fp32, in one pass
+// over the cache; log2 units throughout (p = exp2).
+//
+// What bounds it is the reading of the cache: G query heads share a key, so a
+// byte read carries only G (16-bit) to 4 G (4-bit) multiply-adds. The design
+// is around keeping bulk copies in flight:
+//  - A record (16 tokens of one head: keys, values and their scales) is one
+//    contiguous piece of memory. Each warp has its own ring of STAGES records
+//    in shared memory, filled by one bulk copy each (one lane issues, an
+//    mbarrier counts the bytes), so warps run free of each other.
+//  - The matrix products are transposed, S^T[key][head] = K Q^T and
+//    O^T[d][head] = V^T P^T, so that the 16 rows of an mma.sync are 16 keys or
+//    16 columns and its 8 columns are heads: up to 8 heads of a group cost no
+//    padding. tcgen05 would want 128 keys a tile for the same 8 columns and a
+//    round trip of P through shared memory; at these intensities the tensor
+//    pipe is nowhere near its limit either way.
+//  - FP8 and NVFP4 codes are expanded in registers to f16, exactly (E2M1 times
+//    its E4M3 block scale has 6 significant bits); the power-of-two row scales
+//    never touch them: the key's multiplies its scores, the value's is added
+//    to the exponent of its probabilities. The query is scaled by a power of
+//    two into f16 range.
+//  - The maximum is lazy: it moves only when a score passes it by 8 (in log2),
+//    so the accumulators are seldom rescaled, and p <= 2^8 loses nothing.
+//
+// Work is split evenly over all records of all sequences and heads, whatever
+// their lengths: CTA c takes records [c * per, (c + 1) * per) of the sequence
+// of (sequence, head, record). A (sequence, head) that falls to one CTA is
+// written at once; otherwise each CTA writes its partial output and log-sum,
+// and a second kernel joins them. Both orders are fixed, so results do not
+// vary from run to run.
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "kvcache.cuh"
+#include "types.cuh"
+
+namespace moe4 {
+
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kW = 4;              // warps of a CTA
+constexpr int kMaxCtas = 640;      // partial outputs the workspace holds: two a CTA
+constexpr int kMaxB = 4096;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 8.f;      // lazy maximum, log2
+
+struct AttnArgs {
+  const void *q;
+  const uint8_t *data;
+  const int32_t *table, *lens;
+  const float *sinks;
+  void *out;
+  float *lse;
+  unsigned int *status;
+  int64_t *per;      // records a CTA
+  int *starts;       // [B + 1] first record of each sequence, as if of one head
+  float *part_o;     // [2 kMaxCtas][NH][D]
+  float *part_lse;   // [2 kMaxCtas][NH], log2
+  int64_t qsb, qsh, osb, osh, ts;
+  int q_type, B, heads, kv_heads, G, GB, window, page, pages, max_pages, ctas, min_per;
+  float scale;       // scale * log2 e
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <bool BF>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (BF)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// low half from x, high half from y
+template <bool BF>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  uint32_t r;
+  if (BF)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t b) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)b));
+  return h;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// 8 E2M1 codes to 4 pairs
+__device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t *h) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+
+// One contiguous piece of global memory into shared memory; 16-byte aligned
+// on both sides, bytes a multiple of 16 (records are multiples of 32).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// Tokens of sequence b that are read: [first, len), in records [lo, lo + n), n >= 1.
+struct Span {
+  int len, first, lo, n;
+};
+
+__device__ __forceinline__ Span span_of(const AttnArgs &a, int b) {
+  Span s;
+  const int cap = a.max_pages * a.page;
+  s.len = min(max(a.lens[b], 0), cap);
+  s.first = a.window > 0 ? max(0, s.len - a.window) : 0;
+  s.lo = s.first >> 4;
+  s.n = max(1, ((s.len + 15) >> 4) - s.lo);
+  return s;
+}
+
+// Compile-time shape: NT column tiles of 8 heads a CTA.
+template <int FMT, int D, int NT>
+struct Shape {
+  static constexpr bool kBf = FMT == MOE_KV_BF16;
+  static constexpr bool kQuant = FMT >= MOE_KV_FP8;
+  static constexpr int kRow = kv_row(FMT, D);
+  static constexpr int kRec = kv_record(FMT, D);
+  static constexpr int kStage = (kRec + 127) / 128 * 128;
+  static constexpr int kStages = kRec >= 16384 ? 2 : kRec >= 8192 ? 2 : kRec >= 4096 ? 3 : 4;
+  static constexpr int kHeads = 8 * NT;
+  static constexpr int kLdo = D + 4;  // row of the joining buffer, padded against bank conflicts
+  static constexpr int kJoin = kW * kHeads * kLdo * 4;
+  static constexpr int kMl = kW * kHeads * 3 * 4;
+  static constexpr int kRing = kW * kStages * kStage;
+  static constexpr int kFixed = kRing + kJoin + kMl + kW * kStages * 8;
+};
+
+// A warp's way through its records: the records first + warp, + kW, ... of
+// each (sequence, head) of the CTA's range, one after another.
+struct Cursor {
+  int64_t u;     // work position of the current (sequence, head)'s first record in this range
+  int b, hb;     // sequence; kv head * GB + block of heads
+  int first;     // the range's first record in it (relative to the span)
+  int rec, end;  // next record of this warp in it; end of the range in it
+  Span s;
+};
+
+template <int FMT, int D, int NT>
+__global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
+  using S = Shape<FMT, D, NT>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint8_t *ring = smem;
+  float *join_o = reinterpret_cast<float *>(smem + S::kRing);
+  float *join_ml = reinterpret_cast<float *>(smem + S::kRing + S::kJoin);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kRing + S::kJoin + S::kMl);
+  int *start = reinterpret_cast<int *>(smem + S::kFixed);  // [B + 1] first record of each sequence
+  __shared__ int warp_sum[kW];
+  __shared__ int total_s;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int r = lane >> 2, c = lane & 3;
+  const uint32_t bar0 = smem_u32(bars + warp * S::kStages);
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < S::kStages; ++i) mbar_init(bar0 + 8 * i, 1);
+    fence_mbar_init();
+  }
+  pdl_wait();
+  pdl_trigger();
+
+  // first record of every sequence: running sum of their record counts
+  int base = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kW * 32) {
+    const int b = b0 + tid;
+    int n = 0;
+    if (b < a.B) {
+      n = span_of(a, b).n;
+      const int len = a.lens[b];
+      if (blockIdx.x == 0 && (len < 0 || len > a.max_pages * a.page)) raise_status(a.status, MOE_ERR_BAD_INDEX);
+    }
+    int x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kAll, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    int before = base;
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+      if (w < warp) before += warp_sum[w];
+      base += warp_sum[w];
+    }
+    if (b < a.B) start[b] = before + x - n;
+    __syncthreads();
+  }
+  if (tid == 0) {
+    start[a.B] = base;
+    total_s = base;
+  }
+  __syncthreads();
+  const int HB = a.kv_heads * a.GB;
+  const int64_t total = (int64_t)total_s * HB;
+  const int64_t per = max((total + a.ctas - 1) / a.ctas, (int64_t)a.min_per);
+  if (blockIdx.x == 0) {  // what the joining kernel needs of this
+    if (tid == 0) *a.per = per;
+    for (int b = tid; b <= a.B; b += kW * 32) a.starts[b] = start[b];
+  }
+  const int64_t u0 = (int64_t)blockIdx.x * per, u1 = min(u0 + per, total);
+  if (u0 >= u1) return;
+
+  auto enter = [&](Cursor &k, int64_t u) {  // the (sequence, head) that work position u falls in
+    k.u = u;
+    if (u >= u1) return;
+    int lo = 0, hi = a.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if ((int64_t)start[mid] * HB <= u)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    k.b = lo;
+    k.s = span_of(a, lo);
+    const int64_t in = u - (int64_t)start[lo] * HB;
+    k.hb = (int)(in / k.s.n);
+    k.first = (int)(in % k.s.n);
+    k.rec = k.first + warp;
+    k.end = (int)min((int64_t)k.s.n, k.first + (u1 - u));
+  };
+
+  // ------------------------------------------------ issuing copies ahead
+  Cursor is;
+  enter(is, u0);
+  int issued = 0;          // copies issued by this warp
+  int page_ids = 0;        // lane i: page of the record 'rec_base + kW * i' of the issuing cursor
+  int rec_base = 0;
+  unsigned missing = 0;    // ring slots whose record lies in no page (bit a stage)
+  auto issue = [&]() {
+    while (is.u < u1 && is.rec >= is.end) enter(is, is.u + (is.end - is.first));
+    if (is.u >= u1) return;
+    if (is.rec == is.first + warp || is.rec >= rec_base + 32 * kW) {
+      rec_base = is.rec;
+      const int rr = rec_base + kW * lane;
+      page_ids = -1;
+      if (rr < is.end && is.s.len > 0) page_ids = a.table[is.b * a.ts + (is.s.lo + rr) * 16 / a.page];
+    }
+    const int pg = __shfl_sync(kAll, page_ids, (is.rec - rec_base) / kW);
+    const int slot = issued % S::kStages;
+    const bool ok = pg >= 0 && pg < a.pages;
+    if (lane == 0) {
+      if (ok) {
+        const int off = ((is.s.lo + is.rec) * 16 % a.page) >> 4;
+        const int64_t rec = ((int64_t)pg * a.kv_heads + is.hb / a.GB) * (a.page >> 4) + off;
+        mbar_arrive_expect_tx(bar0 + 8 * slot, S::kRec);
+        bulk_load(smem_u32(ring) + (warp * S::kStages + slot) * S::kStage, a.data + rec * S::kRec, S::kRec,
+                  bar0 + 8 * slot);
+      } else {
+        if (is.s.len > 0) raise_status(a.status, MOE_ERR_BAD_INDEX);
+        mbar_arrive(bar0 + 8 * slot);
+      }
+    }
+    missing = ok ? missing & ~(1u << slot) : missing | (1u << slot);
+    ++issued;
+    is.rec += kW;
+  };
+#pragma unroll 1
+  for (int i = 0; i < S::kStages; ++i) issue();
+
+  bool dead = false;  // a copy did not arrive in time: issue no more
+  int done = 0;       // records consumed
+  int dead_at = 0;    // the first that did not arrive
+  Cursor cu;
+  enter(cu, u0);
+  while (cu.u < u1) {
+    const int kvh = cu.hb / a.GB, h0 = kvh * a.G + (cu.hb % a.GB) * S::kHeads;
+    const int nh = min(S::kHeads, a.G - (cu.hb % a.GB) * S::kHeads);
+    // ---- the query of this (sequence, heads): B fragments, head r of each tile
+    uint32_t qf[NT][D / 16][2];
+    float qs[NT][2];  // factor of the scores of heads 2c, 2c + 1
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int h = 8 * nt + r;
+      const uint16_t *qp = static_cast<const uint16_t *>(a.q) + cu.b * a.qsb + (int64_t)(h0 + h) * a.qsh;
+      uint32_t raw[D / 8];
+#pragma unroll
+      for (int e = 0; e < D / 8; ++e) {  // pairs 2e, 2e + 1 of this lane's D / 4 columns
+        int d;
+        if (!S::kQuant)
+          d = (e >> 1) * 16 + (e & 1) * 8 + 2 * c;
+        else if (S::kRow == 256)
+          d = (e >> 4) * 128 + 32 * c + (e & 15) * 2;
+        else
+          d = c * (D / 4) + 2 * e;
+        raw[e] = h < nh ? *reinterpret_cast<const uint32_t *>(qp + d) : 0u;
+      }
+      qs[nt][0] = qs[nt][1] = a.scale;
+      if (S::kQuant) {  // f16 times a power of two that brings the largest to [2^14, 2^15)
+        float2 f[D / 8];
+        float amax = 0.f;
+#pragma unroll
+        for (int e = 0; e < D / 8; ++e) {
+          if (a.q_type == MOE_BF16)
+            f[e] = make_float2(__uint_as_float(raw[e] << 16), __uint_as_float(raw[e] & 0xFFFF0000u));
+          else
+            f[e] = __half22float2(*reinterpret_cast<const __half2 *>(&raw[e]));
+          amax = fmaxf(amax, fmaxf(fabsf(f[e].x), fabsf(f[e].y)));
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, 2));
+        // exponent of amax, kept to where 2^e and 2^-e are normal fp32
+        const int e14 = min(max((int)(__float_as_uint(amax) >> 23) - 127 - 14, -112), 112);
+        const float up = __uint_as_float((uint32_t)(127 - e14) << 23);
+#pragma unroll
+        for (int e = 0; e < D / 8; ++e) raw[e] = pack2<false>(f[e].x * up, f[e].y * up);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int ex = __shfl_sync(kAll, e14, (2 * c + x) * 4);
+          qs[nt][x] = a.scale * __uint_as_float((uint32_t)(127 + ex) << 23);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < D / 8; ++e) qf[nt][e >> 1][e & 1] = raw[e];
+    }
+
+    float m[NT][2], l[NT][2], mw[NT][2];  // maximum and sum of p; maximum of p times the value's row scale
+    float o[NT][D / 16][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        m[nt][x] = mw[nt][x] = -INFINITY;
+        l[nt][x] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[nt][i][x] = 0.f;
+    }
+
+#pragma unroll 1
+    for (; cu.rec < cu.end; cu.rec += kW) {
+      const int slot = done % S::kStages;
+      if (!dead && !mbar_wait(bar0 + 8 * slot, (done / S::kStages) & 1)) {
+        if (lane == 0) raise_status(a.status, MOE_ERR_TIMEOUT);
+        dead = true;
+      }
+      if (!dead) dead_at = done + 1;
+      dead = __any_sync(kAll, dead);
+      const bool skip = dead || ((missing >> slot) & 1u);
+      const uint8_t *st = ring + (warp * S::kStages + slot) * S::kStage;
+      const uint32_t st32 = smem_u32(st);
+      if (!skip) {
+        // ---- S^T = K Q^T
+        float sc[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) sc[nt][x] = 0.f;
+        if constexpr (!S::kQuant) {
+          const int key = (lane & 7) + (lane & 8);
+          const int half = lane >> 4;
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            uint32_t af[4];
+            ldsm4(af, st32 + kv_place(S::kRow, key, 32 * ks + 16 * half));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma<S::kBf>(sc[nt], af, qf[nt][ks][0], qf[nt][ks][1]);
+          }
+        } else if constexpr (FMT == MOE_KV_FP8) {
+#pragma unroll
+          for (int p = 0; p < D / 64; ++p) {  // 16 codes of rows r and r + 8
+            const int col = S::kRow == 256 ? (p >> 1) * 128 + 32 * c + (p & 1) * 16 : c * (D / 4) + 16 * p;
+            const uint4 x = *reinterpret_cast<const uint4 *>(st + kv_place(S::kRow, r, col));
+            const uint4 y = *reinterpret_cast<const uint4 *>(st + kv_place(S::kRow, r + 8, col));
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t af[4] = {e4m3x2_f16x2(xs[k] & 0xFFFFu), e4m3x2_f16x2(ys[k] & 0xFFFFu),
+                                      e4m3x2_f16x2(xs[k] >> 16), e4m3x2_f16x2(ys[k] >> 16)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma<false>(sc[nt], af, qf[nt][4 * p + k][0], qf[nt][4 * p + k][1]);
+            }
+          }
+        } else {
+          const uint8_t *bs = st + kv_scales_at(FMT, D);
+#pragma unroll
+          for (int p = 0; p < D / 64; ++p) {  // a block of 16: 8 bytes of rows r and r + 8
+            const int blk = c * (D / 64) + p;
+            const uint2 x = *reinterpret_cast<const uint2 *>(st + kv_place(S::kRow, r, 8 * blk));
+            const uint2 y = *reinterpret_cast<const uint2 *>(st + kv_place(S::kRow, r + 8, 8 * blk));
+            const uint32_t sx = bs[16 * blk + r], sy = bs[16 * blk + r + 8];
+            const uint32_t fx = e4m3x2_f16x2(sx | (sx << 8)), fy = e4m3x2_f16x2(sy | (sy << 8));
+            uint32_t hx[8], hy[8];
+            e2m1x8_f16(x.x, hx);
+            e2m1x8_f16(x.y, hx + 4);
+            e2m1x8_f16(y.x, hy);
+            e2m1x8_f16(y.y, hy + 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t af[4] = {hmul2(hx[2 * k], fx), hmul2(hy[2 * k], fy), hmul2(hx[2 * k + 1], fx),
+                                      hmul2(hy[2 * k + 1], fy)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma<false>(sc[nt], af, qf[nt][4 * p + k][0], qf[nt][4 * p + k][1]);
+            }
+          }
+        }
+        // ---- scores in log2, masked; t = score + log2 of the value's row scale
+        const int pos = (cu.s.lo + cu.rec) * 16 + r;
+        const bool in0 = pos >= cu.s.first && pos < cu.s.len, in1 = pos + 8 >= cu.s.first && pos + 8 < cu.s.len;
+        float kx0 = 1.f, kx1 = 1.f, vx0 = 0.f, vx1 = 0.f;
+        if (S::kQuant) {
+          const uint8_t *ex = st + kv_exps_at(FMT, D);
+          const uint32_t k0 = ex[r], k1 = ex[r + 8], v0 = ex[16 + r], v1 = ex[24 + r];
+          const float nan = __int_as_float(0x7fc00000);
+          kx0 = k0 == 255u ? nan : __uint_as_float(k0 << 23);
+          kx1 = k1 == 255u ? nan : __uint_as_float(k1 << 23);
+          vx0 = v0 == 255u ? nan : (float)((int)v0 - 127);
+          vx1 = v1 == 255u ? nan : (float)((int)v1 - 127);
+        }
+        float tw[NT][4];
+        bool grow = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            float s = sc[nt][x] * qs[nt][x & 1];
+            if (S::kQuant) s *= x < 2 ? kx0 : kx1;
+            s = (x < 2 ? in0 : in1) ? s : -INFINITY;
+            sc[nt][x] = s;
+            grow = grow || s > m[nt][x & 1] + kSlack;
+            if (S::kQuant) {
+              tw[nt][x] = (x < 2 ? in0 : in1) ? s + (x < 2 ? vx0 : vx1) : -INFINITY;
+              grow = grow || tw[nt][x] > mw[nt][x & 1] + kSlack;
+            }
+          }
+        if (__any_sync(kAll, grow)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              float t = fmaxf(sc[nt][x], sc[nt][x + 2]);
+#pragma unroll
+              for (int sh = 4; sh < 32; sh <<= 1) t = fmaxf(t, __shfl_xor_sync(kAll, t, sh));
+              t = fmaxf(t, m[nt][x]);
+              l[nt][x] *= m[nt][x] == t ? 1.f : ex2(m[nt][x] - t);
+              float f = m[nt][x] == t ? 1.f : ex2(m[nt][x] - t);
+              m[nt][x] = t;
+              if (S::kQuant) {
+                float w = fmaxf(tw[nt][x], tw[nt][x + 2]);
+#pragma unroll
+                for (int sh = 4; sh < 32; sh <<= 1) w = fmaxf(w, __shfl_xor_sync(kAll, w, sh));
+                w = fmaxf(w, mw[nt][x]);
+                f = mw[nt][x] == w ? 1.f : ex2(mw[nt][x] - w);
+                mw[nt][x] = w;
+              }
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                o[nt][i][x] *= f;
+                o[nt][i][x + 2] *= f;
+              }
+            }
+        }
+        // ---- p, its sum, and P^T as B fragments
+        uint32_t pf[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float w[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float ref = m[nt][x & 1] == -INFINITY ? 0.f : m[nt][x & 1];
+            const float p = ex2(sc[nt][x] - ref);
+            l[nt][x & 1] += p;
+            w[x] = p;
+            if (S::kQuant) {
+              const float rw = mw[nt][x & 1] == -INFINITY ? 0.f : mw[nt][x & 1];
+              w[x] = ex2(tw[nt][x] - rw);
+            }
+          }
+          pf[nt][0] = transpose8(pack2<S::kBf>(w[0], w[1]));
+          pf[nt][1] = transpose8(pack2<S::kBf>(w[2], w[3]));
+        }
+        // ---- O^T += V^T P^T
+        const bool whole = __all_sync(kAll, in0 && in1);
+        if constexpr (!S::kQuant) {
+          const int key = (lane & 7) + ((lane >> 4) << 3);
+          const int half = (lane >> 3) & 1;
+          // values of tokens that are not read may be anything: 0 * NaN must not come in
+          uint32_t keep[2] = {kAll, kAll};
+          if (!whole) {
+            const int k0 = (cu.s.lo + cu.rec) * 16 + 2 * c;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int k = k0 + 8 * x;
+              keep[x] = (k >= cu.s.first && k < cu.s.len ? 0xFFFFu : 0u) |
+                        (k + 1 >= cu.s.first && k + 1 < cu.s.len ? 0xFFFF0000u : 0u);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            uint32_t af[4];
+            ldsm4t(af, st32 + 16 * S::kRow + kv_place(S::kRow, key, 32 * i + 16 * half));
+            if (!whole) {
+              af[0] &= keep[0];
+              af[1] &= keep[0];
+              af[2] &= keep[1];
+              af[3] &= keep[1];
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma<S::kBf>(o[nt][i], af, pf[nt][0], pf[nt][1]);
+          }
+        } else {
+          // lane: columns r * D / 8 .. of tokens 2c, 2c + 1, 2c + 8, 2c + 9
+          const uint8_t *vs = st + 16 * S::kRow;
+          const uint8_t *bs = st + kv_scales_at(FMT, D) + D;
+#pragma unroll
+          for (int p = 0; p < D / 64; ++p) {  // 8 columns at a time
+            uint32_t h[4][4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int key = 2 * c + (x & 1) + (x >> 1) * 8;
+              const int col = r * (D / 8) + 8 * p;
+              const bool in = whole || ((cu.s.lo + cu.rec) * 16 + key >= cu.s.first &&
+                                        (cu.s.lo + cu.rec) * 16 + key < cu.s.len);
+              if constexpr (FMT == MOE_KV_FP8) {
+                const uint2 v = in ? *reinterpret_cast<const uint2 *>(vs + kv_place(S::kRow, key, col)) : make_uint2(0, 0);
+                h[x][0] = e4m3x2_f16x2(v.x & 0xFFFFu);
+                h[x][1] = e4m3x2_f16x2(v.x >> 16);
+                h[x][2] = e4m3x2_f16x2(v.y & 0xFFFFu);
+                h[x][3] = e4m3x2_f16x2(v.y >> 16);
+              } else {
+                const uint32_t v = *reinterpret_cast<const uint32_t *>(vs + kv_place(S::kRow, key, col / 2));
+                const uint32_t sb = in ? bs[(col >> 4) * 16 + key] : 0u;
+                const uint32_t f = e4m3x2_f16x2(sb | (sb << 8));
+                e2m1x8_f16(v, h[x]);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) h[x][y] = hmul2(h[x][y], f);
+              }
+            }
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const uint32_t af[4] = {__byte_perm(h[0][y], h[1][y], 0x5410), __byte_perm(h[0][y], h[1][y], 0x7632),
+                                      __byte_perm(h[2][y], h[3][y], 0x5410), __byte_perm(h[2][y], h[3][y], 0x7632)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma<false>(o[nt][4 * p + y], af, pf[nt][0], pf[nt][1]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      ++done;
+      if (!dead) issue();
+    }
+
+    // ---- the warps' sums joined: this CTA's share of the (sequence, heads)
+    __syncthreads();  // the buffers are free
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float s = l[nt][x];
+#pragma unroll
+        for (int sh = 4; sh < 32; sh <<= 1) s += __shfl_xor_sync(kAll, s, sh);
+        const int h = 8 * nt + 2 * c + x;
+        if (r == 0) {
+          float *ml = join_ml + (warp * S::kHeads + h) * 3;
+          ml[0] = m[nt][x];
+          ml[1] = s;
+          ml[2] = S::kQuant ? mw[nt][x] : m[nt][x];
+        }
+        float *po = join_o + (warp * S::kHeads + h) * S::kLdo;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          if (!S::kQuant) {
+            po[16 * i + r] = o[nt][i][x];
+            po[16 * i + 8 + r] = o[nt][i][x + 2];
+          } else {
+            po[r * (D / 8) + 2 * i] = o[nt][i][x];
+            po[r * (D / 8) + 2 * i + 1] = o[nt][i][x + 2];
+          }
+        }
+      }
+    __syncthreads();
+    const bool all = cu.first == 0 && cu.end == cu.s.n;
+    const int pslot = 2 * blockIdx.x + (cu.u > u0 ? 1 : 0);
+    for (int at = tid; at < nh * (D / 4); at += kW * 32) {
+      const int h = at / (D / 4), d = at % (D / 4) * 4;
+      float M = -INFINITY, MW = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kW; ++w) {
+        M = fmaxf(M, join_ml[(w * S::kHeads + h) * 3]);
+        MW = fmaxf(MW, join_ml[(w * S::kHeads + h) * 3 + 2]);
+      }
+      float L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+      const float Mr = M == -INFINITY ? 0.f : M, MWr = MW == -INFINITY ? 0.f : MW;
+#pragma unroll
+      for (int w = 0; w < kW; ++w) {
+        const float *ml = join_ml + (w * S::kHeads + h) * 3;
+        L += ml[1] * ex2(ml[0] - Mr);
+        const float f = ex2(ml[2] - MWr);
+        const float4 v = *reinterpret_cast<const float4 *>(join_o + (w * S::kHeads + h) * S::kLdo + d);
+        acc[0] += v.x * f;
+        acc[1] += v.y * f;
+        acc[2] += v.z * f;
+        acc[3] += v.w * f;
+      }
+      float lse2 = L == 0.f ? -INFINITY : Mr + log2f(L);
+      float g = L == 0.f ? 0.f : ex2(MWr - Mr) / L;  // L is at least 2^-kSlack
+      if (all) {
+        if (a.sinks) {  // one more logit without a value
+          const float sk = a.sinks[h0 + h] * kLog2e;
+          const float top = fmaxf(lse2, sk);
+          const float sum = ex2(lse2 - top) + ex2(sk - top);
+          const float with = top == -INFINITY ? -INFINITY : top + log2f(sum);
+          if (L != 0.f) g *= top == -INFINITY ? 1.f : ex2(lse2 - with);
+          lse2 = with;
+        }
+        uint2 pk;
+        if (a.q_type == MOE_BF16)
+          pk = make_uint2(pack2<true>(acc[0] * g, acc[1] * g), pack2<true>(acc[2] * g, acc[3] * g));
+        else
+          pk = make_uint2(pack2<false>(acc[0] * g, acc[1] * g), pack2<false>(acc[2] * g, acc[3] * g));
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + cu.b * a.osb + (int64_t)(h0 + h) * a.osh + d) = pk;
+        if (a.lse && d == 0) a.lse[(int64_t)cu.b * a.heads + h0 + h] = lse2 / kLog2e;
+      } else {
+        *reinterpret_cast<float4 *>(a.part_o + ((int64_t)pslot * S::kHeads + h) * D + d) =
+            make_float4(acc[0] * g, acc[1] * g, acc[2] * g, acc[3] * g);
+        if (d == 0) a.part_lse[pslot * S::kHeads + h] = lse2;
+      }
+    }
+    enter(cu, cu.u + (cu.end - cu.first));
+  }
+  // a wait that ran out leaves copies in flight: wait for them, with the same limit
+  if (dead)
+    for (int i = dead_at; i < issued; ++i) mbar_wait(bar0 + 8 * (i % S::kStages), (i / S::kStages) & 1);
+}
+
+// Joins the partial outputs of one (sequence, kv head, block of heads):
+// grid (B * HB, heads of a block), 256 threads; the threads of a group of
+// D / 4 take 4 columns each, the groups take the partials in turn.
+template <int D, int NT>
+__global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
+  constexpr int kHeads = 8 * NT;
+  constexpr int kGroups = 256 / (D / 4);
+  __shared__ float wts[kMaxCtas];
+  __shared__ float red[32];
+  __shared__ float4 acc_s[kGroups][D / 4];
+  pdl_wait();
+  pdl_trigger();
+  const int HB = a.kv_heads * a.GB;
+  const int b = blockIdx.x / HB, hb = blockIdx.x % HB;
+  const int64_t per = *a.per;
+  const int s0 = a.starts[b], n = a.starts[b + 1] - s0;
+  const int64_t first = (int64_t)s0 * HB + (int64_t)hb * n, last = first + n - 1;
+  const int c0 = (int)(first / per), c1 = (int)(last / per);
+  if (c0 == c1) return;
+  const int parts = c1 - c0 + 1;
+  const int nh = min(kHeads, a.G - hb % a.GB * kHeads);
+  const int h0 = hb / a.GB * a.G + hb % a.GB * kHeads;
+  // CTA c0 reached it after its own start unless it begins there
+  const int slot0 = 2 * c0 + (first > c0 * per ? 1 : 0);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int h = blockIdx.y; h < nh; h += gridDim.y) {
+    float top = -INFINITY;
+    bool bad = false;
+    for (int i = tid; i < parts; i += 256) {
+      const float v = a.part_lse[(i == 0 ? slot0 : 2 * (c0 + i)) * kHeads + h];
+      wts[i] = v;
+      top = fmaxf(top, v);
+      bad = bad || v != v;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+    if (lane == 0) red[warp] = top;
+    bad = __syncthreads_or(bad);
+    top = red[0];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) top = fmaxf(top, red[w]);
+    const float ref = top == -INFINITY ? 0.f : top;
+    __syncthreads();
+    float sum = 0.f;
+    for (int i = tid; i < parts; i += 256) {
+      const float w = ex2(wts[i] - ref);
+      wts[i] = w;
+      sum += w;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+    if (lane == 0) red[warp] = sum;
+    __syncthreads();
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) sum += red[w];
+    float lse2 = sum == 0.f ? -INFINITY : ref + log2f(sum);
+    float g = sum == 0.f ? 0.f : 1.f / sum;
+    if (bad) g = lse2 = __int_as_float(0x7fc00000);
+    if (a.sinks) {
+      const float sk = a.sinks[h0 + h] * kLog2e;
+      const float hi = fmaxf(lse2, sk);
+      const float with = hi == -INFINITY ? -INFINITY : hi + log2f(ex2(lse2 - hi) + ex2(sk - hi));
+      if (sum != 0.f && hi != -INFINITY) g *= ex2(lse2 - with);
+      lse2 = with;
+    }
+    const int grp = tid / (D / 4), d4 = tid % (D / 4);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = grp; i < parts; i += kGroups) {
+      const float w = wts[i];
+      const float4 v = *reinterpret_cast<const float4 *>(
+          a.part_o + ((int64_t)(i == 0 ? slot0 : 2 * (c0 + i)) * kHeads + h) * D + 4 * d4);
+      acc.x += w * v.x;
+      acc.y += w * v.y;
+      acc.z += w * v.z;
+      acc.w += w * v.w;
+    }
+    acc_s[grp][d4] = acc;
+    __syncthreads();
+    if (tid < D / 4) {
+#pragma unroll
+      for (int i = 1; i < kGroups; ++i) {
+        const float4 v = acc_s[i][tid];
+        acc.x += v.x;
+        acc.y += v.y;
+        acc.z += v.z;
+        acc.w += v.w;
+      }
+      uint2 pk;
+      if (a.q_type == MOE_BF16)
+        pk = make_uint2(pack2<true>(acc.x * g, acc.y * g), pack2<true>(acc.z * g, acc.w * g));
+      else
+        pk = make_uint2(pack2<false>(acc.x * g, acc.y * g), pack2<false>(acc.z * g, acc.w * g));
+      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + b * a.osb + (int64_t)(h0 + h) * a.osh + 4 * tid) = pk;
+      if (a.lse && tid == 0) a.lse[(int64_t)b * a.heads + h0 + h] = lse2 / kLog2e;
+    }
+    __syncthreads();
+  }
+}
+
+// column tiles of 8 heads a CTA takes: the accumulators of 16 heads at D = 256 would not fit registers
+int tiles_of(int G, int D) { return G > 8 && D <= 128 ? 2 : 1; }
+
+template <int FMT, int D, int NT>
+moe_status_t go(AttnArgs &a, cudaStream_t stream, int *launches) {
+  using S = Shape<FMT, D, NT>;
+  const int smem = S::kFixed + (a.B + 1) * 4;
+  static int occ = 0, sms = 0, occ_smem = 0;  // of this kernel on this device
+  auto kern = attn_kernel<FMT, D, NT>;
+  if (occ == 0 || occ_smem != smem) {
+    int dev = 0, n = 0, o = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kFixed + (kMaxB + 1) * 4) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, kern, kW * 32, smem) != cudaSuccess || o < 1)
+      return MOE_ERR_CUDA;
+    occ = o;
+    occ_smem = smem;
+    sms = n;
+  }
+  const int64_t bound = (int64_t)a.B * a.kv_heads * a.GB *
+                        ((a.window > 0 ? std::min<int64_t>(a.window + 15, (int64_t)a.max_pages * a.page)
+                                       : (int64_t)a.max_pages * a.page) / 16 + 1);
+  a.min_per = kW;
+  a.ctas = (int)std::min<int64_t>(std::min(sms * occ, kMaxCtas), (bound + a.min_per - 1) / a.min_per);
+  if (launch_pdl(kern, dim3(a.ctas), dim3(kW * 32), smem, stream, a) != cudaSuccess) return MOE_ERR_CUDA;
+  if (launches) ++*launches;
+  if (a.ctas > 1) {
+    const int64_t groups = (int64_t)a.B * a.kv_heads * a.GB;
+    const dim3 grid((unsigned)groups, groups <= 2048 ? (unsigned)std::min(a.G, S::kHeads) : 1u);
+    if (launch_pdl(attn_join_kernel<D, NT>, grid, dim3(256), 0, stream, a) != cudaSuccess) return MOE_ERR_CUDA;
+    if (launches) ++*launches;
+  }
+  return MOE_OK;
+}
+
+template <int FMT>
+moe_status_t by_dim(AttnArgs &a, int D, cudaStream_t stream, int *launches) {
+  const int nt = tiles_of(a.G, D);
+  if (D == 64) return nt == 1 ? go<FMT, 64, 1>(a, stream, launches) : go<FMT, 64, 2>(a, stream, launches);
+  if (D == 128) return nt == 1 ? go<FMT, 128, 1>(a, stream, launches) : go<FMT, 128, 2>(a, stream, launches);
+  return go<FMT, 256, 1>(a, stream, launches);
+}
+
+inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+}  // namespace
+
+size_t attn_workspace(int G, int D) {
+  const size_t heads = 8 * (size_t)tiles_of(G, D);
+  return up256(MOE_STATUS_BYTES) + up256((kMaxB + 3) * 4) + up256(2 * kMaxCtas * heads * 4) +
+         up256(2 * kMaxCtas * heads * D * 4);
+}
+
+moe_status_t launch_attn_decode(const void *q, int q_type, int64_t qsb, int64_t qsh, const moe_kv_cache_t &c,
+                                const int32_t *table, int64_t ts, int max_pages, const int32_t *lens, int B,
+                                int heads, float scale, int window, const float *sinks, void *out, int64_t osb,
+                                int64_t osh, float *lse, void *ws, cudaStream_t stream, int *launches) {
+  if (B == 0) return MOE_OK;
+  if (B > kMaxB) return MOE_ERR_UNSUPPORTED;
+  AttnArgs a = {};
+  a.q = q;
+  a.data = static_cast<const uint8_t *>(c.data);
+  a.table = table;
+  a.lens = lens;
+  a.sinks = sinks;
+  a.out = out;
+  a.lse = lse;
+  a.qsb = qsb;
+  a.qsh = qsh;
+  a.osb = osb;
+  a.osh = osh;
+  a.ts = ts;
+  a.q_type = q_type;
+  a.B = B;
+  a.heads = heads;
+  a.kv_heads = c.kv_heads;
+  a.G = heads / c.kv_heads;
+  const int H = 8 * tiles_of(a.G, c.head_dim);
+  a.GB = (a.G + H - 1) / H;
+  a.window = window;
+  a.page = c.page_size;
+  a.pages = c.num_pages;
+  a.max_pages = max_pages;
+  a.scale = scale * kLog2e;
+  uint8_t *w = static_cast<uint8_t *>(ws);
+  a.status = reinterpret_cast<unsigned int *>(w);
+  w += up256(MOE_STATUS_BYTES);
+  a.per = reinterpret_cast<int64_t *>(w);
+  a.starts = reinterpret_cast<int *>(w + 8);
+  w += up256((kMaxB + 3) * 4);
+  a.part_lse = reinterpret_cast<float *>(w);
+  w += up256(2 * kMaxCtas * (size_t)H * 4);
+  a.part_o = reinterpret_cast<float *>(w);
+  switch (c.fmt) {
+    case MOE_KV_BF16: return by_dim<MOE_KV_BF16>(a, c.head_dim, stream, launches);
+    case MOE_KV_FP16: return by_dim<MOE_KV_FP16>(a, c.head_dim, stream, launches);
+    case MOE_KV_FP8: return by_dim<MOE_KV_FP8>(a, c.head_dim, stream, launches);
+    default: return by_dim<MOE_KV_NVFP4>(a, c.head_dim, stream, launches);
+  }
+}
+
+}  // namespace moe4

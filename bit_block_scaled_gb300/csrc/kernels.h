@@ -74,6 +74,32 @@ moe_status_t forward_fixed_workspace(const uint16_t *x, const float *logits, con
                                      uint16_t *out, uint32_t *status_out, void *ws, size_t ws_bytes,
                                      cudaStream_t st);
 
+// Kernels launched by the last call on this thread (moe_last_launch_count).
+int *launch_counter();
+
+moe_status_t launch_group_route(const void *logits, int type, int64_t ld, const float *bias, int T, int E, int k,
+                                const moe_router_t &r, int32_t *ids, float *weights, cudaStream_t stream,
+                                int *launches);
+
+moe_status_t launch_residual_norm(const void *z, int64_t zs, const void *res, int64_t rs, const void *gate,
+                                  int64_t gst, int64_t gsh, int T, int H, int type, int res_type,
+                                  const moe_norm_t *post, float alpha, void *h, int64_t hs, const moe_norm_t *pre,
+                                  void *y, int64_t ys, cudaStream_t stream, int *launches);
+
+moe_status_t launch_kv_write(const void *k, const void *v, int type, int64_t kst, int64_t ksh, int64_t vst,
+                             int64_t vsh, const int32_t *slots, int T, const moe_kv_cache_t &c, unsigned int *status,
+                             cudaStream_t stream, int *launches);
+moe_status_t launch_kv_read(const moe_kv_cache_t &c, const int32_t *slots, int n, void *ko, void *vo, int type,
+                            int64_t kst, int64_t ksh, int64_t vst, int64_t vsh, unsigned int *status,
+                            cudaStream_t stream, int *launches);
+
+// Workspace bytes for groups of G query heads.
+size_t attn_workspace(int G, int D);
+moe_status_t launch_attn_decode(const void *q, int q_type, int64_t qsb, int64_t qsh, const moe_kv_cache_t &c,
+                                const int32_t *table, int64_t ts, int max_pages, const int32_t *lens, int B,
+                                int heads, float scale, int window, const float *sinks, void *out, int64_t osb,
+                                int64_t osh, float *lse, void *ws, cudaStream_t stream, int *launches);
+
 moe_status_t launch_unpermute(const uint16_t *y, const int32_t *row_pos, int T, int k, int H, int P_max,
                               uint16_t *out, unsigned int *status, cudaStream_t stream, int *launches);
 

@@ -347,6 +347,170 @@ moe_status_t moe_import_gptq_int4(const int32_t *qweight, const int32_t *qzeros,
 moe_status_t moe_import_modelopt_global_scale(float weight_scale_2, int E,
                                               float *gscale);
 
+/* ---------------------------------------------------------------------------
+ * The rest of a decoder block around the layer: grouped routing, the norms
+ * before and after a block, a paged key-value cache in few bits, and the
+ * attention of one new token over it. They follow the conventions above,
+ * except that tensors may have strides where a stride is an argument (in
+ * elements; the innermost dimension is always contiguous). There is no
+ * counterpart on the source pages.
+ * ------------------------------------------------------------------------- */
+
+typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_dtype_t;
+
+/* Scores of the grouped router: softmax over all E experts, or the sigmoid. */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
+
+/* A group's score: its largest selection score, or the sum of the two largest
+ * s + bias (groups of at least two experts). */
+typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score_t;
+
+typedef struct {
+  int32_t score;       /* moe_score_t                                          */
+  int32_t n_group;     /* experts are n_group runs of E / n_group; 1..32       */
+  int32_t topk_group;  /* groups kept, 1..n_group                              */
+  int32_t group_score; /* moe_group_score_t                                    */
+  int32_t renormalize; /* weights divided by their sum over the chosen         */
+  float scale;         /* factor on the weights, after that                    */
+} moe_router_t;
+
+/* Routing with groups. l = logits[t] (bf16, fp16 or fp32, rows `ld` apart),
+ * s = softmax(l) or sigmoid(l). The selection score is c = s + sel_bias (fp32
+ * [E]), or the logit itself when sel_bias is NULL (both scores rise with it).
+ * The topk_group groups of the largest group score are kept, then the top_k
+ * experts of the largest c in them; equal scores go to the lower index. Out:
+ * topk_ids int32 [T][k] in descending c, topk_weights fp32 [T][k]: s of the
+ * chosen (the bias never enters), renormalised if asked, times scale.
+ * Scores are compared as the real numbers they are, not as rounded fp32: rows
+ * whose fp32 scores lie closer than their error are decided in 64 bits (what
+ * 64 bits do not tell apart, and no tie, may go either way).
+ * NaN and infinite logits as in moe_route_topk: NaN ranks and weighs as -inf,
+ * a softmax whose maximum is infinite is shared among the logits equal to it;
+ * renormalised weights whose sum is 0 are 1/k each.
+ * E <= 256, top_k <= min(8, topk_group * E / n_group), E % n_group = 0. */
+moe_status_t moe_route_grouped(const void *logits, int logits_type, int64_t ld,
+                               const float *sel_bias, int T, int E, int k,
+                               const moe_router_t *router, int32_t *topk_ids,
+                               float *topk_weights, void *ws, moe_stream_t stream);
+
+typedef enum { MOE_NORM_RMS = 0, MOE_NORM_LAYER = 1 } moe_norm_kind_t;
+
+/* RMS: x / sqrt(mean(x^2) + eps) * (weight + offset); LAYER: (x - mean) /
+ * sqrt(var + eps) * (weight + offset) + bias. weight and bias are [H] of
+ * `type`; NULL weight = 1 (offset is then not added), NULL bias = 0. */
+typedef struct {
+  int32_t kind; /* moe_norm_kind_t              */
+  int32_t type; /* moe_dtype_t of weight, bias  */
+  float eps;
+  float offset; /* 1 for weights stored around 0 */
+  const void *weight;
+  const void *bias;
+} moe_norm_t;
+
+/* The seam between two blocks, in one pass over each row:
+ *   u = alpha * gate * post(z);  h_out = residual + u;  y_out = pre(h)
+ * z, gate, y_out are [T][H] of `type`, residual and h_out of `res_type`
+ * (`type` or fp32); rows lie *_stride apart. gate: one value an element
+ * (gate_stride_t >= H, gate_stride_h = 1), a row (gate_stride_h = 0) or a
+ * column (gate_stride_t = 0, gate_stride_h = 1); NULL = 1. post, pre: NULL =
+ * identity for post, and pre and y_out are both given or both NULL. z NULL:
+ * u = 0 (post and gate NULL too); residual NULL: 0; h_out NULL: h is not
+ * written. Sums are fp32; y_out is taken from h before its rounding to
+ * res_type. h_out may be residual and y_out may be z (same strides).
+ * 1 <= H <= 16384, any H; a multiple of 8 with such strides is fastest. */
+moe_status_t moe_residual_norm(const void *z, int64_t z_stride,
+                               const void *residual, int64_t residual_stride,
+                               const void *gate, int64_t gate_stride_t,
+                               int64_t gate_stride_h, int T, int H, int type,
+                               int res_type, const moe_norm_t *post, float alpha,
+                               void *h_out, int64_t h_stride,
+                               const moe_norm_t *pre, void *y_out,
+                               int64_t y_stride, moe_stream_t stream);
+
+/* Paged key-value cache. `data` is [num_pages][kv_heads][page_size / 16]
+ * records of moe_kv_record_bytes(fmt, head_dim) bytes; a record holds 16
+ * consecutive tokens of one head:
+ *   K codes [16][R], V codes [16][R] (R = 2 D, D or D / 2 bytes a row), then
+ *   NVFP4: K block scales E4M3 [D / 16][16], V block scales E4M3 [D / 16][16],
+ *   FP8 and NVFP4: K row exponents [16], V row exponents [16] (bytes).
+ * Byte p of the codes of token i lies at (i * R + p) ^ (16 f(i)), where f(i)
+ * is i & 7 for R >= 128, i & 6 for R = 64 and (i >> 1) & 2 for R = 32: the
+ * 16-byte pieces of every 128 bytes in an order that lets the lanes of a warp
+ * read a copy of the record in shared memory without bank conflicts.
+ * Values: BF16, FP16 as they are; FP8: E4M3 code * 2^(row exponent - 127);
+ * NVFP4: E2M1 code (two a byte, the even index in the low nibble) * E4M3
+ * block scale of its 16 values * 2^(row exponent - 127). */
+typedef enum { MOE_KV_BF16 = 0, MOE_KV_FP16 = 1, MOE_KV_FP8 = 2, MOE_KV_NVFP4 = 3 } moe_kv_format_t;
+
+typedef struct {
+  int32_t fmt; /* moe_kv_format_t                                      */
+  int32_t num_pages, page_size; /* page_size a multiple of 16, <= 4096;
+                                   num_pages * page_size < 2^31        */
+  int32_t kv_heads, head_dim;   /* head_dim 64, 128 or 256             */
+  void *data;
+} moe_kv_cache_t;
+
+/* Bytes of one record, 0 for a format or head_dim that is not built. Host only. */
+int64_t moe_kv_record_bytes(int fmt, int head_dim);
+
+/* Writes the keys and values [T][kv_heads][D] (of `type`; element strides
+ * over tokens and heads, multiples of 8) of T tokens into the cache: token t
+ * goes to slot slots[t] = page * page_size + offset; a negative slot skips
+ * the token, one past the cache is skipped and latches MOE_ERR_BAD_INDEX. The
+ * slots of one call must be distinct. Quantisation, per token and head: the
+ * row scale r is the least power of two (exponent -127..127) with amax / r <=
+ * 448 (FP8) or 6 * 448 (NVFP4); FP8 codes are E4M3 of x / r; NVFP4 block
+ * scales are s = E4M3(amax16 / r / 6), its codes E2M1 of x / r / s, 0 where s
+ * is 0. Roundings are to nearest, ties to even, and saturate; all-zero rows
+ * have exponent 0. A row that holds a NaN or an infinity is stored as row
+ * exponent 255 with zero codes and reads back as NaN. BF16 and FP16 caches
+ * take the values rounded to their type. */
+moe_status_t moe_kv_write(const void *k, const void *v, int type,
+                          int64_t k_stride_t, int64_t k_stride_h,
+                          int64_t v_stride_t, int64_t v_stride_h,
+                          const int32_t *slots, int T, const moe_kv_cache_t *cache,
+                          void *ws, moe_stream_t stream);
+
+/* Reads tokens back: k_out, v_out [n][kv_heads][D] of `type`, strides as in
+ * moe_kv_write. A negative slot gives zeros, one past the cache gives zeros
+ * and latches MOE_ERR_BAD_INDEX. Either output may be NULL. */
+moe_status_t moe_kv_read(const moe_kv_cache_t *cache, const int32_t *slots, int n,
+                         void *k_out, void *v_out, int type, int64_t k_stride_t,
+                         int64_t k_stride_h, int64_t v_stride_t, int64_t v_stride_h,
+                         void *ws, moe_stream_t stream);
+
+/* Workspace bytes of moe_attn_decode (status word included). Host only. */
+moe_status_t moe_attn_workspace_size(int q_heads, int kv_heads, int head_dim,
+                                     size_t *bytes);
+
+/* Attention of one new token a sequence over the cache. Sequence b has
+ * seq_lens[b] cached tokens (the new one among them), token i of it in page
+ * block_table[b * table_stride + i / page_size]; query head h reads kv head
+ * h / (q_heads / kv_heads). With n = min(window, seq_lens[b]) (window 0: all)
+ *   out[b][h] = sum_i p_i v_i,  p = softmax over the last n tokens i and, if
+ *   sinks (fp32 [q_heads]) is given, one more logit sinks[h] without a value,
+ *   of the logits scale * q[b][h] . k_i.
+ * q and out are bf16 or fp16 (q_type) [B][q_heads][D] with strides (multiples
+ * of 8); a BF16 or FP16 cache takes a query of its own type. lse (fp32
+ * [B][q_heads], or NULL) receives the natural log of the sum of exponentials,
+ * the sink's included. A sequence of length 0 gives zeros, and lse = sinks[h]
+ * or -inf. A length past the table or negative is taken as the table's
+ * capacity or 0 and latches MOE_ERR_BAD_INDEX; so does a page number outside
+ * the cache, whose tokens are left out.
+ * Entries of the table past a sequence's last page are not read; what cache
+ * slots past its length hold does not matter, NaN included. ws: >=
+ * moe_attn_workspace_size bytes, its content need not be kept between calls
+ * (the status word is). q_heads a multiple of kv_heads, at most 128 for each;
+ * B <= 4096. Deterministic: repeated calls give bit-identical outputs. */
+moe_status_t moe_attn_decode(const void *q, int q_type, int64_t q_stride_b,
+                             int64_t q_stride_h, const moe_kv_cache_t *cache,
+                             const int32_t *block_table, int64_t table_stride,
+                             int max_pages, const int32_t *seq_lens, int B,
+                             int q_heads, float scale, int window,
+                             const float *sinks, void *out, int64_t out_stride_b,
+                             int64_t out_stride_h, float *lse, void *ws,
+                             size_t ws_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
