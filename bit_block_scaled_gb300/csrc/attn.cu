@@ -23,8 +23,10 @@
 //    never touch them: the key's multiplies its scores, the value's is added
 //    to the exponent of its probabilities. The query is scaled by a power of
 //    two into f16 range.
-//  - The maximum is lazy: it moves only when a score passes it by 8 (in log2),
-//    so the accumulators are seldom rescaled, and p <= 2^8 loses nothing.
+//  - The maximum is lazy: it moves only when a score passes it by 4 (in log2),
+//    so the accumulators are seldom rescaled. Where p is multiplied as f16 it
+//    is lifted by 2^11, to at most 2^15: what falls under f16's normal range
+//    (relative precision is lost there) is 2^-25 of the largest.
 //
 // Work is split evenly over all records of all sequences and heads, whatever
 // their lengths: CTA c takes records [c * per, (c + 1) * per) of the sequence
@@ -48,7 +50,7 @@ constexpr int kW = 4;              // warps of a CTA
 constexpr int kMaxCtas = 640;      // partial outputs the workspace holds: two a CTA
 constexpr int kMaxB = 4096;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kSlack = 8.f;      // lazy maximum, log2
+constexpr float kSlack = 4.f;      // lazy maximum, log2
 
 struct AttnArgs {
   const void *q;
@@ -160,6 +162,7 @@ template <int FMT, int D, int NT>
 struct Shape {
   static constexpr bool kBf = FMT == MOE_KV_BF16;
   static constexpr bool kQuant = FMT >= MOE_KV_FP8;
+  static constexpr float kLift = kBf ? 0.f : 11.f;  // log2, of the p that are multiplied
   static constexpr int kRow = kv_row(FMT, D);
   static constexpr int kRec = kv_record(FMT, D);
   static constexpr int kStage = (kRec + 127) / 128 * 128;
@@ -506,12 +509,12 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
           float w[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const float ref = m[nt][x & 1] == -INFINITY ? 0.f : m[nt][x & 1];
+            const float ref = m[nt][x & 1] == -INFINITY ? 0.f : m[nt][x & 1] - (S::kQuant ? 0.f : S::kLift);
             const float p = ex2(sc[nt][x] - ref);
             l[nt][x & 1] += p;
             w[x] = p;
             if (S::kQuant) {
-              const float rw = mw[nt][x & 1] == -INFINITY ? 0.f : mw[nt][x & 1];
+              const float rw = mw[nt][x & 1] == -INFINITY ? 0.f : mw[nt][x & 1] - S::kLift;
               w[x] = ex2(tw[nt][x] - rw);
             }
           }
@@ -602,9 +605,9 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
         const int h = 8 * nt + 2 * c + x;
         if (r == 0) {
           float *ml = join_ml + (warp * S::kHeads + h) * 3;
-          ml[0] = m[nt][x];
+          ml[0] = m[nt][x] - (S::kQuant ? 0.f : S::kLift);
           ml[1] = s;
-          ml[2] = S::kQuant ? mw[nt][x] : m[nt][x];
+          ml[2] = (S::kQuant ? mw[nt][x] : m[nt][x]) - S::kLift;
         }
         float *po = join_o + (warp * S::kHeads + h) * S::kLdo;
 #pragma unroll

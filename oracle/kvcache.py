@@ -113,13 +113,14 @@ def values(data, fmt, D):
 
 def attend(q, keys, vals, table, lens, scale, window=0, sinks=None):
     """q [B, heads, D]; keys, vals as from ``values``; page numbers outside the cache leave their tokens out.
-    Returns out [B, heads, D], lse [B, heads], and sum_i p_i |v_i| and the largest scale * sum |q||k| (for error bounds)."""
+    Returns out [B, heads, D], lse [B, heads], and for error bounds sum_i p_i |v_i|, the largest scale * sum |q||k|
+    and n times the largest p_i max |v_i|."""
     q = np.asarray(q, dtype=np.float64)
     B, heads, D = q.shape
     P, H, page, _ = keys.shape
     G = heads // H
     out, mag = np.zeros((B, heads, D)), np.zeros((B, heads, D))
-    lse, size = np.full((B, heads), -np.inf), np.zeros((B, heads))
+    lse, size, peak = np.full((B, heads), -np.inf), np.zeros((B, heads)), np.zeros((B, heads))
     for b in range(B):
         n = int(min(max(lens[b], 0), table.shape[1] * page))
         at = [i for i in range(max(0, n - window) if window else 0, n) if 0 <= table[b, i // page] < P]
@@ -139,4 +140,5 @@ def attend(q, keys, vals, table, lens, scale, window=0, sinks=None):
                 out[b, h] = (p / tot) @ v
                 mag[b, h] = (p / tot) @ np.abs(v)
                 size[b, h] = abs(scale) * (np.abs(k) @ np.abs(q[b, h])).max()
-    return out, lse, mag, size
+                peak[b, h] = len(at) * (p / tot * np.abs(v).max(axis=1)).max()
+    return out, lse, mag, size, peak

@@ -97,11 +97,11 @@ def test_attention_closed_forms():
     keys, vals = np.zeros((1, 1, 16, 2)), np.zeros((1, 1, 16, 2))
     vals[0, 0, :3, 0] = [1.0, 2.0, 6.0]
     q = np.zeros((1, 1, 2))
-    out, lse, _, _ = KV.attend(q, keys, vals, np.array([[0]]), [3], 1.0)
+    out, lse, _, _, _ = KV.attend(q, keys, vals, np.array([[0]]), [3], 1.0)
     assert np.allclose(out[0, 0], [3.0, 0.0]) and np.allclose(lse, np.log(3))
-    out, lse, _, _ = KV.attend(q, keys, vals, np.array([[0]]), [3], 1.0, window=1, sinks=np.array([0.0]))
+    out, lse, _, _, _ = KV.attend(q, keys, vals, np.array([[0]]), [3], 1.0, window=1, sinks=np.array([0.0]))
     assert np.allclose(out[0, 0], [3.0, 0.0]) and np.allclose(lse, np.log(2))
-    out, lse, _, _ = KV.attend(q, keys, vals, np.array([[0]]), [0], 1.0)
+    out, lse, _, _, _ = KV.attend(q, keys, vals, np.array([[0]]), [0], 1.0)
     assert np.all(out == 0) and np.all(lse == -np.inf)
-    out, lse, _, _ = KV.attend(q, keys, vals, np.array([[7]]), [3], 1.0)
+    out, lse, _, _, _ = KV.attend(q, keys, vals, np.array([[7]]), [3], 1.0)
     assert np.all(out == 0) and np.all(lse == -np.inf)
