@@ -29,11 +29,14 @@
 //    (relative precision is lost there) is 2^-25 of the largest.
 //
 // Work is split evenly over all records of all sequences and heads, whatever
-// their lengths: CTA c takes records [c * per, (c + 1) * per) of the sequence
-// of (sequence, head, record). A (sequence, head) that falls to one CTA is
-// written at once; otherwise each CTA writes its partial output and log-sum,
-// and a second kernel joins them. Both orders are fixed, so results do not
-// vary from run to run.
+// their lengths. Lay the records out one (sequence, head) after another, each
+// preceded by kLead empty units, which stand for the time that beginning and
+// ending one takes; CTA c takes units [c * per, (c + 1) * per) and each of its
+// warps a quarter of them. A (sequence, head) that falls to one warp is written
+// from its registers; what is shared by warps of a CTA is joined in shared
+// memory, once at the end; what is shared by CTAs goes to the workspace as a
+// partial output with its log-sum, and a second kernel joins those. All orders
+// are fixed, so results do not vary from run to run.
 #include <algorithm>
 
 #include "common.cuh"
@@ -49,6 +52,7 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kW = 4;              // warps of a CTA
 constexpr int kMaxCtas = 640;      // partial outputs the workspace holds: two a CTA
 constexpr int kMaxB = 4096;
+constexpr int kLead = 4;           // empty units before each (sequence, head)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 4.f;      // lazy maximum, log2
 
@@ -60,12 +64,12 @@ struct AttnArgs {
   void *out;
   float *lse;
   unsigned int *status;
-  int64_t *per;      // records a CTA
+  int64_t *per;      // units a CTA
   int *starts;       // [B + 1] first record of each sequence, as if of one head
   float *part_o;     // [2 kMaxCtas][NH][D]
   float *part_lse;   // [2 kMaxCtas][NH], log2
   int64_t qsb, qsh, osb, osh, ts;
-  int q_type, B, heads, kv_heads, G, GB, window, page, pages, max_pages, ctas, min_per;
+  int q_type, B, heads, kv_heads, G, GB, window, page, pages, max_pages, ctas;
   float scale;       // scale * log2 e
 };
 
@@ -142,6 +146,12 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                : "memory");
 }
 
+// Units of a CTA: a multiple of the warps.
+__device__ __forceinline__ int64_t units_a_cta(int64_t total, int ctas) {
+  const int64_t each = (total + ctas - 1) / ctas;
+  return (each + kW - 1) / kW * kW;
+}
+
 // Tokens of sequence b that are read: [first, len), in records [lo, lo + n), n >= 1.
 struct Span {
   int len, first, lo, n;
@@ -170,40 +180,53 @@ struct Shape {
   static constexpr int kHeads = 8 * NT;
   static constexpr int kLdo = D + 4;  // row of the joining buffer, padded against bank conflicts
   static constexpr int kJoin = kW * kHeads * kLdo * 4;
-  static constexpr int kMl = kW * kHeads * 3 * 4;
+  static constexpr int kMl = 2 * kW * kHeads * 3 * 4;
+  static_assert(kStages * kStage >= kHeads * kLdo * 4, "a partial output fits the ring");
   static constexpr int kRing = kW * kStages * kStage;
   static constexpr int kFixed = kRing + kJoin + kMl + kW * kStages * 8;
 };
 
-// A warp's way through its records: the records first + warp, + kW, ... of
-// each (sequence, head) of the CTA's range, one after another.
-struct Cursor {
-  int64_t u;     // work position of the current (sequence, head)'s first record in this range
-  int b, hb;     // sequence; kv head * GB + block of heads
-  int first;     // the range's first record in it (relative to the span)
-  int rec, end;  // next record of this warp in it; end of the range in it
+// One (sequence, head) of a warp's range.
+struct Seg {
+  int64_t at;         // its first unit
+  int b, hb;          // sequence; kv head * GB + block of heads
+  int rec, end;       // this warp's records of it, relative to the span
   Span s;
 };
+
+// log2-sum `lse2` with the sink's logit, and the factor that the output takes.
+__device__ __forceinline__ float with_sink(const AttnArgs &a, int head, float lse2, float &g) {
+  if (!a.sinks) return lse2;
+  const float sk = a.sinks[head] * kLog2e;
+  const float top = fmaxf(lse2, sk);
+  if (top == -INFINITY) return lse2;
+  const float all = top + log2f(ex2(lse2 - top) + ex2(sk - top));
+  if (lse2 != -INFINITY) g *= ex2(lse2 - all);
+  return all;
+}
 
 template <int FMT, int D, int NT>
 __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
   using S = Shape<FMT, D, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
-  uint8_t *ring = smem;
-  float *join_o = reinterpret_cast<float *>(smem + S::kRing);
-  float *join_ml = reinterpret_cast<float *>(smem + S::kRing + S::kJoin);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int r = lane >> 2, c = lane & 3;
+  // ring of records; once it is drained, the warp's last partial output
+  uint8_t *ring = smem + warp * S::kStages * S::kStage;
+  const uint32_t ring32 = smem_u32(ring);
+  float *join_o = reinterpret_cast<float *>(smem + S::kRing);                // [kW] first partial outputs
+  float *join_ml = reinterpret_cast<float *>(smem + S::kRing + S::kJoin);    // [2 kW][heads][3]
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kRing + S::kJoin + S::kMl);
   int *start = reinterpret_cast<int *>(smem + S::kFixed);  // [B + 1] first record of each sequence
   __shared__ int warp_sum[kW];
-  __shared__ int total_s;
+  __shared__ int seg_of[kW][2], ends0[kW];  // (sequence, head) of each warp's first and last partial, or -1
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int r = lane >> 2, c = lane & 3;
   const uint32_t bar0 = smem_u32(bars + warp * S::kStages);
   if (lane == 0) {
 #pragma unroll
     for (int i = 0; i < S::kStages; ++i) mbar_init(bar0 + 8 * i, 1);
     fence_mbar_init();
+    seg_of[warp][0] = seg_of[warp][1] = -1;
   }
   pdl_wait();
   pdl_trigger();
@@ -235,58 +258,84 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
     if (b < a.B) start[b] = before + x - n;
     __syncthreads();
   }
-  if (tid == 0) {
-    start[a.B] = base;
-    total_s = base;
-  }
+  if (tid == 0) start[a.B] = base;
   __syncthreads();
   const int HB = a.kv_heads * a.GB;
-  const int64_t total = (int64_t)total_s * HB;
-  const int64_t per = max((total + a.ctas - 1) / a.ctas, (int64_t)a.min_per);
+  const int64_t total = ((int64_t)base + (int64_t)a.B * kLead) * HB;
+  const int64_t per = units_a_cta(total, a.ctas);
   if (blockIdx.x == 0) {  // what the joining kernel needs of this
     if (tid == 0) *a.per = per;
     for (int b = tid; b <= a.B; b += kW * 32) a.starts[b] = start[b];
   }
-  const int64_t u0 = (int64_t)blockIdx.x * per, u1 = min(u0 + per, total);
-  if (u0 >= u1) return;
+  const int64_t cta0 = (int64_t)blockIdx.x * per;
+  if (cta0 >= total) return;
+  const int64_t u0 = cta0 + warp * (per / kW), u1 = min(u0 + per / kW, total);
 
-  auto enter = [&](Cursor &k, int64_t u) {  // the (sequence, head) that work position u falls in
-    k.u = u;
-    if (u >= u1) return;
+  // the records of the (sequence, head) k.b, k.hb that begins at unit k.at
+  auto fill = [&](Seg &k) {
+    k.s = span_of(a, k.b);
+    const int64_t r0 = k.at + kLead;  // unit of record 0
+    k.rec = (int)max((int64_t)0, u0 - r0);
+    k.end = (int)min((int64_t)k.s.n, u1 - r0);
+  };
+  // on to the next one; false at the end of the range
+  auto next = [&](Seg &k) {
+    k.at += k.s.n + kLead;
+    if (k.at >= u1) return false;
+    if (++k.hb == HB) {
+      k.hb = 0;
+      ++k.b;
+    }
+    fill(k);
+    return true;
+  };
+  Seg cu;
+  bool more = u0 < u1;
+  if (more) {
     int lo = 0, hi = a.B;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if ((int64_t)start[mid] * HB <= u)
+      if (((int64_t)start[mid] + (int64_t)mid * kLead) * HB <= u0)
         lo = mid;
       else
         hi = mid;
     }
-    k.b = lo;
-    k.s = span_of(a, lo);
-    const int64_t in = u - (int64_t)start[lo] * HB;
-    k.hb = (int)(in / k.s.n);
-    k.first = (int)(in % k.s.n);
-    k.rec = k.first + warp;
-    k.end = (int)min((int64_t)k.s.n, k.first + (u1 - u));
-  };
+    const int64_t at = ((int64_t)start[lo] + (int64_t)lo * kLead) * HB;
+    const int units = start[lo + 1] - start[lo] + kLead;
+    cu.b = lo;
+    cu.hb = (int)((u0 - at) / units);
+    cu.at = at + (int64_t)cu.hb * units;
+    fill(cu);
+  }
 
-  // ------------------------------------------------ issuing copies ahead
-  Cursor is;
-  enter(is, u0);
+  // ------------------------------------------------ copies, issued ahead of their use
+  Seg is = cu;
+  bool is_more = more;
   int issued = 0;          // copies issued by this warp
-  int page_ids = 0;        // lane i: page of the record 'rec_base + kW * i' of the issuing cursor
-  int rec_base = 0;
+  int ids = -1, ids_next = -1;  // pages of records batch .. batch + 31 of the issuing segment, and of the 32 after
+  int batch = 0;
+  bool fresh = true;
   unsigned missing = 0;    // ring slots whose record lies in no page (bit a stage)
+  auto page_of = [&](int rec) {
+    return rec < is.end && is.s.len > 0 ? a.table[is.b * a.ts + (is.s.lo + rec) * 16 / a.page] : -1;
+  };
   auto issue = [&]() {
-    while (is.u < u1 && is.rec >= is.end) enter(is, is.u + (is.end - is.first));
-    if (is.u >= u1) return;
-    if (is.rec == is.first + warp || is.rec >= rec_base + 32 * kW) {
-      rec_base = is.rec;
-      const int rr = rec_base + kW * lane;
-      page_ids = -1;
-      if (rr < is.end && is.s.len > 0) page_ids = a.table[is.b * a.ts + (is.s.lo + rr) * 16 / a.page];
+    while (is_more && is.rec >= is.end) {
+      is_more = next(is);
+      fresh = true;
     }
-    const int pg = __shfl_sync(kAll, page_ids, (is.rec - rec_base) / kW);
+    if (!is_more) return;
+    if (fresh) {
+      fresh = false;
+      batch = is.rec;
+      ids = page_of(batch + lane);
+      ids_next = page_of(batch + 32 + lane);
+    } else if (is.rec == batch + 32) {
+      batch = is.rec;
+      ids = ids_next;
+      ids_next = page_of(batch + 32 + lane);
+    }
+    const int pg = __shfl_sync(kAll, ids, is.rec - batch);
     const int slot = issued % S::kStages;
     const bool ok = pg >= 0 && pg < a.pages;
     if (lane == 0) {
@@ -294,8 +343,7 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
         const int off = ((is.s.lo + is.rec) * 16 % a.page) >> 4;
         const int64_t rec = ((int64_t)pg * a.kv_heads + is.hb / a.GB) * (a.page >> 4) + off;
         mbar_arrive_expect_tx(bar0 + 8 * slot, S::kRec);
-        bulk_load(smem_u32(ring) + (warp * S::kStages + slot) * S::kStage, a.data + rec * S::kRec, S::kRec,
-                  bar0 + 8 * slot);
+        bulk_load(ring32 + slot * S::kStage, a.data + rec * S::kRec, S::kRec, bar0 + 8 * slot);
       } else {
         if (is.s.len > 0) raise_status(a.status, MOE_ERR_BAD_INDEX);
         mbar_arrive(bar0 + 8 * slot);
@@ -303,7 +351,7 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
     }
     missing = ok ? missing & ~(1u << slot) : missing | (1u << slot);
     ++issued;
-    is.rec += kW;
+    ++is.rec;
   };
 #pragma unroll 1
   for (int i = 0; i < S::kStages; ++i) issue();
@@ -311,9 +359,9 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
   bool dead = false;  // a copy did not arrive in time: issue no more
   int done = 0;       // records consumed
   int dead_at = 0;    // the first that did not arrive
-  Cursor cu;
-  enter(cu, u0);
-  while (cu.u < u1) {
+  for (; more; more = next(cu)) {
+    if (cu.rec >= cu.end) continue;  // only empty units of it
+    const bool begins = cu.rec == 0, ends = cu.end == cu.s.n;
     const int kvh = cu.hb / a.GB, h0 = kvh * a.G + (cu.hb % a.GB) * S::kHeads;
     const int nh = min(S::kHeads, a.G - (cu.hb % a.GB) * S::kHeads);
     // ---- the query of this (sequence, heads): B fragments, head r of each tile
@@ -380,7 +428,7 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
     }
 
 #pragma unroll 1
-    for (; cu.rec < cu.end; cu.rec += kW) {
+    for (; cu.rec < cu.end; ++cu.rec) {
       const int slot = done % S::kStages;
       if (!dead && !mbar_wait(bar0 + 8 * slot, (done / S::kStages) & 1)) {
         if (lane == 0) raise_status(a.status, MOE_ERR_TIMEOUT);
@@ -389,7 +437,7 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
       if (!dead) dead_at = done + 1;
       dead = __any_sync(kAll, dead);
       const bool skip = dead || ((missing >> slot) & 1u);
-      const uint8_t *st = ring + (warp * S::kStages + slot) * S::kStage;
+      const uint8_t *st = ring + slot * S::kStage;
       const uint32_t st32 = smem_u32(st);
       if (!skip) {
         // ---- S^T = K Q^T
@@ -593,87 +641,130 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
       if (!dead) issue();
     }
 
-    // ---- the warps' sums joined: this CTA's share of the (sequence, heads)
-    __syncthreads();  // the buffers are free
+    // ---- the sum of p over the lanes that share a head
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        float s = l[nt][x];
 #pragma unroll
-        for (int sh = 4; sh < 32; sh <<= 1) s += __shfl_xor_sync(kAll, s, sh);
-        const int h = 8 * nt + 2 * c + x;
-        if (r == 0) {
-          float *ml = join_ml + (warp * S::kHeads + h) * 3;
-          ml[0] = m[nt][x] - (S::kQuant ? 0.f : S::kLift);
-          ml[1] = s;
-          ml[2] = (S::kQuant ? mw[nt][x] : m[nt][x]) - S::kLift;
+        for (int sh = 4; sh < 32; sh <<= 1) l[nt][x] += __shfl_xor_sync(kAll, l[nt][x], sh);
+        if (!S::kQuant) mw[nt][x] = m[nt][x];
+        mw[nt][x] -= S::kLift;
+        if (!S::kQuant) m[nt][x] -= S::kLift;
+      }
+    if (begins && ends) {  // all of it: written from here
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int h = 8 * nt + 2 * c + x;
+          if (h >= nh) continue;
+          const bool none = l[nt][x] == 0.f;  // l is at least 2^-kSlack otherwise
+          float g = none ? 0.f : ex2(mw[nt][x] - m[nt][x]) / l[nt][x];
+          const float lse2 = with_sink(a, h0 + h, none ? -INFINITY : m[nt][x] + log2f(l[nt][x]), g);
+          uint16_t *po = static_cast<uint16_t *>(a.out) + cu.b * a.osb + (int64_t)(h0 + h) * a.osh;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const float v0 = o[nt][i][x] * g, v1 = o[nt][i][x + 2] * g;
+            const uint32_t pk = a.q_type == MOE_BF16 ? pack2<true>(v0, v1) : pack2<false>(v0, v1);
+            if (S::kQuant) {
+              *reinterpret_cast<uint32_t *>(po + r * (D / 8) + 2 * i) = pk;
+            } else {
+              po[16 * i + r] = (uint16_t)pk;
+              po[16 * i + 8 + r] = (uint16_t)(pk >> 16);
+            }
+          }
+          if (a.lse && r == 0) a.lse[(int64_t)cu.b * a.heads + h0 + h] = lse2 / kLog2e;
         }
-        float *po = join_o + (warp * S::kHeads + h) * S::kLdo;
+    } else {
+      // partial: one that began before this warp's range in the first place, else (the range's last) in the ring
+      const int second = begins ? 1 : 0;
+      float *po = second ? reinterpret_cast<float *>(ring) : join_o + warp * S::kHeads * S::kLdo;
+      float *ml = join_ml + (2 * warp + second) * S::kHeads * 3;
+      if (lane == 0) {
+        seg_of[warp][second] = cu.b * HB + cu.hb;
+        if (!second) ends0[warp] = ends;
+      }
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          if (!S::kQuant) {
-            po[16 * i + r] = o[nt][i][x];
-            po[16 * i + 8 + r] = o[nt][i][x + 2];
-          } else {
-            po[r * (D / 8) + 2 * i] = o[nt][i][x];
-            po[r * (D / 8) + 2 * i + 1] = o[nt][i][x + 2];
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int h = 8 * nt + 2 * c + x;
+          if (r == 0) {
+            ml[3 * h] = m[nt][x];
+            ml[3 * h + 1] = l[nt][x];
+            ml[3 * h + 2] = mw[nt][x];
+          }
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const int d = S::kQuant ? r * (D / 8) + 2 * i : 16 * i + r;
+            po[h * S::kLdo + d] = o[nt][i][x];
+            po[h * S::kLdo + d + (S::kQuant ? 1 : 8)] = o[nt][i][x + 2];
           }
         }
-      }
-    __syncthreads();
-    const bool all = cu.first == 0 && cu.end == cu.s.n;
-    const int pslot = 2 * blockIdx.x + (cu.u > u0 ? 1 : 0);
+    }
+  }
+  // a wait that ran out leaves copies in flight: wait for them, with the same limit
+  if (dead)
+    for (int i = dead_at; i < issued; ++i) mbar_wait(bar0 + 8 * (i % S::kStages), (i / S::kStages) & 1);
+
+  // ---------------- what the warps share: chains of a partial and the first partials of the warps after it
+  __syncthreads();
+  for (int lead = -1; lead < kW; ++lead) {
+    const int w0 = max(lead, 0), second = lead >= 0;
+    const int seg = seg_of[w0][second];
+    if (seg < 0) continue;
+    int last = w0;  // warp of the chain's last part
+    bool ended = !second && ends0[0];
+    while (!ended && last + 1 < kW && seg_of[last + 1][0] == seg) {
+      ++last;
+      ended = ends0[last];
+    }
+    const int b = seg / HB, hb = seg % HB;
+    const int h0 = hb / a.GB * a.G + hb % a.GB * S::kHeads, nh = min(S::kHeads, a.G - hb % a.GB * S::kHeads);
+    const bool all = second && ended;
+    const int pslot = 2 * blockIdx.x + second;
     for (int at = tid; at < nh * (D / 4); at += kW * 32) {
       const int h = at / (D / 4), d = at % (D / 4) * 4;
       float M = -INFINITY, MW = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kW; ++w) {
-        M = fmaxf(M, join_ml[(w * S::kHeads + h) * 3]);
-        MW = fmaxf(MW, join_ml[(w * S::kHeads + h) * 3 + 2]);
+      for (int w = w0; w <= last; ++w) {
+        const float *ml = join_ml + ((2 * w + (w == w0 ? second : 0)) * S::kHeads + h) * 3;
+        M = fmaxf(M, ml[0]);
+        MW = fmaxf(MW, ml[2]);
       }
       float L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
       const float Mr = M == -INFINITY ? 0.f : M, MWr = MW == -INFINITY ? 0.f : MW;
-#pragma unroll
-      for (int w = 0; w < kW; ++w) {
-        const float *ml = join_ml + (w * S::kHeads + h) * 3;
+      for (int w = w0; w <= last; ++w) {
+        const bool in_ring = w == w0 && second;
+        const float *ml = join_ml + ((2 * w + in_ring) * S::kHeads + h) * 3;
+        const float *po = in_ring ? reinterpret_cast<const float *>(smem + w * S::kStages * S::kStage)
+                                  : join_o + w * S::kHeads * S::kLdo;
         L += ml[1] * ex2(ml[0] - Mr);
         const float f = ex2(ml[2] - MWr);
-        const float4 v = *reinterpret_cast<const float4 *>(join_o + (w * S::kHeads + h) * S::kLdo + d);
+        const float4 v = *reinterpret_cast<const float4 *>(po + h * S::kLdo + d);
         acc[0] += v.x * f;
         acc[1] += v.y * f;
         acc[2] += v.z * f;
         acc[3] += v.w * f;
       }
       float lse2 = L == 0.f ? -INFINITY : Mr + log2f(L);
-      float g = L == 0.f ? 0.f : ex2(MWr - Mr) / L;  // L is at least 2^-kSlack
+      float g = L == 0.f ? 0.f : ex2(MWr - Mr) / L;
       if (all) {
-        if (a.sinks) {  // one more logit without a value
-          const float sk = a.sinks[h0 + h] * kLog2e;
-          const float top = fmaxf(lse2, sk);
-          const float sum = ex2(lse2 - top) + ex2(sk - top);
-          const float with = top == -INFINITY ? -INFINITY : top + log2f(sum);
-          if (L != 0.f) g *= top == -INFINITY ? 1.f : ex2(lse2 - with);
-          lse2 = with;
-        }
+        lse2 = with_sink(a, h0 + h, lse2, g);
         uint2 pk;
         if (a.q_type == MOE_BF16)
           pk = make_uint2(pack2<true>(acc[0] * g, acc[1] * g), pack2<true>(acc[2] * g, acc[3] * g));
         else
           pk = make_uint2(pack2<false>(acc[0] * g, acc[1] * g), pack2<false>(acc[2] * g, acc[3] * g));
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + cu.b * a.osb + (int64_t)(h0 + h) * a.osh + d) = pk;
-        if (a.lse && d == 0) a.lse[(int64_t)cu.b * a.heads + h0 + h] = lse2 / kLog2e;
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + b * a.osb + (int64_t)(h0 + h) * a.osh + d) = pk;
+        if (a.lse && d == 0) a.lse[(int64_t)b * a.heads + h0 + h] = lse2 / kLog2e;
       } else {
         *reinterpret_cast<float4 *>(a.part_o + ((int64_t)pslot * S::kHeads + h) * D + d) =
             make_float4(acc[0] * g, acc[1] * g, acc[2] * g, acc[3] * g);
         if (d == 0) a.part_lse[pslot * S::kHeads + h] = lse2;
       }
     }
-    enter(cu, cu.u + (cu.end - cu.first));
   }
-  // a wait that ran out leaves copies in flight: wait for them, with the same limit
-  if (dead)
-    for (int i = dead_at; i < issued; ++i) mbar_wait(bar0 + 8 * (i % S::kStages), (i / S::kStages) & 1);
 }
 
 // Joins the partial outputs of one (sequence, kv head, block of heads):
@@ -692,14 +783,13 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
   const int b = blockIdx.x / HB, hb = blockIdx.x % HB;
   const int64_t per = *a.per;
   const int s0 = a.starts[b], n = a.starts[b + 1] - s0;
-  const int64_t first = (int64_t)s0 * HB + (int64_t)hb * n, last = first + n - 1;
+  const int64_t first = ((int64_t)s0 + (int64_t)b * kLead) * HB + (int64_t)hb * (n + kLead) + kLead, last = first + n - 1;
   const int c0 = (int)(first / per), c1 = (int)(last / per);
   if (c0 == c1) return;
   const int parts = c1 - c0 + 1;
   const int nh = min(kHeads, a.G - hb % a.GB * kHeads);
   const int h0 = hb / a.GB * a.G + hb % a.GB * kHeads;
-  // CTA c0 reached it after its own start unless it begins there
-  const int slot0 = 2 * c0 + (first > c0 * per ? 1 : 0);
+  const int slot0 = 2 * c0 + 1;  // it begins in CTA c0, and in the others it began before
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   for (int h = blockIdx.y; h < nh; h += gridDim.y) {
     float top = -INFINITY;
@@ -735,13 +825,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
     float lse2 = sum == 0.f ? -INFINITY : ref + log2f(sum);
     float g = sum == 0.f ? 0.f : 1.f / sum;
     if (bad) g = lse2 = __int_as_float(0x7fc00000);
-    if (a.sinks) {
-      const float sk = a.sinks[h0 + h] * kLog2e;
-      const float hi = fmaxf(lse2, sk);
-      const float with = hi == -INFINITY ? -INFINITY : hi + log2f(ex2(lse2 - hi) + ex2(sk - hi));
-      if (sum != 0.f && hi != -INFINITY) g *= ex2(lse2 - with);
-      lse2 = with;
-    }
+    lse2 = with_sink(a, h0 + h, lse2, g);
     const int grp = tid / (D / 4), d4 = tid % (D / 4);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
@@ -801,8 +885,7 @@ moe_status_t go(AttnArgs &a, cudaStream_t stream, int *launches) {
   const int64_t bound = (int64_t)a.B * a.kv_heads * a.GB *
                         ((a.window > 0 ? std::min<int64_t>(a.window + 15, (int64_t)a.max_pages * a.page)
                                        : (int64_t)a.max_pages * a.page) / 16 + 1);
-  a.min_per = kW;
-  a.ctas = (int)std::min<int64_t>(std::min(sms * occ, kMaxCtas), (bound + a.min_per - 1) / a.min_per);
+  a.ctas = (int)std::min<int64_t>(std::min(sms * occ, kMaxCtas), (bound + kW - 1) / kW);
   if (launch_pdl(kern, dim3(a.ctas), dim3(kW * 32), smem, stream, a) != cudaSuccess) return MOE_ERR_CUDA;
   if (launches) ++*launches;
   if (a.ctas > 1) {
