@@ -176,8 +176,20 @@ struct Shape {
   static constexpr int kRow = kv_row(FMT, D);
   static constexpr int kRec = kv_record(FMT, D);
   static constexpr int kStage = (kRec + 127) / 128 * 128;
-  static constexpr int kStages = kRec >= 16384 ? 2 : kRec >= 8192 ? 2 : kRec >= 4096 ? 3 : 4;
+  // records in flight a warp, and how many of them are asked for at a time
+  static constexpr int kStages = kRec >= 8192 ? 2 : kRec >= 4096 ? 3 : kRec >= 2048 ? 4 : 8;
+  static constexpr int kGroup = kStages / 2;
   static constexpr int kHeads = 8 * NT;
+  // FP8, NVFP4: codes of a lane's load of a key (16 bytes, 8 of a 32-byte row), and of a value
+  static constexpr int kKeyCodes = (kRow >= 64 ? 16 : 8) * (FMT == MOE_KV_NVFP4 ? 2 : 1);
+  static constexpr int kValCodes = D / 8 < 16 * (FMT == MOE_KV_NVFP4 ? 2 : 1) ? D / 8 : 16 * (FMT == MOE_KV_NVFP4 ? 2 : 1);
+  // column of code e of a key's lane c (of 4), and of a value's lane r (of 8): loads lie next to each other by lane
+  __host__ __device__ static constexpr int key_col(int c, int e) {
+    return e / kKeyCodes * 4 * kKeyCodes + c * kKeyCodes + e % kKeyCodes;
+  }
+  __host__ __device__ static constexpr int val_col(int r, int e) {
+    return e / kValCodes * 8 * kValCodes + r * kValCodes + e % kValCodes;
+  }
   static constexpr int kLdo = D + 4;  // row of the joining buffer, padded against bank conflicts
   static constexpr int kJoin = kW * kHeads * kLdo * 4;
   static constexpr int kMl = 2 * kW * kHeads * 3 * 4;
@@ -210,7 +222,10 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
   using S = Shape<FMT, D, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int r = lane >> 2, c = lane & 3;
+  const int r = lane >> 2, c = lane & 3;  // row and column of mma fragments
+  // Tokens that rows r and r + 8 of S^T stand for: r and r + 8, or for FP8 and NVFP4 two neighbours, in an order in
+  // which the lanes of every load of keys and of values fall into different banks.
+  const int key0 = !S::kQuant ? r : r & 1 ? 8 + 2 * ((r >> 1) ^ 2) : r;
   // ring of records; once it is drained, the warp's last partial output
   uint8_t *ring = smem + warp * S::kStages * S::kStage;
   const uint32_t ring32 = smem_u32(ring);
@@ -311,37 +326,36 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
   // ------------------------------------------------ copies, issued ahead of their use
   Seg is = cu;
   bool is_more = more;
-  int issued = 0;          // copies issued by this warp
+  int issued = 0;  // copies issued by this warp
   int ids = -1, ids_next = -1;  // pages of records batch .. batch + 31 of the issuing segment, and of the 32 after
   int batch = 0;
   bool fresh = true;
   unsigned missing = 0;    // ring slots whose record lies in no page (bit a stage)
+  const int page16 = a.page >> 4;
   auto page_of = [&](int rec) {
-    return rec < is.end && is.s.len > 0 ? a.table[is.b * a.ts + (is.s.lo + rec) * 16 / a.page] : -1;
+    return rec < is.end && is.s.len > 0 ? a.table[is.b * a.ts + (is.s.lo + rec) / page16] : -1;
   };
+  // asks for up to kGroup records of one segment, lane i for the i-th; the ring has room for them
   auto issue = [&]() {
     while (is_more && is.rec >= is.end) {
       is_more = next(is);
       fresh = true;
     }
     if (!is_more) return;
-    if (fresh) {
+    if (fresh || is.rec == batch + 32) {
+      ids = fresh ? page_of(is.rec + lane) : ids_next;
+      batch = is.rec;
       fresh = false;
-      batch = is.rec;
-      ids = page_of(batch + lane);
-      ids_next = page_of(batch + 32 + lane);
-    } else if (is.rec == batch + 32) {
-      batch = is.rec;
-      ids = ids_next;
       ids_next = page_of(batch + 32 + lane);
     }
-    const int pg = __shfl_sync(kAll, ids, is.rec - batch);
-    const int slot = issued % S::kStages;
-    const bool ok = pg >= 0 && pg < a.pages;
-    if (lane == 0) {
+    const int n = min(min(S::kGroup, is.end - is.rec), batch + 32 - is.rec);
+    const int pg = __shfl_sync(kAll, ids, (is.rec - batch + lane) & 31);
+    const int slot = (issued + lane) % S::kStages;
+    const bool mine = lane < n, ok = pg >= 0 && pg < a.pages;
+    if (mine) {
       if (ok) {
-        const int off = ((is.s.lo + is.rec) * 16 % a.page) >> 4;
-        const int64_t rec = ((int64_t)pg * a.kv_heads + is.hb / a.GB) * (a.page >> 4) + off;
+        const int off = (is.s.lo + is.rec + lane) % page16;
+        const int64_t rec = ((int64_t)pg * a.kv_heads + is.hb / a.GB) * page16 + off;
         mbar_arrive_expect_tx(bar0 + 8 * slot, S::kRec);
         bulk_load(ring32 + slot * S::kStage, a.data + rec * S::kRec, S::kRec, bar0 + 8 * slot);
       } else {
@@ -349,12 +363,17 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
         mbar_arrive(bar0 + 8 * slot);
       }
     }
-    missing = ok ? missing & ~(1u << slot) : missing | (1u << slot);
-    ++issued;
-    ++is.rec;
+    const unsigned lost = __ballot_sync(kAll, mine && !ok);
+    if (lost | missing)
+      for (int i = 0; i < n; ++i) {
+        const unsigned bit = 1u << ((issued + i) % S::kStages);
+        missing = (lost >> i) & 1u ? missing | bit : missing & ~bit;
+      }
+    issued += n;
+    is.rec += n;
   };
 #pragma unroll 1
-  for (int i = 0; i < S::kStages; ++i) issue();
+  for (int i = 0; i < S::kStages / S::kGroup; ++i) issue();
 
   bool dead = false;  // a copy did not arrive in time: issue no more
   int done = 0;       // records consumed
@@ -377,10 +396,8 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
         int d;
         if (!S::kQuant)
           d = (e >> 1) * 16 + (e & 1) * 8 + 2 * c;
-        else if (S::kRow == 256)
-          d = (e >> 4) * 128 + 32 * c + (e & 15) * 2;
         else
-          d = c * (D / 4) + 2 * e;
+          d = S::key_col(c, 2 * e);
         raw[e] = h < nh ? *reinterpret_cast<const uint32_t *>(qp + d) : 0u;
       }
       qs[nt][0] = qs[nt][1] = a.scale;
@@ -412,14 +429,16 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
       for (int e = 0; e < D / 8; ++e) qf[nt][e >> 1][e & 1] = raw[e];
     }
 
-    float m[NT][2], l[NT][2], mw[NT][2];  // maximum and sum of p; maximum of p times the value's row scale
+    // lazy maxima, of the scores (ref, thr) and of the scores with the value's row scale (refw, thrw): exponentials
+    // are taken against ref, a score above thr moves it
+    float ref[NT][2], thr[NT][2], refw[NT][2], thrw[NT][2], l[NT][2];
     float o[NT][D / 16][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        m[nt][x] = mw[nt][x] = -INFINITY;
-        l[nt][x] = 0.f;
+        ref[nt][x] = refw[nt][x] = l[nt][x] = 0.f;
+        thr[nt][x] = thrw[nt][x] = -INFINITY;
       }
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
@@ -430,16 +449,20 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
 #pragma unroll 1
     for (; cu.rec < cu.end; ++cu.rec) {
       const int slot = done % S::kStages;
-      if (!dead && !mbar_wait(bar0 + 8 * slot, (done / S::kStages) & 1)) {
-        if (lane == 0) raise_status(a.status, MOE_ERR_TIMEOUT);
-        dead = true;
+      if (!dead) {
+        const bool late = !mbar_wait(bar0 + 8 * slot, (done / S::kStages) & 1);
+        if (__any_sync(kAll, late)) {
+          if (late) raise_status(a.status, MOE_ERR_TIMEOUT);
+          dead = true;
+          dead_at = done;
+        }
       }
-      if (!dead) dead_at = done + 1;
-      dead = __any_sync(kAll, dead);
-      const bool skip = dead || ((missing >> slot) & 1u);
-      const uint8_t *st = ring + slot * S::kStage;
-      const uint32_t st32 = smem_u32(st);
-      if (!skip) {
+      if (!dead && !((missing >> slot) & 1u)) {
+        const uint8_t *st = ring + slot * S::kStage;
+        const uint32_t st32 = ring32 + slot * S::kStage;
+        const int pos = (cu.s.lo + cu.rec) * 16;
+        const bool edge = pos < cu.s.first || pos + 16 > cu.s.len;  // not all of its tokens are read
+        auto read = [&](int key) { return pos + key >= cu.s.first && pos + key < cu.s.len; };
         // ---- S^T = K Q^T
         float sc[NT][4];
 #pragma unroll
@@ -456,93 +479,107 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma<S::kBf>(sc[nt], af, qf[nt][ks][0], qf[nt][ks][1]);
           }
-        } else if constexpr (FMT == MOE_KV_FP8) {
-#pragma unroll
-          for (int p = 0; p < D / 64; ++p) {  // 16 codes of rows r and r + 8
-            const int col = S::kRow == 256 ? (p >> 1) * 128 + 32 * c + (p & 1) * 16 : c * (D / 4) + 16 * p;
-            const uint4 x = *reinterpret_cast<const uint4 *>(st + kv_place(S::kRow, r, col));
-            const uint4 y = *reinterpret_cast<const uint4 *>(st + kv_place(S::kRow, r + 8, col));
-            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t af[4] = {e4m3x2_f16x2(xs[k] & 0xFFFFu), e4m3x2_f16x2(ys[k] & 0xFFFFu),
-                                      e4m3x2_f16x2(xs[k] >> 16), e4m3x2_f16x2(ys[k] >> 16)};
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma<false>(sc[nt], af, qf[nt][4 * p + k][0], qf[nt][4 * p + k][1]);
-            }
-          }
         } else {
-          const uint8_t *bs = st + kv_scales_at(FMT, D);
 #pragma unroll
-          for (int p = 0; p < D / 64; ++p) {  // a block of 16: 8 bytes of rows r and r + 8
-            const int blk = c * (D / 64) + p;
-            const uint2 x = *reinterpret_cast<const uint2 *>(st + kv_place(S::kRow, r, 8 * blk));
-            const uint2 y = *reinterpret_cast<const uint2 *>(st + kv_place(S::kRow, r + 8, 8 * blk));
-            const uint32_t sx = bs[16 * blk + r], sy = bs[16 * blk + r + 8];
-            const uint32_t fx = e4m3x2_f16x2(sx | (sx << 8)), fy = e4m3x2_f16x2(sy | (sy << 8));
-            uint32_t hx[8], hy[8];
-            e2m1x8_f16(x.x, hx);
-            e2m1x8_f16(x.y, hx + 4);
-            e2m1x8_f16(y.x, hy);
-            e2m1x8_f16(y.y, hy + 4);
+          for (int p = 0; p < D / 4 / S::kKeyCodes; ++p) {  // one load of each of the two keys
+            const int col = S::key_col(c, p * S::kKeyCodes);
+            if constexpr (FMT == MOE_KV_FP8) {
+              const uint4 x = *reinterpret_cast<const uint4 *>(st + kv_place(S::kRow, key0, col));
+              const uint4 y = *reinterpret_cast<const uint4 *>(st + kv_place(S::kRow, key0 + 1, col));
+              const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t af[4] = {hmul2(hx[2 * k], fx), hmul2(hy[2 * k], fy), hmul2(hx[2 * k + 1], fx),
-                                      hmul2(hy[2 * k + 1], fy)};
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t af[4] = {e4m3x2_f16x2(xs[k] & 0xFFFFu), e4m3x2_f16x2(ys[k] & 0xFFFFu),
+                                        e4m3x2_f16x2(xs[k] >> 16), e4m3x2_f16x2(ys[k] >> 16)};
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma<false>(sc[nt], af, qf[nt][4 * p + k][0], qf[nt][4 * p + k][1]);
+                for (int nt = 0; nt < NT; ++nt) mma<false>(sc[nt], af, qf[nt][4 * p + k][0], qf[nt][4 * p + k][1]);
+              }
+            } else {
+              uint32_t xs[4], ys[4];
+              if constexpr (S::kKeyCodes == 32) {
+                *reinterpret_cast<uint4 *>(xs) = *reinterpret_cast<const uint4 *>(st + kv_place(S::kRow, key0, col / 2));
+                *reinterpret_cast<uint4 *>(ys) = *reinterpret_cast<const uint4 *>(st + kv_place(S::kRow, key0 + 1, col / 2));
+              } else {
+                *reinterpret_cast<uint2 *>(xs) = *reinterpret_cast<const uint2 *>(st + kv_place(S::kRow, key0, col / 2));
+                *reinterpret_cast<uint2 *>(ys) = *reinterpret_cast<const uint2 *>(st + kv_place(S::kRow, key0 + 1, col / 2));
+              }
+#pragma unroll
+              for (int b = 0; b < S::kKeyCodes / 16; ++b) {  // a block of 16
+                const uint32_t s2 = e4m3x2_f16x2(*reinterpret_cast<const uint16_t *>(
+                    st + kv_scales_at(FMT, D) + 16 * (col / 16 + b) + key0));  // scales of both keys
+                const uint32_t fx = __byte_perm(s2, 0, 0x1010), fy = __byte_perm(s2, 0, 0x3232);
+                uint32_t hx[8], hy[8];
+                e2m1x8_f16(xs[2 * b], hx);
+                e2m1x8_f16(xs[2 * b + 1], hx + 4);
+                e2m1x8_f16(ys[2 * b], hy);
+                e2m1x8_f16(ys[2 * b + 1], hy + 4);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const uint32_t af[4] = {hmul2(hx[2 * k], fx), hmul2(hy[2 * k], fy), hmul2(hx[2 * k + 1], fx),
+                                          hmul2(hy[2 * k + 1], fy)};
+                  const int ks = (p * (S::kKeyCodes / 16) + b) * 4 + k;
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) mma<false>(sc[nt], af, qf[nt][ks][0], qf[nt][ks][1]);
+                }
+              }
             }
           }
         }
-        // ---- scores in log2, masked; t = score + log2 of the value's row scale
-        const int pos = (cu.s.lo + cu.rec) * 16 + r;
-        const bool in0 = pos >= cu.s.first && pos < cu.s.len, in1 = pos + 8 >= cu.s.first && pos + 8 < cu.s.len;
-        float kx0 = 1.f, kx1 = 1.f, vx0 = 0.f, vx1 = 0.f;
-        if (S::kQuant) {
-          const uint8_t *ex = st + kv_exps_at(FMT, D);
-          const uint32_t k0 = ex[r], k1 = ex[r + 8], v0 = ex[16 + r], v1 = ex[24 + r];
-          const float nan = __int_as_float(0x7fc00000);
-          kx0 = k0 == 255u ? nan : __uint_as_float(k0 << 23);
-          kx1 = k1 == 255u ? nan : __uint_as_float(k1 << 23);
-          vx0 = v0 == 255u ? nan : (float)((int)v0 - 127);
-          vx1 = v1 == 255u ? nan : (float)((int)v1 - 127);
-        }
+        // ---- scores in log2; tw = score + log2 of the value's row scale
         float tw[NT][4];
-        bool grow = false;
+        float kx[2] = {1.f, 1.f}, vx[2] = {0.f, 0.f};
+        if constexpr (S::kQuant) {
+          const uint8_t *ex = st + kv_exps_at(FMT, D) + key0;
+          const uint32_t k2 = *reinterpret_cast<const uint16_t *>(ex), v2 = *reinterpret_cast<const uint16_t *>(ex + 16);
+          // 255 marks a row with a NaN, its codes are 0: 0 * 2^128 makes the key's score NaN by itself
+          kx[0] = __uint_as_float((k2 & 255u) << 23);
+          kx[1] = __uint_as_float((k2 >> 8) << 23);
+          const float nan = __int_as_float(0x7fc00000);
+          const uint32_t v0 = v2 & 255u, v1 = v2 >> 8;
+          vx[0] = v0 == 255u ? nan : __uint_as_float(0x4B000000u | v0) - 8388735.f;  // v0 - 127
+          vx[1] = v1 == 255u ? nan : __uint_as_float(0x4B000000u | v1) - 8388735.f;
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            float s = sc[nt][x] * qs[nt][x & 1];
-            if (S::kQuant) s *= x < 2 ? kx0 : kx1;
-            s = (x < 2 ? in0 : in1) ? s : -INFINITY;
-            sc[nt][x] = s;
-            grow = grow || s > m[nt][x & 1] + kSlack;
-            if (S::kQuant) {
-              tw[nt][x] = (x < 2 ? in0 : in1) ? s + (x < 2 ? vx0 : vx1) : -INFINITY;
-              grow = grow || tw[nt][x] > mw[nt][x & 1] + kSlack;
-            }
+            sc[nt][x] *= S::kQuant ? qs[nt][x & 1] * kx[x >> 1] : qs[nt][x & 1];
+            if (S::kQuant) tw[nt][x] = sc[nt][x] + vx[x >> 1];
+          }
+        if (edge) {
+          const bool in[2] = {read(key0), read(S::kQuant ? key0 + 1 : key0 + 8)};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (!in[x >> 1]) sc[nt][x] = tw[nt][x] = -INFINITY;
+        }
+        bool grow = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            grow |= fmaxf(sc[nt][x], sc[nt][x + 2]) > thr[nt][x];
+            if (S::kQuant) grow |= fmaxf(tw[nt][x], tw[nt][x + 2]) > thrw[nt][x];
           }
         if (__any_sync(kAll, grow)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              float t = fmaxf(sc[nt][x], sc[nt][x + 2]);
+              // the maximum over the record's keys, lifted where the exponentials are multiplied as f16
+              auto move = [&](float t, float lift, float &rf, float &th) {
 #pragma unroll
-              for (int sh = 4; sh < 32; sh <<= 1) t = fmaxf(t, __shfl_xor_sync(kAll, t, sh));
-              t = fmaxf(t, m[nt][x]);
-              l[nt][x] *= m[nt][x] == t ? 1.f : ex2(m[nt][x] - t);
-              float f = m[nt][x] == t ? 1.f : ex2(m[nt][x] - t);
-              m[nt][x] = t;
-              if (S::kQuant) {
-                float w = fmaxf(tw[nt][x], tw[nt][x + 2]);
-#pragma unroll
-                for (int sh = 4; sh < 32; sh <<= 1) w = fmaxf(w, __shfl_xor_sync(kAll, w, sh));
-                w = fmaxf(w, mw[nt][x]);
-                f = mw[nt][x] == w ? 1.f : ex2(mw[nt][x] - w);
-                mw[nt][x] = w;
-              }
+                for (int sh = 4; sh < 32; sh <<= 1) t = fmaxf(t, __shfl_xor_sync(kAll, t, sh));
+                const float old = th == -INFINITY ? -INFINITY : rf + lift;
+                if (!(t > old)) return 1.f;
+                rf = t - lift;
+                th = t + kSlack;
+                return ex2(old - t);
+              };
+              float f = move(fmaxf(sc[nt][x], sc[nt][x + 2]), S::kQuant ? 0.f : S::kLift, ref[nt][x], thr[nt][x]);
+              l[nt][x] *= f;
+              if (S::kQuant) f = move(fmaxf(tw[nt][x], tw[nt][x + 2]), S::kLift, refw[nt][x], thrw[nt][x]);
 #pragma unroll
               for (int i = 0; i < D / 16; ++i) {
                 o[nt][i][x] *= f;
@@ -550,46 +587,34 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
               }
             }
         }
-        // ---- p, its sum, and P^T as B fragments
+        // ---- p, its sum, and P^T as B fragments: lane (r, c) gets head r, rows 2c, 2c + 1 (pf[0]) and + 8 (pf[1])
         uint32_t pf[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float w[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const float ref = m[nt][x & 1] == -INFINITY ? 0.f : m[nt][x & 1] - (S::kQuant ? 0.f : S::kLift);
-            const float p = ex2(sc[nt][x] - ref);
+            const float p = ex2(sc[nt][x] - ref[nt][x & 1]);
             l[nt][x & 1] += p;
-            w[x] = p;
-            if (S::kQuant) {
-              const float rw = mw[nt][x & 1] == -INFINITY ? 0.f : mw[nt][x & 1] - S::kLift;
-              w[x] = ex2(tw[nt][x] - rw);
-            }
+            w[x] = S::kQuant ? ex2(tw[nt][x] - refw[nt][x & 1]) : p;
           }
           pf[nt][0] = transpose8(pack2<S::kBf>(w[0], w[1]));
           pf[nt][1] = transpose8(pack2<S::kBf>(w[2], w[3]));
         }
-        // ---- O^T += V^T P^T
-        const bool whole = __all_sync(kAll, in0 && in1);
+        // ---- O^T += V^T P^T; values of tokens that are not read may be anything (0 * NaN must not come in)
         if constexpr (!S::kQuant) {
           const int key = (lane & 7) + ((lane >> 4) << 3);
           const int half = (lane >> 3) & 1;
-          // values of tokens that are not read may be anything: 0 * NaN must not come in
           uint32_t keep[2] = {kAll, kAll};
-          if (!whole) {
-            const int k0 = (cu.s.lo + cu.rec) * 16 + 2 * c;
+          if (edge)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const int k = k0 + 8 * x;
-              keep[x] = (k >= cu.s.first && k < cu.s.len ? 0xFFFFu : 0u) |
-                        (k + 1 >= cu.s.first && k + 1 < cu.s.len ? 0xFFFF0000u : 0u);
-            }
-          }
+            for (int x = 0; x < 2; ++x)
+              keep[x] = (read(2 * c + 8 * x) ? 0xFFFFu : 0u) | (read(2 * c + 1 + 8 * x) ? 0xFFFF0000u : 0u);
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
             uint32_t af[4];
             ldsm4t(af, st32 + 16 * S::kRow + kv_place(S::kRow, key, 32 * i + 16 * half));
-            if (!whole) {
+            if (edge) {
               af[0] &= keep[0];
               af[1] &= keep[0];
               af[2] &= keep[1];
@@ -599,58 +624,104 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
             for (int nt = 0; nt < NT; ++nt) mma<S::kBf>(o[nt][i], af, pf[nt][0], pf[nt][1]);
           }
         } else {
-          // lane: columns r * D / 8 .. of tokens 2c, 2c + 1, 2c + 8, 2c + 9
+          // A register of two neighbouring columns of one value is used as it is expanded: the k index of the product
+          // is (token, column parity), with P in the even places for the even columns (o[..][2t]) and in the odd ones
+          // for the odd columns (o[..][2t + 1]). That doubles the mma count, of a pipe that is a quarter busy, and
+          // saves a byte permutation for every two values of a pipe that is the limit.
+          const int tok[4] = {2 * c, 8 + 2 * (c ^ 2), 2 * c + 1, 9 + 2 * (c ^ 2)};  // in pf[0], pf[0], pf[1], pf[1]
+          uint32_t pe[NT][4], po[NT][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              pe[nt][2 * k] = pf[nt][k] & 0xFFFFu;
+              pe[nt][2 * k + 1] = pf[nt][k] >> 16;
+              po[nt][2 * k] = pf[nt][k] << 16;
+              po[nt][2 * k + 1] = pf[nt][k] & 0xFFFF0000u;
+            }
           const uint8_t *vs = st + 16 * S::kRow;
-          const uint8_t *bs = st + kv_scales_at(FMT, D) + D;
 #pragma unroll
-          for (int p = 0; p < D / 64; ++p) {  // 8 columns at a time
-            uint32_t h[4][4];
+          for (int p = 0; p < D / 8 / S::kValCodes; ++p) {  // one load of each of the four tokens
+            const int col = S::val_col(r, p * S::kValCodes);
+            uint32_t h[4][S::kValCodes / 2];
+            if constexpr (FMT == MOE_KV_FP8) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int key = 2 * c + (x & 1) + (x >> 1) * 8;
-              const int col = r * (D / 8) + 8 * p;
-              const bool in = whole || ((cu.s.lo + cu.rec) * 16 + key >= cu.s.first &&
-                                        (cu.s.lo + cu.rec) * 16 + key < cu.s.len);
-              if constexpr (FMT == MOE_KV_FP8) {
-                const uint2 v = in ? *reinterpret_cast<const uint2 *>(vs + kv_place(S::kRow, key, col)) : make_uint2(0, 0);
-                h[x][0] = e4m3x2_f16x2(v.x & 0xFFFFu);
-                h[x][1] = e4m3x2_f16x2(v.x >> 16);
-                h[x][2] = e4m3x2_f16x2(v.y & 0xFFFFu);
-                h[x][3] = e4m3x2_f16x2(v.y >> 16);
-              } else {
-                const uint32_t v = *reinterpret_cast<const uint32_t *>(vs + kv_place(S::kRow, key, col / 2));
-                const uint32_t sb = in ? bs[(col >> 4) * 16 + key] : 0u;
-                const uint32_t f = e4m3x2_f16x2(sb | (sb << 8));
-                e2m1x8_f16(v, h[x]);
+              for (int k = 0; k < 4; ++k) {
+                uint32_t w[S::kValCodes / 4];
+                if constexpr (S::kValCodes == 16)
+                  *reinterpret_cast<uint4 *>(w) = *reinterpret_cast<const uint4 *>(vs + kv_place(S::kRow, tok[k], col));
+                else
+                  *reinterpret_cast<uint2 *>(w) = *reinterpret_cast<const uint2 *>(vs + kv_place(S::kRow, tok[k], col));
+                if (edge && !read(tok[k]))
 #pragma unroll
-                for (int y = 0; y < 4; ++y) h[x][y] = hmul2(h[x][y], f);
+                  for (int y = 0; y < S::kValCodes / 4; ++y) w[y] = 0u;
+#pragma unroll
+                for (int y = 0; y < S::kValCodes / 4; ++y) {
+                  h[k][2 * y] = e4m3x2_f16x2(w[y] & 0xFFFFu);
+                  h[k][2 * y + 1] = e4m3x2_f16x2(w[y] >> 16);
+                }
               }
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                uint32_t w[S::kValCodes / 8];
+                const uint8_t *src = vs + kv_place(S::kRow, tok[k], col / 2);
+                if constexpr (S::kValCodes == 32)
+                  *reinterpret_cast<uint4 *>(w) = *reinterpret_cast<const uint4 *>(src);
+                else if constexpr (S::kValCodes == 16)
+                  *reinterpret_cast<uint2 *>(w) = *reinterpret_cast<const uint2 *>(src);
+                else
+                  w[0] = *reinterpret_cast<const uint32_t *>(src);
+#pragma unroll
+                for (int y = 0; y < S::kValCodes / 8; ++y) e2m1x8_f16(w[y], h[k] + 4 * y);
+              }
+#pragma unroll
+              for (int b = 0; b < (S::kValCodes + 15) / 16; ++b)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {  // tokens tok[k] and tok[k + 2] are neighbours
+                  uint32_t s2 = *reinterpret_cast<const uint16_t *>(st + kv_scales_at(FMT, D) + D +
+                                                                    16 * (col / 16 + b) + tok[k]);
+                  if (edge) s2 &= (read(tok[k]) ? 0xFFu : 0u) | (read(tok[k + 2]) ? 0xFF00u : 0u);
+                  s2 = e4m3x2_f16x2(s2);
+                  const uint32_t f0 = __byte_perm(s2, 0, 0x1010), f1 = __byte_perm(s2, 0, 0x3232);
+#pragma unroll
+                  for (int y = 0; y < (S::kValCodes < 16 ? 4 : 8); ++y) {
+                    h[k][8 * b + y] = hmul2(h[k][8 * b + y], f0);
+                    h[k + 2][8 * b + y] = hmul2(h[k + 2][8 * b + y], f1);
+                  }
+                }
             }
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const uint32_t af[4] = {__byte_perm(h[0][y], h[1][y], 0x5410), __byte_perm(h[0][y], h[1][y], 0x7632),
-                                      __byte_perm(h[2][y], h[3][y], 0x5410), __byte_perm(h[2][y], h[3][y], 0x7632)};
+            for (int t = 0; t < S::kValCodes / 4; ++t)  // rows r and r + 8: pairs 2t and 2t + 1
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma<false>(o[nt][4 * p + y], af, pf[nt][0], pf[nt][1]);
-            }
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t af[4] = {h[2 * k][2 * t], h[2 * k][2 * t + 1], h[2 * k + 1][2 * t],
+                                        h[2 * k + 1][2 * t + 1]};
+                const int at = 2 * (p * (S::kValCodes / 4) + t);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  mma<false>(o[nt][at], af, pe[nt][2 * k], pe[nt][2 * k + 1]);
+                  mma<false>(o[nt][at + 1], af, po[nt][2 * k], po[nt][2 * k + 1]);
+                }
+              }
           }
         }
       }
       __syncwarp();
       ++done;
-      if (!dead) issue();
+      if (!dead && issued - done <= S::kStages - S::kGroup) issue();
     }
 
-    // ---- the sum of p over the lanes that share a head
+    // ---- the maxima as they are, and the sum of p over the lanes that share a head
+    float m[NT][2], mw[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) l[nt][x] += __shfl_xor_sync(kAll, l[nt][x], sh);
-        if (!S::kQuant) mw[nt][x] = m[nt][x];
-        mw[nt][x] -= S::kLift;
-        if (!S::kQuant) m[nt][x] -= S::kLift;
+        m[nt][x] = thr[nt][x] == -INFINITY && l[nt][x] == 0.f ? -INFINITY : ref[nt][x];
+        mw[nt][x] = !S::kQuant ? m[nt][x] : thrw[nt][x] == -INFINITY && l[nt][x] == 0.f ? -INFINITY : refw[nt][x];
       }
     if (begins && ends) {  // all of it: written from here
 #pragma unroll
@@ -663,15 +734,22 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
           float g = none ? 0.f : ex2(mw[nt][x] - m[nt][x]) / l[nt][x];
           const float lse2 = with_sink(a, h0 + h, none ? -INFINITY : m[nt][x] + log2f(l[nt][x]), g);
           uint16_t *po = static_cast<uint16_t *>(a.out) + cu.b * a.osb + (int64_t)(h0 + h) * a.osh;
+          auto pack = [&](float v0, float v1) {
+            return a.q_type == MOE_BF16 ? pack2<true>(v0 * g, v1 * g) : pack2<false>(v0 * g, v1 * g);
+          };
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            const float v0 = o[nt][i][x] * g, v1 = o[nt][i][x + 2] * g;
-            const uint32_t pk = a.q_type == MOE_BF16 ? pack2<true>(v0, v1) : pack2<false>(v0, v1);
+          for (int i = 0; i < D / 16; i += 2) {
+            const float(&e)[4] = o[nt][i];
+            const float(&f)[4] = o[nt][i + 1];
             if (S::kQuant) {
-              *reinterpret_cast<uint32_t *>(po + r * (D / 8) + 2 * i) = pk;
+              *reinterpret_cast<uint2 *>(po + S::val_col(r, 2 * i)) =
+                  make_uint2(pack(e[x], f[x]), pack(e[x + 2], f[x + 2]));
             } else {
-              po[16 * i + r] = (uint16_t)pk;
-              po[16 * i + 8 + r] = (uint16_t)(pk >> 16);
+              const uint32_t u = pack(e[x], e[x + 2]), v = pack(f[x], f[x + 2]);
+              po[16 * i + r] = (uint16_t)u;
+              po[16 * i + 8 + r] = (uint16_t)(u >> 16);
+              po[16 * i + 16 + r] = (uint16_t)v;
+              po[16 * i + 24 + r] = (uint16_t)(v >> 16);
             }
           }
           if (a.lse && r == 0) a.lse[(int64_t)cu.b * a.heads + h0 + h] = lse2 / kLog2e;
@@ -697,9 +775,9 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
           }
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
-            const int d = S::kQuant ? r * (D / 8) + 2 * i : 16 * i + r;
+            const int d = S::kQuant ? S::val_col(r, 2 * (i & ~1)) + (i & 1) : 16 * i + r;
             po[h * S::kLdo + d] = o[nt][i][x];
-            po[h * S::kLdo + d + (S::kQuant ? 1 : 8)] = o[nt][i][x + 2];
+            po[h * S::kLdo + d + (S::kQuant ? 2 : 8)] = o[nt][i][x + 2];
           }
         }
     }
