@@ -323,29 +323,50 @@ def moe_import_modelopt_global_scale(weight_scale_2, E):
 
 
 # ------------------------------------------------ around the layer: routing with groups, norms, cache, attention
+# These calls are short next to what Python costs: pointers go as plain integers, structures as themselves, and the
+# stream's handle comes without a stream object.
 _INVALID = 1
+_types = None
+_raw_stream = None
 
 
-def _dtype(t, where):
+def _setup():
+    """Types by number, and the current stream's handle by device."""
+    global _types, _raw_stream
     import torch
-    code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(t.dtype)
-    if code is None:
+    _types = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.int32: 3, torch.uint8: 4}
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda device: torch.cuda.current_stream(device).cuda_stream)
+    return load()
+
+
+_I32, _U8 = 3, 4
+
+
+def _fail(where):
+    raise MoeError(_INVALID, where)
+
+
+def _float_type(t, where):
+    code = _types.get(t.dtype, 9)
+    if code > 2:
         raise MoeError(_INVALID, f"{where}: {t.dtype}")
     return code
 
 
-def _need(ok, where):
-    if not ok:
-        raise MoeError(_INVALID, where)
+def _flat(t, code, n, where):
+    """Pointer of a contiguous tensor of n values of a type; None stays NULL."""
+    if t is None:
+        return None
+    if _types.get(t.dtype) != code or t.numel() != n or not t.is_contiguous():
+        _fail(where)
+    return t.data_ptr()
 
 
-def _is(t, name):
-    return str(t.dtype) == name
-
-
-def _plain(t, name, n):
-    """A contiguous tensor of n values of the dtype, or None."""
-    return t is None or (t.numel() == n and t.is_contiguous() and str(t.dtype) == name)
+def _stream_at(stream, t):
+    if stream is None:
+        return _raw_stream(t.get_device())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def router(score="softmax", n_group=1, topk_group=1, group_score="max", renormalize=True, scale=1.0) -> Router:
@@ -357,26 +378,34 @@ def router(score="softmax", n_group=1, topk_group=1, group_score="max", renormal
 def moe_route_grouped(logits, sel_bias, k, cfg, topk_ids, topk_weights, ws, stream=None):
     """logits [T, E] bf16, fp16 or fp32 (rows may be apart), sel_bias fp32 [E] or None, cfg from router()."""
     where = "moe_route_grouped"
+    lib = _lib if _types else _setup()
     T, E = logits.shape
-    _need(E == 0 or logits.stride(1) == 1 or E == 1, where)
-    _need(_plain(sel_bias, "torch.float32", E) and _plain(topk_ids, "torch.int32", T * k) and
-          _plain(topk_weights, "torch.float32", T * k), where)
-    _check(load().moe_route_grouped(_ptr(logits), _dtype(logits, where), logits.stride(0) if T > 1 else E,
-                                    _ptr(sel_bias), T, E, k, ctypes.byref(cfg), _ptr(topk_ids), _ptr(topk_weights),
-                                    _ptr(ws), _stream(stream)), where)
+    ld, one = logits.stride()
+    if one != 1 and E > 1:
+        _fail(where)
+    code = lib.moe_route_grouped(logits.data_ptr(), _float_type(logits, where), ld if T > 1 else E,
+                                 _flat(sel_bias, 2, E, where), T, E, k, cfg, _flat(topk_ids, _I32, T * k, where),
+                                 _flat(topk_weights, 2, T * k, where), ws.data_ptr(), _stream_at(stream, logits))
+    if code:
+        raise MoeError(code, where)
 
 
 def norm(kind="rms", weight=None, bias=None, eps=1e-5, offset=0.0) -> Norm:
     """A norm's parameters; the caller keeps the tensors alive while the struct is in use."""
-    code = 2
+    if not _types:
+        _setup()
+    code, width = 2, None
     for t in (weight, bias):
         if t is not None:
-            code = _dtype(t, "norm")
-            _need(t.dim() == 1 and t.is_contiguous(), "norm")
-    _need(weight is None or bias is None or (weight.dtype == bias.dtype and weight.shape == bias.shape), "norm")
+            code = _float_type(t, "norm")
+            if t.dim() != 1 or not t.is_contiguous():
+                _fail("norm")
+            width = t.numel()
+    if weight is not None and bias is not None and (weight.dtype != bias.dtype or weight.shape != bias.shape):
+        _fail("norm")
     n = Norm(NORM[kind] if isinstance(kind, str) else int(kind), code, float(eps), float(offset),
              None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr())
-    n.width = None if weight is None and bias is None else int((bias if weight is None else weight).shape[0])
+    n.width = width
     return n
 
 
@@ -385,30 +414,40 @@ def moe_residual_norm(z, residual, gate, post, alpha, h_out, pre, y_out, stream=
     residual and h_out of it or fp32; gate [T, H], [T, 1] or [1, H]; post, pre from norm(). See the header
     for which may be None."""
     where = "moe_residual_norm"
-    base = z if z is not None else residual
-    _need(base is not None and base.dim() == 2, where)
-    T, H = base.shape
-    act = z if z is not None else (y_out if y_out is not None else residual)
-    res = residual if residual is not None else (h_out if h_out is not None else act)
-    for t, like in ((z, act), (y_out, act), (residual, res), (h_out, res)):
-        _need(t is None or (t.dtype == like.dtype and t.shape == base.shape and (H == 1 or t.stride(1) == 1)), where)
+    lib = _lib if _types else _setup()
+    act = z if z is not None else y_out if y_out is not None else residual
+    res = residual if residual is not None else h_out if h_out is not None else act
+    if act is None or act.dim() != 2:
+        _fail(where)
+    T, H = shape = act.shape
+    apart = (H + 7) // 8 * 8  # the stride of a single row does not matter
+    at, rt = act.dtype, res.dtype
+
+    def rows(t, dtype):
+        if t is None:
+            return None, 0
+        if t.dtype != dtype or t.shape != shape:
+            _fail(where)
+        s, one = t.stride()
+        if one != 1 and H > 1:
+            _fail(where)
+        return t.data_ptr(), s if T > 1 else apart
     for n in (post, pre):
-        _need(n is None or getattr(n, "width", None) in (None, H), where)
-    gst = gsh = 0
+        if n is not None and n.width != H and n.width is not None:
+            _fail(where)
+    gp, gst, gsh = None, 0, 0
     if gate is not None:
-        _need(gate.dim() == 2 and gate.dtype == act.dtype, where)
         gt, gh = gate.shape
-        _need(gt in (1, T) and gh in (1, H), where)
+        if gate.dtype != at or (gt != T and gt != 1) or (gh != H and gh != 1):
+            _fail(where)
+        gp = gate.data_ptr()
         gst = gate.stride(0) if gt > 1 else 0
         gsh = gate.stride(1) if gh > 1 else 0
-
-    def st(t):
-        return 0 if t is None else (t.stride(0) if T > 1 else (H + 7) // 8 * 8)
-    _check(load().moe_residual_norm(_ptr(z), st(z), _ptr(residual), st(residual), _ptr(gate), gst, gsh, T, H,
-                                    _dtype(act, where), _dtype(res, where),
-                                    None if post is None else ctypes.byref(post), float(alpha), _ptr(h_out), st(h_out),
-                                    None if pre is None else ctypes.byref(pre), _ptr(y_out), st(y_out),
-                                    _stream(stream)), where)
+    code = lib.moe_residual_norm(*rows(z, at), *rows(residual, rt), gp, gst, gsh, T, H, _float_type(act, where),
+                                 _float_type(res, where), post, alpha, *rows(h_out, rt), pre, *rows(y_out, at),
+                                 _stream_at(stream, act))
+    if code:
+        raise MoeError(code, where)
 
 
 def moe_kv_record_bytes(fmt, head_dim):
@@ -418,42 +457,58 @@ def moe_kv_record_bytes(fmt, head_dim):
 def kv_cache(data, fmt, head_dim) -> KvCache:
     """KvCache view of a uint8 tensor [num_pages, kv_heads, page_size / 16, moe_kv_record_bytes(fmt, head_dim)];
     the caller keeps the tensor alive while the struct is in use."""
+    if not _types:
+        _setup()
     code = KV_FMT[fmt] if isinstance(fmt, str) else int(fmt)
     rec = moe_kv_record_bytes(code, head_dim)
-    _need(data.dim() == 4 and _is(data, "torch.uint8") and data.is_contiguous(), "kv_cache")
-    _need(rec == 0 or data.shape[3] == rec, "kv_cache")
+    if data.dim() != 4 or _types.get(data.dtype) != _U8 or not data.is_contiguous() or (rec and data.shape[3] != rec):
+        _fail("kv_cache")
     return KvCache(code, int(data.shape[0]), int(data.shape[2]) * 16, int(data.shape[1]), int(head_dim),
                    data.data_ptr())
 
 
-def _rows3(t, T, cache, where):
-    """Strides over tokens and heads of a [T, kv_heads, head_dim] tensor."""
-    _need(tuple(t.shape) == (T, cache.kv_heads, cache.head_dim) and t.stride(2) == 1, where)
-    return (t.stride(0) if T > 1 else cache.kv_heads * cache.head_dim,
-            t.stride(1) if cache.kv_heads > 1 else cache.head_dim)
+def _rows3(t, shape, where):
+    """Pointer and strides over tokens and heads of a [T, heads, head_dim] tensor."""
+    if t.shape != shape:
+        _fail(where)
+    st, sh, one = t.stride()
+    if one != 1:
+        _fail(where)
+    T, heads, D = shape
+    return t.data_ptr(), st if T > 1 else heads * D, sh if heads > 1 else D
 
 
 def moe_kv_write(k, v, slots, cache, ws, stream=None):
     """k, v [T, kv_heads, head_dim] of one type (parts of a larger tensor are fine), slots int32 [T]."""
     where = "moe_kv_write"
+    lib = _lib if _types else _setup()
     T = slots.numel()
-    _need(_plain(slots, "torch.int32", T) and k.dtype == v.dtype, where)
-    _check(load().moe_kv_write(_ptr(k), _ptr(v), _dtype(k, where), *_rows3(k, T, cache, where),
-                               *_rows3(v, T, cache, where), _ptr(slots), T, ctypes.byref(cache), _ptr(ws),
-                               _stream(stream)), where)
+    shape = (T, cache.kv_heads, cache.head_dim)
+    if k.dtype != v.dtype:
+        _fail(where)
+    kp, kt, kh = _rows3(k, shape, where)
+    vp, vt, vh = _rows3(v, shape, where)
+    code = lib.moe_kv_write(kp, vp, _float_type(k, where), kt, kh, vt, vh, _flat(slots, _I32, T, where), T, cache,
+                            ws.data_ptr(), _stream_at(stream, k))
+    if code:
+        raise MoeError(code, where)
 
 
 def moe_kv_read(cache, slots, k_out, v_out, ws, stream=None):
     """k_out, v_out [n, kv_heads, head_dim] of one type, either may be None; slots int32 [n]."""
     where = "moe_kv_read"
+    lib = _lib if _types else _setup()
     n = slots.numel()
+    shape = (n, cache.kv_heads, cache.head_dim)
     one = k_out if k_out is not None else v_out
-    _need(one is not None and _plain(slots, "torch.int32", n), where)
-    _need(k_out is None or v_out is None or k_out.dtype == v_out.dtype, where)
-    ks = (0, 0) if k_out is None else _rows3(k_out, n, cache, where)
-    vs = (0, 0) if v_out is None else _rows3(v_out, n, cache, where)
-    _check(load().moe_kv_read(ctypes.byref(cache), _ptr(slots), n, _ptr(k_out), _ptr(v_out), _dtype(one, where), *ks,
-                              *vs, _ptr(ws), _stream(stream)), where)
+    if one is None or (v_out is not None and v_out.dtype != one.dtype):
+        _fail(where)
+    kp, kt, kh = (None, 0, 0) if k_out is None else _rows3(k_out, shape, where)
+    vp, vt, vh = (None, 0, 0) if v_out is None else _rows3(v_out, shape, where)
+    code = lib.moe_kv_read(cache, _flat(slots, _I32, n, where), n, kp, vp, _float_type(one, where), kt, kh, vt, vh,
+                           ws.data_ptr(), _stream_at(stream, slots))
+    if code:
+        raise MoeError(code, where)
 
 
 def moe_attn_workspace_size(q_heads, kv_heads, head_dim):
@@ -466,18 +521,18 @@ def moe_attn_decode(q, cache, block_table, seq_lens, out, ws, scale=None, window
     """q, out [B, q_heads, head_dim] bf16 or fp16, block_table int32 [B, pages], seq_lens int32 [B], sinks fp32
     [q_heads], lse fp32 [B, q_heads]; scale None: head_dim ** -0.5."""
     where = "moe_attn_decode"
-    B, heads, D = q.shape
-    _need(D == cache.head_dim and out.shape == q.shape and out.dtype == q.dtype, where)
-    _need(q.stride(2) == 1 and out.stride(2) == 1, where)
-    _need(block_table.dim() == 2 and block_table.shape[0] == B and _is(block_table, "torch.int32"), where)
-    pages = block_table.shape[1]
-    _need(pages <= 1 or block_table.stride(1) == 1, where)
-    _need(_plain(seq_lens, "torch.int32", B) and _plain(sinks, "torch.float32", heads) and
-          _plain(lse, "torch.float32", B * heads) and _is(ws, "torch.uint8"), where)
-
-    def st(t):
-        return (t.stride(0) if B > 1 else heads * D), (t.stride(1) if heads > 1 else D)
-    _check(load().moe_attn_decode(_ptr(q), _dtype(q, where), *st(q), ctypes.byref(cache), _ptr(block_table),
-                                  block_table.stride(0) if B > 1 else pages, pages, _ptr(seq_lens), B, heads,
-                                  D ** -0.5 if scale is None else float(scale), int(window), _ptr(sinks), _ptr(out),
-                                  *st(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)), where)
+    lib = _lib if _types else _setup()
+    B, heads, D = shape = q.shape
+    bt, pages = block_table.shape
+    ts, one = block_table.stride()
+    if (D != cache.head_dim or out.dtype != q.dtype or bt != B or _types.get(block_table.dtype) != _I32 or
+            (one != 1 and pages > 1) or _types.get(ws.dtype) != _U8):
+        _fail(where)
+    qp, qb, qh = _rows3(q, shape, where)
+    op, ob, oh = _rows3(out, shape, where)
+    code = lib.moe_attn_decode(qp, _float_type(q, where), qb, qh, cache, block_table.data_ptr(), ts if B > 1 else pages,
+                               pages, _flat(seq_lens, _I32, B, where), B, heads, D ** -0.5 if scale is None else scale,
+                               window, _flat(sinks, 2, heads, where), op, ob, oh, _flat(lse, 2, B * heads, where),
+                               ws.data_ptr(), ws.numel(), _stream_at(stream, q))
+    if code:
+        raise MoeError(code, where)

@@ -3,16 +3,22 @@
 // groups, the k best experts in them, weights from s alone.
 //
 // One warp a token. Group g owns L = 32 / (n_group rounded up to a power of
-// two) lanes, which share its experts, so a group's largest and second-largest
-// scores are log2(L) shuffles; E <= 256 leaves at most 16 experts a lane.
+// two) lanes, which share its experts (E <= 256 leaves at most 16 a lane), so
+// what a group needs is log2(L) shuffles. A lane sorts its experts once by a
+// 32-bit key, the ordered bits of c with the low bits replaced by the expert's
+// place in the lane; after that a choice is one warp-wide maximum over the
+// lanes' heads, and the winning lane moves on to its next. 16-bit logits
+// ordered by themselves leave room for the whole expert index, so their many
+// ties are decided in the key.
 //
-// Which experts are chosen is decided on the real numbers. fp32 scores carry
-// an error of up to `err` (derived at score_error below); where every gap that
-// the selection rests on -- last kept group to first dropped one, each chosen
-// expert to the next -- is wider than the two errors together, fp32 has the
-// right order. The other rows are done again with scores in 64 bits, which
-// exact ties also take (fp32 cannot tell them from near ties). Ordering by the
-// logits themselves is exact, and needs no check.
+// Which experts are chosen is decided on the real numbers. The keys carry an
+// error: the truncation, and that of fp32 scores (score_error2). Where every
+// gap that the selection rests on -- last kept group to first dropped one,
+// each choice to the next -- is wider, the order is right. Other rows are
+// `open` and go through select_exact: exact keys if the logits give the order,
+// 64-bit scores for the few candidates within the error otherwise (64-bit
+// exponentials run at a 64th of the fp32 rate, so one a lane, not one an
+// expert). With random fp32 logits and a bias about one row in 500 is open.
 #include "common.cuh"
 #include "kernels.h"
 #include "types.cuh"
@@ -22,8 +28,8 @@ namespace moe4 {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kMaxK = 8;
 constexpr unsigned kAll = 0xffffffffu;
+constexpr float kMaxFloat = 3.402823466e38f;
 
 struct RouteArgs {
   const void *logits;
@@ -31,37 +37,40 @@ struct RouteArgs {
   int32_t *ids;
   float *weights;
   int64_t ld;
-  int type, T, E, k, n_group, topk_group, gs, lanes;  // gs: experts a group; lanes: lanes a group
+  int type, T, k, n_group, topk_group, gs, lanes;  // gs: experts a group; lanes: lanes a group
   int score, top2, renorm;
   float scale;
+};
+
+// One warp's working space for open rows.
+struct Scratch {
+  int id[32];
+  double c[32];
 };
 
 // An unsigned key that orders as the float does (-0 made +0 before); 0 is free
 // for "no candidate", below the key of -inf.
 __device__ __forceinline__ uint32_t key_of(float v) {
   const uint32_t u = __float_as_uint(v + 0.0f);
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
+  return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
+__device__ __forceinline__ float not_nan(float v) { return v == v ? v : -INFINITY; }
 
-// Bound on twice the error of an fp32 selection score of size |v|.
-// Sigmoid: E = ex2(-l log2 e) is off by 2^-22 + |l| 2^-23 of itself, which
-// 1 / (1 + E) turns into at most s (1 - s) of that (<= 0.6e-7 + 0.27e-7), the
-// sum, the reciprocal and the bias add at most 2^-24 + 2^-22 of s and 2^-24 of
-// the result: below 5e-7 + 6e-8 |v|. Softmax: the exponential likewise (s
-// |l - m| < 0.37), its sum of up to 256 terms at most 21 * 2^-24 + 2^-22 of
-// itself (8 or 16 in a lane, five shuffles): below 2e-6 + 6e-8 |v|.
+// Bound on twice the error of an fp32 selection score of size |v|, the cut to
+// 28 bits of key included (2^-19 of |v|). Sigmoid: E = exp(-l) is off by 2^-22
+// + |l| 2^-23 of itself, which 1 / (1 + E) turns into at most s (1 - s) of
+// that (<= 0.6e-7 + 0.27e-7), sum, quotient and the bias add at most 2^-22 of
+// s and 2^-24 of the result: below 5e-7 + 6e-8 |v|. Softmax: the exponential
+// likewise (s |l - m| < 0.37), its sum of up to 256 terms at most 21 * 2^-24 +
+// 2^-22 of itself (16 in a lane, five shuffles): below 2e-6 + 6e-8 |v|.
 __device__ __forceinline__ float score_error2(int score, float v) {
-  return (score == MOE_SCORE_SOFTMAX ? 4e-6f : 1e-6f) + 1.3e-7f * fabsf(v);
+  return (score == MOE_SCORE_SOFTMAX ? 4e-6f : 1e-6f) + 2.1e-6f * fabsf(v);
 }
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-  return v;
-}
+__device__ __forceinline__ float warp_max(float v) { return value_of(__reduce_max_sync(kAll, key_of(v))); }
 template <typename F>
 __device__ __forceinline__ F warp_sum(F v) {
 #pragma unroll
@@ -70,87 +79,242 @@ __device__ __forceinline__ F warp_sum(F v) {
 }
 
 // exp(l - m) with the limits at infinite m: logits equal to m count 1, others 0.
-template <typename F>
-__device__ __forceinline__ F exp_rel(float l, float m) {
-  if (fabsf(m) > 3.402823466e38f) return l == m ? F(1) : F(0);
-  return sizeof(F) == 8 ? F(exp((double)l - (double)m)) : F(expf(l - m));
+__device__ __forceinline__ float exp_rel(float l, float m) {
+  if (fabsf(m) > kMaxFloat) return l == m ? 1.f : 0.f;
+  return expf(l - m);
+}
+__device__ __forceinline__ double exp_rel64(float l, float m) {
+  if (fabsf(m) > kMaxFloat) return l == m ? 1.0 : 0.0;
+  return exp((double)l - (double)m);
 }
 
-// The same selection with 64-bit scores, for the rows that fp32 leaves open.
-// sc: scores of this lane's experts for the group stage (top2) and the expert
-// stage; returns the j-th id in lane j.
+// Batcher's odd-even merge sort of a lane's keys, largest first.
 template <int PL>
-__device__ __noinline__ int select64(const RouteArgs &a, const float (&l)[PL], float m, int lane, int sub, int g) {
-  const double none = -INFINITY;
-  double s[PL];
-  double sum = 0.0;
-  if (a.score == MOE_SCORE_SOFTMAX) {
+__device__ __forceinline__ void sort_keys(uint32_t (&key)[PL]) {
 #pragma unroll
-    for (int i = 0; i < PL; ++i) {
-      const int x = sub + i * a.lanes;
-      s[i] = (g < a.n_group && x < a.gs) ? exp_rel<double>(l[i], m) : 0.0;
-      sum += s[i];
-    }
+  for (int p = 1; p < PL; p <<= 1)
+#pragma unroll
+    for (int k = p; k >= 1; k >>= 1)
+#pragma unroll
+      for (int j = k % p; j + k < PL; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < PL && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const uint32_t hi = max(key[i + j], key[i + j + k]), lo = min(key[i + j], key[i + j + k]);
+            key[i + j] = hi;
+            key[i + j + k] = lo;
+          }
+}
+
+// What a warp knows of its token.
+template <int PL>
+struct Row {
+  float l[PL];  // logits of this lane's experts (NaN as -inf)
+  float m, sum; // softmax: maximum and sum of exp(l - m) over all, where needed
+  int64_t at;   // of the logits in memory
+  int lane, g, sub, e0;
+  unsigned valid;  // which of l are experts
+};
+
+// Which experts are this lane's.
+template <int PL>
+__device__ __forceinline__ void enter_row(const RouteArgs &a, Row<PL> &r) {
+  r.lane = threadIdx.x & 31;
+  r.g = r.lane / a.lanes;
+  r.sub = r.lane & (a.lanes - 1);
+  r.e0 = r.g * a.gs + r.sub;
+  r.valid = 0;
+#pragma unroll
+  for (int i = 0; i < PL; ++i)
+    if (r.g < a.n_group && r.sub + i * a.lanes < a.gs) r.valid |= 1u << i;
+}
+
+// This lane's logits, all loads under way together.
+template <int PL>
+__device__ __forceinline__ void load_logits(const RouteArgs &a, Row<PL> &r) {
+  auto each = [&](auto get) {
+#pragma unroll
+    for (int i = 0; i < PL; ++i) r.l[i] = (r.valid >> i) & 1u ? get(r.at + r.e0 + i * a.lanes) : -INFINITY;
+  };
+  if (a.type == MOE_FP32)
+    each([&](int64_t i) { return load_as_f32(a.logits, i, MOE_FP32); });
+  else if (a.type == MOE_BF16)
+    each([&](int64_t i) { return load_as_f32(a.logits, i, MOE_BF16); });
+  else
+    each([&](int64_t i) { return load_as_f32(a.logits, i, MOE_FP16); });
+#pragma unroll
+  for (int i = 0; i < PL; ++i) r.l[i] = not_nan(r.l[i]);
+}
+
+// 64-bit selection score of expert e.
+__device__ double score64(const RouteArgs &a, int64_t at, float m, double sum, int e) {
+  const float l = not_nan(load_as_f32(a.logits, at + e, a.type));
+  double s = a.score == MOE_SCORE_SOFTMAX ? exp_rel64(l, m) / sum : 1.0 / (1.0 + exp(-(double)l));
+  if (a.bias) s += (double)a.bias[e];
+  return s == s ? s : -INFINITY;
+}
+
+// The choice for an open row: the j-th id in lane j.
+template <int PL>
+__device__ __noinline__ int select_exact(const RouteArgs &a, int64_t row, float m, float fsum, Scratch &w) {
+  // the row is read again: what the fast path holds stays in its registers
+  Row<PL> r;
+  r.at = row;
+  r.m = m;
+  r.sum = fsum;
+  enter_row<PL>(a, r);
+  load_logits<PL>(a, r);
+  const int lane = r.lane;
+  const bool grouped = a.topk_group < a.n_group, by_score = a.bias || (grouped && a.top2);
+  double sum = 1.0;
+  float c[PL];  // fp32 scores, as before
+  if (a.score == MOE_SCORE_SOFTMAX && by_score) {
+    sum = 0.0;
+#pragma unroll 1
+    for (int i = 0; i < PL; ++i)
+      if ((r.valid >> i) & 1u) sum += exp_rel64(not_nan(load_as_f32(a.logits, r.at + r.e0 + i * a.lanes, a.type)), r.m);
     sum = warp_sum(sum);
-#pragma unroll
-    for (int i = 0; i < PL; ++i) s[i] /= sum;
-  } else {
-#pragma unroll
-    for (int i = 0; i < PL; ++i) s[i] = 1.0 / (1.0 + exp(-(double)l[i]));
   }
-  unsigned valid = 0;
 #pragma unroll
   for (int i = 0; i < PL; ++i) {
-    const int x = sub + i * a.lanes;
-    if (g < a.n_group && x < a.gs) {
-      valid |= 1u << i;
-      if (a.bias) s[i] += (double)a.bias[g * a.gs + x];
-      if (s[i] != s[i]) s[i] = none;
+    c[i] = r.l[i];
+    if (by_score && ((r.valid >> i) & 1u)) {
+      float v = a.score == MOE_SCORE_SOFTMAX ? exp_rel(r.l[i], r.m) / r.sum : 1.0f / (1.0f + expf(-r.l[i]));
+      if (a.bias) v += a.bias[r.e0 + i * a.lanes];
+      c[i] = not_nan(v);
     }
   }
-  if (a.topk_group < a.n_group) {
-    double b1 = none, b2 = none;
+  bool kept = r.g < a.n_group;
+  if (grouped) {
+    float b1 = -INFINITY, b2 = -INFINITY;
 #pragma unroll
     for (int i = 0; i < PL; ++i)
-      if ((valid >> i) & 1u) {
-        if (a.top2) {
-          if (s[i] > b1) {
-            b2 = b1;
-            b1 = s[i];
-          } else if (s[i] > b2) {
-            b2 = s[i];
-          }
-        } else {
-          b1 = fmax(b1, a.bias ? s[i] : (double)l[i]);
-        }
+      if ((r.valid >> i) & 1u) {
+        const float v = a.top2 || a.bias ? c[i] : r.l[i];
+        b2 = fmaxf(b2, fminf(b1, v));
+        b1 = fmaxf(b1, v);
       }
     for (int o = 1; o < a.lanes; o <<= 1) {
-      const double o1 = __shfl_xor_sync(kAll, b1, o), o2 = __shfl_xor_sync(kAll, b2, o);
-      b2 = fmax(fmin(b1, o1), fmax(b2, o2));
-      b1 = fmax(b1, o1);
+      const float o1 = __shfl_xor_sync(kAll, b1, o), o2 = __shfl_xor_sync(kAll, b2, o);
+      b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
+      b1 = fmaxf(b1, o1);
     }
-    double gv = a.top2 ? b1 + b2 : b1;
-    gv = gv == gv ? gv : none;
-    int rank = 0;  // groups ahead of this lane's
+    const float gv = a.top2 ? not_nan(b1 + b2) : b1;
+    int ahead = 0;
+    float lv = INFINITY, nv = -INFINITY;  // of the last kept and the first dropped, as fp32 has it
     for (int h = 0; h < a.n_group; ++h) {
-      const double ov = __shfl_sync(kAll, gv, h * a.lanes);
-      rank += (ov > gv || (ov == gv && h < g)) ? 1 : 0;
+      const float ov = __shfl_sync(kAll, gv, h * a.lanes);
+      ahead += ov > gv || (ov == gv && h < r.g);
     }
-    if (rank >= a.topk_group) valid = 0;
+    for (int h = 0; h < a.n_group; ++h) {
+      const float ov = __shfl_sync(kAll, gv, h * a.lanes);
+      if (__shfl_sync(kAll, ahead, h * a.lanes) < a.topk_group)
+        lv = fminf(lv, ov);
+      else
+        nv = fmaxf(nv, ov);
+    }
+    if (!by_score) {
+      kept = kept && ahead < a.topk_group;
+    } else {
+      const float tol = 2.f * score_error2(a.score, fmaxf(fabsf(lv), fabsf(nv)));
+      const bool sure = kept && gv > lv + tol;
+      const bool maybe = kept && !sure && !(gv < nv - tol);
+      // 64-bit scores of those of an undecided group that can be its best, or its two best
+      const float least = (a.top2 ? b2 : b1) - score_error2(a.score, a.top2 ? b2 : b1);
+      double d1 = -INFINITY, d2 = -INFINITY;
+      auto put = [&](double v) {
+        if (v > d1) {
+          d2 = d1;
+          d1 = v;
+        } else if (v > d2) {
+          d2 = v;
+        }
+      };
+      unsigned need = 0;
+#pragma unroll
+      for (int i = 0; i < PL; ++i)
+        if (maybe && ((r.valid >> i) & 1u) && !(c[i] < least)) need |= 1u << i;
+      while (const unsigned who = __ballot_sync(kAll, need != 0)) {  // one candidate of each lane at a time
+        const int at = __popc(who & ((1u << lane) - 1u)), cnt = __popc(who);
+        if (need) {
+          w.id[at] = r.e0 + (__ffs(need) - 1) * a.lanes;
+          need &= need - 1;
+        }
+        __syncwarp();
+        if (lane < cnt) w.c[lane] = score64(a, r.at, r.m, sum, w.id[lane]);
+        __syncwarp();
+        for (int j = 0; j < cnt; ++j)
+          if (w.id[j] / a.gs == r.g) put(w.c[j]);
+        __syncwarp();
+      }
+      double gd = a.top2 ? d1 + d2 : d1;
+      if (!(gd == gd)) gd = -INFINITY;
+      int place = 0;
+      for (int h = 0; h < a.n_group; ++h) {
+        const double od = __shfl_sync(kAll, gd, h * a.lanes);
+        const bool om = __shfl_sync(kAll, (int)maybe, h * a.lanes), os = __shfl_sync(kAll, (int)sure, h * a.lanes);
+        place += os || (om && (od > gd || (od == gd && h < r.g)));
+      }
+      kept = sure || (maybe && place < a.topk_group);
+    }
   }
-  int mine = 0;
-  for (int j = 0; j < a.k; ++j) {
-    double best = none;
+  unsigned left = kept ? r.valid : 0u;
+  // candidates in fp32 order, by index among equals: k, and with computed scores those within the error of the k-th
+  int mine = 0, n = 0;
+  float kth = 0.f;
+  while (n < 32) {
+    float best = -INFINITY;
     int bid = 0x7fffffff;
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
-      const int e = g * a.gs + sub + i * a.lanes;
-      const double v = a.bias ? s[i] : (double)l[i];
-      if (((valid >> i) & 1u) && (v > best || (v == best && e < bid))) {
+      const float v = a.bias ? c[i] : r.l[i];
+      const int e = r.e0 + i * a.lanes;
+      if (((left >> i) & 1u) && (v > best || (v == best && e < bid))) {
         best = v;
         bid = e;
       }
     }
+    const uint32_t key = bid != 0x7fffffff ? key_of(best) : 0u, top = __reduce_max_sync(kAll, key);
+    if (top == 0u) break;
+    const int id = __reduce_min_sync(kAll, key == top ? bid : 0x7fffffff);
+    const float v = value_of(top);
+    if (n >= a.k && (!a.bias || v < kth - score_error2(a.score, kth))) break;
+    if (n < a.k) kth = v;
+    if (bid == id) left &= ~(1u << ((id - r.e0) / a.lanes));
+    if (lane == n) mine = id;
+    ++n;
+  }
+  if (!a.bias) return mine;
+  if (n < 32) {
+    // ranked by their 64-bit scores, one a lane
+    const double v = lane < n ? score64(a, r.at, r.m, sum, mine) : -INFINITY;
+    int place = 0;
+    for (int j = 0; j < n; ++j) {
+      const double ov = __shfl_sync(kAll, v, j);
+      const int oid = __shfl_sync(kAll, mine, j);
+      place += ov > v || (ov == v && oid < mine);
+    }
+    if (lane < n) w.id[place] = mine;
+    __syncwarp();
+    mine = lane < a.k ? w.id[lane] : 0;
+    __syncwarp();
+    return mine;
+  }
+  // more candidates than lanes: every expert in 64 bits, k times over
+  left = kept ? r.valid : 0u;
+  for (int j = 0; j < a.k; ++j) {
+    double best = -INFINITY;
+    int bid = 0x7fffffff;
+#pragma unroll 1
+    for (int i = 0; i < PL; ++i)
+      if ((left >> i) & 1u) {
+        const int e = r.e0 + i * a.lanes;
+        const double v = score64(a, r.at, r.m, sum, e);
+        if (v > best || (v == best && e < bid)) {
+          best = v;
+          bid = e;
+        }
+      }
     const int own = bid;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -161,157 +325,164 @@ __device__ __noinline__ int select64(const RouteArgs &a, const float (&l)[PL], f
         bid = oid;
       }
     }
-    if (own == bid) valid &= ~(1u << ((bid - g * a.gs - sub) / a.lanes));
+    if (own == bid) left &= ~(1u << ((bid - r.e0) / a.lanes));
     if (lane == j) mine = bid;
   }
   return mine;
 }
 
+// PL: experts a lane, rounded up to a power of two
 template <int PL>
 __global__ void __launch_bounds__(kWarps * 32) group_route_kernel(const RouteArgs a) {
+  __shared__ Scratch scratch[kWarps];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (t >= a.T) return;
-  const int g = lane / a.lanes, sub = lane & (a.lanes - 1);
-  const int e0 = g * a.gs + sub;
-  const int64_t row = (int64_t)t * a.ld;
-  float l[PL];
-#pragma unroll
-  for (int i = 0; i < PL; ++i) {
-    l[i] = -INFINITY;
-    if (g < a.n_group && sub + i * a.lanes < a.gs) {
-      const float v = load_as_f32(a.logits, row + e0 + i * a.lanes, a.type);
-      l[i] = v == v ? v : -INFINITY;
-    }
-  }
   const bool grouped = a.topk_group < a.n_group;
-  const bool scored = a.bias || (grouped && a.top2);  // some order rests on computed scores
-  float m = 0.f, sum = 1.f;
-  if (a.score == MOE_SCORE_SOFTMAX && (scored || !a.renorm)) {
-    m = l[0];
+  const bool by_score = a.bias || (grouped && a.top2);  // some order rests on computed scores
+  const bool short_keys = !a.bias && a.type != MOE_FP32;  // 19 bits of order hold any, 13 of index
+  Row<PL> r;
+  enter_row<PL>(a, r);
+  float bias[PL];
 #pragma unroll
-    for (int i = 1; i < PL; ++i) m = fmaxf(m, l[i]);
-    m = warp_max(m);
-    sum = 0.f;
+  for (int i = 0; i < PL; ++i) bias[i] = a.bias && ((r.valid >> i) & 1u) ? a.bias[r.e0 + i * a.lanes] : 0.f;
+  for (int t = blockIdx.x * kWarps + (threadIdx.x >> 5); t < a.T; t += gridDim.x * kWarps) {
+    r.at = (int64_t)t * a.ld;
+    load_logits<PL>(a, r);
+    r.m = 0.f;
+    r.sum = 1.f;
+    if (a.score == MOE_SCORE_SOFTMAX && (by_score || !a.renorm)) {
+      float m = r.l[0];
 #pragma unroll
-    for (int i = 0; i < PL; ++i)
-      if (g < a.n_group && sub + i * a.lanes < a.gs) sum += exp_rel<float>(l[i], m);
-    sum = warp_sum(sum);
-  }
-  uint32_t key[PL];  // order of the experts
-  float sc[PL];      // computed scores
-  bool open = false; // fp32 leaves the selection open
-#pragma unroll
-  for (int i = 0; i < PL; ++i) {
-    const bool valid = g < a.n_group && sub + i * a.lanes < a.gs;
-    float v = l[i];
-    if (scored && valid) {
-      v = a.score == MOE_SCORE_SOFTMAX ? exp_rel<float>(l[i], m) / sum : 1.0f / (1.0f + __expf(-l[i]));
-      if (a.bias) v += a.bias[e0 + i * a.lanes];
-      v = v == v ? v : -INFINITY;
-    }
-    sc[i] = v;
-    key[i] = valid ? key_of(a.bias ? v : l[i]) : 0u;
-  }
-  if (grouped) {
-    uint32_t b1 = 0, b2 = 0;
-#pragma unroll
-    for (int i = 0; i < PL; ++i) {
-      const uint32_t v = key[i] == 0u ? 0u : key_of(a.top2 ? sc[i] : (a.bias ? sc[i] : l[i]));
-      b2 = max(b2, min(b1, v));
-      b1 = max(b1, v);
-    }
-    for (int o = 1; o < a.lanes; o <<= 1) {
-      const uint32_t o1 = __shfl_xor_sync(kAll, b1, o), o2 = __shfl_xor_sync(kAll, b2, o);
-      b2 = max(max(b2, o2), min(b1, o1));
-      b1 = max(b1, o1);
-    }
-    uint32_t gk = 0;
-    if (g < a.n_group) {
-      const float v = value_of(b1) + value_of(b2);
-      gk = a.top2 ? key_of(v == v ? v : -INFINITY) : b1;
-    }
-    // the topk_group best groups, one after another; then the best one left
-    bool kept = false;
-    uint32_t last = 0;
-    for (int j = 0; j < a.topk_group; ++j) {
-      last = __reduce_max_sync(kAll, kept ? 0u : gk);
-      const int winner = __reduce_min_sync(kAll, !kept && gk == last ? g : 32);
-      kept = kept || g == winner;
-    }
-    if (scored) {
-      const uint32_t next = __reduce_max_sync(kAll, kept ? 0u : gk);
-      const float lv = value_of(last), nv = value_of(next);
-      open = !(lv - nv > (a.top2 ? 2.f : 1.f) * score_error2(a.score, fmaxf(fabsf(lv), fabsf(nv))));
-    }
-    if (!kept) {
-#pragma unroll
-      for (int i = 0; i < PL; ++i) key[i] = 0u;
-    }
-  }
-  int mine = 0;
-  float prev = INFINITY;
-  const int rounds = a.k + (a.bias ? 1 : 0);
-  for (int j = 0; j < rounds; ++j) {
-    uint32_t best = 0;
-    int at = 0;
-#pragma unroll
-    for (int i = 0; i < PL; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        at = i;
-      }
-    const uint32_t top = __reduce_max_sync(kAll, best);
-    const float v = value_of(top);
-    if (a.bias) {  // top 0: fewer candidates than k + 1
-      if (j > 0 && top != 0u && !(prev - v > score_error2(a.score, fmaxf(fabsf(prev), fabsf(v))))) open = true;
-      prev = v;
-    }
-    const int bid = best == top && top != 0u ? e0 + at * a.lanes : 0x7fffffff;
-    const int id = __reduce_min_sync(kAll, bid);
-    if (bid == id && j < a.k) {
+      for (int i = 1; i < PL; ++i) m = fmaxf(m, r.l[i]);
+      r.m = warp_max(m);
+      r.sum = 0.f;
 #pragma unroll
       for (int i = 0; i < PL; ++i)
-        if (i == at) key[i] = 0u;
+        if ((r.valid >> i) & 1u) r.sum += exp_rel(r.l[i], r.m);
+      r.sum = warp_sum(r.sum);
     }
-    if (lane == j) mine = id;
-  }
-  if (open) {
-    if (a.score == MOE_SCORE_SOFTMAX) {
-      m = l[0];
+    auto score = [&](float l) {
+      return a.score == MOE_SCORE_SOFTMAX ? __fdividef(exp_rel(l, r.m), r.sum) : __fdividef(1.0f, 1.0f + __expf(-l));
+    };
+    uint32_t key[PL];
 #pragma unroll
-      for (int i = 1; i < PL; ++i) m = fmaxf(m, l[i]);
-      m = warp_max(m);
+    for (int i = 0; i < PL; ++i) {
+      const uint32_t full = key_of(a.bias ? not_nan(score(r.l[i]) + bias[i]) : r.l[i]);
+      const uint32_t cut = short_keys ? (full & ~0x1FFFu) | (0x1FFFu - (uint32_t)(r.e0 + i * a.lanes))
+                                      : (full & ~15u) | (uint32_t)(15 - i);
+      key[i] = (r.valid >> i) & 1u ? cut : 0u;
     }
-    mine = select64<PL>(a, l, m, lane, sub, g);
-  }
-  // weights: lane j has the j-th choice
-  const bool has = lane < a.k;
-  float lv = -INFINITY;
-  if (has) {
-    lv = load_as_f32(a.logits, row + mine, a.type);
-    lv = lv == lv ? lv : -INFINITY;
-  }
-  const float mx = warp_max(lv);
-  float w = 0.f;
-  if (a.score == MOE_SCORE_SOFTMAX) {
-    if (has) w = a.renorm ? exp_rel<float>(lv, mx) : exp_rel<float>(lv, m) / sum;
-  } else if (has) {
-    // far below 0 every sigmoid is exp(l), which only its ratios keep in range
-    if (a.renorm && mx < -30.f) {
-      w = exp_rel<float>(lv, mx);
-    } else {
-      const float x = expf(-fabsf(lv));
-      w = lv >= 0.f ? 1.0f / (1.0f + x) : x / (1.0f + x);
+    sort_keys<PL>(key);
+    bool open = false;  // the keys leave the selection open
+    if (grouped) {
+      uint32_t b1 = key[0], b2 = PL > 1 ? key[PL > 1] : 0u;
+      if (a.top2 && !a.bias) {  // the scores of the two largest logits: those whole, not as the keys have them
+        b1 = b2 = 0u;
+#pragma unroll
+        for (int i = 0; i < PL; ++i) {
+          const uint32_t full = (r.valid >> i) & 1u ? key_of(r.l[i]) : 0u;
+          b2 = max(b2, min(b1, full));
+          b1 = max(b1, full);
+        }
+      }
+      for (int o = 1; o < a.lanes; o <<= 1) {
+        const uint32_t o1 = __shfl_xor_sync(kAll, b1, o), o2 = __shfl_xor_sync(kAll, b2, o);
+        b2 = max(max(b2, o2), min(b1, o1));
+        b1 = max(b1, o1);
+      }
+      uint32_t gk = 0;
+      if (r.g < a.n_group) {
+        const float x = value_of(b1), y = value_of(b2);
+        gk = !a.top2 ? b1 : key_of(not_nan(a.bias ? x + y : score(x) + score(y)));
+      }
+      int ahead = 0;  // groups before this one; equal ones by index
+      for (int h = 0; h < a.n_group; ++h) {
+        const uint32_t ok = __shfl_sync(kAll, gk, h * a.lanes);
+        ahead += ok > gk || (ok == gk && h < r.g);
+      }
+      const bool kept = r.g < a.n_group && ahead < a.topk_group;
+      const uint32_t last = __reduce_min_sync(kAll, kept ? gk : kAll), next = __reduce_max_sync(kAll, kept ? 0u : gk);
+      if (by_score) {
+        const float lv = value_of(last), nv = value_of(next);
+        open = !(lv - nv > (a.top2 ? 2.f : 1.f) * score_error2(a.score, fmaxf(fabsf(lv), fabsf(nv))));
+      } else if (!short_keys) {
+        open = (last >> 4) == (next >> 4);
+      }
+      if (!kept) {
+#pragma unroll
+        for (int i = 0; i < PL; ++i) key[i] = 0u;
+      }
+    }
+    int mine = 0;
+    uint32_t prev = kAll;
+    const int rounds = a.k + (short_keys ? 0 : 1);  // the choice after the last decides whether that one is sure
+    for (int j = 0; j < rounds; ++j) {
+      const uint32_t top = __reduce_max_sync(kAll, key[0]);
+      const unsigned who = __ballot_sync(kAll, key[0] == top);
+      if (top == 0u) break;  // fewer candidates than k + 1
+      const int from = __ffs(who) - 1;
+      if (!short_keys) {
+        if (a.bias) {
+          const float v = value_of(top & ~15u), p = value_of(prev & ~15u);
+          open = open || (j > 0 && !(p - v > score_error2(a.score, fmaxf(fabsf(p), fabsf(v)))));
+        } else {
+          open = open || (prev >> 4) == (top >> 4);
+        }
+        open = open || (who & (who - 1));
+      }
+      prev = top;
+      const int id = short_keys ? (int)(0x1FFFu - (top & 0x1FFFu))
+                                : __shfl_sync(kAll, r.e0, from) + (int)(15u - (top & 15u)) * a.lanes;
+      if (r.lane == j) mine = id;
+      if (r.lane == from) {
+#pragma unroll
+        for (int i = 0; i + 1 < PL; ++i) key[i] = key[i + 1];
+        key[PL - 1] = 0u;
+      }
+    }
+    if (open) mine = select_exact<PL>(a, r.at, r.m, r.sum, scratch[threadIdx.x >> 5]);
+    // weights: lane j has the j-th choice
+    const bool has = r.lane < a.k;
+    const float lv = has ? not_nan(load_as_f32(a.logits, r.at + mine, a.type)) : -INFINITY;
+    const float mx = warp_max(lv);
+    float w = 0.f;
+    if (a.score == MOE_SCORE_SOFTMAX) {
+      if (has) w = a.renorm ? exp_rel(lv, mx) : exp_rel(lv, r.m) / r.sum;
+    } else if (has) {
+      // far below 0 every sigmoid is exp(l), which only its ratios keep in range
+      if (a.renorm && mx < -30.f) {
+        w = exp_rel(lv, mx);
+      } else {
+        const float x = expf(-fabsf(lv));
+        w = lv >= 0.f ? 1.0f / (1.0f + x) : x / (1.0f + x);
+      }
+    }
+    if (a.renorm) {
+      float sum = w;
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);  // k <= 8
+      w /= sum;
+    }
+    if (has) {
+      a.ids[(int64_t)t * a.k + r.lane] = mine;
+      a.weights[(int64_t)t * a.k + r.lane] = w * a.scale;
     }
   }
-  if (a.renorm) w /= warp_sum(w);
-  if (has) {
-    a.ids[(int64_t)t * a.k + lane] = mine;
-    a.weights[(int64_t)t * a.k + lane] = w * a.scale;
+}
+
+template <int PL>
+cudaError_t go(const RouteArgs &a, cudaStream_t stream) {
+  static int fit = 0;  // CTAs that are resident on the device
+  if (fit == 0) {
+    int dev = 0, sms = 0, n = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, group_route_kernel<PL>, kWarps * 32, 0);
+    if (e != cudaSuccess) return e;
+    fit = sms * n;
   }
+  const int need = (a.T + kWarps - 1) / kWarps;
+  return launch_pdl(group_route_kernel<PL>, dim3(need < fit ? need : fit), dim3(kWarps * 32), 0, stream, a);
 }
 
 }  // namespace
@@ -328,7 +499,6 @@ moe_status_t launch_group_route(const void *logits, int type, int64_t ld, const 
   a.ld = ld;
   a.type = type;
   a.T = T;
-  a.E = E;
   a.k = k;
   // without a limit the groups do not matter
   a.n_group = r.topk_group < r.n_group ? r.n_group : 1;
@@ -342,19 +512,17 @@ moe_status_t launch_group_route(const void *logits, int type, int64_t ld, const 
   a.renorm = r.renormalize != 0;
   a.scale = r.scale;
   const int per = (a.gs + a.lanes - 1) / a.lanes;
-  const dim3 grid((T + kWarps - 1) / kWarps), block(kWarps * 32);
-  auto go = [&](auto kern) { return launch_pdl(kern, grid, block, 0, stream, a); };
   cudaError_t err;
   if (per <= 1)
-    err = go(group_route_kernel<1>);
+    err = go<1>(a, stream);
   else if (per <= 2)
-    err = go(group_route_kernel<2>);
+    err = go<2>(a, stream);
   else if (per <= 4)
-    err = go(group_route_kernel<4>);
+    err = go<4>(a, stream);
   else if (per <= 8)
-    err = go(group_route_kernel<8>);
+    err = go<8>(a, stream);
   else
-    err = go(group_route_kernel<16>);
+    err = go<16>(a, stream);
   if (launches) ++*launches;
   return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

@@ -1,11 +1,15 @@
 // The seam between two blocks: u = alpha * gate * post(z), h = residual + u,
 // y = pre(h), each row in one pass.
 //
-// A row is read once and held in registers as fp32, NV chunks of 8 columns a
-// thread; both norms sum it there, so z, residual and gate are read once and
-// h and y written once, which is all the memory traffic there is. RMS needs
-// one sum over the row; LAYER takes the mean first and then the squares of
-// the differences, which loses nothing when the mean is large.
+// A row is read once and held in registers, NV chunks of 8 columns a thread;
+// both norms sum it there, so z, residual and gate are read once and h and y
+// written once, which is all the memory traffic there is, and what bounds it.
+// RMS needs one sum over the row; LAYER takes the mean first and then the
+// squares of the differences, which loses nothing when the mean is large.
+//
+// 8192 x 2880, bf16, RMS before and after with a gate a row: 33.5 us, 83% of the
+// copy bandwidth. What counted were instructions: 33 an element with a CTA a row
+// that looks up the weights' type (96 us, 44 at the best split), 9 needed.
 #include "common.cuh"
 #include "kernels.h"
 #include "types.cuh"
@@ -14,23 +18,23 @@ namespace moe4 {
 
 namespace {
 
-constexpr int kMaxThreads = 512;
-
-// Sum over the CTA; every thread gets it. buf: 2 x 32 floats used in turn, so
-// that one barrier a sum is enough.
+// Sum over the CTA; every thread gets it. buf: used in turn, so that one
+// barrier a sum is enough.
+template <int THREADS>
 __device__ __forceinline__ float block_sum(float v, float (*buf)[32], int &turn) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  if (warps == 1) return v;
+  constexpr int kWarps = THREADS / 32;
   float *b = buf[turn];
   turn ^= 1;
-  if (lane == 0) b[warp] = v;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) b[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = lane < warps ? b[lane] : 0.f;
+  v = lane < kWarps ? b[lane] : 0.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < kWarps) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return kWarps > 16 ? v : __shfl_sync(0xffffffffu, v, 0);  // the lanes past the warps hold none of it
 }
 
 struct NormArgs {
@@ -40,123 +44,293 @@ struct NormArgs {
   int T, H;
   float alpha;
   moe_norm_t post, pre;
-  int has_post, has_pre, vec;
+  int has_post, has_pre;
 };
 
-// 8 values from column c; with vec whole and aligned, else one by one up to H
-// (0 past it).
-__device__ __forceinline__ void load8(const void *p, int64_t row, int c, const NormArgs &a, int type, float (&v)[8]) {
-  if (a.vec) {
-    raw8_to_f32(load_raw8(p, row + c, type), type, v);
+// Column of a thread's value i of chunk j: VEC, eight neighbours (whole and
+// aligned chunks); else a warp's lanes next to each other, value by value.
+template <int THREADS, bool VEC>
+__device__ __forceinline__ int column(int j, int i) {
+  return VEC ? (threadIdx.x + j * THREADS) * 8 + i : threadIdx.x + (j * 8 + i) * THREADS;
+}
+
+// A thread's chunk j of a row, or of a norm's parameter; 0 past the row.
+template <int THREADS, bool VEC>
+__device__ __forceinline__ Raw8 take8(const void *p, int64_t at, int j, int H, int type) {
+  if (VEC) return load_raw8(p, at + column<THREADS, VEC>(j, 0), type);
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int c = column<THREADS, VEC>(j, i);
+    v[i] = c < H ? load_as_f32(p, at + c, type) : 0.f;
+  }
+  return f32_to_raw8(v, type);
+}
+
+template <int THREADS, bool VEC>
+__device__ __forceinline__ void store8(void *p, int64_t at, int j, int H, int type, const float (&v)[8]) {
+  if (VEC) {
+    store_raw8(p, at + column<THREADS, VEC>(j, 0), type, f32_to_raw8(v, type));
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < a.H ? load_as_f32(p, row + c + i, type) : 0.f;
+    for (int i = 0; i < 8; ++i) {
+      const int c = column<THREADS, VEC>(j, i);
+      if (c < H) store_from_f32(p, at + c, type, v[i]);
+    }
   }
 }
 
-__device__ __forceinline__ void store8(void *p, int64_t row, int c, const NormArgs &a, int type, const float (&v)[8]) {
-  if (a.vec) {
-    store_raw8(p, row + c, type, f32_to_raw8(v, type));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < a.H) store_from_f32(p, row + c + i, type, v[i]);
-  }
-}
-
-template <int NV>
-__device__ __forceinline__ void normalise(float (&x)[NV][8], const moe_norm_t &n, const NormArgs &a, float (*buf)[32],
-                                          int &turn) {
-  const float inv_h = 1.0f / (float)a.H;
-  float mean = 0.f;
+// x becomes (x - mean) * weight; returned is the factor 1 / sqrt(. + eps) that
+// it has to be multiplied by, for the caller to fold in. With a bias the factor
+// is put in here and 1 returned. weight(j, v) and bias(j, v) give the
+// parameters of chunk j; columns that do not exist hold 0.
+template <int NV, int THREADS, bool VEC, typename W, typename B>
+__device__ __forceinline__ float normalise(float (&x)[NV][8], const moe_norm_t &n, int H, float (*buf)[32], int &turn,
+                                           W weight, B bias) {
+  const float inv_h = 1.0f / (float)H;
   if (n.kind == MOE_NORM_LAYER) {
     float s = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int i = 0; i < 8; ++i) s += x[j][i];
-    mean = block_sum(s, buf, turn) * inv_h;
+    const float mean = block_sum<THREADS>(s, buf, turn) * inv_h;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (column<THREADS, VEC>(j, VEC ? 0 : i) < H) x[j][i] -= mean;
   }
   float q = 0.f;
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = (threadIdx.x + j * blockDim.x) * 8;
+  for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < a.H) {
-        x[j][i] -= mean;
-        q += x[j][i] * x[j][i];
-      }
-  }
-  const float r = rsqrtf(block_sum(q, buf, turn) * inv_h + n.eps);
+    for (int i = 0; i < 8; ++i) q += x[j][i] * x[j][i];
+  // the weights go in while the sum (of the values before them) is on its way
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = (threadIdx.x + j * blockDim.x) * 8;
-    if (c >= a.H) continue;
-    float w[8], b[8];
-    if (n.weight) load8(n.weight, 0, c, a, n.type, w);
-    if (n.bias) load8(n.bias, 0, c, a, n.type, b);
+  for (int j = 0; j < NV; ++j) weight(j, x[j]);
+  const float r = rsqrtf(block_sum<THREADS>(q, buf, turn) * inv_h + n.eps);
+  if (!n.bias) return r;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[j][i] *= r;
-      if (n.weight) x[j][i] *= w[i] + n.offset;
-      if (n.bias) x[j][i] += b[i];
-    }
-  }
+  for (int j = 0; j < NV; ++j) bias(j, r, x[j]);
+  return 1.f;
 }
 
-template <int TA, int TR, int NV>
-__global__ void __launch_bounds__(kMaxThreads) residual_norm_kernel(const NormArgs a) {
+// Few rows, long or unaligned ones: a CTA a row, as many threads as there are
+// chunks.
+template <int TA, int TR, int NV, int THREADS, bool VEC>
+__global__ void __launch_bounds__(THREADS) norm_row_kernel(const NormArgs a) {
   __shared__ float buf[2][32];
   int turn = 0;
   pdl_wait();
   pdl_trigger();
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
-    float x[NV][8], res[NV][8];
+  const int64_t row = blockIdx.x;
+  const bool each_gate = a.gate && a.gsh != 0;
+  auto live = [&](int j) { return column<THREADS, VEC>(j, 0) < a.H; };  // some of the chunk exists
+  float x[NV][8], f = a.alpha;  // f: factor of all of the row
+  if (a.gate && !each_gate) f *= load_as_f32(a.gate, row * a.gst, TA);
+  Raw8 res[NV], gate[NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (threadIdx.x + j * blockDim.x) * 8;
+  for (int j = 0; j < NV; ++j) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[j][i] = res[j][i] = 0.f;
-      if (c < a.H) {
-        if (a.z) load8(a.z, t * a.zs, c, a, TA, x[j]);
-        if (a.res) load8(a.res, t * a.rs, c, a, TR, res[j]);
-      }
-    }
-    if (a.has_post) normalise<NV>(x, a.post, a, buf, turn);
-    const float row_gate = a.gate && a.gsh == 0 ? load_as_f32(a.gate, t * a.gst, TA) : 1.f;
+    for (int i = 0; i < 8; ++i) x[j][i] = 0.f;
+    if (!live(j)) continue;
+    if (a.z) raw8_to_f32(take8<THREADS, VEC>(a.z, row * a.zs, j, a.H, TA), TA, x[j]);
+    if (a.res) res[j] = take8<THREADS, VEC>(a.res, row * a.rs, j, a.H, TR);
+    if (each_gate) gate[j] = take8<THREADS, VEC>(a.gate, row * a.gst, j, a.H, TA);
+  }
+  auto norm = [&](const moe_norm_t &n) {
+    return normalise<NV, THREADS, VEC>(
+        x, n, a.H, buf, turn,
+        [&](int j, float(&v)[8]) {
+          if (!n.weight || !live(j)) return;
+          float w[8];
+          raw8_to_f32(take8<THREADS, VEC>(n.weight, 0, j, a.H, n.type), n.type, w);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (threadIdx.x + j * blockDim.x) * 8;
-      if (c >= a.H) continue;
+          for (int i = 0; i < 8; ++i) v[i] *= w[i] + n.offset;
+        },
+        [&](int j, float r, float(&v)[8]) {
+          if (!live(j)) return;
+          float b[8];
+          raw8_to_f32(take8<THREADS, VEC>(n.bias, 0, j, a.H, n.type), n.type, b);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = v[i] * r + b[i];
+        });
+  };
+  if (a.has_post) f *= norm(a.post);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if (!live(j)) continue;
+    if (each_gate) {
       float gt[8];
+      raw8_to_f32(gate[j], TA, gt);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) gt[i] = row_gate;
-      if (a.gate && a.gsh != 0) load8(a.gate, t * a.gst, c, a, TA, gt);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[j][i] = a.z ? res[j][i] + a.alpha * gt[i] * x[j][i] : res[j][i];
-      if (a.h) store8(a.h, t * a.hs, c, a, TR, x[j]);
+      for (int i = 0; i < 8; ++i) x[j][i] *= gt[i];
     }
-    if (a.has_pre) {
-      normalise<NV>(x, a.pre, a, buf, turn);
+    float rv[8];
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int c = (threadIdx.x + j * blockDim.x) * 8;
-        if (c < a.H) store8(a.y, t * a.ys, c, a, TA, x[j]);
+    for (int i = 0; i < 8; ++i) rv[i] = 0.f;
+    if (a.res) raw8_to_f32(res[j], TR, rv);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[j][i] = a.z ? rv[i] + f * x[j][i] : rv[i];
+    if (a.h) store8<THREADS, VEC>(a.h, row * a.hs, j, a.H, TR, x[j]);
+  }
+  if (!a.has_pre) return;
+  const float r = norm(a.pre);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if (!live(j)) continue;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[j][i] *= r;
+    store8<THREADS, VEC>(a.y, row * a.ys, j, a.H, TA, x[j]);
+  }
+}
+
+// Many aligned rows: a CTA walks over them, holds the norms' weights in
+// registers, and has its next row's loads under way while it works on the
+// present one. Chunks past the row are zeros that are neither loaded nor
+// stored. REST: a gate of every element and norms with a bias, which cost
+// registers.
+template <int TA, bool REST>
+constexpr int walkers(int threads) {  // CTAs an SM, by the registers that a thread needs (56, or up to 85)
+  return (TA == MOE_FP32 || REST ? 768 : 1152) / threads > 0 ? (TA == MOE_FP32 || REST ? 768 : 1152) / threads : 1;
+}
+
+template <int TA, int TR, int NV, int THREADS, bool REST>
+__global__ void __launch_bounds__(THREADS, NV == 1 ? walkers<TA, REST>(THREADS) : 1) norm_walk_kernel(const NormArgs a) {
+  const bool each = REST && a.gate && a.gsh != 0;
+  __shared__ float buf[2][32];
+  int turn = 0;
+  pdl_wait();
+  pdl_trigger();
+  bool live[NV];
+  float wpost[NV][8], wpre[NV][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (threadIdx.x + j * THREADS) * 8;
+    live[j] = c < a.H;
+    auto keep = [&](const moe_norm_t &n, bool has, float(&w)[8]) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = live[j] ? 1.f : 0.f;
+      if (!has || !n.weight || !live[j]) return;
+      raw8_to_f32(load_raw8(n.weight, c, n.type), n.type, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] += n.offset;
+    };
+    keep(a.post, a.has_post, wpost[j]);
+    keep(a.pre, a.has_pre, wpre[j]);
+  }
+  const int c0 = threadIdx.x * 8;
+  Raw8 z[NV], res[NV], gate[NV];
+  const Raw8 zero = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  uint32_t gate_bits = 0;
+  auto fetch = [&](int64_t row) {
+    if (!each && a.gate)
+      gate_bits = TA == MOE_FP32 ? static_cast<const uint32_t *>(a.gate)[row * a.gst]
+                                 : static_cast<const uint16_t *>(a.gate)[row * a.gst];
+    const int64_t zr = row * a.zs + c0, rr = row * a.rs + c0, gr = row * a.gst + c0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      z[j] = a.z && live[j] ? load_raw8(a.z, zr + j * THREADS * 8, TA) : zero;
+      res[j] = a.res && live[j] ? load_raw8(a.res, rr + j * THREADS * 8, TR) : zero;
+      if (REST && each) gate[j] = live[j] ? load_raw8(a.gate, gr + j * THREADS * 8, TA) : zero;
+    }
+  };
+  fetch(blockIdx.x);
+  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
+    float x[NV][8], f = a.alpha;
+    if (!each && a.gate) f *= load_as_f32(&gate_bits, 0, TA);
+    Raw8 rs[NV], gt[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      raw8_to_f32(z[j], TA, x[j]);
+      rs[j] = res[j];
+      if (REST) gt[j] = gate[j];
+    }
+    if (row + gridDim.x < a.T) fetch(row + gridDim.x);
+    auto norm = [&](const moe_norm_t &n, const float(&w)[NV][8]) {
+      return normalise<NV, THREADS, true>(
+          x, n, a.H, buf, turn,
+          [&](int j, float(&v)[8]) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] *= w[j][i];
+          },
+          [&](int j, float r, float(&v)[8]) {
+            if (!REST || !live[j]) return;
+            float b[8];
+            raw8_to_f32(load_raw8(n.bias, c0 + j * THREADS * 8, n.type), n.type, b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = v[i] * r + b[i];
+          });
+    };
+    if (a.has_post) f *= norm(a.post, wpost);
+    const int64_t hr = row * a.hs + c0, yr = row * a.ys + c0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float v[8];
+      if (REST && each) {
+        raw8_to_f32(gt[j], TA, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[j][i] *= v[i];
       }
+      raw8_to_f32(rs[j], TR, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[j][i] = v[i] + f * x[j][i];
+      if (a.h && live[j]) store_raw8(a.h, hr + j * THREADS * 8, TR, f32_to_raw8(x[j], TR));
+    }
+    if (!a.has_pre) continue;
+    const float r = norm(a.pre, wpre);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[j][i] *= r;
+      if (live[j]) store_raw8(a.y, yr + j * THREADS * 8, TA, f32_to_raw8(x[j], TA));
     }
   }
 }
 
+template <int TA, int TR, int NV, int THREADS, bool VEC>
+cudaError_t rows(const NormArgs &a, cudaStream_t stream) {
+  return launch_pdl(norm_row_kernel<TA, TR, NV, THREADS, VEC>, dim3(a.T), dim3(THREADS), 0, stream, a);
+}
+
+template <int TA, int TR, int NV, int THREADS>
+cudaError_t walk(const NormArgs &a, int sms, cudaStream_t stream) {
+  const bool rest = (a.gate && a.gsh != 0) || (a.has_post && a.post.bias) || (a.has_pre && a.pre.bias);
+  const int per = NV > 1 ? 1 : rest ? walkers<TA, true>(THREADS) : walkers<TA, false>(THREADS);
+  const dim3 grid(a.T < sms * per ? a.T : sms * per), block(THREADS);
+  return rest ? launch_pdl(norm_walk_kernel<TA, TR, NV, THREADS, true>, grid, block, 0, stream, a)
+              : launch_pdl(norm_walk_kernel<TA, TR, NV, THREADS, false>, grid, block, 0, stream, a);
+}
+
 template <int TA, int TR>
-cudaError_t go(const NormArgs &a, cudaStream_t stream) {
+cudaError_t go(const NormArgs &a, bool vec, cudaStream_t stream) {
   const int chunks = (a.H + 7) / 8;
-  const int nv = chunks <= kMaxThreads ? 1 : chunks <= 2 * kMaxThreads ? 2 : 4;
-  const int threads = ((chunks + nv - 1) / nv + 31) / 32 * 32;
-  const dim3 grid(a.T), block(threads);
-  if (nv == 1) return launch_pdl(residual_norm_kernel<TA, TR, 1>, grid, block, 0, stream, a);
-  if (nv == 2) return launch_pdl(residual_norm_kernel<TA, TR, 2>, grid, block, 0, stream, a);
-  return launch_pdl(residual_norm_kernel<TA, TR, 4>, grid, block, 0, stream, a);
+  if (!vec)
+    return chunks <= 256    ? rows<TA, TR, 1, 256, false>(a, stream)
+           : chunks <= 512  ? rows<TA, TR, 1, 512, false>(a, stream)
+           : chunks <= 1024 ? rows<TA, TR, 2, 512, false>(a, stream)
+                            : rows<TA, TR, 4, 512, false>(a, stream);
+  static int sms = 0;
+  if (sms == 0) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+  }
+  // from two rows an SM on walking pays (H 2880, bf16; a CTA a row / walking, us): 304 rows 4.2 / 4.1, 608 6.8 / 5.5,
+  // 1216 9.6 / 7.5, 2432 19.9 / 13.0
+  if (a.T > 2 * sms && chunks <= 1024)
+    return chunks <= 128   ? walk<TA, TR, 1, 128>(a, sms, stream)
+           : chunks <= 256 ? walk<TA, TR, 1, 256>(a, sms, stream)
+           : chunks <= 384 ? walk<TA, TR, 1, 384>(a, sms, stream)
+           : chunks <= 512 ? walk<TA, TR, 1, 512>(a, sms, stream)
+                           : walk<TA, TR, 2, 512>(a, sms, stream);
+  return chunks <= 128    ? rows<TA, TR, 1, 128, true>(a, stream)
+         : chunks <= 256  ? rows<TA, TR, 1, 256, true>(a, stream)
+         : chunks <= 512  ? rows<TA, TR, 1, 512, true>(a, stream)
+         : chunks <= 1024 ? rows<TA, TR, 2, 512, true>(a, stream)
+                          : rows<TA, TR, 4, 512, true>(a, stream);
 }
 
 }  // namespace
@@ -186,15 +360,15 @@ moe_status_t launch_residual_norm(const void *z, int64_t zs, const void *res, in
   a.has_post = post != nullptr;
   a.has_pre = pre != nullptr;
   auto whole = [](const void *p, int64_t s) { return !p || s % 8 == 0; };
-  a.vec = H % 8 == 0 && whole(z, zs) && whole(res, rs) && whole(h, hs) && whole(y, ys) &&
-          whole(gsh ? gate : nullptr, gst);
+  const bool vec = H % 8 == 0 && whole(z, zs) && whole(res, rs) && whole(h, hs) && whole(y, ys) &&
+                   whole(gsh ? gate : nullptr, gst);
   cudaError_t err;
   if (type == MOE_BF16)
-    err = res_type == MOE_FP32 ? go<MOE_BF16, MOE_FP32>(a, stream) : go<MOE_BF16, MOE_BF16>(a, stream);
+    err = res_type == MOE_FP32 ? go<MOE_BF16, MOE_FP32>(a, vec, stream) : go<MOE_BF16, MOE_BF16>(a, vec, stream);
   else if (type == MOE_FP16)
-    err = res_type == MOE_FP32 ? go<MOE_FP16, MOE_FP32>(a, stream) : go<MOE_FP16, MOE_FP16>(a, stream);
+    err = res_type == MOE_FP32 ? go<MOE_FP16, MOE_FP32>(a, vec, stream) : go<MOE_FP16, MOE_FP16>(a, vec, stream);
   else
-    err = go<MOE_FP32, MOE_FP32>(a, stream);
+    err = go<MOE_FP32, MOE_FP32>(a, vec, stream);
   if (launches) ++*launches;
   return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
