@@ -15,10 +15,12 @@
 // error: the truncation, and that of fp32 scores (score_error2). Where every
 // gap that the selection rests on -- last kept group to first dropped one,
 // each choice to the next -- is wider, the order is right. Other rows are
-// `open` and go through select_exact: exact keys if the logits give the order,
-// 64-bit scores for the few candidates within the error otherwise (64-bit
-// exponentials run at a 64th of the fp32 rate, so one a lane, not one an
-// expert). With random fp32 logits and a bias about one row in 500 is open.
+// `open`. Where it is the order of the k + 1 first that is, they are ranked by
+// 64-bit scores, one a lane (64-bit exponentials run at a 64th of the fp32
+// rate); that is about one row in 400 with random fp32 logits and a bias.
+// Undecided groups, and more candidates, go through select_exact, which has
+// its loops rolled up: run by a warp in ten thousand, its instructions come
+// from memory each time.
 #include "common.cuh"
 #include "kernels.h"
 #include "types.cuh"
@@ -46,6 +48,7 @@ struct RouteArgs {
 struct Scratch {
   int id[32];
   double c[32];
+  float order[256];  // what orders the experts, in fp32
 };
 
 // An unsigned key that orders as the float does (-0 made +0 before); 0 is free
@@ -59,16 +62,18 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 }
 __device__ __forceinline__ float not_nan(float v) { return v == v ? v : -INFINITY; }
 
-// Bound on twice the error of an fp32 selection score of size |v|, the cut to
-// 28 bits of key included (2^-19 of |v|). Sigmoid: E = exp(-l) is off by 2^-22
-// + |l| 2^-23 of itself, which 1 / (1 + E) turns into at most s (1 - s) of
-// that (<= 0.6e-7 + 0.27e-7), sum, quotient and the bias add at most 2^-22 of
-// s and 2^-24 of the result: below 5e-7 + 6e-8 |v|. Softmax: the exponential
-// likewise (s |l - m| < 0.37), its sum of up to 256 terms at most 21 * 2^-24 +
-// 2^-22 of itself (16 in a lane, five shuffles): below 2e-6 + 6e-8 |v|.
+// Bound on twice the error of an fp32 selection score of size |v|. Sigmoid: E =
+// exp(-l) is off by 2^-22 + |l| 2^-23 of itself, which 1 / (1 + E) turns into
+// at most s (1 - s) of that (<= 0.6e-7 + 0.27e-7), sum, quotient and the bias
+// add at most 2^-22 of s and 2^-24 of the result: below 5e-7 + 6e-8 |v|.
+// Softmax: the exponential likewise (s |l - m| < 0.37), its sum of up to 256
+// terms at most 21 * 2^-24 + 2^-22 of itself (16 in a lane, five shuffles):
+// below 2e-6 + 6e-8 |v|.
 __device__ __forceinline__ float score_error2(int score, float v) {
-  return (score == MOE_SCORE_SOFTMAX ? 4e-6f : 1e-6f) + 2.1e-6f * fabsf(v);
+  return (score == MOE_SCORE_SOFTMAX ? 4e-6f : 1e-6f) + 1.3e-7f * fabsf(v);
 }
+// The same for a score cut to the 28 bits of a key (2^-19 of it).
+__device__ __forceinline__ float key_error2(int score, float v) { return score_error2(score, v) + 2e-6f * fabsf(v); }
 
 __device__ __forceinline__ float warp_max(float v) { return value_of(__reduce_max_sync(kAll, key_of(v))); }
 template <typename F>
@@ -146,131 +151,146 @@ __device__ __forceinline__ void load_logits(const RouteArgs &a, Row<PL> &r) {
   for (int i = 0; i < PL; ++i) r.l[i] = not_nan(r.l[i]);
 }
 
-// 64-bit selection score of expert e.
-__device__ double score64(const RouteArgs &a, int64_t at, float m, double sum, int e) {
+// What orders expert e, in 64 bits.
+__device__ double order64(const RouteArgs &a, int64_t at, float m, double sum, int e, bool scored) {
   const float l = not_nan(load_as_f32(a.logits, at + e, a.type));
+  if (!scored) return l;
   double s = a.score == MOE_SCORE_SOFTMAX ? exp_rel64(l, m) / sum : 1.0 / (1.0 + exp(-(double)l));
   if (a.bias) s += (double)a.bias[e];
   return s == s ? s : -INFINITY;
 }
 
-// The choice for an open row: the j-th id in lane j.
-template <int PL>
-__device__ __noinline__ int select_exact(const RouteArgs &a, int64_t row, float m, float fsum, Scratch &w) {
-  // the row is read again: what the fast path holds stays in its registers
-  Row<PL> r;
-  r.at = row;
-  r.m = m;
-  r.sum = fsum;
-  enter_row<PL>(a, r);
-  load_logits<PL>(a, r);
-  const int lane = r.lane;
-  const bool grouped = a.topk_group < a.n_group, by_score = a.bias || (grouped && a.top2);
-  double sum = 1.0;
-  float c[PL];  // fp32 scores, as before
-  if (a.score == MOE_SCORE_SOFTMAX && by_score) {
-    sum = 0.0;
+// Sum of the softmax's exponentials in 64 bits, over the warp.
+__device__ double sum64(const RouteArgs &a, int64_t at, float m, int experts) {
+  double sum = 0.0;
 #pragma unroll 1
-    for (int i = 0; i < PL; ++i)
-      if ((r.valid >> i) & 1u) sum += exp_rel64(not_nan(load_as_f32(a.logits, r.at + r.e0 + i * a.lanes, a.type)), r.m);
-    sum = warp_sum(sum);
+  for (int e = threadIdx.x & 31; e < experts; e += 32) sum += exp_rel64(not_nan(load_as_f32(a.logits, at + e, a.type)), m);
+  return warp_sum(sum);
+}
+
+// n <= 32 candidates, one a lane, into the order of their 64-bit scores.
+__device__ __noinline__ int rank64(const RouteArgs &a, int64_t at, float m, int experts, int n, int mine, Scratch &w) {
+  const int lane = threadIdx.x & 31;
+  const double sum = a.bias && a.score == MOE_SCORE_SOFTMAX ? sum64(a, at, m, experts) : 1.0;
+  const double v = lane < n ? order64(a, at, m, sum, mine, a.bias) : 0.0;
+  int place = 0;
+#pragma unroll 1
+  for (int j = 0; j < n; ++j) {
+    const double ov = __shfl_sync(kAll, v, j);
+    const int oid = __shfl_sync(kAll, mine, j);
+    place += ov > v || (ov == v && oid < mine);
   }
-#pragma unroll
-  for (int i = 0; i < PL; ++i) {
-    c[i] = r.l[i];
-    if (by_score && ((r.valid >> i) & 1u)) {
-      float v = a.score == MOE_SCORE_SOFTMAX ? exp_rel(r.l[i], r.m) / r.sum : 1.0f / (1.0f + expf(-r.l[i]));
-      if (a.bias) v += a.bias[r.e0 + i * a.lanes];
-      c[i] = not_nan(v);
-    }
+  if (lane < n) w.id[place] = mine;
+  __syncwarp();
+  mine = lane < a.k ? w.id[lane] : 0;
+  __syncwarp();
+  return mine;
+}
+
+// The choice for an open row, the j-th id in lane j, from the logits on.
+__device__ __noinline__ int select_exact(const RouteArgs &a, int64_t at, float m, float fsum, Scratch &w) {
+  const int lane = threadIdx.x & 31, g = lane / a.lanes, sub = lane & (a.lanes - 1), e0 = g * a.gs + sub;
+  const int experts = a.n_group * a.gs;
+  const int mine_n = g < a.n_group && sub < a.gs ? (a.gs - sub + a.lanes - 1) / a.lanes : 0;  // experts of this lane
+  const bool grouped = a.topk_group < a.n_group, scored = a.bias || (grouped && a.top2);
+  const double sum = scored && a.score == MOE_SCORE_SOFTMAX ? sum64(a, at, m, experts) : 1.0;
+  auto score32 = [&](int e) {
+    const float l = not_nan(load_as_f32(a.logits, at + e, a.type));
+    if (!scored) return l;
+    float v = a.score == MOE_SCORE_SOFTMAX ? exp_rel(l, m) / fsum : 1.0f / (1.0f + expf(-l));
+    if (a.bias) v += a.bias[e];
+    return not_nan(v);
+  };
+  float b1 = -INFINITY, b2 = -INFINITY;  // the two best of the group
+#pragma unroll 1
+  for (int i = 0; i < mine_n; ++i) {
+    const int e = e0 + i * a.lanes;
+    const float v = score32(e);
+    w.order[e] = v;
+    b2 = fmaxf(b2, fminf(b1, v));
+    b1 = fmaxf(b1, v);
   }
-  bool kept = r.g < a.n_group;
+  bool kept = g < a.n_group;
   if (grouped) {
-    float b1 = -INFINITY, b2 = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < PL; ++i)
-      if ((r.valid >> i) & 1u) {
-        const float v = a.top2 || a.bias ? c[i] : r.l[i];
-        b2 = fmaxf(b2, fminf(b1, v));
-        b1 = fmaxf(b1, v);
-      }
+#pragma unroll 1
     for (int o = 1; o < a.lanes; o <<= 1) {
       const float o1 = __shfl_xor_sync(kAll, b1, o), o2 = __shfl_xor_sync(kAll, b2, o);
       b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
       b1 = fmaxf(b1, o1);
     }
-    const float gv = a.top2 ? not_nan(b1 + b2) : b1;
+    const float gv = g < a.n_group ? (a.top2 ? not_nan(b1 + b2) : b1) : -INFINITY;
     int ahead = 0;
-    float lv = INFINITY, nv = -INFINITY;  // of the last kept and the first dropped, as fp32 has it
+#pragma unroll 1
     for (int h = 0; h < a.n_group; ++h) {
       const float ov = __shfl_sync(kAll, gv, h * a.lanes);
-      ahead += ov > gv || (ov == gv && h < r.g);
+      ahead += ov > gv || (ov == gv && h < g);
     }
-    for (int h = 0; h < a.n_group; ++h) {
-      const float ov = __shfl_sync(kAll, gv, h * a.lanes);
-      if (__shfl_sync(kAll, ahead, h * a.lanes) < a.topk_group)
-        lv = fminf(lv, ov);
-      else
-        nv = fmaxf(nv, ov);
-    }
-    if (!by_score) {
+    if (!scored) {
       kept = kept && ahead < a.topk_group;
     } else {
+      // the last kept and the first dropped as fp32 has it; those that are within the error of the other side
+      const unsigned in = __ballot_sync(kAll, kept && ahead == a.topk_group - 1),
+                     out = __ballot_sync(kAll, kept && ahead == a.topk_group);
+      const float lv = __shfl_sync(kAll, gv, __ffs(in) - 1), nv = __shfl_sync(kAll, gv, __ffs(out) - 1);
       const float tol = 2.f * score_error2(a.score, fmaxf(fabsf(lv), fabsf(nv)));
       const bool sure = kept && gv > lv + tol;
       const bool maybe = kept && !sure && !(gv < nv - tol);
       // 64-bit scores of those of an undecided group that can be its best, or its two best
-      const float least = (a.top2 ? b2 : b1) - score_error2(a.score, a.top2 ? b2 : b1);
+      const float edge = a.top2 ? b2 : b1, least = edge - score_error2(a.score, edge);
       double d1 = -INFINITY, d2 = -INFINITY;
-      auto put = [&](double v) {
-        if (v > d1) {
-          d2 = d1;
-          d1 = v;
-        } else if (v > d2) {
-          d2 = v;
-        }
-      };
-      unsigned need = 0;
-#pragma unroll
-      for (int i = 0; i < PL; ++i)
-        if (maybe && ((r.valid >> i) & 1u) && !(c[i] < least)) need |= 1u << i;
-      while (const unsigned who = __ballot_sync(kAll, need != 0)) {  // one candidate of each lane at a time
-        const int at = __popc(who & ((1u << lane) - 1u)), cnt = __popc(who);
-        if (need) {
-          w.id[at] = r.e0 + (__ffs(need) - 1) * a.lanes;
-          need &= need - 1;
-        }
+      int i = 0;
+#pragma unroll 1
+      while (true) {  // one candidate of each lane at a time
+        while (maybe && i < mine_n && w.order[e0 + i * a.lanes] < least) ++i;
+        const bool need = maybe && i < mine_n;
+        const unsigned who = __ballot_sync(kAll, need);
+        if (!who) break;
+        const int to = __popc(who & ((1u << lane) - 1u)), cnt = __popc(who);
+        if (need) w.id[to] = e0 + i * a.lanes;
+        ++i;
         __syncwarp();
-        if (lane < cnt) w.c[lane] = score64(a, r.at, r.m, sum, w.id[lane]);
+        if (lane < cnt) w.c[lane] = order64(a, at, m, sum, w.id[lane], true);
         __syncwarp();
+#pragma unroll 1
         for (int j = 0; j < cnt; ++j)
-          if (w.id[j] / a.gs == r.g) put(w.c[j]);
+          if (w.id[j] / a.gs == g) {
+            const double v = w.c[j];
+            d2 = fmax(d2, fmin(d1, v));
+            d1 = fmax(d1, v);
+          }
         __syncwarp();
       }
       double gd = a.top2 ? d1 + d2 : d1;
       if (!(gd == gd)) gd = -INFINITY;
       int place = 0;
+#pragma unroll 1
       for (int h = 0; h < a.n_group; ++h) {
         const double od = __shfl_sync(kAll, gd, h * a.lanes);
         const bool om = __shfl_sync(kAll, (int)maybe, h * a.lanes), os = __shfl_sync(kAll, (int)sure, h * a.lanes);
-        place += os || (om && (od > gd || (od == gd && h < r.g)));
+        place += os || (om && (od > gd || (od == gd && h < g)));
       }
       kept = sure || (maybe && place < a.topk_group);
     }
   }
-  unsigned left = kept ? r.valid : 0u;
+  if (scored && !a.bias) {  // the logits order the experts of the kept groups
+#pragma unroll 1
+    for (int i = 0; i < mine_n; ++i)
+      w.order[e0 + i * a.lanes] = not_nan(load_as_f32(a.logits, at + e0 + i * a.lanes, a.type));
+  }
   // candidates in fp32 order, by index among equals: k, and with computed scores those within the error of the k-th
+  const unsigned all = kept ? (1u << mine_n) - 1u : 0u;
+  unsigned left = all;
   int mine = 0, n = 0;
   float kth = 0.f;
+#pragma unroll 1
   while (n < 32) {
     float best = -INFINITY;
     int bid = 0x7fffffff;
-#pragma unroll
-    for (int i = 0; i < PL; ++i) {
-      const float v = a.bias ? c[i] : r.l[i];
-      const int e = r.e0 + i * a.lanes;
-      if (((left >> i) & 1u) && (v > best || (v == best && e < bid))) {
-        best = v;
+#pragma unroll 1
+    for (unsigned l = left; l; l &= l - 1) {
+      const int e = e0 + (__ffs(l) - 1) * a.lanes;
+      if (bid == 0x7fffffff || w.order[e] > best) {
+        best = w.order[e];
         bid = e;
       }
     }
@@ -280,52 +300,38 @@ __device__ __noinline__ int select_exact(const RouteArgs &a, int64_t row, float 
     const float v = value_of(top);
     if (n >= a.k && (!a.bias || v < kth - score_error2(a.score, kth))) break;
     if (n < a.k) kth = v;
-    if (bid == id) left &= ~(1u << ((id - r.e0) / a.lanes));
+    if (bid == id) left &= ~(1u << ((id - e0) / a.lanes));
     if (lane == n) mine = id;
     ++n;
   }
   if (!a.bias) return mine;
-  if (n < 32) {
-    // ranked by their 64-bit scores, one a lane
-    const double v = lane < n ? score64(a, r.at, r.m, sum, mine) : -INFINITY;
-    int place = 0;
-    for (int j = 0; j < n; ++j) {
-      const double ov = __shfl_sync(kAll, v, j);
-      const int oid = __shfl_sync(kAll, mine, j);
-      place += ov > v || (ov == v && oid < mine);
-    }
-    if (lane < n) w.id[place] = mine;
-    __syncwarp();
-    mine = lane < a.k ? w.id[lane] : 0;
-    __syncwarp();
-    return mine;
-  }
+  if (n < 32) return rank64(a, at, m, experts, n, mine, w);
   // more candidates than lanes: every expert in 64 bits, k times over
-  left = kept ? r.valid : 0u;
+  left = all;
+#pragma unroll 1
   for (int j = 0; j < a.k; ++j) {
     double best = -INFINITY;
     int bid = 0x7fffffff;
 #pragma unroll 1
-    for (int i = 0; i < PL; ++i)
-      if ((left >> i) & 1u) {
-        const int e = r.e0 + i * a.lanes;
-        const double v = score64(a, r.at, r.m, sum, e);
-        if (v > best || (v == best && e < bid)) {
-          best = v;
-          bid = e;
-        }
+    for (unsigned l = left; l; l &= l - 1) {
+      const int e = e0 + (__ffs(l) - 1) * a.lanes;
+      const double v = order64(a, at, m, sum, e, true);
+      if (bid == 0x7fffffff || v > best) {
+        best = v;
+        bid = e;
       }
+    }
     const int own = bid;
-#pragma unroll
+#pragma unroll 1
     for (int o = 16; o > 0; o >>= 1) {
       const double ov = __shfl_xor_sync(kAll, best, o);
       const int oid = __shfl_xor_sync(kAll, bid, o);
-      if (ov > best || (ov == best && oid < bid)) {
+      if (oid != 0x7fffffff && (bid == 0x7fffffff || ov > best || (ov == best && oid < bid))) {
         best = ov;
         bid = oid;
       }
     }
-    if (own == bid) left &= ~(1u << ((bid - r.e0) / a.lanes));
+    if (own == bid) left &= ~(1u << ((bid - e0) / a.lanes));
     if (lane == j) mine = bid;
   }
   return mine;
@@ -333,7 +339,7 @@ __device__ __noinline__ int select_exact(const RouteArgs &a, int64_t row, float 
 
 // PL: experts a lane, rounded up to a power of two
 template <int PL>
-__global__ void __launch_bounds__(kWarps * 32) group_route_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, PL <= 8 ? 7 : 5) group_route_kernel(const RouteArgs a) {
   __shared__ Scratch scratch[kWarps];
   pdl_wait();
   pdl_trigger();
@@ -364,25 +370,25 @@ __global__ void __launch_bounds__(kWarps * 32) group_route_kernel(const RouteArg
     auto score = [&](float l) {
       return a.score == MOE_SCORE_SOFTMAX ? __fdividef(exp_rel(l, r.m), r.sum) : __fdividef(1.0f, 1.0f + __expf(-l));
     };
-    uint32_t key[PL];
+    uint32_t key[PL], full[PL];
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
-      const uint32_t full = key_of(a.bias ? not_nan(score(r.l[i]) + bias[i]) : r.l[i]);
-      const uint32_t cut = short_keys ? (full & ~0x1FFFu) | (0x1FFFu - (uint32_t)(r.e0 + i * a.lanes))
-                                      : (full & ~15u) | (uint32_t)(15 - i);
-      key[i] = (r.valid >> i) & 1u ? cut : 0u;
+      full[i] = (r.valid >> i) & 1u ? key_of(a.bias ? not_nan(score(r.l[i]) + bias[i]) : r.l[i]) : 0u;
+      const uint32_t cut = short_keys ? (full[i] & ~0x1FFFu) | (0x1FFFu - (uint32_t)(r.e0 + i * a.lanes))
+                                      : (full[i] & ~15u) | (uint32_t)(15 - i);
+      key[i] = full[i] ? cut : 0u;
     }
     sort_keys<PL>(key);
-    bool open = false;  // the keys leave the selection open
+    bool open = false;         // the groups, or too many candidates, are undecided
+    bool open_order = false;   // so is the order of the first k + 1
     if (grouped) {
       uint32_t b1 = key[0], b2 = PL > 1 ? key[PL > 1] : 0u;
-      if (a.top2 && !a.bias) {  // the scores of the two largest logits: those whole, not as the keys have them
+      if (by_score) {  // whole, not as the keys have them: the scores, or the logits whose scores are wanted
         b1 = b2 = 0u;
 #pragma unroll
         for (int i = 0; i < PL; ++i) {
-          const uint32_t full = (r.valid >> i) & 1u ? key_of(r.l[i]) : 0u;
-          b2 = max(b2, min(b1, full));
-          b1 = max(b1, full);
+          b2 = max(b2, min(b1, full[i]));
+          b1 = max(b1, full[i]);
         }
       }
       for (int o = 1; o < a.lanes; o <<= 1) {
@@ -414,21 +420,27 @@ __global__ void __launch_bounds__(kWarps * 32) group_route_kernel(const RouteArg
       }
     }
     int mine = 0;
-    uint32_t prev = kAll;
-    const int rounds = a.k + (short_keys ? 0 : 1);  // the choice after the last decides whether that one is sure
+    uint32_t prev = kAll, kth = 0;
+    int candidates = 0;
+    // the two after the last choice decide whether that one is sure, and whether the first k + 1 are all that matter
+    const int rounds = a.k + (short_keys ? 0 : 2);
     for (int j = 0; j < rounds; ++j) {
       const uint32_t top = __reduce_max_sync(kAll, key[0]);
       const unsigned who = __ballot_sync(kAll, key[0] == top);
-      if (top == 0u) break;  // fewer candidates than k + 1
+      if (top == 0u) break;  // fewer candidates than k + 2
+      candidates = j + 1;
       const int from = __ffs(who) - 1;
       if (!short_keys) {
-        if (a.bias) {
-          const float v = value_of(top & ~15u), p = value_of(prev & ~15u);
-          open = open || (j > 0 && !(p - v > score_error2(a.score, fmaxf(fabsf(p), fabsf(v)))));
-        } else {
-          open = open || (prev >> 4) == (top >> 4);
-        }
-        open = open || (who & (who - 1));
+        auto close = [&](uint32_t hi, uint32_t lo) {
+          if (!a.bias) return (hi >> 4) == (lo >> 4);
+          const float p = value_of(hi & ~15u), v = value_of(lo & ~15u);
+          return !(p - v > key_error2(a.score, fmaxf(fabsf(p), fabsf(v))));
+        };
+        if (j == a.k + 1)
+          open = open || close(kth, top);
+        else if (j > 0)
+          open_order = open_order || close(prev, top);
+        if (j == a.k - 1) kth = top;
       }
       prev = top;
       const int id = short_keys ? (int)(0x1FFFu - (top & 0x1FFFu))
@@ -440,7 +452,10 @@ __global__ void __launch_bounds__(kWarps * 32) group_route_kernel(const RouteArg
         key[PL - 1] = 0u;
       }
     }
-    if (open) mine = select_exact<PL>(a, r.at, r.m, r.sum, scratch[threadIdx.x >> 5]);
+    if (open)
+      mine = select_exact(a, r.at, r.m, r.sum, scratch[threadIdx.x >> 5]);
+    else if (open_order)
+      mine = rank64(a, r.at, r.m, a.n_group * a.gs, min(a.k + 1, candidates), mine, scratch[threadIdx.x >> 5]);
     // weights: lane j has the j-th choice
     const bool has = r.lane < a.k;
     const float lv = has ? not_nan(load_as_f32(a.logits, r.at + mine, a.type)) : -INFINITY;
