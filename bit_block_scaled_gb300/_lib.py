@@ -57,7 +57,8 @@ class Router(ctypes.Structure):
 
 class Norm(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("type", ctypes.c_int32), ("eps", ctypes.c_float),
-                ("offset", ctypes.c_float), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+                ("offset", ctypes.c_float), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("width", ctypes.c_int32)]  # behind moe_norm_t: the parameters' length, for the binding's check
 
 
 class KvCache(ctypes.Structure):
@@ -323,50 +324,31 @@ def moe_import_modelopt_global_scale(weight_scale_2, E):
 
 
 # ------------------------------------------------ around the layer: routing with groups, norms, cache, attention
-# These calls are short next to what Python costs: pointers go as plain integers, structures as themselves, and the
-# stream's handle comes without a stream object.
+# Their tensors are looked at in C++ (csrc/binding.cpp): the calls are as short as Python's own work on them.
 _INVALID = 1
-_types = None
-_raw_stream = None
+_fast = None
 
 
 def _setup():
-    """Types by number, and the current stream's handle by device."""
-    global _types, _raw_stream
-    import torch
-    _types = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.int32: 3, torch.uint8: 4}
-    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-        lambda device: torch.cuda.current_stream(device).cuda_stream)
-    return load()
+    """The C++ part of the binding (once). Raises ImportError when it is missing."""
+    global _fast
+    load()
+    import importlib.machinery
+    import importlib.util
 
-
-_I32, _U8 = 3, 4
+    import torch  # noqa: F401  its libraries first
+    path = os.path.join(HERE, "_binding.so")
+    if not os.path.exists(path):
+        raise ImportError(f"the binding is not built ({path} missing); run bit_block_scaled_gb300.build.build()")
+    loader = importlib.machinery.ExtensionFileLoader("_binding", path)
+    mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_binding", loader))
+    loader.exec_module(mod)
+    _fast = mod
+    return mod
 
 
 def _fail(where):
     raise MoeError(_INVALID, where)
-
-
-def _float_type(t, where):
-    code = _types.get(t.dtype, 9)
-    if code > 2:
-        raise MoeError(_INVALID, f"{where}: {t.dtype}")
-    return code
-
-
-def _flat(t, code, n, where):
-    """Pointer of a contiguous tensor of n values of a type; None stays NULL."""
-    if t is None:
-        return None
-    if _types.get(t.dtype) != code or t.numel() != n or not t.is_contiguous():
-        _fail(where)
-    return t.data_ptr()
-
-
-def _stream_at(stream, t):
-    if stream is None:
-        return _raw_stream(t.get_device())
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def router(score="softmax", n_group=1, topk_group=1, group_score="max", renormalize=True, scale=1.0) -> Router:
@@ -377,77 +359,34 @@ def router(score="softmax", n_group=1, topk_group=1, group_score="max", renormal
 
 def moe_route_grouped(logits, sel_bias, k, cfg, topk_ids, topk_weights, ws, stream=None):
     """logits [T, E] bf16, fp16 or fp32 (rows may be apart), sel_bias fp32 [E] or None, cfg from router()."""
-    where = "moe_route_grouped"
-    lib = _lib if _types else _setup()
-    T, E = logits.shape
-    ld, one = logits.stride()
-    if one != 1 and E > 1:
-        _fail(where)
-    code = lib.moe_route_grouped(logits.data_ptr(), _float_type(logits, where), ld if T > 1 else E,
-                                 _flat(sel_bias, 2, E, where), T, E, k, cfg, _flat(topk_ids, _I32, T * k, where),
-                                 _flat(topk_weights, 2, T * k, where), ws.data_ptr(), _stream_at(stream, logits))
+    code = (_fast or _setup()).route_grouped(logits, sel_bias, k, cfg, topk_ids, topk_weights, ws, stream)
     if code:
-        raise MoeError(code, where)
+        raise MoeError(code, "moe_route_grouped")
 
 
 def norm(kind="rms", weight=None, bias=None, eps=1e-5, offset=0.0) -> Norm:
     """A norm's parameters; the caller keeps the tensors alive while the struct is in use."""
-    if not _types:
-        _setup()
-    code, width = 2, None
+    import torch
+    code, width = 2, 0
     for t in (weight, bias):
         if t is not None:
-            code = _float_type(t, "norm")
-            if t.dim() != 1 or not t.is_contiguous():
+            code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(t.dtype, -1)
+            if code < 0 or t.dim() != 1 or not t.is_contiguous():
                 _fail("norm")
             width = t.numel()
     if weight is not None and bias is not None and (weight.dtype != bias.dtype or weight.shape != bias.shape):
         _fail("norm")
-    n = Norm(NORM[kind] if isinstance(kind, str) else int(kind), code, float(eps), float(offset),
-             None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr())
-    n.width = width
-    return n
+    return Norm(NORM[kind] if isinstance(kind, str) else int(kind), code, float(eps), float(offset),
+                None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr(), width)
 
 
 def moe_residual_norm(z, residual, gate, post, alpha, h_out, pre, y_out, stream=None):
     """h_out = residual + alpha * gate * post(z); y_out = pre(h_out). z, gate, y_out [T, H] of one type,
     residual and h_out of it or fp32; gate [T, H], [T, 1] or [1, H]; post, pre from norm(). See the header
     for which may be None."""
-    where = "moe_residual_norm"
-    lib = _lib if _types else _setup()
-    act = z if z is not None else y_out if y_out is not None else residual
-    res = residual if residual is not None else h_out if h_out is not None else act
-    if act is None or act.dim() != 2:
-        _fail(where)
-    T, H = shape = act.shape
-    apart = (H + 7) // 8 * 8  # the stride of a single row does not matter
-    at, rt = act.dtype, res.dtype
-
-    def rows(t, dtype):
-        if t is None:
-            return None, 0
-        if t.dtype != dtype or t.shape != shape:
-            _fail(where)
-        s, one = t.stride()
-        if one != 1 and H > 1:
-            _fail(where)
-        return t.data_ptr(), s if T > 1 else apart
-    for n in (post, pre):
-        if n is not None and n.width != H and n.width is not None:
-            _fail(where)
-    gp, gst, gsh = None, 0, 0
-    if gate is not None:
-        gt, gh = gate.shape
-        if gate.dtype != at or (gt != T and gt != 1) or (gh != H and gh != 1):
-            _fail(where)
-        gp = gate.data_ptr()
-        gst = gate.stride(0) if gt > 1 else 0
-        gsh = gate.stride(1) if gh > 1 else 0
-    code = lib.moe_residual_norm(*rows(z, at), *rows(residual, rt), gp, gst, gsh, T, H, _float_type(act, where),
-                                 _float_type(res, where), post, alpha, *rows(h_out, rt), pre, *rows(y_out, at),
-                                 _stream_at(stream, act))
+    code = (_fast or _setup()).residual_norm(z, residual, gate, post, alpha, h_out, pre, y_out, stream)
     if code:
-        raise MoeError(code, where)
+        raise MoeError(code, "moe_residual_norm")
 
 
 def moe_kv_record_bytes(fmt, head_dim):
@@ -457,58 +396,27 @@ def moe_kv_record_bytes(fmt, head_dim):
 def kv_cache(data, fmt, head_dim) -> KvCache:
     """KvCache view of a uint8 tensor [num_pages, kv_heads, page_size / 16, moe_kv_record_bytes(fmt, head_dim)];
     the caller keeps the tensor alive while the struct is in use."""
-    if not _types:
-        _setup()
+    import torch
     code = KV_FMT[fmt] if isinstance(fmt, str) else int(fmt)
     rec = moe_kv_record_bytes(code, head_dim)
-    if data.dim() != 4 or _types.get(data.dtype) != _U8 or not data.is_contiguous() or (rec and data.shape[3] != rec):
+    if data.dim() != 4 or data.dtype != torch.uint8 or not data.is_contiguous() or (rec and data.shape[3] != rec):
         _fail("kv_cache")
     return KvCache(code, int(data.shape[0]), int(data.shape[2]) * 16, int(data.shape[1]), int(head_dim),
                    data.data_ptr())
 
 
-def _rows3(t, shape, where):
-    """Pointer and strides over tokens and heads of a [T, heads, head_dim] tensor."""
-    if t.shape != shape:
-        _fail(where)
-    st, sh, one = t.stride()
-    if one != 1:
-        _fail(where)
-    T, heads, D = shape
-    return t.data_ptr(), st if T > 1 else heads * D, sh if heads > 1 else D
-
-
 def moe_kv_write(k, v, slots, cache, ws, stream=None):
     """k, v [T, kv_heads, head_dim] of one type (parts of a larger tensor are fine), slots int32 [T]."""
-    where = "moe_kv_write"
-    lib = _lib if _types else _setup()
-    T = slots.numel()
-    shape = (T, cache.kv_heads, cache.head_dim)
-    if k.dtype != v.dtype:
-        _fail(where)
-    kp, kt, kh = _rows3(k, shape, where)
-    vp, vt, vh = _rows3(v, shape, where)
-    code = lib.moe_kv_write(kp, vp, _float_type(k, where), kt, kh, vt, vh, _flat(slots, _I32, T, where), T, cache,
-                            ws.data_ptr(), _stream_at(stream, k))
+    code = (_fast or _setup()).kv_write(k, v, slots, cache, ws, stream)
     if code:
-        raise MoeError(code, where)
+        raise MoeError(code, "moe_kv_write")
 
 
 def moe_kv_read(cache, slots, k_out, v_out, ws, stream=None):
     """k_out, v_out [n, kv_heads, head_dim] of one type, either may be None; slots int32 [n]."""
-    where = "moe_kv_read"
-    lib = _lib if _types else _setup()
-    n = slots.numel()
-    shape = (n, cache.kv_heads, cache.head_dim)
-    one = k_out if k_out is not None else v_out
-    if one is None or (v_out is not None and v_out.dtype != one.dtype):
-        _fail(where)
-    kp, kt, kh = (None, 0, 0) if k_out is None else _rows3(k_out, shape, where)
-    vp, vt, vh = (None, 0, 0) if v_out is None else _rows3(v_out, shape, where)
-    code = lib.moe_kv_read(cache, _flat(slots, _I32, n, where), n, kp, vp, _float_type(one, where), kt, kh, vt, vh,
-                           ws.data_ptr(), _stream_at(stream, slots))
+    code = (_fast or _setup()).kv_read(cache, slots, k_out, v_out, ws, stream)
     if code:
-        raise MoeError(code, where)
+        raise MoeError(code, "moe_kv_read")
 
 
 def moe_attn_workspace_size(q_heads, kv_heads, head_dim):
@@ -520,19 +428,8 @@ def moe_attn_workspace_size(q_heads, kv_heads, head_dim):
 def moe_attn_decode(q, cache, block_table, seq_lens, out, ws, scale=None, window=0, sinks=None, lse=None, stream=None):
     """q, out [B, q_heads, head_dim] bf16 or fp16, block_table int32 [B, pages], seq_lens int32 [B], sinks fp32
     [q_heads], lse fp32 [B, q_heads]; scale None: head_dim ** -0.5."""
-    where = "moe_attn_decode"
-    lib = _lib if _types else _setup()
-    B, heads, D = shape = q.shape
-    bt, pages = block_table.shape
-    ts, one = block_table.stride()
-    if (D != cache.head_dim or out.dtype != q.dtype or bt != B or _types.get(block_table.dtype) != _I32 or
-            (one != 1 and pages > 1) or _types.get(ws.dtype) != _U8):
-        _fail(where)
-    qp, qb, qh = _rows3(q, shape, where)
-    op, ob, oh = _rows3(out, shape, where)
-    code = lib.moe_attn_decode(qp, _float_type(q, where), qb, qh, cache, block_table.data_ptr(), ts if B > 1 else pages,
-                               pages, _flat(seq_lens, _I32, B, where), B, heads, D ** -0.5 if scale is None else scale,
-                               window, _flat(sinks, 2, heads, where), op, ob, oh, _flat(lse, 2, B * heads, where),
-                               ws.data_ptr(), ws.numel(), _stream_at(stream, q))
+    if scale is None:
+        scale = cache.head_dim ** -0.5
+    code = (_fast or _setup()).attn_decode(q, cache, block_table, seq_lens, out, ws, scale, window, sinks, lse, stream)
     if code:
-        raise MoeError(code, where)
+        raise MoeError(code, "moe_attn_decode")

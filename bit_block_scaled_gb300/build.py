@@ -2,18 +2,22 @@
 
 Each .cu file is compiled to an object in parallel, then linked into a shared
 library next to this file. cudart is linked statically, so the library has no
-dependency beyond the CUDA driver.
+dependency beyond the CUDA driver. Beside it stands _binding.so, the C++ part of
+the Python binding (csrc/binding.cpp), which is built against the installed
+PyTorch.
 """
 import concurrent.futures as cf
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe4.so")
+BINDING = os.path.join(HERE, "_binding.so")
 SOURCES = ["api.cu", "route.cu", "align.cu", "gemm.cu", "unpermute.cu", "static_ws.cu", "convert.cu",
            "block_api.cu", "group_route.cu", "norm.cu", "kvcache.cu", "attn.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -26,6 +30,22 @@ def nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found")
+
+
+def _binding_command():
+    """Compiles the C++ binding to an object; its libraries come at the link."""
+    import torch
+    top = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    obj = os.path.join(BUILD, "binding.o")
+    inc = [os.path.join(top, "include"), os.path.join(top, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+                *(x for i in inc for x in ("-isystem", i)), "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    lib = os.path.join(top, "lib")
+    link = ["g++", "-shared", "-o", BINDING + ".tmp", obj, LIB, "-Wl,-rpath,$ORIGIN", f"-L{lib}",
+            f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    return obj, compile_, link
 
 
 def _stale(obj, deps):
@@ -49,6 +69,10 @@ def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
         if force or _stale(o, [s] + headers):
             jobs.append([cc, *ARCH, *FLAGS, *extra_flags, "-c", s, "-o", o])
 
+    obj, compile_, link_binding = _binding_command()
+    if force or _stale(obj, [os.path.join(CSRC, "binding.cpp"), headers[-1]]):
+        jobs.append(compile_)
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
@@ -58,14 +82,20 @@ def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
             if verbose or r.returncode != 0:
                 sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
             if r.returncode != 0:
-                raise RuntimeError(f"nvcc failed for {cmd[-3]}")
+                raise RuntimeError(f"compiling {cmd[-3]} failed")
     if force or jobs or not os.path.exists(LIB):
-        cmd = [cc, *ARCH, "-shared", "-o", LIB + ".tmp", *objs]
+        cmd = [cc, *ARCH, "-shared", "-Xlinker", "-soname=libmoe4.so", "-o", LIB + ".tmp", *objs]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
             raise RuntimeError("link failed")
         os.replace(LIB + ".tmp", LIB)
+    if force or jobs or not os.path.exists(BINDING):
+        r = subprocess.run(link_binding, capture_output=True, text=True)
+        if r.returncode != 0:
+            sys.stderr.write(" ".join(link_binding) + "\n" + r.stdout + r.stderr)
+            raise RuntimeError("linking the binding failed")
+        os.replace(BINDING + ".tmp", BINDING)
     return LIB
 
 
