@@ -36,7 +36,8 @@
 // from its registers; what is shared by warps of a CTA is joined in shared
 // memory, once at the end; what is shared by CTAs goes to the workspace as a
 // partial output with its log-sum, and a second kernel joins those. All orders
-// are fixed, so results do not vary from run to run.
+// are fixed, so results do not vary from run to run. Where no (sequence, head)
+// can be long, CTAs take whole ones and the second kernel is not needed.
 #include <algorithm>
 
 #include "common.cuh"
@@ -52,6 +53,7 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kW = 4;              // warps of a CTA
 constexpr int kMaxCtas = 640;      // partial outputs the workspace holds: two a CTA
 constexpr int kMaxB = 4096;
+constexpr int kJoinThreads = 128;
 constexpr int kLead = 4;           // empty units before each (sequence, head)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 4.f;      // lazy maximum, log2
@@ -69,7 +71,7 @@ struct AttnArgs {
   float *part_o;     // [2 kMaxCtas][NH][D]
   float *part_lse;   // [2 kMaxCtas][NH], log2
   int64_t qsb, qsh, osb, osh, ts;
-  int q_type, B, heads, kv_heads, G, GB, window, page, pages, max_pages, ctas;
+  int q_type, B, heads, kv_heads, G, GB, window, page, pages, max_pages, ctas, whole;
   float scale;       // scale * log2 e
 };
 
@@ -144,12 +146,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
-}
-
-// Units of a CTA: a multiple of the warps.
-__device__ __forceinline__ int64_t units_a_cta(int64_t total, int ctas) {
-  const int64_t each = (total + ctas - 1) / ctas;
-  return (each + kW - 1) / kW * kW;
 }
 
 // Tokens of sequence b that are read: [first, len), in records [lo, lo + n), n >= 1.
@@ -277,14 +273,28 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
   __syncthreads();
   const int HB = a.kv_heads * a.GB;
   const int64_t total = ((int64_t)base + (int64_t)a.B * kLead) * HB;
-  const int64_t per = units_a_cta(total, a.ctas);
-  if (blockIdx.x == 0) {  // what the joining kernel needs of this
-    if (tid == 0) *a.per = per;
-    for (int b = tid; b <= a.B; b += kW * 32) a.starts[b] = start[b];
+  int64_t cta0, cta1;  // this CTA's units
+  if (a.whole) {
+    auto unit_of = [&](int64_t seg) {  // first unit of a (sequence, head)
+      const int b = (int)(seg / HB), hb = (int)(seg % HB);
+      const int64_t at = ((int64_t)start[b] + (int64_t)b * kLead) * HB;
+      return b < a.B ? at + (int64_t)hb * (start[b + 1] - start[b] + kLead) : total;
+    };
+    const int64_t segs = (int64_t)a.B * HB;
+    cta0 = unit_of(segs * blockIdx.x / a.ctas);
+    cta1 = unit_of(segs * (blockIdx.x + 1) / a.ctas);
+  } else {
+    const int64_t per = (total + a.ctas - 1) / a.ctas;
+    if (blockIdx.x == 0) {  // what the joining kernel needs of this
+      if (tid == 0) *a.per = per;
+      for (int b = tid; b <= a.B; b += kW * 32) a.starts[b] = start[b];
+    }
+    cta0 = (int64_t)blockIdx.x * per;
+    cta1 = min(cta0 + per, total);
   }
-  const int64_t cta0 = (int64_t)blockIdx.x * per;
-  if (cta0 >= total) return;
-  const int64_t u0 = cta0 + warp * (per / kW), u1 = min(u0 + per / kW, total);
+  if (cta0 >= cta1) return;
+  const int64_t share = (cta1 - cta0 + kW - 1) / kW;
+  const int64_t u0 = min(cta0 + warp * share, cta1), u1 = min(u0 + share, cta1);
 
   // the records of the (sequence, head) k.b, k.hb that begins at unit k.at
   auto fill = [&](Seg &k) {
@@ -845,97 +855,91 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
   }
 }
 
-// Joins the partial outputs of one (sequence, kv head, block of heads):
-// grid (B * HB, heads of a block), 256 threads; the threads of a group of
-// D / 4 take 4 columns each, the groups take the partials in turn.
+// Joins the partial outputs of one (sequence, kv head, block of heads), if
+// there are several: grid (B * HB, slices of the heads). A warp a head turns
+// the partials' log-sums into weights; then a thread takes 4 columns of a head,
+// and where there are fewer of those than threads, every so many-th partial.
 template <int D, int NT>
-__global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
-  constexpr int kHeads = 8 * NT;
-  constexpr int kGroups = 256 / (D / 4);
-  __shared__ float wts[kMaxCtas];
-  __shared__ float red[32];
-  __shared__ float4 acc_s[kGroups][D / 4];
-  pdl_wait();
-  pdl_trigger();
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a) {
+  constexpr int kHeads = 8 * NT, kWarps = kJoinThreads / 32, kCols = D / 4;
+  extern __shared__ float wts[];  // [heads of this slice][parts]
+  __shared__ float4 acc_s[kJoinThreads];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int HB = a.kv_heads * a.GB;
   const int b = blockIdx.x / HB, hb = blockIdx.x % HB;
+  const int nh = min(kHeads, a.G - hb % a.GB * kHeads), h0 = hb / a.GB * a.G + hb % a.GB * kHeads;
+  // heads of this slice
+  const int each = (nh + gridDim.y - 1) / gridDim.y, from = blockIdx.y * each, heads = min(each, nh - from);
+  pdl_wait();
+  pdl_trigger();
   const int64_t per = *a.per;
   const int s0 = a.starts[b], n = a.starts[b + 1] - s0;
   const int64_t first = ((int64_t)s0 + (int64_t)b * kLead) * HB + (int64_t)hb * (n + kLead) + kLead, last = first + n - 1;
   const int c0 = (int)(first / per), c1 = (int)(last / per);
-  if (c0 == c1) return;
+  if (c0 == c1 || heads <= 0) return;
   const int parts = c1 - c0 + 1;
-  const int nh = min(kHeads, a.G - hb % a.GB * kHeads);
-  const int h0 = hb / a.GB * a.G + hb % a.GB * kHeads;
-  const int slot0 = 2 * c0 + 1;  // it begins in CTA c0, and in the others it began before
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int h = blockIdx.y; h < nh; h += gridDim.y) {
+  // it begins in CTA c0, and in the others it began before
+  auto slot = [&](int i) { return i == 0 ? 2 * c0 + 1 : 2 * (c0 + i); };
+  for (int k = warp; k < heads; k += kWarps) {
+    const int h = from + k;
     float top = -INFINITY;
     bool bad = false;
-    for (int i = tid; i < parts; i += 256) {
-      const float v = a.part_lse[(i == 0 ? slot0 : 2 * (c0 + i)) * kHeads + h];
-      wts[i] = v;
+    for (int i = lane; i < parts; i += 32) {
+      const float v = a.part_lse[slot(i) * kHeads + h];
+      wts[k * parts + i] = v;
       top = fmaxf(top, v);
       bad = bad || v != v;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-    if (lane == 0) red[warp] = top;
-    bad = __syncthreads_or(bad);
-    top = red[0];
-#pragma unroll
-    for (int w = 1; w < 8; ++w) top = fmaxf(top, red[w]);
     const float ref = top == -INFINITY ? 0.f : top;
-    __syncthreads();
     float sum = 0.f;
-    for (int i = tid; i < parts; i += 256) {
-      const float w = ex2(wts[i] - ref);
-      wts[i] = w;
-      sum += w;
-    }
+    for (int i = lane; i < parts; i += 32) sum += ex2(wts[k * parts + i] - ref);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-    if (lane == 0) red[warp] = sum;
-    __syncthreads();
-    sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) sum += red[w];
     float lse2 = sum == 0.f ? -INFINITY : ref + log2f(sum);
     float g = sum == 0.f ? 0.f : 1.f / sum;
-    if (bad) g = lse2 = __int_as_float(0x7fc00000);
+    if (__any_sync(kAll, bad)) g = lse2 = __int_as_float(0x7fc00000);
     lse2 = with_sink(a, h0 + h, lse2, g);
-    const int grp = tid / (D / 4), d4 = tid % (D / 4);
+    for (int i = lane; i < parts; i += 32) wts[k * parts + i] = g * ex2(wts[k * parts + i] - ref);
+    if (a.lse && lane == 0) a.lse[(int64_t)b * a.heads + h0 + h] = lse2 / kLog2e;
+  }
+  __syncthreads();
+  const int items = heads * kCols, groups = max(1, kJoinThreads / items);
+  for (int base = 0; base < items; base += kJoinThreads) {
+    const int at = groups > 1 ? tid % items : base + tid, grp = groups > 1 ? tid / items : 0;
+    const bool live = at < items && grp < groups;
+    const int k = at / kCols, d = at % kCols * 4;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = grp; i < parts; i += kGroups) {
-      const float w = wts[i];
-      const float4 v = *reinterpret_cast<const float4 *>(
-          a.part_o + ((int64_t)(i == 0 ? slot0 : 2 * (c0 + i)) * kHeads + h) * D + 4 * d4);
-      acc.x += w * v.x;
-      acc.y += w * v.y;
-      acc.z += w * v.z;
-      acc.w += w * v.w;
-    }
-    acc_s[grp][d4] = acc;
-    __syncthreads();
-    if (tid < D / 4) {
-#pragma unroll
-      for (int i = 1; i < kGroups; ++i) {
-        const float4 v = acc_s[i][tid];
-        acc.x += v.x;
-        acc.y += v.y;
-        acc.z += v.z;
-        acc.w += v.w;
+    if (live) {
+      const float *src = a.part_o + (int64_t)(from + k) * D + d;
+#pragma unroll 8
+      for (int i = grp; i < parts; i += groups) {
+        const float w = wts[k * parts + i];
+        const float4 v = *reinterpret_cast<const float4 *>(src + (int64_t)slot(i) * (kHeads * D));
+        acc.x += w * v.x;
+        acc.y += w * v.y;
+        acc.z += w * v.z;
+        acc.w += w * v.w;
       }
-      uint2 pk;
-      if (a.q_type == MOE_BF16)
-        pk = make_uint2(pack2<true>(acc.x * g, acc.y * g), pack2<true>(acc.z * g, acc.w * g));
-      else
-        pk = make_uint2(pack2<false>(acc.x * g, acc.y * g), pack2<false>(acc.z * g, acc.w * g));
-      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + b * a.osb + (int64_t)(h0 + h) * a.osh + 4 * tid) = pk;
-      if (a.lse && tid == 0) a.lse[(int64_t)b * a.heads + h0 + h] = lse2 / kLog2e;
     }
-    __syncthreads();
+    if (groups > 1) {
+      acc_s[tid] = acc;
+      __syncthreads();
+      if (live && grp == 0)
+        for (int i = 1; i < groups; ++i) {
+          const float4 v = acc_s[i * items + at];
+          acc.x += v.x;
+          acc.y += v.y;
+          acc.z += v.z;
+          acc.w += v.w;
+        }
+    }
+    if (live && grp == 0) {
+      const uint2 pk = a.q_type == MOE_BF16 ? make_uint2(pack2<true>(acc.x, acc.y), pack2<true>(acc.z, acc.w))
+                                            : make_uint2(pack2<false>(acc.x, acc.y), pack2<false>(acc.z, acc.w));
+      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + b * a.osb + (int64_t)(h0 + from + k) * a.osh + d) = pk;
+    }
   }
 }
 
@@ -960,16 +964,25 @@ moe_status_t go(AttnArgs &a, cudaStream_t stream, int *launches) {
     occ_smem = smem;
     sms = n;
   }
-  const int64_t bound = (int64_t)a.B * a.kv_heads * a.GB *
-                        ((a.window > 0 ? std::min<int64_t>(a.window + 15, (int64_t)a.max_pages * a.page)
-                                       : (int64_t)a.max_pages * a.page) / 16 + 1);
-  a.ctas = (int)std::min<int64_t>(std::min(sms * occ, kMaxCtas), (bound + kW - 1) / kW);
+  // the most records that a (sequence, head) can have
+  const int64_t tokens = (int64_t)a.max_pages * a.page, span = a.window > 0 ? std::min<int64_t>(a.window + 15, tokens) : tokens;
+  const int64_t most = span / 16 + 1, groups = (int64_t)a.B * a.kv_heads * a.GB;
+  // Whole ones: where splitting leaves a warp less than two records, and up to 32 records where there is one for every
+  // SM (48 sequences with a window of 128 on 4 heads: @@W@@ us instead of 11.6; unequal lengths cost at most what 32 take)
+  a.whole = most <= 2 * kW || (most <= 32 && groups >= sms);
+  const int64_t fit = std::min(sms * occ, kMaxCtas);
+  a.ctas = (int)std::min<int64_t>(fit, a.whole ? groups : (groups * (most + kLead) + 2 * kW - 1) / (2 * kW));
   if (launch_pdl(kern, dim3(a.ctas), dim3(kW * 32), smem, stream, a) != cudaSuccess) return MOE_ERR_CUDA;
   if (launches) ++*launches;
-  if (a.ctas > 1) {
-    const int64_t groups = (int64_t)a.B * a.kv_heads * a.GB;
-    const dim3 grid((unsigned)groups, groups <= 2048 ? (unsigned)std::min(a.G, S::kHeads) : 1u);
-    if (launch_pdl(attn_join_kernel<D, NT>, grid, dim3(256), 0, stream, a) != cudaSuccess) return MOE_ERR_CUDA;
+  if (a.ctas > 1 && !a.whole) {
+    // few groups: their heads apart, so that more SMs share the work
+    const int heads = std::min(a.G, S::kHeads);
+    const int slices = (int)std::min<int64_t>(heads, std::max<int64_t>(1, 2 * sms / groups));
+    const int each = (heads + slices - 1) / slices;
+    const int wts = each * a.ctas * 4;  // at most 16 heads of all CTAs: 40 KB
+    if (launch_pdl(attn_join_kernel<D, NT>, dim3((unsigned)groups, slices), dim3(kJoinThreads), wts, stream, a) !=
+        cudaSuccess)
+      return MOE_ERR_CUDA;
     if (launches) ++*launches;
   }
   return MOE_OK;

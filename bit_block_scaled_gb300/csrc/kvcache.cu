@@ -29,26 +29,19 @@ struct KvArgs {
   const int32_t *slots;
   unsigned int *status;
   int64_t kst, ksh, vst, vsh;
-  int64_t rows;  // T * heads
-  int type, T, heads, D, page, pages;
+  uint32_t rows;  // T * heads
+  int type, heads, D, log_n, page, pages;
 };
 
-// 2^e for e in -63..64 (half of any row exponent), exactly.
-__device__ __forceinline__ float pow2_half(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+// 2^e for e in -127..127, exactly (2^-127 is a subnormal).
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(e == -127 ? 0x00400000u : (uint32_t)(e + 127) << 23); }
 
-// x * 2^e for |e| <= 127, one step at a time so that 2^127 and 2^-127 work.
-__device__ __forceinline__ float times_pow2(float x, int e) {
-  const int h = e >> 1;
-  return x * pow2_half(h) * pow2_half(e - h);
-}
-
-// Least e in -127..127 with amax * 2^-e <= top = m 2^x (m in [1/2, 1)); 0 gives -127.
-__device__ __forceinline__ int row_exponent(float amax, float m, int x) {
-  if (amax == 0.f) return -127;
-  int e;
-  const float f = frexpf(amax, &e);
-  e += (f > m ? 1 : 0) - x;
-  return min(max(e, -127), 127);
+// Least e in -127..127 with amax * 2^-e <= top, 2^x > top >= 2^(x - 1); amax
+// below fp32's normal range gives -127, as 0 does.
+__device__ __forceinline__ int row_exponent(float amax, float top, int x) {
+  const uint32_t a = __float_as_uint(amax);
+  const int over = (a & 0x7fffffu) > (__float_as_uint(top) & 0x7fffffu) ? 1 : 0;
+  return max((int)(a >> 23) - 126 - x + over, -127);
 }
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
@@ -94,41 +87,66 @@ __device__ __forceinline__ void e2m1x8_f32(uint32_t w, float (&v)[8]) {
   }
 }
 
-// Quantises a lane's 8 values x of a row and stores its codes (and the scales
+// Largest magnitude of a lane's 8 values, as the bits of that type: they order
+// as the magnitudes do, with infinities and NaN above all numbers.
+template <int TYPE>
+__device__ __forceinline__ uint32_t abs_max(const Raw8 &r) {
+  const uint32_t a[4] = {r.a.x, r.a.y, r.a.z, r.a.w}, b[4] = {r.b.x, r.b.y, r.b.z, r.b.w};
+  if (TYPE == MOE_FP32) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max(m, max(a[i] & 0x7fffffffu, b[i] & 0x7fffffffu));
+    return m;
+  }
+  const uint32_t m = __vmaxu2(__vmaxu2(a[0] & 0x7fff7fffu, a[1] & 0x7fff7fffu),
+                              __vmaxu2(a[2] & 0x7fff7fffu, a[3] & 0x7fff7fffu));
+  return max(m & 0xffffu, m >> 16);
+}
+template <int TYPE>
+__device__ __forceinline__ float from_bits(uint32_t b) {
+  if (TYPE == MOE_FP32) return __uint_as_float(b);
+  if (TYPE == MOE_BF16) return __uint_as_float(b << 16);
+  return __half2float(__ushort_as_half((unsigned short)b));
+}
+
+// Quantises a lane's 8 values of a row and stores its codes (and the scales
 // that fall to this lane). rec: the record; i: token in it; part: 0 keys, 1
 // values; j: lane of the row; n: lanes of the row.
-template <int FMT>
-__device__ __forceinline__ void put8(uint8_t *rec, int i, int part, int j, int n, int D, float (&x)[8], bool live) {
+template <int FMT, int TYPE>
+__device__ __forceinline__ void put8(uint8_t *rec, int i, int part, int j, int n, int D, const Raw8 &raw, bool live) {
   const int row = kv_row(FMT, D);
   uint8_t *codes = rec + part * 16 * row;
+  float x[8];
   if (FMT == MOE_KV_BF16 || FMT == MOE_KV_FP16) {
-    const Raw8 r = f32_to_raw8(x, FMT == MOE_KV_BF16 ? MOE_BF16 : MOE_FP16);
+    constexpr int kTo = FMT == MOE_KV_BF16 ? MOE_BF16 : MOE_FP16;
+    Raw8 r = raw;
+    if (TYPE != kTo) {
+      raw8_to_f32(raw, TYPE, x);
+      r = f32_to_raw8(x, kTo);
+    }
     if (live) *reinterpret_cast<uint4 *>(codes + kv_place(row, i, 16 * j)) = r.a;
     return;
   }
-  float m = 0.f;
-  bool bad = false;
+  const uint32_t own = abs_max<TYPE>(raw);
+  uint32_t top = own;
+  for (int o = 1; o < n; o <<= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
+  constexpr uint32_t kInf = TYPE == MOE_FP32 ? 0x7f800000u : TYPE == MOE_BF16 ? 0x7f80u : 0x7c00u;
+  const bool bad = top >= kInf;
+  const int e = FMT == MOE_KV_FP8 ? row_exponent(from_bits<TYPE>(top), 448.f, 9) : row_exponent(from_bits<TYPE>(top), 2688.f, 12);
+  const float up = pow2(-e);  // e is at most 119 for finite values; a bad row's codes are not used
+  raw8_to_f32(raw, TYPE, x);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    m = fmaxf(m, fabsf(x[e]));
-    bad = bad || !(fabsf(x[e]) <= 3.402823466e38f);
-  }
-  if (bad) m = INFINITY;
-  float amax = m;
-  for (int o = 1; o < n; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, o));
-  bad = !(amax <= 3.402823466e38f);
-  const int e = bad ? 0 : FMT == MOE_KV_FP8 ? row_exponent(amax, 448.f / 512.f, 9) : row_exponent(amax, 2688.f / 4096.f, 12);
-#pragma unroll
-  for (int q = 0; q < 8; ++q) x[q] = bad ? 0.f : times_pow2(x[q], -e);
+  for (int q = 0; q < 8; ++q) x[q] *= up;
   if (FMT == MOE_KV_FP8) {
     uint2 c;
     c.x = e4m3x2(x[0], x[1]) | (e4m3x2(x[2], x[3]) << 16);
     c.y = e4m3x2(x[4], x[5]) | (e4m3x2(x[6], x[7]) << 16);
+    if (bad) c = make_uint2(0, 0);
     if (live) *reinterpret_cast<uint2 *>(codes + kv_place(row, i, 8 * j)) = c;
   } else {
-    m = bad ? 0.f : times_pow2(m, -e);
-    m = fmaxf(m, __shfl_xor_sync(kAll, m, 1));  // two lanes hold a block of 16
-    const uint32_t sb = e4m3x2(m / 6.0f, 0.f) & 0xFFu;
+    // two lanes hold a block of 16
+    const float m = from_bits<TYPE>(max(own, __shfl_xor_sync(kAll, own, 1))) * up;
+    const uint32_t sb = bad ? 0u : e4m3x2(m / 6.0f, 0.f) & 0xFFu;
     const float s = e4m3x2_f32(sb).x;
 #pragma unroll
     for (int q = 0; q < 8; ++q) x[q] = s > 0.f ? x[q] / s : 0.f;
@@ -141,103 +159,132 @@ __device__ __forceinline__ void put8(uint8_t *rec, int i, int part, int j, int n
   if (live && j == 0) rec[kv_exps_at(FMT, D) + part * 16 + i] = (uint8_t)(bad ? 255 : e + 127);
 }
 
+// A lane's 8 values of a row as they are stored.
 template <int FMT>
-__device__ __forceinline__ void get8(const uint8_t *rec, int i, int part, int j, int D, float (&x)[8]) {
-  const int row = kv_row(FMT, D);
-  const uint8_t *codes = rec + part * 16 * row;
-  if (FMT == MOE_KV_BF16 || FMT == MOE_KV_FP16) {
-    Raw8 r;
-    r.a = *reinterpret_cast<const uint4 *>(codes + kv_place(row, i, 16 * j));
-    raw8_to_f32(r, FMT == MOE_KV_BF16 ? MOE_BF16 : MOE_FP16, x);
-    return;
-  }
-  const int e8 = rec[kv_exps_at(FMT, D) + part * 16 + i];
-  if (FMT == MOE_KV_FP8) {
-    const uint2 c = *reinterpret_cast<const uint2 *>(codes + kv_place(row, i, 8 * j));
-    const uint32_t w[4] = {c.x & 0xFFFFu, c.x >> 16, c.y & 0xFFFFu, c.y >> 16};
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float2 f = e4m3x2_f32(w[q]);
-      x[2 * q] = f.x;
-      x[2 * q + 1] = f.y;
+struct Stored {
+  uint4 codes;  // 16, 8 or 4 bytes of it
+  uint32_t block_scale, exponent;
+  __device__ __forceinline__ void load(const uint8_t *rec, int i, int part, int j, int D) {
+    const int row = kv_row(FMT, D);
+    const uint8_t *p = rec + part * 16 * row;
+    if (FMT == MOE_KV_BF16 || FMT == MOE_KV_FP16) {
+      codes = *reinterpret_cast<const uint4 *>(p + kv_place(row, i, 16 * j));
+      return;
     }
-  } else {
-    e2m1x8_f32(*reinterpret_cast<const uint32_t *>(codes + kv_place(row, i, 4 * j)), x);
-    const float s = e4m3x2_f32(rec[kv_scales_at(FMT, D) + part * D + (j >> 1) * 16 + i]).x;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) x[q] *= s;
+    exponent = rec[kv_exps_at(FMT, D) + part * 16 + i];
+    if (FMT == MOE_KV_FP8) {
+      const uint2 c = *reinterpret_cast<const uint2 *>(p + kv_place(row, i, 8 * j));
+      codes.x = c.x;
+      codes.y = c.y;
+    } else {
+      codes.x = *reinterpret_cast<const uint32_t *>(p + kv_place(row, i, 4 * j));
+      block_scale = rec[kv_scales_at(FMT, D) + part * D + (j >> 1) * 16 + i];
+    }
   }
+  __device__ __forceinline__ void expand(float (&x)[8]) const {
+    if (FMT == MOE_KV_BF16 || FMT == MOE_KV_FP16) {
+      raw8_to_f32(Raw8{codes, codes}, FMT == MOE_KV_BF16 ? MOE_BF16 : MOE_FP16, x);
+      return;
+    }
+    float down = exponent == 255u ? __int_as_float(0x7fc00000) : pow2((int)exponent - 127);
+    if (FMT == MOE_KV_FP8) {
+      const uint32_t w[4] = {codes.x & 0xFFFFu, codes.x >> 16, codes.y & 0xFFFFu, codes.y >> 16};
 #pragma unroll
-  for (int q = 0; q < 8; ++q) x[q] = e8 == 255 ? __int_as_float(0x7fc00000) : times_pow2(x[q], e8 - 127);
-}
+      for (int q = 0; q < 4; ++q) {
+        const float2 f = e4m3x2_f32(w[q]);
+        x[2 * q] = f.x;
+        x[2 * q + 1] = f.y;
+      }
+    } else {
+      e2m1x8_f32(codes.x, x);
+      const float s = e4m3x2_f32(block_scale).x;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) x[q] *= s;  // apart from 2^e, whose product with s may leave fp32's normal range
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) x[q] *= down;
+  }
+};
 
-// The record of a slot, or null.
-__device__ __forceinline__ uint8_t *record_of(const KvArgs &a, int fmt, int slot, int head) {
-  const int page = slot / a.page, off = slot % a.page;
-  return a.data + (((int64_t)page * a.heads + head) * (a.page >> 4) + (off >> 4)) * kv_record(fmt, a.D);
-}
-
-// grid: every lane one (token, head, 8 columns) of the keys and of the values
-template <int FMT, bool WRITE>
+// Every lane R (token, head, 8 columns) of the keys and of the values, R * (128
+// >> a.log_n) rows a CTA, 1 << a.log_n lanes a row. All loads that do not
+// depend on one another come first: with few instructions a row, the time goes
+// into waiting for memory.
+template <int FMT, int TYPE, bool WRITE, int R>
 __global__ void __launch_bounds__(kThreads) kv_kernel(const KvArgs a) {
   pdl_wait();
   pdl_trigger();
-  const int n = a.D >> 3;  // lanes of a row: 8, 16 or 32
-  const int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int64_t r = at / n;
-  const int j = (int)(at % n);
-  bool live = r < a.rows;
-  const int t = live ? (int)(r / a.heads) : 0, head = live ? (int)(r % a.heads) : 0;
-  int slot = a.slots[t];
-  if (slot >= a.pages * a.page) {
-    if (live && j == 0) raise_status(a.status, MOE_ERR_BAD_INDEX);
-    slot = -1;
-  }
-  const bool held = slot >= 0;
-  uint8_t *rec = held ? record_of(a, FMT, slot, head) : nullptr;
-  const int i = held ? slot % a.page & 15 : 0;
-  float x[8];
-  if (WRITE) {
-    live = live && held;
-    float y[8];
+  const int n = 1 << a.log_n, j = threadIdx.x & (n - 1);
+  const uint32_t per = kThreads >> a.log_n, r0 = blockIdx.x * (per * R) + (threadIdx.x >> a.log_n);
+  bool live[R], held[R];
+  uint32_t t[R], head[R];
+  int slot[R];
+  Raw8 k[R], v[R];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) x[q] = y[q] = 0.f;
-    if (live) {
-      raw8_to_f32(load_raw8(a.k, t * a.kst + head * a.ksh + 8 * j, a.type), a.type, x);
-      raw8_to_f32(load_raw8(a.v, t * a.vst + head * a.vsh + 8 * j, a.type), a.type, y);
+  for (int x = 0; x < R; ++x) {
+    const uint32_t r = r0 + x * per;
+    live[x] = r < a.rows;
+    t[x] = live[x] ? r / (uint32_t)a.heads : 0;
+    head[x] = live[x] ? r - t[x] * a.heads : 0;
+    slot[x] = a.slots[t[x]];
+    if (WRITE) {
+      k[x] = load_raw8(a.k, (int64_t)t[x] * a.kst + (int64_t)head[x] * a.ksh + 8 * j, TYPE);
+      v[x] = load_raw8(a.v, (int64_t)t[x] * a.vst + (int64_t)head[x] * a.vsh + 8 * j, TYPE);
     }
-    put8<FMT>(rec, i, 0, j, n, a.D, x, live);
-    put8<FMT>(rec, i, 1, j, n, a.D, y, live);
-  } else if (live) {
+  }
+  uint8_t *rec[R];
+  Stored<FMT> ks[R], vs[R];
 #pragma unroll
-    for (int part = 0; part < 2; ++part) {
-      void *o = part ? a.vo : a.ko;
-      if (!o) continue;
+  for (int x = 0; x < R; ++x) {
+    if (slot[x] >= a.pages * a.page) {
+      if (live[x] && j == 0) raise_status(a.status, MOE_ERR_BAD_INDEX);
+      slot[x] = -1;
+    }
+    held[x] = live[x] && slot[x] >= 0;
+    rec[x] = nullptr;
+    if (held[x]) {
+      const uint32_t block = (uint32_t)slot[x] >> 4, page16 = (uint32_t)a.page >> 4, page = block / page16;
+      rec[x] = a.data + (((int64_t)page * a.heads + head[x]) * page16 + (block - page * page16)) * kv_record(FMT, a.D);
+      if (!WRITE) {
+        if (a.ko) ks[x].load(rec[x], slot[x] & 15, 0, j, a.D);
+        if (a.vo) vs[x].load(rec[x], slot[x] & 15, 1, j, a.D);
+      }
+    }
+  }
 #pragma unroll
-      for (int q = 0; q < 8; ++q) x[q] = 0.f;
-      if (held) get8<FMT>(rec, i, part, j, a.D, x);
-      store_raw8(o, part ? t * a.vst + head * a.vsh + 8 * j : t * a.kst + head * a.ksh + 8 * j, a.type,
-                 f32_to_raw8(x, a.type));
+  for (int x = 0; x < R; ++x) {
+    if (WRITE) {
+      put8<FMT, TYPE>(rec[x], slot[x] & 15, 0, j, n, a.D, k[x], held[x]);
+      put8<FMT, TYPE>(rec[x], slot[x] & 15, 1, j, n, a.D, v[x], held[x]);
+    } else if (live[x]) {
+      float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (a.ko) {
+        if (held[x]) ks[x].expand(y);
+        store_raw8(a.ko, (int64_t)t[x] * a.kst + (int64_t)head[x] * a.ksh + 8 * j, TYPE, f32_to_raw8(y, TYPE));
+      }
+      if (a.vo) {
+        if (held[x]) vs[x].expand(y);
+        store_raw8(a.vo, (int64_t)t[x] * a.vst + (int64_t)head[x] * a.vsh + 8 * j, TYPE, f32_to_raw8(y, TYPE));
+      }
     }
   }
 }
 
 template <bool WRITE>
 moe_status_t launch(const KvArgs &a, int fmt, cudaStream_t stream, int *launches) {
-  const int64_t lanes = a.rows * (a.D >> 3);
-  const int64_t ctas = (lanes + kThreads - 1) / kThreads;
-  if (ctas == 0) return MOE_OK;
-  if (ctas > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)ctas), block(kThreads);
-  cudaError_t err;
-  if (fmt == MOE_KV_BF16)
-    err = launch_pdl(kv_kernel<MOE_KV_BF16, WRITE>, grid, block, 0, stream, a);
-  else if (fmt == MOE_KV_FP16)
-    err = launch_pdl(kv_kernel<MOE_KV_FP16, WRITE>, grid, block, 0, stream, a);
-  else if (fmt == MOE_KV_FP8)
-    err = launch_pdl(kv_kernel<MOE_KV_FP8, WRITE>, grid, block, 0, stream, a);
-  else
-    err = launch_pdl(kv_kernel<MOE_KV_NVFP4, WRITE>, grid, block, 0, stream, a);
+  // one row a lane until there are CTAs enough for every SM twice over (304), then four
+  const uint32_t per = kThreads >> a.log_n;
+  const bool many = a.rows > 4 * 304 * per;
+  const uint32_t step = many ? 4 * per : per;
+  const dim3 grid(a.rows / step + (a.rows % step != 0)), block(kThreads);
+  using Kernel = void (*)(KvArgs);
+#define MOE4_KV(F, T) {kv_kernel<F, T, WRITE, 1>, kv_kernel<F, T, WRITE, 4>}
+#define MOE4_KV_TYPES(F) {MOE4_KV(F, MOE_BF16), MOE4_KV(F, MOE_FP16), MOE4_KV(F, MOE_FP32)}
+  static const Kernel kernels[4][3][2] = {MOE4_KV_TYPES(MOE_KV_BF16), MOE4_KV_TYPES(MOE_KV_FP16),
+                                          MOE4_KV_TYPES(MOE_KV_FP8), MOE4_KV_TYPES(MOE_KV_NVFP4)};
+#undef MOE4_KV_TYPES
+#undef MOE4_KV
+  const cudaError_t err = launch_pdl(kernels[fmt][a.type][many], grid, block, 0, stream, a);
   if (launches) ++*launches;
   return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
@@ -252,11 +299,11 @@ KvArgs args_of(const moe_kv_cache_t &c, const int32_t *slots, int T, int type, i
   a.ksh = ksh;
   a.vst = vst;
   a.vsh = vsh;
-  a.rows = (int64_t)T * c.kv_heads;
+  a.rows = (uint32_t)((int64_t)T * c.kv_heads);
   a.type = type;
-  a.T = T;
   a.heads = c.kv_heads;
   a.D = c.head_dim;
+  a.log_n = c.head_dim == 64 ? 3 : c.head_dim == 128 ? 4 : 5;
   a.page = c.page_size;
   a.pages = c.num_pages;
   return a;
@@ -267,6 +314,7 @@ KvArgs args_of(const moe_kv_cache_t &c, const int32_t *slots, int T, int type, i
 moe_status_t launch_kv_write(const void *k, const void *v, int type, int64_t kst, int64_t ksh, int64_t vst,
                              int64_t vsh, const int32_t *slots, int T, const moe_kv_cache_t &c, unsigned int *status,
                              cudaStream_t stream, int *launches) {
+  if ((int64_t)T * c.kv_heads >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
   KvArgs a = args_of(c, slots, T, type, kst, ksh, vst, vsh, status);
   a.k = k;
   a.v = v;
@@ -276,6 +324,7 @@ moe_status_t launch_kv_write(const void *k, const void *v, int type, int64_t kst
 moe_status_t launch_kv_read(const moe_kv_cache_t &c, const int32_t *slots, int n, void *ko, void *vo, int type,
                             int64_t kst, int64_t ksh, int64_t vst, int64_t vsh, unsigned int *status,
                             cudaStream_t stream, int *launches) {
+  if ((int64_t)n * c.kv_heads >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
   KvArgs a = args_of(c, slots, n, type, kst, ksh, vst, vsh, status);
   a.ko = ko;
   a.vo = vo;
