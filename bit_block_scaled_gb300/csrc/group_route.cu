@@ -4,23 +4,22 @@
 //
 // One warp a token. Group g owns L = 32 / (n_group rounded up to a power of
 // two) lanes, which share its experts (E <= 256 leaves at most 16 a lane), so
-// what a group needs is log2(L) shuffles. A lane sorts its experts once by a
-// 32-bit key, the ordered bits of c with the low bits replaced by the expert's
-// place in the lane; after that a choice is one warp-wide maximum over the
-// lanes' heads, and the winning lane moves on to its next. 16-bit logits
-// ordered by themselves leave room for the whole expert index, so their many
-// ties are decided in the key.
+// what a group needs is log2(L) shuffles. An expert's key is the upper 24
+// ordered bits of c with the expert's index below them; each lane sorts its
+// keys, and five merges of sorted lists of 4 or 8 leave the whole warp with the
+// k best in order. 16-bit logits ordered by themselves fit the 24 bits, so
+// their many ties are decided by the index in the key.
 //
-// Which experts are chosen is decided on the real numbers. The keys carry an
-// error: the truncation, and that of fp32 scores (score_error2). Where every
-// gap that the selection rests on -- last kept group to first dropped one,
-// each choice to the next -- is wider, the order is right. Other rows are
-// `open`. Where it is the order of the k + 1 first that is, they are ranked by
-// 64-bit scores, one a lane (64-bit exponentials run at a 64th of the fp32
-// rate); that is about one row in 400 with random fp32 logits and a bias.
-// Undecided groups, and more candidates, go through select_exact, which has
-// its loops rolled up: run by a warp in ten thousand, its instructions come
-// from memory each time.
+// Which experts are chosen is decided on the real numbers. Keys and fp32 scores
+// carry errors (key_error2, score_error2). Where every gap that the selection
+// rests on is wider than them, the keys are right. Otherwise the candidates'
+// scores are computed as pairs of floats (pair_score, off by 1e-9 at most), one
+// a lane, and where even those are close, in 64 bits: a 64-bit exponential
+// takes a warp 3 us, a pair 0.2. What is left -- groups too close for pairs,
+// softmax scores, more than 32 candidates -- goes through select_exact, 16 us
+// for a row, with its loops rolled up because its instructions come from memory
+// each time. 8192 random rows of 256 experts in 8 groups with a bias: some 200
+// with close choices and one in two calls with close groups.
 #include "common.cuh"
 #include "kernels.h"
 #include "types.cuh"
@@ -72,8 +71,8 @@ __device__ __forceinline__ float not_nan(float v) { return v == v ? v : -INFINIT
 __device__ __forceinline__ float score_error2(int score, float v) {
   return (score == MOE_SCORE_SOFTMAX ? 4e-6f : 1e-6f) + 1.3e-7f * fabsf(v);
 }
-// The same for a score cut to the 28 bits of a key (2^-19 of it).
-__device__ __forceinline__ float key_error2(int score, float v) { return score_error2(score, v) + 2e-6f * fabsf(v); }
+// The same for a score cut to the 24 bits of a key (2^-15 of it).
+__device__ __forceinline__ float key_error2(int score, float v) { return score_error2(score, v) + 3.1e-5f * fabsf(v); }
 
 __device__ __forceinline__ float warp_max(float v) { return value_of(__reduce_max_sync(kAll, key_of(v))); }
 template <typename F>
@@ -111,44 +110,48 @@ __device__ __forceinline__ void sort_keys(uint32_t (&key)[PL]) {
           }
 }
 
-// What a warp knows of its token.
-template <int PL>
-struct Row {
-  float l[PL];  // logits of this lane's experts (NaN as -inf)
-  float m, sum; // softmax: maximum and sum of exp(l - m) over all, where needed
-  int64_t at;   // of the logits in memory
-  int lane, g, sub, e0;
-  unsigned valid;  // which of l are experts
-};
-
-// Which experts are this lane's.
-template <int PL>
-__device__ __forceinline__ void enter_row(const RouteArgs &a, Row<PL> &r) {
-  r.lane = threadIdx.x & 31;
-  r.g = r.lane / a.lanes;
-  r.sub = r.lane & (a.lanes - 1);
-  r.e0 = r.g * a.gs + r.sub;
-  r.valid = 0;
+// Merges each lane's KL sorted keys with those of the lane o away, both keeping
+// the KL best in order: the larger of key i and the other's key KL - 1 - i are
+// the best, in a bitonic order that log2(KL) exchanges sort.
+template <int KL>
+__device__ __forceinline__ void merge_keys(uint32_t (&key)[KL], int o) {
+  uint32_t other[KL];
 #pragma unroll
-  for (int i = 0; i < PL; ++i)
-    if (r.g < a.n_group && r.sub + i * a.lanes < a.gs) r.valid |= 1u << i;
+  for (int i = 0; i < KL; ++i) other[i] = __shfl_xor_sync(kAll, key[KL - 1 - i], o);
+#pragma unroll
+  for (int i = 0; i < KL; ++i) key[i] = max(key[i], other[i]);
+#pragma unroll
+  for (int d = KL / 2; d > 0; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < KL; ++i)
+      if ((i & d) == 0) {
+        const uint32_t hi = max(key[i], key[i + d]), lo = min(key[i], key[i + d]);
+        key[i] = hi;
+        key[i + d] = lo;
+      }
 }
 
-// This lane's logits, all loads under way together.
+// This lane's logits (NaN as -inf, -inf where there is no expert), all loads
+// under way together.
 template <int PL>
-__device__ __forceinline__ void load_logits(const RouteArgs &a, Row<PL> &r) {
+__device__ __forceinline__ void load_logits(const RouteArgs &a, int64_t at, const int (&id)[PL], unsigned valid,
+                                            float (&l)[PL]) {
   auto each = [&](auto get) {
 #pragma unroll
-    for (int i = 0; i < PL; ++i) r.l[i] = (r.valid >> i) & 1u ? get(r.at + r.e0 + i * a.lanes) : -INFINITY;
+    for (int i = 0; i < PL; ++i) l[i] = (valid >> i) & 1u ? get(id[i]) : -INFINITY;
   };
-  if (a.type == MOE_FP32)
-    each([&](int64_t i) { return load_as_f32(a.logits, i, MOE_FP32); });
-  else if (a.type == MOE_BF16)
-    each([&](int64_t i) { return load_as_f32(a.logits, i, MOE_BF16); });
-  else
-    each([&](int64_t i) { return load_as_f32(a.logits, i, MOE_FP16); });
+  if (a.type == MOE_FP32) {
+    const float *p = static_cast<const float *>(a.logits) + at;
+    each([&](int i) { return p[i]; });
+  } else {
+    const uint16_t *p = static_cast<const uint16_t *>(a.logits) + at;
+    if (a.type == MOE_BF16)
+      each([&](int i) { return load_as_f32(p, i, MOE_BF16); });
+    else
+      each([&](int i) { return load_as_f32(p, i, MOE_FP16); });
+  }
 #pragma unroll
-  for (int i = 0; i < PL; ++i) r.l[i] = not_nan(r.l[i]);
+  for (int i = 0; i < PL; ++i) l[i] = not_nan(l[i]);
 }
 
 // What orders expert e, in 64 bits.
@@ -159,6 +162,53 @@ __device__ double order64(const RouteArgs &a, int64_t at, float m, double sum, i
   if (a.bias) s += (double)a.bias[e];
   return s == s ? s : -INFINITY;
 }
+
+// A number as a float and the part of it below that float's precision.
+struct Pair {
+  float hi, lo;
+};
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+  const float s = a + b, v = s - a;
+  return {s, (a - (s - v)) + (b - v)};
+}
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  Pair s = two_sum(a.hi, b.hi);
+  s.lo += a.lo + b.lo;
+  return two_sum(s.hi, s.lo);
+}
+__device__ __forceinline__ Pair square(Pair a) {
+  const float h = a.hi * a.hi;
+  return two_sum(h, fmaf(a.hi, a.hi, -h) + 2.f * a.hi * a.lo);
+}
+__device__ __forceinline__ float difference(Pair a, Pair b) { return (a.hi - b.hi) + (a.lo - b.lo); }
+
+// sigmoid(l) + b. exp(-l) = 2^n exp(r / 64)^64 with r within ln 2 / 2: the part
+// of the series beyond 1 + x is below 1.5e-5 there, so its fp32 error is 1e-12,
+// which six squarings make 6e-11 of the exponential; the quotient takes one
+// Newton step with its remainder. |l| is held to 80, where the rest is below
+// any tolerance.
+__device__ __forceinline__ Pair pair_score(float l, float b) {
+  const float x = -fminf(fmaxf(l, -80.f), 80.f);
+  const float n = rintf(x * 1.44269504f);
+  // r = x - n ln 2, ln 2 as 0.693145751953125 (16 bits, so that n times it is exact) + 1.42860682030941723e-6
+  Pair r = two_sum(fmaf(n, -0.693145751953125f, x), n * -1.42860682030941723e-6f);
+  r.hi *= 0.015625f;
+  r.lo *= 0.015625f;
+  const float q = r.hi * r.hi * (0.5f + r.hi * (0.166666667f + r.hi * 0.0416666667f));
+  Pair e = two_sum(1.f, r.hi);
+  e.lo += r.lo + q;
+  e = two_sum(e.hi, e.lo);
+#pragma unroll
+  for (int i = 0; i < 6; ++i) e = square(e);
+  const float two_n = __uint_as_float((uint32_t)((int)n + 127) << 23);
+  e.hi *= two_n;
+  e.lo *= two_n;
+  const Pair d = add({1.f, 0.f}, e);
+  const float s = 1.f / d.hi;
+  return add({s, s * (fmaf(-d.hi, s, 1.f) - d.lo * s)}, {b, 0.f});
+}
+// Bound on the error of a difference of two pairs, or of sums of two, of size |v|.
+__device__ __forceinline__ float pair_error2(float v) { return 1e-9f + 1e-12f * fabsf(v); }
 
 // Sum of the softmax's exponentials in 64 bits, over the warp.
 __device__ double sum64(const RouteArgs &a, int64_t at, float m, int experts) {
@@ -337,59 +387,59 @@ __device__ __noinline__ int select_exact(const RouteArgs &a, int64_t at, float m
   return mine;
 }
 
-// PL: experts a lane, rounded up to a power of two
-template <int PL>
+// PL: experts a lane, rounded up to a power of two; KL: choices held, 4 or 8
+template <int PL, int KL>
 __global__ void __launch_bounds__(kWarps * 32, PL <= 8 ? 7 : 5) group_route_kernel(const RouteArgs a) {
   __shared__ Scratch scratch[kWarps];
   pdl_wait();
   pdl_trigger();
   const bool grouped = a.topk_group < a.n_group;
-  const bool by_score = a.bias || (grouped && a.top2);  // some order rests on computed scores
-  const bool short_keys = !a.bias && a.type != MOE_FP32;  // 19 bits of order hold any, 13 of index
-  Row<PL> r;
-  enter_row<PL>(a, r);
+  const bool by_score = a.bias || (grouped && a.top2);    // some order rests on computed scores
+  const bool exact_keys = !a.bias && a.type != MOE_FP32;  // 24 bits hold the logits
+  const int lane = threadIdx.x & 31, g = lane / a.lanes, sub = lane & (a.lanes - 1);
+  Scratch &own = scratch[threadIdx.x >> 5];
+  unsigned valid = 0;
+  int id[PL];
   float bias[PL];
 #pragma unroll
-  for (int i = 0; i < PL; ++i) bias[i] = a.bias && ((r.valid >> i) & 1u) ? a.bias[r.e0 + i * a.lanes] : 0.f;
+  for (int i = 0; i < PL; ++i) {
+    id[i] = g * a.gs + sub + i * a.lanes;
+    if (g < a.n_group && sub + i * a.lanes < a.gs) valid |= 1u << i;
+    bias[i] = a.bias && ((valid >> i) & 1u) ? a.bias[id[i]] : 0.f;
+  }
   for (int t = blockIdx.x * kWarps + (threadIdx.x >> 5); t < a.T; t += gridDim.x * kWarps) {
-    r.at = (int64_t)t * a.ld;
-    load_logits<PL>(a, r);
-    r.m = 0.f;
-    r.sum = 1.f;
+    const int64_t at = (int64_t)t * a.ld;
+    float l[PL], m = 0.f, sum = 1.f;
+    load_logits<PL>(a, at, id, valid, l);
     if (a.score == MOE_SCORE_SOFTMAX && (by_score || !a.renorm)) {
-      float m = r.l[0];
+      m = l[0];
 #pragma unroll
-      for (int i = 1; i < PL; ++i) m = fmaxf(m, r.l[i]);
-      r.m = warp_max(m);
-      r.sum = 0.f;
+      for (int i = 1; i < PL; ++i) m = fmaxf(m, l[i]);
+      m = warp_max(m);
+      sum = 0.f;
 #pragma unroll
       for (int i = 0; i < PL; ++i)
-        if ((r.valid >> i) & 1u) r.sum += exp_rel(r.l[i], r.m);
-      r.sum = warp_sum(r.sum);
+        if ((valid >> i) & 1u) sum += exp_rel(l[i], m);
+      sum = warp_sum(sum);
     }
-    auto score = [&](float l) {
-      return a.score == MOE_SCORE_SOFTMAX ? __fdividef(exp_rel(l, r.m), r.sum) : __fdividef(1.0f, 1.0f + __expf(-l));
+    auto score = [&](float x) {
+      return a.score == MOE_SCORE_SOFTMAX ? __fdividef(exp_rel(x, m), sum) : __fdividef(1.0f, 1.0f + __expf(-x));
     };
-    uint32_t key[PL], full[PL];
+    uint32_t full[PL];  // keys of what orders the experts, whole; 0: no expert
+    if (a.bias) {
 #pragma unroll
-    for (int i = 0; i < PL; ++i) {
-      full[i] = (r.valid >> i) & 1u ? key_of(a.bias ? not_nan(score(r.l[i]) + bias[i]) : r.l[i]) : 0u;
-      const uint32_t cut = short_keys ? (full[i] & ~0x1FFFu) | (0x1FFFu - (uint32_t)(r.e0 + i * a.lanes))
-                                      : (full[i] & ~15u) | (uint32_t)(15 - i);
-      key[i] = full[i] ? cut : 0u;
+      for (int i = 0; i < PL; ++i) full[i] = (valid >> i) & 1u ? key_of(not_nan(score(l[i]) + bias[i])) : 0u;
+    } else {
+#pragma unroll
+      for (int i = 0; i < PL; ++i) full[i] = (valid >> i) & 1u ? key_of(l[i]) : 0u;
     }
-    sort_keys<PL>(key);
-    bool open = false;         // the groups, or too many candidates, are undecided
-    bool open_order = false;   // so is the order of the first k + 1
+    bool open = false;  // the groups are undecided, or there are too many candidates
     if (grouped) {
-      uint32_t b1 = key[0], b2 = PL > 1 ? key[PL > 1] : 0u;
-      if (by_score) {  // whole, not as the keys have them: the scores, or the logits whose scores are wanted
-        b1 = b2 = 0u;
+      uint32_t b1 = 0u, b2 = 0u;
 #pragma unroll
-        for (int i = 0; i < PL; ++i) {
-          b2 = max(b2, min(b1, full[i]));
-          b1 = max(b1, full[i]);
-        }
+      for (int i = 0; i < PL; ++i) {
+        b2 = max(b2, min(b1, full[i]));
+        b1 = max(b1, full[i]);
       }
       for (int o = 1; o < a.lanes; o <<= 1) {
         const uint32_t o1 = __shfl_xor_sync(kAll, b1, o), o2 = __shfl_xor_sync(kAll, b2, o);
@@ -397,72 +447,158 @@ __global__ void __launch_bounds__(kWarps * 32, PL <= 8 ? 7 : 5) group_route_kern
         b1 = max(b1, o1);
       }
       uint32_t gk = 0;
-      if (r.g < a.n_group) {
+      if (g < a.n_group) {
         const float x = value_of(b1), y = value_of(b2);
         gk = !a.top2 ? b1 : key_of(not_nan(a.bias ? x + y : score(x) + score(y)));
       }
       int ahead = 0;  // groups before this one; equal ones by index
       for (int h = 0; h < a.n_group; ++h) {
         const uint32_t ok = __shfl_sync(kAll, gk, h * a.lanes);
-        ahead += ok > gk || (ok == gk && h < r.g);
+        ahead += ok > gk || (ok == gk && h < g);
       }
-      const bool kept = r.g < a.n_group && ahead < a.topk_group;
-      const uint32_t last = __reduce_min_sync(kAll, kept ? gk : kAll), next = __reduce_max_sync(kAll, kept ? 0u : gk);
+      bool kept = g < a.n_group && ahead < a.topk_group;
       if (by_score) {
-        const float lv = value_of(last), nv = value_of(next);
-        open = !(lv - nv > (a.top2 ? 2.f : 1.f) * score_error2(a.score, fmaxf(fabsf(lv), fabsf(nv))));
-      } else if (!short_keys) {
-        open = (last >> 4) == (next >> 4);
+        const float lv = value_of(__reduce_min_sync(kAll, kept ? gk : kAll)),
+                    nv = value_of(__reduce_max_sync(kAll, kept ? 0u : gk));
+        const float tol = (a.top2 ? 2.f : 1.f) * score_error2(a.score, fmaxf(fabsf(lv), fabsf(nv)));
+        open = !(lv - nv > tol);
+        if (open && a.score == MOE_SCORE_SIGMOID) {
+          // pairs for the groups within the error of the other side, of those experts that can be their best (two)
+          const float gv = value_of(gk), edge = value_of(a.top2 ? b2 : b1);
+          const bool sure = g < a.n_group && gv > lv + tol, maybe = g < a.n_group && !sure && !(gv < nv - tol);
+          const uint32_t least = !a.bias ? (a.top2 ? b2 : b1) : key_of(edge - score_error2(a.score, edge));
+          Pair d1 = {-INFINITY, 0.f}, d2 = d1;
+          unsigned need = 0;
+#pragma unroll
+          for (int i = 0; i < PL; ++i)
+            if (maybe && full[i] && full[i] >= least) need |= 1u << i;
+          auto put = [&](Pair v) {
+            if (difference(v, d1) > 0.f || d1.hi == -INFINITY) {
+              d2 = d1;
+              d1 = v;
+            } else if (difference(v, d2) > 0.f || d2.hi == -INFINITY) {
+              d2 = v;
+            }
+          };
+#pragma unroll 1
+          for (; need; need &= need - 1) {
+            const int e = g * a.gs + sub + (__ffs(need) - 1) * a.lanes;
+            put(pair_score(not_nan(load_as_f32(a.logits, at + e, a.type)), a.bias ? a.bias[e] : 0.f));
+          }
+          __syncwarp();
+#pragma unroll 1
+          for (int o = 1; o < a.lanes; o <<= 1) {
+            const Pair o1 = {__shfl_xor_sync(kAll, d1.hi, o), __shfl_xor_sync(kAll, d1.lo, o)},
+                       o2 = {__shfl_xor_sync(kAll, d2.hi, o), __shfl_xor_sync(kAll, d2.lo, o)};
+            if (o1.hi != -INFINITY) put(o1);
+            if (o2.hi != -INFINITY) put(o2);
+          }
+          const Pair gd = a.top2 ? add(d1, d2) : d1;
+          bool near = false;
+          int place = 0;
+#pragma unroll 1
+          for (int h = 0; h < a.n_group; ++h) {
+            const Pair od = {__shfl_sync(kAll, gd.hi, h * a.lanes), __shfl_sync(kAll, gd.lo, h * a.lanes)};
+            const bool om = __shfl_sync(kAll, (int)maybe, h * a.lanes), os = __shfl_sync(kAll, (int)sure, h * a.lanes);
+            const float d = difference(od, gd);
+            place += os || (om && d > 0.f);
+            near = near || (maybe && om && h != g && !(fabsf(d) > 2.f * pair_error2(gd.hi)));
+          }
+          open = __any_sync(kAll, near);
+          kept = sure || (maybe && place < a.topk_group);
+        }
       }
       if (!kept) {
 #pragma unroll
-        for (int i = 0; i < PL; ++i) key[i] = 0u;
+        for (int i = 0; i < PL; ++i) full[i] = 0u;
       }
     }
-    int mine = 0;
-    uint32_t prev = kAll, kth = 0;
-    int candidates = 0;
-    // the two after the last choice decide whether that one is sure, and whether the first k + 1 are all that matter
-    const int rounds = a.k + (short_keys ? 0 : 2);
-    for (int j = 0; j < rounds; ++j) {
-      const uint32_t top = __reduce_max_sync(kAll, key[0]);
-      const unsigned who = __ballot_sync(kAll, key[0] == top);
-      if (top == 0u) break;  // fewer candidates than k + 2
-      candidates = j + 1;
-      const int from = __ffs(who) - 1;
-      if (!short_keys) {
-        auto close = [&](uint32_t hi, uint32_t lo) {
-          if (!a.bias) return (hi >> 4) == (lo >> 4);
-          const float p = value_of(hi & ~15u), v = value_of(lo & ~15u);
-          return !(p - v > key_error2(a.score, fmaxf(fabsf(p), fabsf(v))));
-        };
-        if (j == a.k + 1)
-          open = open || close(kth, top);
-        else if (j > 0)
-          open_order = open_order || close(prev, top);
-        if (j == a.k - 1) kth = top;
-      }
-      prev = top;
-      const int id = short_keys ? (int)(0x1FFFu - (top & 0x1FFFu))
-                                : __shfl_sync(kAll, r.e0, from) + (int)(15u - (top & 15u)) * a.lanes;
-      if (r.lane == j) mine = id;
-      if (r.lane == from) {
+    uint32_t sorted[PL], best[KL];
 #pragma unroll
-        for (int i = 0; i + 1 < PL; ++i) key[i] = key[i + 1];
-        key[PL - 1] = 0u;
-      }
+    for (int i = 0; i < PL; ++i) sorted[i] = full[i] ? (full[i] & ~255u) | (uint32_t)(255 - id[i]) : 0u;
+    sort_keys<PL>(sorted);
+#pragma unroll
+    for (int i = 0; i < KL; ++i) best[i] = i < PL ? sorted[i < PL ? i : 0] : 0u;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) merge_keys<KL>(best, o);
+    // lane j takes the j-th choice
+    uint32_t key = best[0], last = best[0];
+#pragma unroll
+    for (int i = 1; i < KL; ++i) {
+      if (lane == i) key = best[i];
+      if (i == a.k - 1) last = best[i];
     }
-    if (open)
-      mine = select_exact(a, r.at, r.m, r.sum, scratch[threadIdx.x >> 5]);
-    else if (open_order)
-      mine = rank64(a, r.at, r.m, a.n_group * a.gs, min(a.k + 1, candidates), mine, scratch[threadIdx.x >> 5]);
-    // weights: lane j has the j-th choice
-    const bool has = r.lane < a.k;
-    const float lv = has ? not_nan(load_as_f32(a.logits, r.at + mine, a.type)) : -INFINITY;
+    const bool has = lane < a.k;
+    int mine = has ? 255 - (int)(key & 255u) : 0;
+    float lv = has ? not_nan(load_as_f32(a.logits, at + mine, a.type)) : -INFINITY;
+    if (!exact_keys) {
+      // others within the error of the last choice
+      const float lastv = value_of(last & ~255u);
+      const uint32_t edge = a.bias ? key_of(lastv - key_error2(a.score, lastv)) & ~255u : last & ~255u;
+      unsigned extra = 0;
+#pragma unroll
+      for (int i = 0; i < PL; ++i) {
+        const uint32_t x = full[i] ? (full[i] & ~255u) | (uint32_t)(255 - id[i]) : 0u;
+        if (x >= edge && x < last) extra |= 1u << i;
+      }
+      const uint32_t next = __shfl_down_sync(kAll, key, 1);
+      const float p = value_of(key & ~255u), v = value_of(next & ~255u);
+      const bool close = lane + 1 < a.k && (a.bias ? !(p - v > key_error2(a.score, fmaxf(fabsf(p), fabsf(v))))
+                                                   : (key >> 8) == (next >> 8));
+      const bool extras = __any_sync(kAll, extra != 0);
+      bool rank = false;  // by 64-bit scores
+      int n = a.k;        // candidates
+      if (!open && (extras || __any_sync(kAll, close))) {
+        while (const unsigned who = __ballot_sync(kAll, extra != 0)) {  // those beyond the k: behind them, lane by lane
+          const int to = n + __popc(who & ((1u << lane) - 1u));
+          if (extra) {
+            if (to < 32) own.id[to] = g * a.gs + sub + (__ffs(extra) - 1) * a.lanes;
+            extra &= extra - 1;
+          }
+          n += __popc(who);
+        }
+        __syncwarp();
+        if (lane >= a.k && lane < min(n, 32)) mine = own.id[lane];
+        __syncwarp();
+        open = n > 32;
+        rank = a.bias && a.score == MOE_SCORE_SOFTMAX;
+        if (!open && !rank) {
+          const bool in = lane < n;
+          const float x = in ? not_nan(load_as_f32(a.logits, at + mine, a.type)) : 0.f;
+          const Pair c = in && a.bias ? pair_score(x, a.bias[mine]) : Pair{x, 0.f};
+          int place = 0;
+          bool near = false;
+#pragma unroll 1
+          for (int j = 0; j < n; ++j) {
+            const Pair o = {__shfl_sync(kAll, c.hi, j), __shfl_sync(kAll, c.lo, j)};
+            const int oid = __shfl_sync(kAll, mine, j);
+            const float d = a.bias ? difference(o, c) : o.hi == c.hi ? 0.f : o.hi > c.hi ? 1.f : -1.f;
+            place += d > 0.f || (d == 0.f && oid < mine);
+            near = near || (in && j != lane && a.bias && !(fabsf(d) > pair_error2(c.hi)));
+          }
+          rank = __any_sync(kAll, near);
+          if (!rank) {
+            if (in) own.id[place] = mine;
+            __syncwarp();
+            if (has) mine = own.id[lane];
+            __syncwarp();
+          }
+        }
+      }
+      if (open)
+        mine = select_exact(a, at, m, sum, own);
+      else if (rank)
+        mine = rank64(a, at, m, a.n_group * a.gs, n, mine, own);
+      if (has) lv = not_nan(load_as_f32(a.logits, at + mine, a.type));
+    } else if (open) {
+      mine = select_exact(a, at, m, sum, own);
+      if (has) lv = not_nan(load_as_f32(a.logits, at + mine, a.type));
+    }
+    // weights
     const float mx = warp_max(lv);
     float w = 0.f;
     if (a.score == MOE_SCORE_SOFTMAX) {
-      if (has) w = a.renorm ? exp_rel(lv, mx) : exp_rel(lv, r.m) / r.sum;
+      if (has) w = a.renorm ? exp_rel(lv, mx) : exp_rel(lv, m) / sum;
     } else if (has) {
       // far below 0 every sigmoid is exp(l), which only its ratios keep in range
       if (a.renorm && mx < -30.f) {
@@ -473,31 +609,32 @@ __global__ void __launch_bounds__(kWarps * 32, PL <= 8 ? 7 : 5) group_route_kern
       }
     }
     if (a.renorm) {
-      float sum = w;
+      float total = w;
 #pragma unroll
-      for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);  // k <= 8
-      w /= sum;
+      for (int o = 4; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);  // k <= 8
+      w /= total;
     }
     if (has) {
-      a.ids[(int64_t)t * a.k + r.lane] = mine;
-      a.weights[(int64_t)t * a.k + r.lane] = w * a.scale;
+      a.ids[(int64_t)t * a.k + lane] = mine;
+      a.weights[(int64_t)t * a.k + lane] = w * a.scale;
     }
   }
 }
 
-template <int PL>
+template <int PL, int KL>
 cudaError_t go(const RouteArgs &a, cudaStream_t stream) {
+  auto kern = group_route_kernel<PL, KL>;
   static int fit = 0;  // CTAs that are resident on the device
   if (fit == 0) {
     int dev = 0, sms = 0, n = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, group_route_kernel<PL>, kWarps * 32, 0);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kWarps * 32, 0);
     if (e != cudaSuccess) return e;
     fit = sms * n;
   }
   const int need = (a.T + kWarps - 1) / kWarps;
-  return launch_pdl(group_route_kernel<PL>, dim3(need < fit ? need : fit), dim3(kWarps * 32), 0, stream, a);
+  return launch_pdl(kern, dim3(need < fit ? need : fit), dim3(kWarps * 32), 0, stream, a);
 }
 
 }  // namespace
@@ -528,16 +665,17 @@ moe_status_t launch_group_route(const void *logits, int type, int64_t ld, const 
   a.scale = r.scale;
   const int per = (a.gs + a.lanes - 1) / a.lanes;
   cudaError_t err;
+  const bool four = k <= 4;
   if (per <= 1)
-    err = go<1>(a, stream);
+    err = four ? go<1, 4>(a, stream) : go<1, 8>(a, stream);
   else if (per <= 2)
-    err = go<2>(a, stream);
+    err = four ? go<2, 4>(a, stream) : go<2, 8>(a, stream);
   else if (per <= 4)
-    err = go<4>(a, stream);
+    err = four ? go<4, 4>(a, stream) : go<4, 8>(a, stream);
   else if (per <= 8)
-    err = go<8>(a, stream);
+    err = four ? go<8, 4>(a, stream) : go<8, 8>(a, stream);
   else
-    err = go<16>(a, stream);
+    err = four ? go<16, 4>(a, stream) : go<16, 8>(a, stream);
   if (launches) ++*launches;
   return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
