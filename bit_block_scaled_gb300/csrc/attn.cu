@@ -175,10 +175,14 @@ struct Shape {
   // records in flight a warp, and how many of them are asked for at a time
   static constexpr int kStages = kRec >= 8192 ? 2 : kRec >= 4096 ? 3 : kRec >= 2048 ? 4 : 8;
   static constexpr int kGroup = kStages / 2;
+  // records that a warp works on at a time: two of FP8 and NVFP4, whose time is instructions (what is done once a tile,
+  // waiting, voting, branching, is a third of them); 16-bit caches wait for memory
+  static constexpr int kTile = kQuant && NT == 1 && kStages >= 4 ? 2 : 1;
   static constexpr int kHeads = 8 * NT;
   // FP8, NVFP4: codes of a lane's load of a key (16 bytes, 8 of a 32-byte row), and of a value
   static constexpr int kKeyCodes = (kRow >= 64 ? 16 : 8) * (FMT == MOE_KV_NVFP4 ? 2 : 1);
   static constexpr int kValCodes = D / 8 < 16 * (FMT == MOE_KV_NVFP4 ? 2 : 1) ? D / 8 : 16 * (FMT == MOE_KV_NVFP4 ? 2 : 1);
+  static constexpr int kKeyLoads = D / 4 / kKeyCodes, kValLoads = D / 8 / kValCodes;
   // column of code e of a key's lane c (of 4), and of a value's lane r (of 8): loads lie next to each other by lane
   __host__ __device__ static constexpr int key_col(int c, int e) {
     return e / kKeyCodes * 4 * kKeyCodes + c * kKeyCodes + e % kKeyCodes;
@@ -232,6 +236,31 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
   __shared__ int warp_sum[kW];
   __shared__ int seg_of[kW][2], ends0[kW];  // (sequence, head) of each warp's first and last partial, or -1
 
+  // Places of this lane's loads in a record, FP8 and NVFP4. Held in registers (the compiler would rather work them out
+  // again at every use, six instructions each).
+  [[maybe_unused]] int k_at[S::kKeyLoads][2], v_at[S::kValLoads][4], ks_at = 0, vs_at[2] = {0, 0}, ex_at = 0;
+  if constexpr (S::kQuant) {
+    constexpr int kPacked = FMT == MOE_KV_NVFP4 ? 2 : 1;  // codes a byte
+    auto hold = [](int v) {
+      asm volatile("" : "+r"(v));
+      return v;
+    };
+#pragma unroll
+    for (int p = 0; p < S::kKeyLoads; ++p)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        k_at[p][x] = hold(kv_place(S::kRow, key0 + x, S::key_col(c, p * S::kKeyCodes) / kPacked));
+#pragma unroll
+    for (int p = 0; p < S::kValLoads; ++p)
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        v_at[p][x] = hold(16 * S::kRow + kv_place(S::kRow, 2 * c + (x >> 1) + (x & 1 ? 8 + 2 * (c ^ 2) - 2 * c : 0),
+                                                  S::val_col(r, p * S::kValCodes) / kPacked));
+    ks_at = hold(kv_scales_at(FMT, D) + S::key_col(c, 0) + key0);
+    vs_at[0] = hold(kv_scales_at(FMT, D) + D + (S::val_col(r, 0) & ~15) + 2 * c);
+    vs_at[1] = hold(kv_scales_at(FMT, D) + D + (S::val_col(r, 0) & ~15) + 8 + 2 * (c ^ 2));
+    ex_at = hold(kv_exps_at(FMT, D) + key0);
+  }
   const uint32_t bar0 = smem_u32(bars + warp * S::kStages);
   if (lane == 0) {
 #pragma unroll
@@ -457,66 +486,86 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
     }
 
 #pragma unroll 1
-    for (; cu.rec < cu.end; ++cu.rec) {
-      const int slot = done % S::kStages;
-      if (!dead) {
-        const bool late = !mbar_wait(bar0 + 8 * slot, (done / S::kStages) & 1);
-        if (__any_sync(kAll, late)) {
-          if (late) raise_status(a.status, MOE_ERR_TIMEOUT);
-          dead = true;
-          dead_at = done;
+    for (; cu.rec < cu.end; cu.rec += S::kTile) {
+      // kTile records at a time; of one that is not there (past the range, in no page) no token is read
+      const int pos = (cu.s.lo + cu.rec) * 16;
+      bool there[S::kTile], here = true;
+      bool edge = pos < cu.s.first || pos + 16 * S::kTile > cu.s.len;  // not all of the tokens are read
+#pragma unroll
+      for (int n = 0; n < S::kTile; ++n) {
+        const int slot = (done + n) % S::kStages;
+        there[n] = n == 0 || cu.rec + n < cu.end;
+        here = here && (!there[n] || mbar_try_wait(bar0 + 8 * slot, ((done + n) / S::kStages) & 1));
+        there[n] = there[n] && !((missing >> slot) & 1u);
+        edge = edge || !there[n];
+      }
+      if (!dead && !__all_sync(kAll, here)) {  // not all there yet
+        const int n = min(S::kTile, cu.end - cu.rec);
+        for (int i = 0; i < n && !dead; ++i) {
+          const bool late = !mbar_wait(bar0 + 8 * ((done + i) % S::kStages), ((done + i) / S::kStages) & 1);
+          if (__any_sync(kAll, late)) {
+            if (late) raise_status(a.status, MOE_ERR_TIMEOUT);
+            dead = true;
+            dead_at = done + i;
+          }
         }
       }
-      if (!dead && !((missing >> slot) & 1u)) {
-        const uint8_t *st = ring + slot * S::kStage;
-        const uint32_t st32 = ring32 + slot * S::kStage;
-        const int pos = (cu.s.lo + cu.rec) * 16;
-        const bool edge = pos < cu.s.first || pos + 16 > cu.s.len;  // not all of its tokens are read
-        auto read = [&](int key) { return pos + key >= cu.s.first && pos + key < cu.s.len; };
+      if (!dead) {
+        auto read = [&](int n, int key) {
+          return there[n] && pos + 16 * n + key >= cu.s.first && pos + 16 * n + key < cu.s.len;
+        };
+        const uint8_t *st[S::kTile];
+        uint32_t st32[S::kTile];
+#pragma unroll
+        for (int n = 0; n < S::kTile; ++n) {
+          st[n] = ring + (done + n) % S::kStages * S::kStage;
+          st32[n] = ring32 + (done + n) % S::kStages * S::kStage;
+        }
         // ---- S^T = K Q^T
-        float sc[NT][4];
+        float sc[S::kTile][NT][4];
+#pragma unroll
+        for (int n = 0; n < S::kTile; ++n) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) sc[nt][x] = 0.f;
+          for (int x = 0; x < 4; ++x) sc[n][nt][x] = 0.f;
         if constexpr (!S::kQuant) {
           const int key = (lane & 7) + (lane & 8);
           const int half = lane >> 4;
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             uint32_t af[4];
-            ldsm4(af, st32 + kv_place(S::kRow, key, 32 * ks + 16 * half));
+            ldsm4(af, st32[n] + kv_place(S::kRow, key, 32 * ks + 16 * half));
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma<S::kBf>(sc[nt], af, qf[nt][ks][0], qf[nt][ks][1]);
+            for (int nt = 0; nt < NT; ++nt) mma<S::kBf>(sc[n][nt], af, qf[nt][ks][0], qf[nt][ks][1]);
           }
         } else {
 #pragma unroll
-          for (int p = 0; p < D / 4 / S::kKeyCodes; ++p) {  // one load of each of the two keys
-            const int col = S::key_col(c, p * S::kKeyCodes);
+          for (int p = 0; p < S::kKeyLoads; ++p) {  // one load of each of the two keys
             if constexpr (FMT == MOE_KV_FP8) {
-              const uint4 x = *reinterpret_cast<const uint4 *>(st + kv_place(S::kRow, key0, col));
-              const uint4 y = *reinterpret_cast<const uint4 *>(st + kv_place(S::kRow, key0 + 1, col));
+              const uint4 x = *reinterpret_cast<const uint4 *>(st[n] + k_at[p][0]);
+              const uint4 y = *reinterpret_cast<const uint4 *>(st[n] + k_at[p][1]);
               const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 const uint32_t af[4] = {e4m3x2_f16x2(xs[k] & 0xFFFFu), e4m3x2_f16x2(ys[k] & 0xFFFFu),
                                         e4m3x2_f16x2(xs[k] >> 16), e4m3x2_f16x2(ys[k] >> 16)};
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma<false>(sc[nt], af, qf[nt][4 * p + k][0], qf[nt][4 * p + k][1]);
+                for (int nt = 0; nt < NT; ++nt) mma<false>(sc[n][nt], af, qf[nt][4 * p + k][0], qf[nt][4 * p + k][1]);
               }
             } else {
               uint32_t xs[4], ys[4];
               if constexpr (S::kKeyCodes == 32) {
-                *reinterpret_cast<uint4 *>(xs) = *reinterpret_cast<const uint4 *>(st + kv_place(S::kRow, key0, col / 2));
-                *reinterpret_cast<uint4 *>(ys) = *reinterpret_cast<const uint4 *>(st + kv_place(S::kRow, key0 + 1, col / 2));
+                *reinterpret_cast<uint4 *>(xs) = *reinterpret_cast<const uint4 *>(st[n] + k_at[p][0]);
+                *reinterpret_cast<uint4 *>(ys) = *reinterpret_cast<const uint4 *>(st[n] + k_at[p][1]);
               } else {
-                *reinterpret_cast<uint2 *>(xs) = *reinterpret_cast<const uint2 *>(st + kv_place(S::kRow, key0, col / 2));
-                *reinterpret_cast<uint2 *>(ys) = *reinterpret_cast<const uint2 *>(st + kv_place(S::kRow, key0 + 1, col / 2));
+                *reinterpret_cast<uint2 *>(xs) = *reinterpret_cast<const uint2 *>(st[n] + k_at[p][0]);
+                *reinterpret_cast<uint2 *>(ys) = *reinterpret_cast<const uint2 *>(st[n] + k_at[p][1]);
               }
 #pragma unroll
               for (int b = 0; b < S::kKeyCodes / 16; ++b) {  // a block of 16
                 const uint32_t s2 = e4m3x2_f16x2(*reinterpret_cast<const uint16_t *>(
-                    st + kv_scales_at(FMT, D) + 16 * (col / 16 + b) + key0));  // scales of both keys
+                    st[n] + ks_at + 4 * S::kKeyCodes * p + 16 * b));  // scales of both keys
                 const uint32_t fx = __byte_perm(s2, 0, 0x1010), fy = __byte_perm(s2, 0, 0x3232);
                 uint32_t hx[8], hy[8];
                 e2m1x8_f16(xs[2 * b], hx);
@@ -529,17 +578,20 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
                                           hmul2(hy[2 * k + 1], fy)};
                   const int ks = (p * (S::kKeyCodes / 16) + b) * 4 + k;
 #pragma unroll
-                  for (int nt = 0; nt < NT; ++nt) mma<false>(sc[nt], af, qf[nt][ks][0], qf[nt][ks][1]);
+                  for (int nt = 0; nt < NT; ++nt) mma<false>(sc[n][nt], af, qf[nt][ks][0], qf[nt][ks][1]);
                 }
               }
             }
           }
         }
+        }
         // ---- scores in log2; tw = score + log2 of the value's row scale
-        float tw[NT][4];
+        float tw[S::kTile][NT][4];
+#pragma unroll
+        for (int n = 0; n < S::kTile; ++n) {
         float kx[2] = {1.f, 1.f}, vx[2] = {0.f, 0.f};
         if constexpr (S::kQuant) {
-          const uint8_t *ex = st + kv_exps_at(FMT, D) + key0;
+          const uint8_t *ex = st[n] + ex_at;
           const uint32_t k2 = *reinterpret_cast<const uint16_t *>(ex), v2 = *reinterpret_cast<const uint16_t *>(ex + 16);
           // 255 marks a row with a NaN, its codes are 0: 0 * 2^128 makes the key's score NaN by itself
           kx[0] = __uint_as_float((k2 & 255u) << 23);
@@ -553,31 +605,41 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            sc[nt][x] *= S::kQuant ? qs[nt][x & 1] * kx[x >> 1] : qs[nt][x & 1];
-            if (S::kQuant) tw[nt][x] = sc[nt][x] + vx[x >> 1];
+            sc[n][nt][x] *= S::kQuant ? qs[nt][x & 1] * kx[x >> 1] : qs[nt][x & 1];
+            if (S::kQuant) tw[n][nt][x] = sc[n][nt][x] + vx[x >> 1];
           }
         if (edge) {
-          const bool in[2] = {read(key0), read(S::kQuant ? key0 + 1 : key0 + 8)};
+          const bool in[2] = {read(n, key0), read(n, S::kQuant ? key0 + 1 : key0 + 8)};
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-              if (!in[x >> 1]) sc[nt][x] = tw[nt][x] = -INFINITY;
+              if (!in[x >> 1]) sc[n][nt][x] = tw[n][nt][x] = -INFINITY;
         }
+        }
+        // the largest of the lane's tokens
+        float top[NT][2], topw[NT][2];
         bool grow = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            grow |= fmaxf(sc[nt][x], sc[nt][x + 2]) > thr[nt][x];
-            if (S::kQuant) grow |= fmaxf(tw[nt][x], tw[nt][x + 2]) > thrw[nt][x];
+            top[nt][x] = fmaxf(sc[0][nt][x], sc[0][nt][x + 2]);
+            if (S::kTile > 1) top[nt][x] = fmaxf(top[nt][x], fmaxf(sc[S::kTile - 1][nt][x], sc[S::kTile - 1][nt][x + 2]));
+            grow |= top[nt][x] > thr[nt][x];
+            if (S::kQuant) {
+              topw[nt][x] = fmaxf(tw[0][nt][x], tw[0][nt][x + 2]);
+              if (S::kTile > 1)
+                topw[nt][x] = fmaxf(topw[nt][x], fmaxf(tw[S::kTile - 1][nt][x], tw[S::kTile - 1][nt][x + 2]));
+              grow |= topw[nt][x] > thrw[nt][x];
+            }
           }
         if (__any_sync(kAll, grow)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              // the maximum over the record's keys, lifted where the exponentials are multiplied as f16
+              // the maximum over the tokens, lifted where the exponentials are multiplied as f16
               auto move = [&](float t, float lift, float &rf, float &th) {
 #pragma unroll
                 for (int sh = 4; sh < 32; sh <<= 1) t = fmaxf(t, __shfl_xor_sync(kAll, t, sh));
@@ -587,9 +649,9 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
                 th = t + kSlack;
                 return ex2(old - t);
               };
-              float f = move(fmaxf(sc[nt][x], sc[nt][x + 2]), S::kQuant ? 0.f : S::kLift, ref[nt][x], thr[nt][x]);
+              float f = move(top[nt][x], S::kQuant ? 0.f : S::kLift, ref[nt][x], thr[nt][x]);
               l[nt][x] *= f;
-              if (S::kQuant) f = move(fmaxf(tw[nt][x], tw[nt][x + 2]), S::kLift, refw[nt][x], thrw[nt][x]);
+              if (S::kQuant) f = move(topw[nt][x], S::kLift, refw[nt][x], thrw[nt][x]);
 #pragma unroll
               for (int i = 0; i < D / 16; ++i) {
                 o[nt][i][x] *= f;
@@ -598,20 +660,24 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
             }
         }
         // ---- p, its sum, and P^T as B fragments: lane (r, c) gets head r, rows 2c, 2c + 1 (pf[0]) and + 8 (pf[1])
-        uint32_t pf[NT][2];
+        uint32_t pf[S::kTile][NT][2];
+#pragma unroll
+        for (int n = 0; n < S::kTile; ++n)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float w[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const float p = ex2(sc[nt][x] - ref[nt][x & 1]);
+            const float p = ex2(sc[n][nt][x] - ref[nt][x & 1]);
             l[nt][x & 1] += p;
-            w[x] = S::kQuant ? ex2(tw[nt][x] - refw[nt][x & 1]) : p;
+            w[x] = S::kQuant ? ex2(tw[n][nt][x] - refw[nt][x & 1]) : p;
           }
-          pf[nt][0] = transpose8(pack2<S::kBf>(w[0], w[1]));
-          pf[nt][1] = transpose8(pack2<S::kBf>(w[2], w[3]));
+          pf[n][nt][0] = transpose8(pack2<S::kBf>(w[0], w[1]));
+          pf[n][nt][1] = transpose8(pack2<S::kBf>(w[2], w[3]));
         }
         // ---- O^T += V^T P^T; values of tokens that are not read may be anything (0 * NaN must not come in)
+#pragma unroll
+        for (int n = 0; n < S::kTile; ++n) {
         if constexpr (!S::kQuant) {
           const int key = (lane & 7) + ((lane >> 4) << 3);
           const int half = (lane >> 3) & 1;
@@ -619,11 +685,11 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
           if (edge)
 #pragma unroll
             for (int x = 0; x < 2; ++x)
-              keep[x] = (read(2 * c + 8 * x) ? 0xFFFFu : 0u) | (read(2 * c + 1 + 8 * x) ? 0xFFFF0000u : 0u);
+              keep[x] = (read(n, 2 * c + 8 * x) ? 0xFFFFu : 0u) | (read(n, 2 * c + 1 + 8 * x) ? 0xFFFF0000u : 0u);
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
             uint32_t af[4];
-            ldsm4t(af, st32 + 16 * S::kRow + kv_place(S::kRow, key, 32 * i + 16 * half));
+            ldsm4t(af, st32[n] + 16 * S::kRow + kv_place(S::kRow, key, 32 * i + 16 * half));
             if (edge) {
               af[0] &= keep[0];
               af[1] &= keep[0];
@@ -631,7 +697,7 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
               af[3] &= keep[1];
             }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma<S::kBf>(o[nt][i], af, pf[nt][0], pf[nt][1]);
+            for (int nt = 0; nt < NT; ++nt) mma<S::kBf>(o[nt][i], af, pf[n][nt][0], pf[n][nt][1]);
           }
         } else {
           // A register of two neighbouring columns of one value is used as it is expanded: the k index of the product
@@ -644,25 +710,23 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              pe[nt][2 * k] = pf[nt][k] & 0xFFFFu;
-              pe[nt][2 * k + 1] = pf[nt][k] >> 16;
-              po[nt][2 * k] = pf[nt][k] << 16;
-              po[nt][2 * k + 1] = pf[nt][k] & 0xFFFF0000u;
+              pe[nt][2 * k] = pf[n][nt][k] & 0xFFFFu;
+              pe[nt][2 * k + 1] = pf[n][nt][k] >> 16;
+              po[nt][2 * k] = pf[n][nt][k] << 16;
+              po[nt][2 * k + 1] = pf[n][nt][k] & 0xFFFF0000u;
             }
-          const uint8_t *vs = st + 16 * S::kRow;
 #pragma unroll
-          for (int p = 0; p < D / 8 / S::kValCodes; ++p) {  // one load of each of the four tokens
-            const int col = S::val_col(r, p * S::kValCodes);
+          for (int p = 0; p < S::kValLoads; ++p) {  // one load of each of the four tokens
             uint32_t h[4][S::kValCodes / 2];
             if constexpr (FMT == MOE_KV_FP8) {
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 uint32_t w[S::kValCodes / 4];
                 if constexpr (S::kValCodes == 16)
-                  *reinterpret_cast<uint4 *>(w) = *reinterpret_cast<const uint4 *>(vs + kv_place(S::kRow, tok[k], col));
+                  *reinterpret_cast<uint4 *>(w) = *reinterpret_cast<const uint4 *>(st[n] + v_at[p][k]);
                 else
-                  *reinterpret_cast<uint2 *>(w) = *reinterpret_cast<const uint2 *>(vs + kv_place(S::kRow, tok[k], col));
-                if (edge && !read(tok[k]))
+                  *reinterpret_cast<uint2 *>(w) = *reinterpret_cast<const uint2 *>(st[n] + v_at[p][k]);
+                if (edge && !read(n, tok[k]))
 #pragma unroll
                   for (int y = 0; y < S::kValCodes / 4; ++y) w[y] = 0u;
 #pragma unroll
@@ -675,7 +739,7 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 uint32_t w[S::kValCodes / 8];
-                const uint8_t *src = vs + kv_place(S::kRow, tok[k], col / 2);
+                const uint8_t *src = st[n] + v_at[p][k];
                 if constexpr (S::kValCodes == 32)
                   *reinterpret_cast<uint4 *>(w) = *reinterpret_cast<const uint4 *>(src);
                 else if constexpr (S::kValCodes == 16)
@@ -689,9 +753,8 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
               for (int b = 0; b < (S::kValCodes + 15) / 16; ++b)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {  // tokens tok[k] and tok[k + 2] are neighbours
-                  uint32_t s2 = *reinterpret_cast<const uint16_t *>(st + kv_scales_at(FMT, D) + D +
-                                                                    16 * (col / 16 + b) + tok[k]);
-                  if (edge) s2 &= (read(tok[k]) ? 0xFFu : 0u) | (read(tok[k + 2]) ? 0xFF00u : 0u);
+                  uint32_t s2 = *reinterpret_cast<const uint16_t *>(st[n] + vs_at[k] + 8 * S::kValCodes * p + 16 * b);
+                  if (edge) s2 &= (read(n, tok[k]) ? 0xFFu : 0u) | (read(n, tok[k + 2]) ? 0xFF00u : 0u);
                   s2 = e4m3x2_f16x2(s2);
                   const uint32_t f0 = __byte_perm(s2, 0, 0x1010), f1 = __byte_perm(s2, 0, 0x3232);
 #pragma unroll
@@ -716,10 +779,11 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
               }
           }
         }
+        }
       }
       __syncwarp();
-      ++done;
-      if (!dead && issued - done <= S::kStages - S::kGroup) issue();
+      done += min(S::kTile, cu.end - cu.rec);
+      while (!dead && is_more && issued - done <= S::kStages - S::kGroup) issue();
     }
 
     // ---- the maxima as they are, and the sum of p over the lanes that share a head
