@@ -36,8 +36,10 @@
 // from its registers; what is shared by warps of a CTA is joined in shared
 // memory, once at the end; what is shared by CTAs goes to the workspace as a
 // partial output with its log-sum, and a second kernel joins those. All orders
-// are fixed, so results do not vary from run to run. Where no (sequence, head)
-// can be long, CTAs take whole ones and the second kernel is not needed.
+// are fixed, so results do not vary from run to run.
+// The second kernel is not needed in two cases. Where no (sequence, head) can be
+// long, CTAs take whole ones. Where there are few and none is very long, a
+// cluster of 8 CTAs takes one and joins it through distributed shared memory.
 #include <algorithm>
 
 #include "common.cuh"
@@ -54,6 +56,8 @@ constexpr int kW = 4;              // warps of a CTA
 constexpr int kMaxCtas = 640;      // partial outputs the workspace holds: two a CTA
 constexpr int kMaxB = 4096;
 constexpr int kJoinThreads = 128;
+constexpr int kCluster = 8;
+enum { kStream = 0, kWhole = 1, kClustered = 2 };  // how CTAs share the work
 constexpr int kLead = 4;           // empty units before each (sequence, head)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 4.f;      // lazy maximum, log2
@@ -71,7 +75,7 @@ struct AttnArgs {
   float *part_o;     // [2 kMaxCtas][NH][D]
   float *part_lse;   // [2 kMaxCtas][NH], log2
   int64_t qsb, qsh, osb, osh, ts;
-  int q_type, B, heads, kv_heads, G, GB, window, page, pages, max_pages, ctas, whole;
+  int q_type, B, heads, kv_heads, G, GB, window, page, pages, max_pages, ctas, mode;
   float scale;       // scale * log2 e
 };
 
@@ -206,6 +210,27 @@ struct Seg {
   Span s;
 };
 
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Shared memory at this CTA's address `addr` in the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
 // log2-sum `lse2` with the sink's logit, and the factor that the output takes.
 __device__ __forceinline__ float with_sink(const AttnArgs &a, int head, float lse2, float &g) {
   if (!a.sinks) return lse2;
@@ -234,6 +259,7 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kRing + S::kJoin + S::kMl);
   int *start = reinterpret_cast<int *>(smem + S::kFixed);  // [B + 1] first record of each sequence
   __shared__ int warp_sum[kW];
+  __shared__ float share_lse[S::kHeads];     // what this CTA has for its cluster, with the outputs over the rings
   __shared__ int seg_of[kW][2], ends0[kW];  // (sequence, head) of each warp's first and last partial, or -1
 
   // Places of this lane's loads in a record, FP8 and NVFP4. Held in registers (the compiler would rather work them out
@@ -303,7 +329,13 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
   const int HB = a.kv_heads * a.GB;
   const int64_t total = ((int64_t)base + (int64_t)a.B * kLead) * HB;
   int64_t cta0, cta1;  // this CTA's units
-  if (a.whole) {
+  if (a.mode == kClustered) {
+    const int seg = blockIdx.x / kCluster, rank = blockIdx.x % kCluster, b = seg / HB, hb = seg % HB;
+    const int64_t n = start[b + 1] - start[b];
+    const int64_t first = ((int64_t)start[b] + (int64_t)b * kLead) * HB + (int64_t)hb * (n + kLead) + kLead;
+    cta0 = first + n * rank / kCluster;
+    cta1 = first + n * (rank + 1) / kCluster;
+  } else if (a.mode == kWhole) {
     auto unit_of = [&](int64_t seg) {  // first unit of a (sequence, head)
       const int b = (int)(seg / HB), hb = (int)(seg % HB);
       const int64_t at = ((int64_t)start[b] + (int64_t)b * kLead) * HB;
@@ -321,7 +353,7 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
     cta0 = (int64_t)blockIdx.x * per;
     cta1 = min(cta0 + per, total);
   }
-  if (cta0 >= cta1) return;
+  if (cta0 >= cta1 && a.mode != kClustered) return;  // a cluster stays together
   const int64_t share = (cta1 - cta0 + kW - 1) / kW;
   const int64_t u0 = min(cta0 + warp * share, cta1), u1 = min(u0 + share, cta1);
 
@@ -419,7 +451,7 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
   int dead_at = 0;    // the first that did not arrive
   for (; more; more = next(cu)) {
     if (cu.rec >= cu.end) continue;  // only empty units of it
-    const bool begins = cu.rec == 0, ends = cu.end == cu.s.n;
+    const bool begins = cu.rec == 0 && a.mode != kClustered, ends = cu.end == cu.s.n;
     const int kvh = cu.hb / a.GB, h0 = kvh * a.G + (cu.hb % a.GB) * S::kHeads;
     const int nh = min(S::kHeads, a.G - (cu.hb % a.GB) * S::kHeads);
     // ---- the query of this (sequence, heads): B fragments, head r of each tile
@@ -910,6 +942,10 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
           pk = make_uint2(pack2<false>(acc[0] * g, acc[1] * g), pack2<false>(acc[2] * g, acc[3] * g));
         *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + b * a.osb + (int64_t)(h0 + h) * a.osh + d) = pk;
         if (a.lse && d == 0) a.lse[(int64_t)b * a.heads + h0 + h] = lse2 / kLog2e;
+      } else if (a.mode == kClustered) {  // over the rings, which are drained
+        *reinterpret_cast<float4 *>(smem + (h * D + d) * 4) =
+            make_float4(acc[0] * g, acc[1] * g, acc[2] * g, acc[3] * g);
+        if (d == 0) share_lse[h] = lse2;
       } else {
         *reinterpret_cast<float4 *>(a.part_o + ((int64_t)pslot * S::kHeads + h) * D + d) =
             make_float4(acc[0] * g, acc[1] * g, acc[2] * g, acc[3] * g);
@@ -917,6 +953,44 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
       }
     }
   }
+  if (a.mode != kClustered) return;
+
+  // ---------------- the cluster's CTAs joined, 4 columns of a head a thread
+  if (cta0 >= cta1 && tid < S::kHeads) share_lse[tid] = -INFINITY;
+  cluster_sync();
+  const int seg = blockIdx.x / kCluster, rank = blockIdx.x % kCluster, b = seg / HB, hb = seg % HB;
+  const int h0 = hb / a.GB * a.G + hb % a.GB * S::kHeads, nh = min(S::kHeads, a.G - hb % a.GB * S::kHeads);
+  const uint32_t o32 = smem_u32(smem), lse32 = smem_u32(share_lse);
+  for (int at = rank * (kW * 32) + tid; at < nh * (D / 4); at += kCluster * kW * 32) {
+    const int h = at / (D / 4), d = at % (D / 4) * 4;
+    float w[kCluster], top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < kCluster; ++k) {
+      w[k] = ld_cluster(at_rank(lse32 + 4 * h, k));
+      top = fmaxf(top, w[k]);
+    }
+    const float ref = top == -INFINITY ? 0.f : top;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < kCluster; ++k) {
+      if (w[k] == -INFINITY) continue;  // it has nothing
+      w[k] = ex2(w[k] - ref);
+      sum += w[k];
+      const float4 v = ld_cluster4(at_rank(o32 + (h * D + d) * 4, k));
+      acc[0] += w[k] * v.x;
+      acc[1] += w[k] * v.y;
+      acc[2] += w[k] * v.z;
+      acc[3] += w[k] * v.w;
+    }
+    float g = sum == 0.f ? 0.f : 1.f / sum;
+    const float lse2 = with_sink(a, h0 + h, sum == 0.f ? -INFINITY : ref + log2f(sum), g);
+    const uint2 pk = a.q_type == MOE_BF16
+                         ? make_uint2(pack2<true>(acc[0] * g, acc[1] * g), pack2<true>(acc[2] * g, acc[3] * g))
+                         : make_uint2(pack2<false>(acc[0] * g, acc[1] * g), pack2<false>(acc[2] * g, acc[3] * g));
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + b * a.osb + (int64_t)(h0 + h) * a.osh + d) = pk;
+    if (a.lse && d == 0) a.lse[(int64_t)b * a.heads + h0 + h] = lse2 / kLog2e;
+  }
+  cluster_sync();  // the others may still be reading here
 }
 
 // Joins the partial outputs of one (sequence, kv head, block of heads), if
@@ -1029,16 +1103,36 @@ moe_status_t go(AttnArgs &a, cudaStream_t stream, int *launches) {
     sms = n;
   }
   // the most records that a (sequence, head) can have
-  const int64_t tokens = (int64_t)a.max_pages * a.page, span = a.window > 0 ? std::min<int64_t>(a.window + 15, tokens) : tokens;
-  const int64_t most = span / 16 + 1, groups = (int64_t)a.B * a.kv_heads * a.GB;
+  const int64_t tokens = (int64_t)a.max_pages * a.page, groups = (int64_t)a.B * a.kv_heads * a.GB;
+  const int64_t most = a.window > 0 && a.window < tokens ? (a.window + 14) / 16 + 1 : std::max<int64_t>(tokens / 16, 1);
   // Whole ones: where splitting leaves a warp less than two records, and up to 32 records where there is one for every
-  // SM (48 sequences with a window of 128 on 4 heads: @@W@@ us instead of 11.6; unequal lengths cost at most what 32 take)
-  a.whole = most <= 2 * kW || (most <= 32 && groups >= sms);
+  // SM (48 sequences with a window of 128 on 4 heads: 8.9 us instead of 11.6; unequal lengths cost at most what 32 take).
+  // Clusters: up to 256 records (8 a warp) where the clusters' CTAs fit the device two an SM. NVFP4, 64 columns, 8 heads,
+  // us with clusters / with the second kernel: 777 tokens 8.9 / 11.0 (FP8 of 128), 2048 8.9 / 11.0, 4096 11.0 / 11.6, 4
+  // sequences of 4096 12.3 / 15.1, 8192 15.0 / 13.0.
+  a.mode = most <= 2 * kW || (most <= 32 && groups >= sms) ? kWhole
+           : most <= 256 && groups * kCluster <= 2 * sms   ? kClustered
+                                                           : kStream;
   const int64_t fit = std::min(sms * occ, kMaxCtas);
-  a.ctas = (int)std::min<int64_t>(fit, a.whole ? groups : (groups * (most + kLead) + 2 * kW - 1) / (2 * kW));
-  if (launch_pdl(kern, dim3(a.ctas), dim3(kW * 32), smem, stream, a) != cudaSuccess) return MOE_ERR_CUDA;
+  a.ctas = a.mode == kClustered ? (int)groups * kCluster
+           : a.mode == kWhole   ? (int)std::min(fit, groups)
+                                : (int)std::min<int64_t>(fit, (groups * (most + kLead) + 2 * kW - 1) / (2 * kW));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.ctas);
+  cfg.blockDim = dim3(kW * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kCluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.mode == kClustered ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return MOE_ERR_CUDA;
   if (launches) ++*launches;
-  if (a.ctas > 1 && !a.whole) {
+  if (a.ctas > 1 && a.mode == kStream) {
     // few groups: their heads apart, so that more SMs share the work
     const int heads = std::min(a.G, S::kHeads);
     const int slices = (int)std::min<int64_t>(heads, std::max<int64_t>(1, 2 * sms / groups));
