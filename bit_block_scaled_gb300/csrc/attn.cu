@@ -55,7 +55,7 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kW = 4;              // warps of a CTA
 constexpr int kMaxCtas = 640;      // partial outputs the workspace holds: two a CTA
 constexpr int kMaxB = 4096;
-constexpr int kJoinThreads = 128;
+constexpr int kJoinThreads = 256;
 constexpr int kCluster = 8;
 enum { kStream = 0, kWhole = 1, kClustered = 2 };  // how CTAs share the work
 constexpr int kLead = 4;           // empty units before each (sequence, head)
@@ -1018,6 +1018,19 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
   const int parts = c1 - c0 + 1;
   // it begins in CTA c0, and in the others it began before
   auto slot = [&](int i) { return i == 0 ? 2 * c0 + 1 : 2 * (c0 + i); };
+  const int items = heads * kCols, groups = max(1, kJoinThreads / items);
+  // the first partials of the first round are on their way while the weights are made
+  constexpr int kAhead = 8;
+  float4 ahead[kAhead];
+  const int at0 = groups > 1 ? tid % items : tid, grp = groups > 1 ? tid / items : 0;
+  const bool live0 = at0 < items && grp < groups;
+  const float *src0 = a.part_o + (int64_t)(from + at0 / kCols) * D + at0 % kCols * 4;
+#pragma unroll
+  for (int x = 0; x < kAhead; ++x) {
+    const int i = grp + x * groups;
+    ahead[x] = live0 && i < parts ? *reinterpret_cast<const float4 *>(src0 + (int64_t)slot(i) * (kHeads * D))
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
   for (int k = warp; k < heads; k += kWarps) {
     const int h = from + k;
     float top = -INFINITY;
@@ -1043,23 +1056,28 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
     if (a.lse && lane == 0) a.lse[(int64_t)b * a.heads + h0 + h] = lse2 / kLog2e;
   }
   __syncthreads();
-  const int items = heads * kCols, groups = max(1, kJoinThreads / items);
   for (int base = 0; base < items; base += kJoinThreads) {
-    const int at = groups > 1 ? tid % items : base + tid, grp = groups > 1 ? tid / items : 0;
+    const int at = at0 + base;
     const bool live = at < items && grp < groups;
     const int k = at / kCols, d = at % kCols * 4;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto put = [&](int i, float4 v) {
+      const float w = wts[k * parts + i];
+      acc.x += w * v.x;
+      acc.y += w * v.y;
+      acc.z += w * v.z;
+      acc.w += w * v.w;
+    };
     if (live) {
       const float *src = a.part_o + (int64_t)(from + k) * D + d;
-#pragma unroll 8
-      for (int i = grp; i < parts; i += groups) {
-        const float w = wts[k * parts + i];
-        const float4 v = *reinterpret_cast<const float4 *>(src + (int64_t)slot(i) * (kHeads * D));
-        acc.x += w * v.x;
-        acc.y += w * v.y;
-        acc.z += w * v.z;
-        acc.w += w * v.w;
+      int i = grp;
+      if (base == 0) {
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x, i += groups)
+          if (i < parts) put(i, ahead[x]);
       }
+#pragma unroll 4
+      for (; i < parts; i += groups) put(i, *reinterpret_cast<const float4 *>(src + (int64_t)slot(i) * (kHeads * D)));
     }
     if (groups > 1) {
       acc_s[tid] = acc;
