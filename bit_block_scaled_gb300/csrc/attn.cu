@@ -1105,21 +1105,23 @@ int tiles_of(int G, int D) { return G > 8 && D <= 128 ? 2 : 1; }
 template <int FMT, int D, int NT>
 moe_status_t go(AttnArgs &a, cudaStream_t stream, int *launches) {
   using S = Shape<FMT, D, NT>;
-  const int smem = S::kFixed + (a.B + 1) * 4;
-  static int occ = 0, sms = 0, occ_smem = 0;  // of this kernel on this device
+  // shared memory in steps of 1 KB of sequence starts, so that few sizes occur
+  const int step = a.B / 256, smem = S::kFixed + (step + 1) * 1024 + 4;
+  static int occs[kMaxB / 256 + 1] = {}, sms = 0;  // resident CTAs an SM by step
   auto kern = attn_kernel<FMT, D, NT>;
-  if (occ == 0 || occ_smem != smem) {
+  if (occs[step] == 0) {
     int dev = 0, n = 0, o = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kFixed + (kMaxB + 1) * 4) !=
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             S::kFixed + (kMaxB / 256 + 1) * 1024 + 4) !=
             cudaSuccess ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, kern, kW * 32, smem) != cudaSuccess || o < 1)
       return MOE_ERR_CUDA;
-    occ = o;
-    occ_smem = smem;
     sms = n;
+    occs[step] = o;
   }
+  const int occ = occs[step];
   // the most records that a (sequence, head) can have
   const int64_t tokens = (int64_t)a.max_pages * a.page, groups = (int64_t)a.B * a.kv_heads * a.GB;
   const int64_t most = a.window > 0 && a.window < tokens ? (a.window + 14) / 16 + 1 : std::max<int64_t>(tokens / 16, 1);

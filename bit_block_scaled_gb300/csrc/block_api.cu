@@ -63,7 +63,7 @@ moe_status_t moe_route_grouped(const void *logits, int logits_type, int64_t ld, 
                                moe_stream_t stream) {
   int *n = launch_counter();
   *n = 0;
-  if (T < 0 || E < 1 || E > 256 || k < 1 || k > 8 || k > E) return MOE_ERR_INVALID_ARG;
+  if (T < 0 || T > 1 << 28 || E < 1 || E > 256 || k < 1 || k > 8 || k > E) return MOE_ERR_INVALID_ARG;
   if (!valid_dtype(logits_type) || ld < E) return MOE_ERR_INVALID_ARG;
   const moe_status_t s = check_router(router, E, k);
   if (s != MOE_OK) return s;
@@ -165,6 +165,7 @@ moe_status_t moe_attn_decode(const void *q, int q_type, int64_t q_stride_b, int6
   if ((int64_t)max_pages * cache->page_size >= (int64_t)1 << 31) return MOE_ERR_INVALID_ARG;
   // records of all sequences and heads, the most there can be, in 32 bits a CTA
   if ((int64_t)max_pages * (cache->page_size / 16) * B >= (int64_t)1 << 31) return MOE_ERR_INVALID_ARG;
+  if ((int64_t)B * q_heads * 8 >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
   if (B == 0) return MOE_OK;
   if (!aligned16(q) || !aligned16(out) || !aligned4(seq_lens) || (max_pages > 0 && !aligned4(block_table)))
     return MOE_ERR_INVALID_ARG;

@@ -387,7 +387,8 @@ typedef struct {
  * NaN and infinite logits as in moe_route_topk: NaN ranks and weighs as -inf,
  * a softmax whose maximum is infinite is shared among the logits equal to it;
  * renormalised weights whose sum is 0 are 1/k each.
- * E <= 256, top_k <= min(8, topk_group * E / n_group), E % n_group = 0. */
+ * E <= 256, top_k <= min(8, topk_group * E / n_group), E % n_group = 0, T <=
+ * 2^28. */
 moe_status_t moe_route_grouped(const void *logits, int logits_type, int64_t ld,
                                const float *sel_bias, int T, int E, int k,
                                const moe_router_t *router, int32_t *topk_ids,

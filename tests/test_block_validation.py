@@ -167,3 +167,20 @@ def test_attention_workspace():
     assert moe.moe_attn_workspace_size(64, 8, 128) > 0
     assert _code(lambda: moe.moe_attn_workspace_size(7, 2, 128)) == INVALID
     assert _code(lambda: moe.moe_attn_workspace_size(8, 2, 80)) == UNSUPPORTED
+
+
+def test_host_tensors_need_a_stream_that_says_so():
+    """Without a stream the tensors' device gives it: host tensors are refused there, not launched on."""
+    x = torch.zeros(4, 64, dtype=bf16)
+    assert _code(lambda: moe.moe_residual_norm(x, x, None, None, 1.0, x, None, None)) == INVALID
+    assert _code(lambda: moe.moe_route_grouped(torch.zeros(2, 8), None, 2, moe.router(),
+                                               torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, 2), _ws())) == INVALID
+
+
+def test_arguments_of_another_kind():
+    assert _code(lambda: moe.moe_residual_norm([1], None, None, None, 1.0, None, None, None, 0)) == INVALID
+    assert _code(lambda: _norm(z=torch.zeros(4, 64, dtype=bf16), post="rms")) == INVALID
+    assert _code(lambda: _route(ws=_ws(16))) == INVALID
+    x = torch.zeros(2, 64, dtype=bf16)
+    assert _code(lambda: moe.moe_residual_norm(x, x, None, None, "one", x, None, None, 0)) == INVALID
+    assert _code(lambda: moe.moe_residual_norm(x, x, None, None, 1.0, x, None, None, "stream")) == INVALID
