@@ -56,8 +56,9 @@ constexpr int kW = 4;              // warps of a CTA
 constexpr int kMaxCtas = 640;      // partial outputs the workspace holds: two a CTA
 constexpr int kMaxB = 4096;
 constexpr int kJoinThreads = 256;
-constexpr int kCluster = 8;
-enum { kStream = 0, kWhole = 1, kClustered = 2 };  // how CTAs share the work
+constexpr int kCluster = 8;        // CTAs of a cluster, at most
+// How CTAs share the work: even shares of all units, whole (sequence, head)s, one of them, or a cluster one of them.
+enum { kStream = 0, kWhole = 1, kSingle = 2, kClustered = 3 };
 constexpr int kLead = 4;           // empty units before each (sequence, head)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 4.f;      // lazy maximum, log2
@@ -75,7 +76,7 @@ struct AttnArgs {
   float *part_o;     // [2 kMaxCtas][NH][D]
   float *part_lse;   // [2 kMaxCtas][NH], log2
   int64_t qsb, qsh, osb, osh, ts;
-  int q_type, B, heads, kv_heads, G, GB, window, page, pages, max_pages, ctas, mode;
+  int q_type, B, heads, kv_heads, G, GB, window, page, pages, max_pages, ctas, mode, cluster;
   float scale;       // scale * log2 e
 };
 
@@ -297,65 +298,87 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
   pdl_wait();
   pdl_trigger();
 
-  // first record of every sequence: running sum of their record counts
-  int base = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kW * 32) {
-    const int b = b0 + tid;
-    int n = 0;
-    if (b < a.B) {
-      n = span_of(a, b).n;
-      const int len = a.lens[b];
-      if (blockIdx.x == 0 && (len < 0 || len > a.max_pages * a.page)) raise_status(a.status, MOE_ERR_BAD_INDEX);
-    }
-    int x = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(kAll, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) warp_sum[warp] = x;
-    __syncthreads();
-    int before = base;
-#pragma unroll
-    for (int w = 0; w < kW; ++w) {
-      if (w < warp) before += warp_sum[w];
-      base += warp_sum[w];
-    }
-    if (b < a.B) start[b] = before + x - n;
-    __syncthreads();
-  }
-  if (tid == 0) start[a.B] = base;
-  __syncthreads();
   const int HB = a.kv_heads * a.GB;
-  const int64_t total = ((int64_t)base + (int64_t)a.B * kLead) * HB;
+  auto bad_length = [&](int b) { return a.lens[b] < 0 || a.lens[b] > a.max_pages * a.page; };
+  Seg cu;
   int64_t cta0, cta1;  // this CTA's units
-  if (a.mode == kClustered) {
-    const int seg = blockIdx.x / kCluster, rank = blockIdx.x % kCluster, b = seg / HB, hb = seg % HB;
-    const int64_t n = start[b + 1] - start[b];
-    const int64_t first = ((int64_t)start[b] + (int64_t)b * kLead) * HB + (int64_t)hb * (n + kLead) + kLead;
-    cta0 = first + n * rank / kCluster;
-    cta1 = first + n * (rank + 1) / kCluster;
-  } else if (a.mode == kWhole) {
-    auto unit_of = [&](int64_t seg) {  // first unit of a (sequence, head)
-      const int b = (int)(seg / HB), hb = (int)(seg % HB);
-      const int64_t at = ((int64_t)start[b] + (int64_t)b * kLead) * HB;
-      return b < a.B ? at + (int64_t)hb * (start[b + 1] - start[b] + kLead) : total;
-    };
-    const int64_t segs = (int64_t)a.B * HB;
-    cta0 = unit_of(segs * blockIdx.x / a.ctas);
-    cta1 = unit_of(segs * (blockIdx.x + 1) / a.ctas);
+  if (a.mode >= kSingle) {  // which (sequence, head) is known; its records are units 0 .. n
+    const int ranks = a.cluster, seg = blockIdx.x / ranks, rank = blockIdx.x % ranks;
+    cu.b = seg / HB;
+    cu.hb = seg % HB;
+    cu.at = -kLead;
+    const int64_t n = span_of(a, cu.b).n;
+    cta0 = n * rank / ranks;
+    cta1 = n * (rank + 1) / ranks;
+    if (rank == 0 && cu.hb == 0 && tid == 0 && bad_length(cu.b)) raise_status(a.status, MOE_ERR_BAD_INDEX);
+    __syncwarp();  // the barriers are set up
   } else {
-    const int64_t per = (total + a.ctas - 1) / a.ctas;
-    if (blockIdx.x == 0) {  // what the joining kernel needs of this
-      if (tid == 0) *a.per = per;
-      for (int b = tid; b <= a.B; b += kW * 32) a.starts[b] = start[b];
+    // first record of every sequence: running sum of their record counts
+    int base = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kW * 32) {
+      const int b = b0 + tid;
+      int n = 0;
+      if (b < a.B) {
+        n = span_of(a, b).n;
+        if (blockIdx.x == 0 && bad_length(b)) raise_status(a.status, MOE_ERR_BAD_INDEX);
+      }
+      int x = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kAll, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 31) warp_sum[warp] = x;
+      __syncthreads();
+      int before = base;
+#pragma unroll
+      for (int w = 0; w < kW; ++w) {
+        if (w < warp) before += warp_sum[w];
+        base += warp_sum[w];
+      }
+      if (b < a.B) start[b] = before + x - n;
+      __syncthreads();
     }
-    cta0 = (int64_t)blockIdx.x * per;
-    cta1 = min(cta0 + per, total);
+    if (tid == 0) start[a.B] = base;
+    __syncthreads();
+    const int64_t total = ((int64_t)base + (int64_t)a.B * kLead) * HB;
+    if (a.mode == kWhole) {
+      auto unit_of = [&](int64_t seg) {  // first unit of a (sequence, head)
+        const int b = (int)(seg / HB), hb = (int)(seg % HB);
+        const int64_t at = ((int64_t)start[b] + (int64_t)b * kLead) * HB;
+        return b < a.B ? at + (int64_t)hb * (start[b + 1] - start[b] + kLead) : total;
+      };
+      const int64_t segs = (int64_t)a.B * HB;
+      cta0 = unit_of(segs * blockIdx.x / a.ctas);
+      cta1 = unit_of(segs * (blockIdx.x + 1) / a.ctas);
+    } else {
+      const int64_t per = (total + a.ctas - 1) / a.ctas;
+      if (blockIdx.x == 0) {  // what the joining kernel needs of this
+        if (tid == 0) *a.per = per;
+        for (int b = tid; b <= a.B; b += kW * 32) a.starts[b] = start[b];
+      }
+      cta0 = (int64_t)blockIdx.x * per;
+      cta1 = min(cta0 + per, total);
+    }
+    if (cta0 >= cta1) return;
   }
-  if (cta0 >= cta1 && a.mode != kClustered) return;  // a cluster stays together
   const int64_t share = (cta1 - cta0 + kW - 1) / kW;
   const int64_t u0 = min(cta0 + warp * share, cta1), u1 = min(u0 + share, cta1);
+  if (a.mode < kSingle && u0 < u1) {  // the (sequence, head) that u0 falls in
+    int lo = 0, hi = a.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (((int64_t)start[mid] + (int64_t)mid * kLead) * HB <= u0)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    const int64_t at = ((int64_t)start[lo] + (int64_t)lo * kLead) * HB;
+    const int units = start[lo + 1] - start[lo] + kLead;
+    cu.b = lo;
+    cu.hb = (int)((u0 - at) / units);
+    cu.at = at + (int64_t)cu.hb * units;
+  }
 
   // the records of the (sequence, head) k.b, k.hb that begins at unit k.at
   auto fill = [&](Seg &k) {
@@ -375,24 +398,8 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
     fill(k);
     return true;
   };
-  Seg cu;
   bool more = u0 < u1;
-  if (more) {
-    int lo = 0, hi = a.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (((int64_t)start[mid] + (int64_t)mid * kLead) * HB <= u0)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    const int64_t at = ((int64_t)start[lo] + (int64_t)lo * kLead) * HB;
-    const int units = start[lo + 1] - start[lo] + kLead;
-    cu.b = lo;
-    cu.hb = (int)((u0 - at) / units);
-    cu.at = at + (int64_t)cu.hb * units;
-    fill(cu);
-  }
+  if (more) fill(cu);
 
   // ------------------------------------------------ copies, issued ahead of their use
   Seg is = cu;
@@ -958,15 +965,15 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
   // ---------------- the cluster's CTAs joined, 4 columns of a head a thread
   if (cta0 >= cta1 && tid < S::kHeads) share_lse[tid] = -INFINITY;
   cluster_sync();
-  const int seg = blockIdx.x / kCluster, rank = blockIdx.x % kCluster, b = seg / HB, hb = seg % HB;
+  const int seg = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster, b = seg / HB, hb = seg % HB;
   const int h0 = hb / a.GB * a.G + hb % a.GB * S::kHeads, nh = min(S::kHeads, a.G - hb % a.GB * S::kHeads);
   const uint32_t o32 = smem_u32(smem), lse32 = smem_u32(share_lse);
-  for (int at = rank * (kW * 32) + tid; at < nh * (D / 4); at += kCluster * kW * 32) {
+  for (int at = rank * (kW * 32) + tid; at < nh * (D / 4); at += a.cluster * kW * 32) {
     const int h = at / (D / 4), d = at % (D / 4) * 4;
     float w[kCluster], top = -INFINITY, sum = 0.f;
 #pragma unroll
     for (int k = 0; k < kCluster; ++k) {
-      w[k] = ld_cluster(at_rank(lse32 + 4 * h, k));
+      w[k] = k < a.cluster ? ld_cluster(at_rank(lse32 + 4 * h, k)) : -INFINITY;
       top = fmaxf(top, w[k]);
     }
     const float ref = top == -INFINITY ? 0.f : top;
@@ -1125,18 +1132,23 @@ moe_status_t go(AttnArgs &a, cudaStream_t stream, int *launches) {
   // the most records that a (sequence, head) can have
   const int64_t tokens = (int64_t)a.max_pages * a.page, groups = (int64_t)a.B * a.kv_heads * a.GB;
   const int64_t most = a.window > 0 && a.window < tokens ? (a.window + 14) / 16 + 1 : std::max<int64_t>(tokens / 16, 1);
-  // Whole ones: where splitting leaves a warp less than two records, and up to 32 records where there is one for every
-  // SM (48 sequences with a window of 128 on 4 heads: 8.9 us instead of 11.6; unequal lengths cost at most what 32 take).
-  // Clusters: up to 256 records (8 a warp) where the clusters' CTAs fit the device two an SM. NVFP4, 64 columns, 8 heads,
-  // us with clusters / with the second kernel: 777 tokens 8.9 / 11.0 (FP8 of 128), 2048 8.9 / 11.0, 4096 11.0 / 11.6, 4
-  // sequences of 4096 12.3 / 15.1, 8192 15.0 / 13.0.
-  a.mode = most <= 2 * kW || (most <= 32 && groups >= sms) ? kWhole
-           : most <= 256 && groups * kCluster <= 2 * sms   ? kClustered
-                                                           : kStream;
+  // A CTA or a cluster for each (sequence, head), the largest whose CTAs fit two an SM and have a record for every warp,
+  // as long as no warp gets more than 8 records: so much may be lost to unequal lengths. us, this way / by even shares and
+  // the second kernel:
+  //   clusters of 8: 777 tokens in FP8 on 8 heads of 128 8.2 / 10.9; NVFP4 of 64 on 8 heads, 2048 tokens 8.9 / 11.0, 4096
+  //     11.0 / 11.6 (8192, 16 records a warp, 15.0 / 13.0)
+  //   of 4 and 2: 8 x 2048 tokens in BF16 of 128 17.9 / 21.3; unequal lengths: 16 of up to 1024 in BF16 12.3 / 11.0, 8 of
+  //     up to 2048 in FP8 11.3 / 12.3
+  //   single CTAs: 48 sequences with a window of 128 on 4 heads 6.8 / 11.6
+  //   whole ones: 256 sequences of 64 tokens on 8 heads 11.6 / 21.9
   const int64_t fit = std::min(sms * occ, kMaxCtas);
-  a.ctas = a.mode == kClustered ? (int)groups * kCluster
-           : a.mode == kWhole   ? (int)std::min(fit, groups)
-                                : (int)std::min<int64_t>(fit, (groups * (most + kLead) + 2 * kW - 1) / (2 * kW));
+  int c = kCluster;
+  while (c > 1 && (groups * c > 2 * sms || most < c * kW)) c >>= 1;
+  a.mode = most > 8 * kW * c ? kStream : c > 1 ? kClustered : groups <= fit ? kSingle : kWhole;
+  a.cluster = c;
+  a.ctas = a.mode >= kSingle  ? (int)groups * c
+           : a.mode == kWhole ? (int)fit
+                              : (int)std::min<int64_t>(fit, (groups * (most + kLead) + 2 * kW - 1) / (2 * kW));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.ctas);
   cfg.blockDim = dim3(kW * 32);
@@ -1146,7 +1158,7 @@ moe_status_t go(AttnArgs &a, cudaStream_t stream, int *launches) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = kCluster;
+  attr[1].val.clusterDim.x = c;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.mode == kClustered ? 2 : 1;

@@ -140,6 +140,25 @@ def test_split_over_many_blocks(fmt):
     Case([9000], H=1, G=2, D=128, fmt=fmt, page=16).check()
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("lens,H", [
+    ([600, 0, 1, 40, 520], 3),                  # clusters of 8
+    ([300, 5, 0, 259], 8),                      # of 4
+    ([130, 129, 0, 17, 90] * 4, 6),             # of 2
+    ([100, 0, 64, 1] * 10, 5),                  # single CTAs
+    ([33, 0, 128, 64, 7, 90, 15, 1] * 25, 4),   # whole ones, several a CTA
+    ([1100, 0, 3, 1090] * 3, 40),               # even shares
+])
+def test_ways_of_sharing_the_work(fmt, lens, H):
+    c = Case(lens, H=H, G=2, D=64, fmt=fmt, page=16)
+    c.check(sinks=True)
+    if len(lens) < 8:
+        c.check(window=100)
+        t = c.table.clone()
+        t[0, 1] = -1
+        c.check(table=t, status=5)
+
+
 def test_many_short_sequences():
     rng = np.random.default_rng(0)
     Case(rng.integers(0, 40, size=700).tolist(), H=2, G=2, D=64, fmt="fp8").check()
