@@ -59,7 +59,7 @@ constexpr int kJoinThreads = 256;
 constexpr int kCluster = 8;        // CTAs of a cluster, at most
 // How CTAs share the work: even shares of all units, whole (sequence, head)s, one of them, or a cluster one of them.
 enum { kStream = 0, kWhole = 1, kSingle = 2, kClustered = 3 };
-constexpr int kLead = 4;           // empty units before each (sequence, head)
+constexpr int kLead = 5;           // empty units before each (sequence, head)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 4.f;      // lazy maximum, log2
 
