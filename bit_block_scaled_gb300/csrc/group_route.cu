@@ -20,6 +20,8 @@
 // for a row, with its loops rolled up because its instructions come from memory
 // each time. 8192 random rows of 256 experts in 8 groups with a bias: some 200
 // with close choices and one in two calls with close groups.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "types.cuh"
@@ -387,8 +389,9 @@ __device__ __noinline__ int select_exact(const RouteArgs &a, int64_t at, float m
   return mine;
 }
 
-// PL: experts a lane, rounded up to a power of two; KL: choices held, 4 or 8
-template <int PL, int KL>
+// PL: experts a lane, rounded up to a power of two; KL: choices held, 4 or 8;
+// FULL: every lane has PL experts
+template <int PL, int KL, bool FULL>
 __global__ void __launch_bounds__(kWarps * 32, PL <= 8 ? 7 : 5) group_route_kernel(const RouteArgs a) {
   __shared__ Scratch scratch[kWarps];
   pdl_wait();
@@ -404,9 +407,10 @@ __global__ void __launch_bounds__(kWarps * 32, PL <= 8 ? 7 : 5) group_route_kern
 #pragma unroll
   for (int i = 0; i < PL; ++i) {
     id[i] = g * a.gs + sub + i * a.lanes;
-    if (g < a.n_group && sub + i * a.lanes < a.gs) valid |= 1u << i;
+    if (FULL || (g < a.n_group && sub + i * a.lanes < a.gs)) valid |= 1u << i;
     bias[i] = a.bias && ((valid >> i) & 1u) ? a.bias[id[i]] : 0.f;
   }
+  if (FULL) valid = (1u << PL) - 1u;
   for (int t = blockIdx.x * kWarps + (threadIdx.x >> 5); t < a.T; t += gridDim.x * kWarps) {
     const int64_t at = (int64_t)t * a.ld;
     float l[PL], m = 0.f, sum = 1.f;
@@ -535,17 +539,18 @@ __global__ void __launch_bounds__(kWarps * 32, PL <= 8 ? 7 : 5) group_route_kern
       // others within the error of the last choice
       const float lastv = value_of(last & ~255u);
       const uint32_t edge = a.bias ? key_of(lastv - key_error2(a.score, lastv)) & ~255u : last & ~255u;
-      unsigned extra = 0;
+      unsigned within = 0, extra = 0;
 #pragma unroll
-      for (int i = 0; i < PL; ++i) {
-        const uint32_t x = full[i] ? (full[i] & ~255u) | (uint32_t)(255 - id[i]) : 0u;
-        if (x >= edge && x < last) extra |= 1u << i;
-      }
+      for (int i = 0; i < PL; ++i) within += full[i] >= edge ? 1u : 0u;
+      const bool extras = __reduce_add_sync(kAll, within) != (unsigned)a.k;
+      if (extras)
+#pragma unroll
+        for (int i = 0; i < PL; ++i)
+          if (full[i] >= edge && ((full[i] & ~255u) | (uint32_t)(255 - id[i])) < last) extra |= 1u << i;
       const uint32_t next = __shfl_down_sync(kAll, key, 1);
       const float p = value_of(key & ~255u), v = value_of(next & ~255u);
       const bool close = lane + 1 < a.k && (a.bias ? !(p - v > key_error2(a.score, fmaxf(fabsf(p), fabsf(v))))
                                                    : (key >> 8) == (next >> 8));
-      const bool extras = __any_sync(kAll, extra != 0);
       bool rank = false;  // by 64-bit scores
       int n = a.k;        // candidates
       if (!open && (extras || __any_sync(kAll, close))) {
@@ -621,9 +626,9 @@ __global__ void __launch_bounds__(kWarps * 32, PL <= 8 ? 7 : 5) group_route_kern
   }
 }
 
-template <int PL, int KL>
+template <int PL, int KL, bool FULL>
 cudaError_t go(const RouteArgs &a, cudaStream_t stream) {
-  auto kern = group_route_kernel<PL, KL>;
+  auto kern = group_route_kernel<PL, KL, FULL>;
   static int fit = 0;  // CTAs that are resident on the device
   if (fit == 0) {
     int dev = 0, sms = 0, n = 0;
@@ -664,18 +669,18 @@ moe_status_t launch_group_route(const void *logits, int type, int64_t ld, const 
   a.renorm = r.renormalize != 0;
   a.scale = r.scale;
   const int per = (a.gs + a.lanes - 1) / a.lanes;
-  cudaError_t err;
   const bool four = k <= 4;
-  if (per <= 1)
-    err = four ? go<1, 4>(a, stream) : go<1, 8>(a, stream);
-  else if (per <= 2)
-    err = four ? go<2, 4>(a, stream) : go<2, 8>(a, stream);
-  else if (per <= 4)
-    err = four ? go<4, 4>(a, stream) : go<4, 8>(a, stream);
-  else if (per <= 8)
-    err = four ? go<8, 4>(a, stream) : go<8, 8>(a, stream);
-  else
-    err = four ? go<16, 4>(a, stream) : go<16, 8>(a, stream);
+  const bool full = a.n_group * a.lanes == 32 && a.gs % a.lanes == 0;
+  auto sized = [&](auto pl) {
+    constexpr int kPl = decltype(pl)::value;
+    if (full && per == kPl) return four ? go<kPl, 4, true>(a, stream) : go<kPl, 8, true>(a, stream);
+    return four ? go<kPl, 4, false>(a, stream) : go<kPl, 8, false>(a, stream);
+  };
+  const cudaError_t err = per <= 1   ? sized(std::integral_constant<int, 1>())
+                          : per <= 2 ? sized(std::integral_constant<int, 2>())
+                          : per <= 4 ? sized(std::integral_constant<int, 4>())
+                          : per <= 8 ? sized(std::integral_constant<int, 8>())
+                                     : sized(std::integral_constant<int, 16>());
   if (launches) ++*launches;
   return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
