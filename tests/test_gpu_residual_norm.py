@@ -167,3 +167,49 @@ def test_captured_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(h, want[0]) and torch.equal(y, want[1])
+
+
+@pytest.mark.parametrize("H", [1, 5, 7, 9, 65, 1003, 2881, 4090, 8178, 8191])
+def test_many_rows_off_the_grid(H):
+    run(700, H, gate=row)
+    run(700, H, "fp16", "fp32", full, "layer", "layer")
+    run(700, H, "bf16", "fp32", col, None, "rms", alpha=-0.5)
+    run(459, H, "fp32", "fp32", full, "rms", "layer", wtype="bf16")
+
+
+@pytest.mark.parametrize("H,stride", [(640, 643), (641, 648), (100, 109), (3, 4), (8, 9), (13, 14)])
+def test_many_rows_of_another_stride(H, stride):
+    """Rows that lie `stride` apart: the same results as of rows that lie close, and nothing written between them."""
+    T = 613
+    want_h, want_y = run(T, H, "bf16", "fp32", row)
+
+    def apart(dtype, rows=None):
+        t = torch.full((T, stride), -7.0, dtype=dtype, device="cuda")
+        if rows is not None:
+            t[:, :H] = rows
+        return t
+
+    z = apart(torch.bfloat16, rnd(T, H, dtype="bf16", seed=1, std=2.0))
+    r = apart(torch.float32, rnd(T, H, dtype="fp32", seed=2, std=3.0))
+    g = torch.sigmoid(rnd(T, 1, seed=3)).to(torch.bfloat16)
+    h, y = apart(torch.float32), apart(torch.bfloat16)
+    moe.moe_residual_norm(z[:, :H], r[:, :H], g, spec("rms", H, 10)[0], 1.0, h[:, :H], spec("rms", H, 20)[0], y[:, :H])
+    # the sums' order is another: 128 * 2^-24 of a row's largest value, and a step of the output's type
+    top_h, top_y = want_h.abs().amax(1, keepdim=True), want_y.float().abs().amax(1, keepdim=True)
+    assert ((h[:, :H] - want_h).abs() <= 128 * 2.0 ** -24 * (top_h + 8)).all()
+    assert ((y[:, :H].float() - want_y.float()).abs() <= 2.0 ** -7 * want_y.float().abs() + 2.0 ** -16 * top_y).all()
+    assert (h[:, H:] == -7).all() and (y[:, H:] == -7).all()
+    # strides that differ
+    r2, h2, y2 = apart(torch.float32)[:, :H], torch.empty(T, H, device="cuda"), apart(torch.bfloat16)
+    r2.copy_(r[:, :H])
+    moe.moe_residual_norm(z[:, :H], r2, g, spec("rms", H, 10)[0], 1.0, h2, spec("rms", H, 20)[0], y2[:, :H])
+    assert ((h2 - want_h).abs() <= 128 * 2.0 ** -24 * (top_h + 8)).all() and (y2[:, H:] == -7).all()
+
+
+def test_many_rows_in_place_off_the_grid():
+    T, H = 1500, 331
+    want_h, want_y = run(T, H, "bf16", "bf16", row)
+    z, r = rnd(T, H, dtype="bf16", seed=1, std=2.0), rnd(T, H, dtype="bf16", seed=2, std=3.0)
+    g = torch.sigmoid(rnd(T, 1, seed=3)).to(torch.bfloat16)
+    moe.moe_residual_norm(z, r, g, spec("rms", H, 10)[0], 1.0, r, spec("rms", H, 20)[0], z)
+    assert torch.equal(r, want_h) and torch.equal(z, want_y)
