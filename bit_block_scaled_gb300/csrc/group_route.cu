@@ -15,11 +15,12 @@
 // rests on is wider than them, the keys are right. Otherwise the candidates'
 // scores are computed as pairs of floats (pair_score, off by 1e-9 at most), one
 // a lane, and where even those are close, in 64 bits: a 64-bit exponential
-// takes a warp 3 us, a pair 0.2. What is left -- groups too close for pairs,
-// softmax scores, more than 32 candidates -- goes through select_exact, 16 us
-// for a row, with its loops rolled up because its instructions come from memory
-// each time. 8192 random rows of 256 experts in 8 groups with a bias: some 200
-// with close choices and one in two calls with close groups.
+// takes a warp 3 us, a pair 0.2. What is left -- groups too close for pairs, a
+// softmax over infinities, more than 32 candidates -- goes through select_exact,
+// 16 us for a row, with its loops rolled up because its instructions come from
+// memory each time. 8192 random rows of 256 experts in 8 groups with a bias:
+// some 200 with close choices and one in two calls with close groups; 16 us for
+// sigmoids, 20 for softmax (37 with its sum in 64 bits).
 #include <type_traits>
 
 #include "common.cuh"
@@ -184,18 +185,20 @@ __device__ __forceinline__ Pair square(Pair a) {
 }
 __device__ __forceinline__ float difference(Pair a, Pair b) { return (a.hi - b.hi) + (a.lo - b.lo); }
 
-// sigmoid(l) + b. exp(-l) = 2^n exp(r / 64)^64 with r within ln 2 / 2: the part
-// of the series beyond 1 + x is below 1.5e-5 there, so its fp32 error is 1e-12,
-// which six squarings make 6e-11 of the exponential; the quotient takes one
-// Newton step with its remainder. |l| is held to 80, where the rest is below
-// any tolerance.
-__device__ __forceinline__ Pair pair_score(float l, float b) {
-  const float x = -fminf(fmaxf(l, -80.f), 80.f);
-  const float n = rintf(x * 1.44269504f);
+__device__ __forceinline__ Pair quotient(Pair n, Pair d) {
+  const float q = n.hi / d.hi;
+  return {q, (fmaf(-d.hi, q, n.hi) + (n.lo - d.lo * q)) / d.hi};  // a Newton step with the remainder
+}
+
+// exp(x), x.hi in -80..80, as 2^n exp(r / 64)^64 with r within ln 2 / 2: the
+// part of the series beyond 1 + r / 64 is below 1.5e-5 there, so its fp32 error
+// is 1e-12, which six squarings make 6e-11 of the exponential.
+__device__ __noinline__ Pair pair_exp(Pair x) {
+  const float n = rintf(x.hi * 1.44269504f);
   // r = x - n ln 2, ln 2 as 0.693145751953125 (16 bits, so that n times it is exact) + 1.42860682030941723e-6
-  Pair r = two_sum(fmaf(n, -0.693145751953125f, x), n * -1.42860682030941723e-6f);
+  Pair r = two_sum(fmaf(n, -0.693145751953125f, x.hi), n * -1.42860682030941723e-6f);
   r.hi *= 0.015625f;
-  r.lo *= 0.015625f;
+  r.lo = (r.lo + x.lo) * 0.015625f;
   const float q = r.hi * r.hi * (0.5f + r.hi * (0.166666667f + r.hi * 0.0416666667f));
   Pair e = two_sum(1.f, r.hi);
   e.lo += r.lo + q;
@@ -203,13 +206,37 @@ __device__ __forceinline__ Pair pair_score(float l, float b) {
 #pragma unroll
   for (int i = 0; i < 6; ++i) e = square(e);
   const float two_n = __uint_as_float((uint32_t)((int)n + 127) << 23);
-  e.hi *= two_n;
-  e.lo *= two_n;
-  const Pair d = add({1.f, 0.f}, e);
-  const float s = 1.f / d.hi;
-  return add({s, s * (fmaf(-d.hi, s, 1.f) - d.lo * s)}, {b, 0.f});
+  return {e.hi * two_n, e.lo * two_n};
 }
-// Bound on the error of a difference of two pairs, or of sums of two, of size |v|.
+
+// exp(l - m), m finite and at least l; beyond -80 it is below any tolerance.
+__device__ __forceinline__ Pair pair_exp_rel(float l, float m) {
+  Pair x = two_sum(l, -m);
+  if (!(x.hi > -80.f)) x = {-80.f, 0.f};
+  return pair_exp(x);
+}
+
+// The score of a logit, plus b. sum: of a softmax's exponentials.
+__device__ __forceinline__ Pair pair_score(const RouteArgs &a, float l, float b, float m, Pair sum) {
+  if (a.score == MOE_SCORE_SOFTMAX) return add(quotient(pair_exp_rel(l, m), sum), {b, 0.f});
+  const Pair e = pair_exp({-fminf(fmaxf(l, -80.f), 80.f), 0.f});
+  return add(quotient({1.f, 0.f}, add({1.f, 0.f}, e)), {b, 0.f});
+}
+
+// Sum of the softmax's exponentials over the warp, off by 7e-11 of it: their
+// own error and 13 additions' (8 in a lane, five shuffles).
+__device__ __noinline__ Pair pair_sum(const RouteArgs &a, int64_t at, float m) {
+  Pair sum = {0.f, 0.f};
+#pragma unroll 1
+  for (int e = threadIdx.x & 31; e < a.n_group * a.gs; e += 32)
+    sum = add(sum, pair_exp_rel(not_nan(load_as_f32(a.logits, at + e, a.type)), m));
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1) sum = add(sum, {__shfl_xor_sync(kAll, sum.hi, o), __shfl_xor_sync(kAll, sum.lo, o)});
+  return sum;
+}
+
+// Bound on the error of a difference of two pairs, or of sums of two, of size |v|: a softmax score is off by 1.4e-10
+// at most, a sigmoid by less.
 __device__ __forceinline__ float pair_error2(float v) { return 1e-9f + 1e-12f * fabsf(v); }
 
 // Sum of the softmax's exponentials in 64 bits, over the warp.
@@ -437,6 +464,12 @@ __global__ void __launch_bounds__(kWarps * 32, PL <= 8 ? 7 : 5) group_route_kern
 #pragma unroll
       for (int i = 0; i < PL; ++i) full[i] = (valid >> i) & 1u ? key_of(l[i]) : 0u;
     }
+    // pairs decide close choices, but for a softmax over infinities; its sum is taken where a row needs it first
+    const bool pairs = a.score == MOE_SCORE_SIGMOID || fabsf(m) <= kMaxFloat;
+    Pair psum = {0.f, 0.f};
+    auto need_sum = [&] {
+      if (a.score == MOE_SCORE_SOFTMAX && psum.hi == 0.f) psum = pair_sum(a, at, m);
+    };
     bool open = false;  // the groups are undecided, or there are too many candidates
     if (grouped) {
       uint32_t b1 = 0u, b2 = 0u;
@@ -466,7 +499,8 @@ __global__ void __launch_bounds__(kWarps * 32, PL <= 8 ? 7 : 5) group_route_kern
                     nv = value_of(__reduce_max_sync(kAll, kept ? 0u : gk));
         const float tol = (a.top2 ? 2.f : 1.f) * score_error2(a.score, fmaxf(fabsf(lv), fabsf(nv)));
         open = !(lv - nv > tol);
-        if (open && a.score == MOE_SCORE_SIGMOID) {
+        if (open && pairs) {
+          need_sum();
           // pairs for the groups within the error of the other side, of those experts that can be their best (two)
           const float gv = value_of(gk), edge = value_of(a.top2 ? b2 : b1);
           const bool sure = g < a.n_group && gv > lv + tol, maybe = g < a.n_group && !sure && !(gv < nv - tol);
@@ -487,7 +521,7 @@ __global__ void __launch_bounds__(kWarps * 32, PL <= 8 ? 7 : 5) group_route_kern
 #pragma unroll 1
           for (; need; need &= need - 1) {
             const int e = g * a.gs + sub + (__ffs(need) - 1) * a.lanes;
-            put(pair_score(not_nan(load_as_f32(a.logits, at + e, a.type)), a.bias ? a.bias[e] : 0.f));
+            put(pair_score(a, not_nan(load_as_f32(a.logits, at + e, a.type)), a.bias ? a.bias[e] : 0.f, m, psum));
           }
           __syncwarp();
 #pragma unroll 1
@@ -566,11 +600,12 @@ __global__ void __launch_bounds__(kWarps * 32, PL <= 8 ? 7 : 5) group_route_kern
         if (lane >= a.k && lane < min(n, 32)) mine = own.id[lane];
         __syncwarp();
         open = n > 32;
-        rank = a.bias && a.score == MOE_SCORE_SOFTMAX;
+        rank = a.bias && !pairs;
         if (!open && !rank) {
+          if (a.bias) need_sum();
           const bool in = lane < n;
           const float x = in ? not_nan(load_as_f32(a.logits, at + mine, a.type)) : 0.f;
-          const Pair c = in && a.bias ? pair_score(x, a.bias[mine]) : Pair{x, 0.f};
+          const Pair c = in && a.bias ? pair_score(a, x, a.bias[mine], m, psum) : Pair{x, 0.f};
           int place = 0;
           bool near = false;
 #pragma unroll 1

@@ -158,3 +158,16 @@ def test_agrees_with_the_plain_router():
     gid, gw = gpu(l, None, 6)
     assert np.array_equal(ids.cpu().numpy(), gid)
     np.testing.assert_allclose(w.cpu().numpy(), gw, rtol=2e-6)
+
+
+@pytest.mark.parametrize("std,bias_std", [(2.0, 0.003), (2.0, 0.1), (0.01, 1e-6), (30.0, 0.01)])
+def test_softmax_with_a_bias_near_ties(std, bias_std):
+    """Softmax scores of many experts lie close together: a gap of the order of the bias's and of fp32's rounding
+    decides in some rows of every batch. With wide logits most scores vanish beside the bias."""
+    l = draw(3000, 256, seed=5, std=std)
+    l[::7, 40:90] = float("-inf")
+    b = bias_of(256, std=bias_std)
+    b[8:16] = b[:8]  # the bias alone ties
+    for r in (dict(), dict(n_group=8, topk_group=4, group_score="top2"), dict(n_group=8, topk_group=4)):
+        check(l, b, 8, score="softmax", **r)
+    check(l, None, 8, score="softmax", n_group=16, topk_group=5, group_score="top2", renormalize=False)
