@@ -38,8 +38,13 @@
 // partial output with its log-sum, and a second kernel joins those. All orders
 // are fixed, so results do not vary from run to run.
 // The second kernel is not needed in two cases. Where no (sequence, head) can be
-// long, CTAs take whole ones. Where there are few and none is very long, a
-// cluster of 8 CTAs takes one and joins it through distributed shared memory.
+// long, CTAs take whole ones, even shares of the units moved to the nearest
+// beginning of one. Where there are few and none is very long, a cluster of 2, 4
+// or 8 CTAs takes one and joins it through distributed shared memory.
+//
+// 16 sequences of 65536 tokens in BF16, 32 heads on 8 of 128: 610 us, 104% of the
+// copy bandwidth. 32 of 32768, 64 heads on 8 of 64: FP8 199 us, 81%; NVFP4 196 us,
+// 47%, bound by the expansion of its codes.
 #include <algorithm>
 
 #include "common.cuh"
@@ -300,6 +305,23 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
 
   const int HB = a.kv_heads * a.GB;
   auto bad_length = [&](int b) { return a.lens[b] < 0 || a.lens[b] > a.max_pages * a.page; };
+  auto seg_at = [&](int64_t u) {  // the (sequence, head) that unit u falls in
+    int lo = 0, hi = a.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (((int64_t)start[mid] + (int64_t)mid * kLead) * HB <= u)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    const int64_t at = ((int64_t)start[lo] + (int64_t)lo * kLead) * HB;
+    const int units = start[lo + 1] - start[lo] + kLead;
+    Seg s = {};
+    s.b = lo;
+    s.hb = (int)((u - at) / units);
+    s.at = at + (int64_t)s.hb * units;
+    return s;
+  };
   Seg cu;
   int64_t cta0, cta1;  // this CTA's units
   if (a.mode >= kSingle) {  // which (sequence, head) is known; its records are units 0 .. n
@@ -343,14 +365,17 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
     __syncthreads();
     const int64_t total = ((int64_t)base + (int64_t)a.B * kLead) * HB;
     if (a.mode == kWhole) {
-      auto unit_of = [&](int64_t seg) {  // first unit of a (sequence, head)
-        const int b = (int)(seg / HB), hb = (int)(seg % HB);
-        const int64_t at = ((int64_t)start[b] + (int64_t)b * kLead) * HB;
-        return b < a.B ? at + (int64_t)hb * (start[b + 1] - start[b] + kLead) : total;
+      // even shares, moved to the nearest beginning of a (sequence, head)
+      auto whole = [&](int c) {
+        const int64_t u = total * c / a.ctas;
+        if (u >= total) return total;
+        const Seg s = seg_at(u);
+        const int units = start[s.b + 1] - start[s.b] + kLead;
+        return 2 * (u - s.at) < units ? s.at : s.at + units;
       };
-      const int64_t segs = (int64_t)a.B * HB;
-      cta0 = unit_of(segs * blockIdx.x / a.ctas);
-      cta1 = unit_of(segs * (blockIdx.x + 1) / a.ctas);
+      const int64_t edge = whole(blockIdx.x + (lane & 1));  // both searches at once
+      cta0 = __shfl_sync(kAll, edge, 0);
+      cta1 = __shfl_sync(kAll, edge, 1);
     } else {
       const int64_t per = (total + a.ctas - 1) / a.ctas;
       if (blockIdx.x == 0) {  // what the joining kernel needs of this
@@ -364,21 +389,7 @@ __global__ void __launch_bounds__(kW * 32) attn_kernel(const AttnArgs a) {
   }
   const int64_t share = (cta1 - cta0 + kW - 1) / kW;
   const int64_t u0 = min(cta0 + warp * share, cta1), u1 = min(u0 + share, cta1);
-  if (a.mode < kSingle && u0 < u1) {  // the (sequence, head) that u0 falls in
-    int lo = 0, hi = a.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (((int64_t)start[mid] + (int64_t)mid * kLead) * HB <= u0)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    const int64_t at = ((int64_t)start[lo] + (int64_t)lo * kLead) * HB;
-    const int units = start[lo + 1] - start[lo] + kLead;
-    cu.b = lo;
-    cu.hb = (int)((u0 - at) / units);
-    cu.at = at + (int64_t)cu.hb * units;
-  }
+  if (a.mode < kSingle && u0 < u1) cu = seg_at(u0);
 
   // the records of the (sequence, head) k.b, k.hb that begins at unit k.at
   auto fill = [&](Seg &k) {
