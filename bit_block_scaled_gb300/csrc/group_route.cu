@@ -74,7 +74,15 @@ __device__ __forceinline__ float not_nan(float v) { return v == v ? v : -INFINIT
 __device__ __forceinline__ float score_error2(int score, float v) {
   return (score == MOE_SCORE_SOFTMAX ? 4e-6f : 1e-6f) + 1.3e-7f * fabsf(v);
 }
-// The same for a score cut to the 24 bits of a key (2^-15 of it).
+// Bound on the error of a group's score of fp32 value v, whose best are x and y
+// (y only where it takes two), for comparing v - error with another's v + error:
+// the scores' errors are of their own size, which their sum may have lost, and
+// the sum and the difference round by 2^-24 of it each. Infinities are exact.
+__device__ __forceinline__ float group_error(int score, bool two, float x, float y, float v) {
+  auto half = [&](float s) { return fabsf(s) <= kMaxFloat ? 0.5f * score_error2(score, s) : 0.f; };
+  return half(x) + (two ? half(y) : 0.f) + (fabsf(v) <= kMaxFloat ? 1.3e-7f * fabsf(v) : 0.f);
+}
+// Twice the error of a score cut to the 24 bits of a key (2^-15 of it).
 __device__ __forceinline__ float key_error2(int score, float v) { return score_error2(score, v) + 3.1e-5f * fabsf(v); }
 
 __device__ __forceinline__ float warp_max(float v) { return value_of(__reduce_max_sync(kAll, key_of(v))); }
@@ -235,8 +243,8 @@ __device__ __noinline__ Pair pair_sum(const RouteArgs &a, int64_t at, float m) {
   return sum;
 }
 
-// Bound on the error of a difference of two pairs, or of sums of two, of size |v|: a softmax score is off by 1.4e-10
-// at most, a sigmoid by less.
+// Bound on twice the error of a pair of size |v|: a softmax score is off by 1.4e-10 at most, a sigmoid by less; what
+// is added to it rounds by 2^-47 of its size.
 __device__ __forceinline__ float pair_error2(float v) { return 1e-9f + 1e-12f * fabsf(v); }
 
 // Sum of the softmax's exponentials in 64 bits, over the warp.
@@ -264,6 +272,20 @@ __device__ __noinline__ int rank64(const RouteArgs &a, int64_t at, float m, int 
   mine = lane < a.k ? w.id[lane] : 0;
   __syncwarp();
   return mine;
+}
+
+// Of this lane's group, whose score lies in low..high: whether it is surely
+// among the best, and whether it may be all the same.
+__device__ __forceinline__ void place_groups(const RouteArgs &a, int g, float low, float high, bool &sure, bool &maybe) {
+  int may = 0, are = 0;  // groups that may be ahead of it, and that are
+#pragma unroll 1
+  for (int h = 0; h < a.n_group; ++h) {
+    const float ol = __shfl_sync(kAll, low, h * a.lanes), oh = __shfl_sync(kAll, high, h * a.lanes);
+    may += h != g && !(oh < low);
+    are += h != g && ol > high;
+  }
+  sure = g < a.n_group && may < a.topk_group;
+  maybe = g < a.n_group && !sure && are < a.topk_group;
 }
 
 // The choice for an open row, the j-th id in lane j, from the logits on.
@@ -307,13 +329,10 @@ __device__ __noinline__ int select_exact(const RouteArgs &a, int64_t at, float m
     if (!scored) {
       kept = kept && ahead < a.topk_group;
     } else {
-      // the last kept and the first dropped as fp32 has it; those that are within the error of the other side
-      const unsigned in = __ballot_sync(kAll, kept && ahead == a.topk_group - 1),
-                     out = __ballot_sync(kAll, kept && ahead == a.topk_group);
-      const float lv = __shfl_sync(kAll, gv, __ffs(in) - 1), nv = __shfl_sync(kAll, gv, __ffs(out) - 1);
-      const float tol = 2.f * score_error2(a.score, fmaxf(fabsf(lv), fabsf(nv)));
-      const bool sure = kept && gv > lv + tol;
-      const bool maybe = kept && !sure && !(gv < nv - tol);
+      // those that are surely kept as fp32 has it, and those that are within the error of the other side
+      const float ge = group_error(a.score, a.top2, b1, b2, gv), low = gv - ge, high = gv + ge;
+      bool sure, maybe;
+      place_groups(a, g, low, high, sure, maybe);
       // 64-bit scores of those of an undecided group that can be its best, or its two best
       const float edge = a.top2 ? b2 : b1, least = edge - score_error2(a.score, edge);
       double d1 = -INFINITY, d2 = -INFINITY;
@@ -484,9 +503,15 @@ __global__ void __launch_bounds__(kWarps * 32, PL <= 8 ? 7 : 5) group_route_kern
         b1 = max(b1, o1);
       }
       uint32_t gk = 0;
+      float x = 0.f, y = 0.f;  // the group's best two
       if (g < a.n_group) {
-        const float x = value_of(b1), y = value_of(b2);
-        gk = !a.top2 ? b1 : key_of(not_nan(a.bias ? x + y : score(x) + score(y)));
+        x = value_of(b1);
+        y = value_of(b2);
+        if (a.top2 && !a.bias) {
+          x = score(x);
+          y = score(y);
+        }
+        gk = !a.top2 ? b1 : key_of(not_nan(x + y));
       }
       int ahead = 0;  // groups before this one; equal ones by index
       for (int h = 0; h < a.n_group; ++h) {
@@ -495,15 +520,18 @@ __global__ void __launch_bounds__(kWarps * 32, PL <= 8 ? 7 : 5) group_route_kern
       }
       bool kept = g < a.n_group && ahead < a.topk_group;
       if (by_score) {
-        const float lv = value_of(__reduce_min_sync(kAll, kept ? gk : kAll)),
-                    nv = value_of(__reduce_max_sync(kAll, kept ? 0u : gk));
-        const float tol = (a.top2 ? 2.f : 1.f) * score_error2(a.score, fmaxf(fabsf(lv), fabsf(nv)));
-        open = !(lv - nv > tol);
+        // the least that a kept group's score can be, and the most that a dropped one's can
+        const float gv = value_of(gk), ge = g < a.n_group ? group_error(a.score, a.top2, x, y, gv) : 0.f;
+        const float low = gv - ge, high = gv + ge;
+        const float lv = value_of(__reduce_min_sync(kAll, kept ? key_of(low) : kAll)),
+                    nv = value_of(__reduce_max_sync(kAll, kept || g >= a.n_group ? 0u : key_of(high)));
+        open = !(lv > nv);
         if (open && pairs) {
           need_sum();
           // pairs for the groups within the error of the other side, of those experts that can be their best (two)
-          const float gv = value_of(gk), edge = value_of(a.top2 ? b2 : b1);
-          const bool sure = g < a.n_group && gv > lv + tol, maybe = g < a.n_group && !sure && !(gv < nv - tol);
+          const float edge = value_of(a.top2 ? b2 : b1);
+          bool sure, maybe;
+          place_groups(a, g, low, high, sure, maybe);
           const uint32_t least = !a.bias ? (a.top2 ? b2 : b1) : key_of(edge - score_error2(a.score, edge));
           Pair d1 = {-INFINITY, 0.f}, d2 = d1;
           unsigned need = 0;
@@ -532,15 +560,16 @@ __global__ void __launch_bounds__(kWarps * 32, PL <= 8 ? 7 : 5) group_route_kern
             if (o2.hi != -INFINITY) put(o2);
           }
           const Pair gd = a.top2 ? add(d1, d2) : d1;
+          const float gde = pair_error2(d1.hi) + (a.top2 ? pair_error2(d2.hi) : 0.f);  // of the scores' sizes
           bool near = false;
           int place = 0;
 #pragma unroll 1
           for (int h = 0; h < a.n_group; ++h) {
             const Pair od = {__shfl_sync(kAll, gd.hi, h * a.lanes), __shfl_sync(kAll, gd.lo, h * a.lanes)};
             const bool om = __shfl_sync(kAll, (int)maybe, h * a.lanes), os = __shfl_sync(kAll, (int)sure, h * a.lanes);
-            const float d = difference(od, gd);
+            const float d = difference(od, gd), ode = __shfl_sync(kAll, gde, h * a.lanes);
             place += os || (om && d > 0.f);
-            near = near || (maybe && om && h != g && !(fabsf(d) > 2.f * pair_error2(gd.hi)));
+            near = near || (maybe && om && h != g && !(fabsf(d) > 0.5f * (gde + ode)));
           }
           open = __any_sync(kAll, near);
           kept = sure || (maybe && place < a.topk_group);

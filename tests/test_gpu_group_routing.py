@@ -171,3 +171,48 @@ def test_softmax_with_a_bias_near_ties(std, bias_std):
     for r in (dict(), dict(n_group=8, topk_group=4, group_score="top2"), dict(n_group=8, topk_group=4)):
         check(l, b, 8, score="softmax", **r)
     check(l, None, 8, score="softmax", n_group=16, topk_group=5, group_score="top2", renormalize=False)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("n_group,topk_group", [(2, 1), (8, 3)])
+@pytest.mark.parametrize("size,spread", [(64.0, 1e-2), (256.0, 1e-2), (256.0, 1e-4), (1e6, 1e-4), (1e6, 4e-8), (0.0, 1e-2)])
+def test_biases_of_opposite_sign_in_a_group(score, n_group, topk_group, size, spread):
+    """A group's two best scores carry the rounding of their own size, which their sum may have lost: biases +B and -B
+    in a group, larger and smaller B side by side. Groups of two, all of whose experts are chosen with them; the groups
+    of a row are those of the sums in long double, unless the last kept and the first dropped are closer than 64-bit
+    scores of that size resolve (two roundings of each of the two scores of the two groups)."""
+    T, E, k = 20000, 2 * n_group, 2 * topk_group
+    b = np.zeros((n_group, 2), np.float32)
+    b[:, 0] = size * (1.0 if n_group == 2 else np.resize([1.0, 0.5, 1.0, 0.0], n_group))
+    b[:, 1] = -b[:, 0]
+    g = torch.Generator().manual_seed(17)
+    l = torch.randn(T, E, generator=g) * spread
+    ids, _ = gpu(l.cuda(), torch.from_numpy(b.reshape(-1)).cuda(), k, score=score, n_group=n_group,
+                 topk_group=topk_group, group_score="top2")
+    x = l.numpy().astype(np.longdouble)
+    assert np.finfo(np.longdouble).nmant > 60
+    s = np.exp(x) / np.exp(x).sum(axis=1, keepdims=True) if score == "softmax" else 1 / (1 + np.exp(-x))
+    sums = (s.reshape(T, n_group, 2) + b).sum(axis=2)
+    order = np.argsort(-sums, axis=1, kind="stable")
+    ranked = np.take_along_axis(sums, order, axis=1)
+    open_ = ranked[:, topk_group - 1] - ranked[:, topk_group] <= 8 * 2.0 ** -53 * (1 + size)
+    want = np.sort(order[:, :topk_group], axis=1)
+    got = np.sort(ids // 2, axis=1)[:, ::2]
+    wrong = (got != want).any(axis=1) & ~open_
+    assert open_.mean() < 0.6 and not wrong.any(), (int(wrong.sum()), int(open_.sum()))
+
+
+def test_sums_that_lose_what_pairs_of_floats_hold():
+    """Biases of +-1e6 next to scores that differ by a few steps of fp32 (some 2e-9): pairs of floats are off by that
+    much there, so the row has to go on to 64 bits."""
+    T, size = 600000, 1e6
+    rng = np.random.default_rng(5)
+    l = np.repeat(rng.uniform(-0.1, 0.1, size=(T, 1, 2)).astype(np.float32), 2, axis=1)
+    l = (l.view(np.int32) + rng.integers(0, 4, size=l.shape).astype(np.int32)).view(np.float32)
+    b = np.array([size, -size] * 2, np.float32)
+    ids, _ = gpu(torch.from_numpy(l.reshape(T, 4)).cuda(), torch.from_numpy(b).cuda(), 2, score="sigmoid", n_group=2,
+                 topk_group=1, group_score="top2")
+    gap = (1 / (1 + np.exp(-l.astype(np.longdouble)))).sum(axis=2) @ np.array([1.0, -1.0])
+    open_ = np.abs(gap) <= 8 * 2.0 ** -53 * (1 + size)
+    wrong = (ids[:, 0] // 2 != (gap < 0)) & ~open_
+    assert open_.mean() < 0.5 and not wrong.any(), (int(wrong.sum()), int(open_.sum()))
