@@ -48,6 +48,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "device.cuh"
 #include "kernels.h"
 #include "kvcache.cuh"
 #include "types.cuh"
@@ -1125,21 +1126,17 @@ moe_status_t go(AttnArgs &a, cudaStream_t stream, int *launches) {
   using S = Shape<FMT, D, NT>;
   // shared memory in steps of 1 KB of sequence starts, so that few sizes occur
   const int step = a.B / 256, smem = S::kFixed + (step + 1) * 1024 + 4;
-  static int occs[kMaxB / 256 + 1] = {}, sms = 0;  // resident CTAs an SM by step
+  static PerDevice occs[kMaxB / 256 + 1];  // resident CTAs an SM by step
   auto kern = attn_kernel<FMT, D, NT>;
-  if (occs[step] == 0) {
-    int dev = 0, n = 0, o = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             S::kFixed + (kMaxB / 256 + 1) * 1024 + 4) !=
-            cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, kern, kW * 32, smem) != cudaSuccess || o < 1)
-      return MOE_ERR_CUDA;
-    sms = n;
-    occs[step] = o;
-  }
-  const int occ = occs[step];
+  const int sms = sm_count();
+  const int occ = occs[step].get([&] {
+    int n = 0;
+    const bool ok = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         S::kFixed + (kMaxB / 256 + 1) * 1024 + 4) == cudaSuccess &&
+                    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kW * 32, smem) == cudaSuccess;
+    return ok ? n : 0;
+  });
+  if (occ < 1) return MOE_ERR_CUDA;
   // the most records that a (sequence, head) can have
   const int64_t tokens = (int64_t)a.max_pages * a.page, groups = (int64_t)a.B * a.kv_heads * a.GB;
   const int64_t most = a.window > 0 && a.window < tokens ? (a.window + 14) / 16 + 1 : std::max<int64_t>(tokens / 16, 1);

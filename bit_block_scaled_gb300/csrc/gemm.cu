@@ -53,6 +53,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "device.cuh"
 #include "dequant.cuh"
 #include "kernels.h"
 
@@ -805,26 +806,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// Per-device host caches: devices are numbered below kMaxDevices.
-constexpr int kMaxDevices = 64;
 constexpr uint32_t kMaxSmem = 227 * 1024;  // dynamic shared memory a CTA may opt into
-
-int current_device() {
-  int dev = 0;
-  return (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices) ? dev : 0;
-}
-
-// SM count of the current device (queried once per device).
-int sm_count() {
-  static std::atomic<int> cached[kMaxDevices];
-  const int dev = current_device();
-  int n = cached[dev].load(std::memory_order_relaxed);
-  if (n <= 0) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
-    cached[dev].store(n, std::memory_order_relaxed);
-  }
-  return n;
-}
 
 template <int FMT, int EPI, int KPB, bool F16>
 moe_status_t launch_t(const GemmArgs &a, dim3 grid, uint32_t smem, cudaStream_t st) {
@@ -832,13 +814,11 @@ moe_status_t launch_t(const GemmArgs &a, dim3 grid, uint32_t smem, cudaStream_t 
   // the dynamic shared-memory limit is a per-device function attribute: set
   // it once per device to the most any launch asks for (every thread writes
   // the same value, so racing first launches agree)
-  static std::atomic<int> configured[kMaxDevices];
-  std::atomic<int> &done = configured[current_device()];
-  if (!done.load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem) != cudaSuccess)
-      return MOE_ERR_CUDA;
-    done.store(1, std::memory_order_release);
-  }
+  static PerDevice configured;
+  const int set = configured.get([&] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem) == cudaSuccess ? 1 : 0;
+  });
+  if (set < 1) return MOE_ERR_CUDA;
   return launch_pdl(kern, grid, dim3(cta_threads(KPB)), smem, st, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

@@ -24,6 +24,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "device.cuh"
 #include "kernels.h"
 #include "types.cuh"
 
@@ -693,15 +694,13 @@ __global__ void __launch_bounds__(kWarps * 32, PL <= 8 ? 7 : 5) group_route_kern
 template <int PL, int KL, bool FULL>
 cudaError_t go(const RouteArgs &a, cudaStream_t stream) {
   auto kern = group_route_kernel<PL, KL, FULL>;
-  static int fit = 0;  // CTAs that are resident on the device
-  if (fit == 0) {
-    int dev = 0, sms = 0, n = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kWarps * 32, 0);
-    if (e != cudaSuccess) return e;
-    fit = sms * n;
-  }
+  static PerDevice fits;  // CTAs that are resident on the device
+  const int fit = fits.get([&] {
+    int n = 0;
+    const bool ok = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kWarps * 32, 0) == cudaSuccess;
+    return ok ? n * sm_count() : 0;
+  });
+  if (fit < 1) return cudaErrorUnknown;
   const int need = (a.T + kWarps - 1) / kWarps;
   return launch_pdl(kern, dim3(need < fit ? need : fit), dim3(kWarps * 32), 0, stream, a);
 }

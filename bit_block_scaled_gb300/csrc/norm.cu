@@ -11,6 +11,7 @@
 // copy bandwidth. What counted were instructions: 33 an element with a CTA a row
 // that looks up the weights' type (96 us, 44 at the best split), 9 needed.
 #include "common.cuh"
+#include "device.cuh"
 #include "kernels.h"
 #include "types.cuh"
 
@@ -404,13 +405,7 @@ cudaError_t walk(const NormArgs &a, int chunks, int sms, cudaStream_t stream) {
 // vec: whole chunks on the 16-byte grid; a.shift < 0: no common shift
 template <int TA, int TR>
 cudaError_t go(const NormArgs &a, bool vec, cudaStream_t stream) {
-  static int sms = 0;
-  if (sms == 0) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
-  }
+  const int sms = sm_count();
   const int chunks = (a.H + 7) / 8, shifted = (a.H + 7 + 7) / 8;
   const bool rest = (a.gate && a.gsh != 0) || (a.has_post && a.post.bias) || (a.has_pre && a.pre.bias);
   // from two rows an SM on walking pays (H 2880, bf16; a CTA a row / walking, us): 304 rows 4.2 / 4.1, 608 6.8 / 5.5,
