@@ -9,6 +9,7 @@
 
 #include <initializer_list>
 
+#include <c10/core/DeviceGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -78,10 +79,15 @@ T *struct_of(PyObject *o) {
   return p;
 }
 
-// All on one device.
-void together(const Arg &t, std::initializer_list<const Arg *> others) {
-  for (const Arg *o : others) need(!*o || o->t->device() == t.t->device());
-}
+// The one device that all are on, which is current for the rest of the call: the library launches there.
+struct Together {
+  c10::DeviceGuard guard;
+  Together(const Arg &t, std::initializer_list<const Arg *> others) : guard(same(t, others)) {}
+  static c10::Device same(const Arg &t, std::initializer_list<const Arg *> others) {
+    for (const Arg *o : others) need(!*o || o->t->device() == t.t->device());
+    return t.t->device();
+  }
+};
 
 // A workspace that holds the status word.
 void workspace(const Arg &ws) { need((bool)ws && ws.t->is_contiguous() && (int64_t)ws.t->nbytes() >= MOE_STATUS_BYTES); }
@@ -120,7 +126,7 @@ PyObject *route_grouped(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const Arg l(a[0]), bias(a[1]), ids(a[4]), w(a[5]), ws(a[6]);
     need(l && l.dim() == 2 && ids && w);
     workspace(ws);
-    together(l, {&bias, &ids, &w, &ws});
+    const Together on(l, {&bias, &ids, &w, &ws});
     const int64_t T = l.size(0), E = l.size(1);
     const int k = int_of(a[2]);
     need(T <= INT32_MAX && E <= INT32_MAX && k >= 0 && (l.stride(1) == 1 || E <= 1));
@@ -144,7 +150,7 @@ PyObject *residual_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const Arg &act = z ? z : y ? y : r;
     need((bool)act && act.dim() == 2);
     const Arg &res = r ? r : h ? h : act;
-    together(act, {&z, &r, &gate, &h, &y});
+    const Together on(act, {&z, &r, &gate, &h, &y});
     const int64_t T = act.size(0), H = act.size(1);
     need(T <= INT32_MAX && H <= INT32_MAX);
     auto rows = [&](const Arg &t, const Arg &like) -> int64_t {  // its stride over rows
@@ -187,7 +193,7 @@ PyObject *kv_write(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const moe_kv_cache_t *c = struct_of<moe_kv_cache_t>(a[3]);
     need(k && v && slots && c && k.type() == v.type());
     workspace(ws);
-    together(k, {&v, &slots, &ws});
+    const Together on(k, {&v, &slots, &ws});
     const int64_t T = slots.t->numel();
     need(T <= INT32_MAX);
     const Rows3 ks(k, T, c->kv_heads, c->head_dim), vs(v, T, c->kv_heads, c->head_dim);
@@ -204,7 +210,7 @@ PyObject *kv_read(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const Arg &one = k ? k : v;
     need(one && slots && c && (!v || v.type() == one.type()));
     workspace(ws);
-    together(slots, {&k, &v, &ws});
+    const Together on(slots, {&k, &v, &ws});
     const int64_t T = slots.t->numel();
     need(T <= INT32_MAX);
     int64_t s[4] = {0, 0, 0, 0};
@@ -227,7 +233,7 @@ PyObject *attn_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const Arg q(a[0]), table(a[2]), lens(a[3]), out(a[4]), ws(a[5]), sinks(a[8]), lse(a[9]);
     const moe_kv_cache_t *c = struct_of<moe_kv_cache_t>(a[1]);
     need(q && c && table && lens && out && ws && q.dim() == 3 && out.type() == q.type());
-    together(q, {&table, &lens, &out, &ws, &sinks, &lse});
+    const Together on(q, {&table, &lens, &out, &ws, &sinks, &lse});
     const int64_t B = q.size(0), heads = q.size(1), D = q.size(2);
     need(D == c->head_dim && B <= INT32_MAX && heads <= INT32_MAX);
     need(table.dim() == 2 && table.type() == at::kInt && table.size(0) == B && ws.type() == at::kByte);
