@@ -58,12 +58,14 @@ class Router(ctypes.Structure):
 class Norm(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("type", ctypes.c_int32), ("eps", ctypes.c_float),
                 ("offset", ctypes.c_float), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p),
-                ("width", ctypes.c_int32)]  # behind moe_norm_t: the parameters' length, for the binding's check
+                # behind moe_norm_t, for the binding's checks: the parameters' length, where they are (_place)
+                ("width", ctypes.c_int32), ("place", ctypes.c_int32)]
 
 
 class KvCache(ctypes.Structure):
     _fields_ = [("fmt", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
-                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("data", ctypes.c_void_p)]
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("data", ctypes.c_void_p),
+                ("place", ctypes.c_int32)]  # behind moe_kv_cache_t, for the binding's check: where the data is (_place)
 
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
@@ -351,6 +353,12 @@ def _fail(where):
     raise MoeError(_INVALID, where)
 
 
+def _place(t):
+    """Where a tensor is, in a structure that holds its address: CUDA device i as i + 1, host memory as -1, anything
+    else as -2; 0 in a structure that does not say."""
+    return t.device.index + 1 if t.device.type == "cuda" else -1 if t.device.type == "cpu" else -2
+
+
 def router(score="softmax", n_group=1, topk_group=1, group_score="max", renormalize=True, scale=1.0) -> Router:
     return Router(SCORE[score] if isinstance(score, str) else int(score), int(n_group), int(topk_group),
                   GROUP_SCORE[group_score] if isinstance(group_score, str) else int(group_score),
@@ -367,17 +375,18 @@ def moe_route_grouped(logits, sel_bias, k, cfg, topk_ids, topk_weights, ws, stre
 def norm(kind="rms", weight=None, bias=None, eps=1e-5, offset=0.0) -> Norm:
     """A norm's parameters; the caller keeps the tensors alive while the struct is in use."""
     import torch
-    code, width = 2, 0
+    code, width, place = 2, 0, 0
     for t in (weight, bias):
         if t is not None:
             code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(t.dtype, -1)
             if code < 0 or t.dim() != 1 or not t.is_contiguous():
                 _fail("norm")
-            width = t.numel()
-    if weight is not None and bias is not None and (weight.dtype != bias.dtype or weight.shape != bias.shape):
+            width, place = t.numel(), _place(t)
+    if weight is not None and bias is not None and (weight.dtype != bias.dtype or weight.shape != bias.shape or
+                                                    weight.device != bias.device):
         _fail("norm")
     return Norm(NORM[kind] if isinstance(kind, str) else int(kind), code, float(eps), float(offset),
-                None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr(), width)
+                None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr(), width, place)
 
 
 def moe_residual_norm(z, residual, gate, post, alpha, h_out, pre, y_out, stream=None):
@@ -402,7 +411,7 @@ def kv_cache(data, fmt, head_dim) -> KvCache:
     if data.dim() != 4 or data.dtype != torch.uint8 or not data.is_contiguous() or (rec and data.shape[3] != rec):
         _fail("kv_cache")
     return KvCache(code, int(data.shape[0]), int(data.shape[2]) * 16, int(data.shape[1]), int(head_dim),
-                   data.data_ptr())
+                   data.data_ptr(), _place(data))
 
 
 def moe_kv_write(k, v, slots, cache, ws, stream=None):

@@ -89,6 +89,13 @@ struct Together {
   }
 };
 
+// A structure's address is in the memory of t's device, as far as it says (0: it does not): CUDA device i is i + 1,
+// host memory -1, anything else -2.
+void beside(int place, const Arg &t) {
+  const c10::Device d = t.t->device();
+  need(!place || place == (d.is_cuda() ? d.index() + 1 : d.is_cpu() ? -1 : -2));
+}
+
 // A workspace that holds the status word.
 void workspace(const Arg &ws) { need((bool)ws && ws.t->is_contiguous() && (int64_t)ws.t->nbytes() >= MOE_STATUS_BYTES); }
 
@@ -137,10 +144,16 @@ PyObject *route_grouped(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
-// moe_norm_t with the length of its parameters behind it (0: it has none)
-struct SizedNorm {
+// moe_norm_t with the length of its parameters behind it (0: it has none), and where they are
+struct PlacedNorm {
   moe_norm_t norm;
-  int32_t width;
+  int32_t width, place;
+};
+
+// moe_kv_cache_t with where its data is
+struct PlacedCache {
+  moe_kv_cache_t cache;
+  int32_t place;
 };
 
 // z, residual, gate, post, alpha, h_out, pre, y_out, stream
@@ -168,8 +181,12 @@ PyObject *residual_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
       gst = gt > 1 ? gate.stride(0) : 0;
       gsh = gh > 1 ? gate.stride(1) : 0;
     }
-    const SizedNorm *post = struct_of<SizedNorm>(a[3]), *pre = struct_of<SizedNorm>(a[6]);
-    need((!post || !post->width || post->width == H) && (!pre || !pre->width || pre->width == H));
+    const PlacedNorm *post = struct_of<PlacedNorm>(a[3]), *pre = struct_of<PlacedNorm>(a[6]);
+    for (const PlacedNorm *p : {post, pre})
+      if (p) {
+        need(!p->width || p->width == H);
+        beside(p->place, act);
+      }
     return moe_residual_norm(z.ptr(), zs, r.ptr(), rs, gate.ptr(), gst, gsh, (int)T, (int)H, type_code(act.type()),
                              type_code(res.type()), post ? &post->norm : nullptr, float_of(a[4]), h.ptr(), hs,
                              pre ? &pre->norm : nullptr, y.ptr(), ys, stream_of(a[8], act));
@@ -190,10 +207,12 @@ struct Rows3 {
 PyObject *kv_write(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return status(n, 6, [&]() -> int {
     const Arg k(a[0]), v(a[1]), slots(a[2]), ws(a[4]);
-    const moe_kv_cache_t *c = struct_of<moe_kv_cache_t>(a[3]);
-    need(k && v && slots && c && k.type() == v.type());
+    const PlacedCache *pc = struct_of<PlacedCache>(a[3]);
+    need(k && v && slots && pc && k.type() == v.type());
     workspace(ws);
     const Together on(k, {&v, &slots, &ws});
+    beside(pc->place, k);
+    const moe_kv_cache_t *c = &pc->cache;
     const int64_t T = slots.t->numel();
     need(T <= INT32_MAX);
     const Rows3 ks(k, T, c->kv_heads, c->head_dim), vs(v, T, c->kv_heads, c->head_dim);
@@ -206,11 +225,13 @@ PyObject *kv_write(PyObject *, PyObject *const *a, Py_ssize_t n) {
 PyObject *kv_read(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return status(n, 6, [&]() -> int {
     const Arg slots(a[1]), k(a[2]), v(a[3]), ws(a[4]);
-    const moe_kv_cache_t *c = struct_of<moe_kv_cache_t>(a[0]);
+    const PlacedCache *pc = struct_of<PlacedCache>(a[0]);
     const Arg &one = k ? k : v;
-    need(one && slots && c && (!v || v.type() == one.type()));
+    need(one && slots && pc && (!v || v.type() == one.type()));
     workspace(ws);
     const Together on(slots, {&k, &v, &ws});
+    beside(pc->place, slots);
+    const moe_kv_cache_t *c = &pc->cache;
     const int64_t T = slots.t->numel();
     need(T <= INT32_MAX);
     int64_t s[4] = {0, 0, 0, 0};
@@ -231,9 +252,11 @@ PyObject *kv_read(PyObject *, PyObject *const *a, Py_ssize_t n) {
 PyObject *attn_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return status(n, 11, [&]() -> int {
     const Arg q(a[0]), table(a[2]), lens(a[3]), out(a[4]), ws(a[5]), sinks(a[8]), lse(a[9]);
-    const moe_kv_cache_t *c = struct_of<moe_kv_cache_t>(a[1]);
-    need(q && c && table && lens && out && ws && q.dim() == 3 && out.type() == q.type());
+    const PlacedCache *pc = struct_of<PlacedCache>(a[1]);
+    need(q && pc && table && lens && out && ws && q.dim() == 3 && out.type() == q.type());
     const Together on(q, {&table, &lens, &out, &ws, &sinks, &lse});
+    beside(pc->place, q);
+    const moe_kv_cache_t *c = &pc->cache;
     const int64_t B = q.size(0), heads = q.size(1), D = q.size(2);
     need(D == c->head_dim && B <= INT32_MAX && heads <= INT32_MAX);
     need(table.dim() == 2 && table.type() == at::kInt && table.size(0) == B && ws.type() == at::kByte);

@@ -82,3 +82,34 @@ def test_refusals_leave_the_device(fake, name):
     args[last] = mod.tensor(0, args[last])  # on another device than the rest
     assert getattr(binding, name)(*args) == 1
     assert lib.launches() == [] and mod.current() == 0
+
+
+@pytest.mark.parametrize("name", ["kv_write", "kv_read", "attn_decode"])
+def test_a_cache_in_other_memory_is_refused(fake, name):
+    """A cache in host memory (or on another device) would be written and read by a kernel all the same."""
+    binding, mod, lib = fake
+    args = list(calls(lambda t: mod.tensor(1, t))[name])
+    at = next(i for i, a in enumerate(args) if isinstance(a, moe.KvCache))
+    host = torch.zeros(8, 2, 1, moe.moe_kv_record_bytes("fp8", 64), dtype=torch.uint8)
+    args[at] = moe.kv_cache(host, "fp8", 64)
+    assert getattr(binding, name)(*args) == 1 and lib.launches() == []
+    args[at] = moe.kv_cache(mod.tensor(1, host), "fp8", 64)
+    assert getattr(binding, name)(*args) == 0 and len(lib.launches()) > 0
+
+
+@pytest.mark.parametrize("part", ["post", "pre"])
+def test_a_norms_parameters_in_other_memory_are_refused(fake, part):
+    binding, mod, lib = fake
+    x, w = mod.tensor(0, torch.zeros(4, 64, dtype=bf16)), torch.ones(64)
+
+    def run(n, x=x):
+        post, pre, y = (n, None, None) if part == "post" else (None, n, x)
+        return binding.residual_norm(x, x, None, post, 1.0, x, pre, y, 0)
+    assert run(moe.norm("rms", mod.tensor(0, w))) == 0 and len(lib.launches()) == 1
+    assert run(moe.norm("rms", w)) == 1
+    assert run(moe.norm("layer", None, w)) == 1
+    # an address that is null, as it is on this device, stands for no weight
+    assert run(moe.norm("rms", w.to("meta")), torch.zeros(4, 64, dtype=bf16)) == 1
+    assert lib.launches() == []
+    with pytest.raises(moe.MoeError):
+        moe.norm("layer", w, mod.tensor(0, w))
