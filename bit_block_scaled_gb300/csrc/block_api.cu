@@ -47,11 +47,18 @@ moe_status_t check_cache(const moe_kv_cache_t *c) {
 
 // rows of D values, 16-byte aligned
 bool strides8(int64_t t, int64_t h) { return t % 8 == 0 && h % 8 == 0; }
-// no two (outer, inner) positions of n_inner rows of D values overlap
-bool apart(int64_t outer, int64_t inner, int n_inner, int D) {
+// No two of the rows of D values at o * outer + i * inner (o < n_outer, i < n_inner) share an element.
+bool apart(int n_outer, int64_t outer, int n_inner, int64_t inner, int D) {
   if (outer < 0 || inner < 0) return false;
-  if (n_inner > 1 && inner < D) return false;
-  return outer >= (int64_t)(n_inner - 1) * inner + D || (inner >= outer && outer >= D);
+  if ((n_outer > 1 && outer < D) || (n_inner > 1 && inner < D)) return false;
+  if (n_outer <= 1 || n_inner <= 1) return true;
+  // one dimension within the other's step, as in nearly all layouts
+  if ((outer - D) / (n_inner - 1) >= inner || (inner - D) / (n_outer - 1) >= outer) return true;
+  for (int i = 1; i < n_inner; ++i) {  // rows i apart in one dimension and o or o + 1 in the other
+    const __int128 x = (__int128)i * inner, o = x / outer;
+    if ((o < n_outer && x - o * outer < D) || (o + 1 < n_outer && (o + 1) * outer - x < D)) return false;
+  }
+  return true;
 }
 
 }  // namespace
@@ -128,9 +135,9 @@ moe_status_t moe_kv_read(const moe_kv_cache_t *cache, const int32_t *slots, int 
   if (num == 0 || (!k_out && !v_out)) return MOE_OK;
   if ((k_out && !aligned16(k_out)) || (v_out && !aligned16(v_out)) || !aligned4(slots)) return MOE_ERR_INVALID_ARG;
   const int H = cache->kv_heads, D = cache->head_dim;
-  if (k_out && (!strides8(k_stride_t, k_stride_h) || !apart(num > 1 ? k_stride_t : (int64_t)1 << 40, k_stride_h, H, D)))
+  if (k_out && (!strides8(k_stride_t, k_stride_h) || !apart(num, k_stride_t, H, k_stride_h, D)))
     return MOE_ERR_INVALID_ARG;
-  if (v_out && (!strides8(v_stride_t, v_stride_h) || !apart(num > 1 ? v_stride_t : (int64_t)1 << 40, v_stride_h, H, D)))
+  if (v_out && (!strides8(v_stride_t, v_stride_h) || !apart(num, v_stride_t, H, v_stride_h, D)))
     return MOE_ERR_INVALID_ARG;
   return launch_kv_read(*cache, slots, num, k_out, v_out, type, k_stride_t, k_stride_h, v_stride_t, v_stride_h,
                         status_of(ws), (cudaStream_t)stream, n);
@@ -172,8 +179,7 @@ moe_status_t moe_attn_decode(const void *q, int q_type, int64_t q_stride_b, int6
   if ((sinks && !aligned4(sinks)) || (lse && !aligned4(lse))) return MOE_ERR_INVALID_ARG;
   if (!strides8(q_stride_b, q_stride_h) || !strides8(out_stride_b, out_stride_h)) return MOE_ERR_INVALID_ARG;
   if (q_stride_b < 0 || q_stride_h < 0 || (B > 1 && table_stride < max_pages)) return MOE_ERR_INVALID_ARG;
-  if (!apart(B > 1 ? out_stride_b : (int64_t)1 << 40, out_stride_h, q_heads, cache->head_dim))
-    return MOE_ERR_INVALID_ARG;
+  if (!apart(B, out_stride_b, q_heads, out_stride_h, cache->head_dim)) return MOE_ERR_INVALID_ARG;
   return launch_attn_decode(q, q_type, q_stride_b, q_stride_h, *cache, block_table, table_stride, max_pages, seq_lens,
                             B, q_heads, scale, window, sinks, out, out_stride_b, out_stride_h, lse, ws,
                             (cudaStream_t)stream, n);

@@ -184,3 +184,21 @@ def test_arguments_of_another_kind():
     x = torch.zeros(2, 64, dtype=bf16)
     assert _code(lambda: moe.moe_residual_norm(x, x, None, None, "one", x, None, None, 0)) == INVALID
     assert _code(lambda: moe.moe_residual_norm(x, x, None, None, 1.0, x, None, None, "stream")) == INVALID
+
+
+def _strided(shape, strides, dtype=bf16):
+    return torch.zeros(4096, dtype=dtype).as_strided(shape, strides)
+
+
+@pytest.mark.parametrize("strides", [(64, 64), (64, 128), (128, 64 + 8), (8, 1024), (256, 0), (0, 64), (160, 128),
+                                     (128, 160)])
+def test_outputs_whose_rows_meet_are_refused(strides):
+    """Rows (token, head) of three tokens and three heads that share elements would be written by two lanes."""
+    x = _strided((3, 3, 64), strides + (1,))
+    c = moe.kv_cache(torch.zeros(1, 3, 1, KV.record_bytes("fp8", 64), dtype=torch.uint8), "fp8", 64)
+    slots = torch.zeros(3, dtype=torch.int32)
+    for k, v in ((x, None), (None, x)):
+        assert _code(lambda: moe.moe_kv_read(c, slots, k, v, _ws(), 0)) == INVALID
+    q = torch.zeros(3, 3, 64, dtype=bf16)
+    assert _code(lambda: moe.moe_attn_decode(q, c, torch.zeros(3, 2, dtype=torch.int32), slots, x,
+                                             _ws(moe.moe_attn_workspace_size(3, 3, 64)), stream=0)) == INVALID

@@ -1,5 +1,5 @@
-"""What the calls around the layer keep between launches is a device's own: a process may use them on several. Two
-devices of a stand-in for the CUDA runtime, 152 and 100 SMs."""
+"""The calls around the layer over a stand-in for the CUDA runtime with two devices, of 152 and 100 SMs. What they keep
+between launches is a device's own: a process may use them on several."""
 import threading
 
 import pytest
@@ -62,3 +62,17 @@ def test_first_calls_of_several_threads(lib):
     for t in threads:
         t.join()
     assert codes == [0] * 8 and all(l[2][0] > 0 for l in lib.launches())
+
+
+@pytest.mark.parametrize("T,H,t,h", [(3, 3, 192, 64), (3, 3, 64, 192), (3, 3, 200, 64), (3, 3, 64, 256), (1, 3, 0, 64), (1, 3, 0, 72), (3, 1, 64, 0), (1, 1, 0, 0), (2, 3, 64, 128), (3, 2, 128, 64), (2, 1, 1 << 40, 0),
+                                     (2, 3, 1 << 40, 64), (2, 3, 64, 1 << 40),
+                                     (3, 3, 128, 192), (3, 3, 192, 128)])
+def test_outputs_whose_rows_lie_apart_are_taken(lib, T, H, t, h):
+    """Tokens or heads outermost, spaces between them, strides of dimensions of one."""
+    P = 1 << 20
+    c = fake_cuda.moe.KvCache(2, 8, 16, H, 64, P)
+    assert lib.lib.moe_kv_read(c, P, T, P, None, 0, t, h, 0, 0, P, None) == 0
+    assert lib.lib.moe_kv_read(c, P, T, None, P, 0, 0, 0, t, h, P, None) == 0
+    assert lib.lib.moe_attn_decode(P, 0, H * 64, 64, c, P, 2, 2, P, T, H, 0.1, 0, None, P, t, h, None, P, 1 << 30, None) == 0
+    assert len(lib.launches()) == 3
+    assert lib.lib.moe_kv_read(c, P, 3, P, None, 0, 1 << 60, 1 << 60, 0, 0, P, None) == (1 if H > 1 else 0)
