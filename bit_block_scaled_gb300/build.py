@@ -3,11 +3,13 @@
 Each .cu file is compiled to an object in parallel, then linked into a shared
 library next to this file. cudart is linked statically, so the library has no
 dependency beyond the CUDA driver. Beside it stands _binding.so, the C++ part of
-the Python binding (csrc/binding.cpp), which is built against the installed
-PyTorch.
+the Python binding (csrc/binding.cpp), which is built with g++ (or $CXX) against
+the installed PyTorch; without a PyTorch with CUDA or a C++ compiler the library
+is built alone.
 """
 import concurrent.futures as cf
 import os
+import shlex
 import shutil
 import subprocess
 import sys
@@ -33,17 +35,23 @@ def nvcc() -> str:
 
 
 def _binding_command():
-    """Compiles the C++ binding to an object; its libraries come at the link."""
-    import torch
+    """The binding's object, the command that compiles it and the one that links it; None without what they need."""
+    cxx = shlex.split(os.environ.get("CXX") or shutil.which("g++") or "")
+    try:
+        import torch
+    except ImportError:
+        return None
+    if not cxx or torch.version.cuda is None:
+        return None
     top = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     obj = os.path.join(BUILD, "binding.o")
     inc = [os.path.join(top, "include"), os.path.join(top, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
-    compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+    compile_ = [*cxx, "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
                 *(x for i in inc for x in ("-isystem", i)), "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
     lib = os.path.join(top, "lib")
-    link = ["g++", "-shared", "-o", BINDING + ".tmp", obj, LIB, "-Wl,-rpath,$ORIGIN", f"-L{lib}",
+    link = [*cxx, "-shared", "-o", BINDING + ".tmp", obj, LIB, "-Wl,-rpath,$ORIGIN", f"-L{lib}",
             f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     return obj, compile_, link
 
@@ -69,32 +77,34 @@ def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
         if force or _stale(o, [s] + headers):
             jobs.append([cc, *ARCH, *FLAGS, *extra_flags, "-c", s, "-o", o])
 
-    obj, compile_, link_binding = _binding_command()
-    if force or _stale(obj, [os.path.join(CSRC, "binding.cpp"), headers[-1]]):
-        jobs.append(compile_)
+    binding = _binding_command()
+    lib_jobs = len(jobs)
+    if binding and (force or _stale(binding[0], [os.path.join(CSRC, "binding.cpp"), headers[-1]])):
+        jobs.append(binding[1])
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
 
-    with cf.ThreadPoolExecutor(max_workers=len(jobs) or 1) as ex:
-        for cmd, r in ex.map(run, jobs):
-            if verbose or r.returncode != 0:
-                sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
-            if r.returncode != 0:
-                raise RuntimeError(f"compiling {cmd[-3]} failed")
-    if force or jobs or not os.path.exists(LIB):
-        cmd = [cc, *ARCH, "-shared", "-Xlinker", "-soname=libmoe4.so", "-o", LIB + ".tmp", *objs]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
+    def checked(cmd, r, what):
+        if verbose or r.returncode != 0:
             sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
-            raise RuntimeError("link failed")
-        os.replace(LIB + ".tmp", LIB)
-    if force or jobs or not os.path.exists(BINDING):
-        r = subprocess.run(link_binding, capture_output=True, text=True)
         if r.returncode != 0:
-            sys.stderr.write(" ".join(link_binding) + "\n" + r.stdout + r.stderr)
-            raise RuntimeError("linking the binding failed")
+            raise RuntimeError(f"{what} failed")
+
+    with cf.ThreadPoolExecutor(max_workers=len(jobs) or 1) as ex:
+        done = list(ex.map(run, jobs))
+    # the library first, whatever becomes of the binding
+    for cmd, r in done[:lib_jobs]:
+        checked(cmd, r, f"compiling {cmd[-3]}")
+    if force or lib_jobs or not os.path.exists(LIB):
+        cmd = [cc, *ARCH, "-shared", "-Xlinker", "-soname=libmoe4.so", "-o", LIB + ".tmp", *objs]
+        checked(*run(cmd), "linking the library")
+        os.replace(LIB + ".tmp", LIB)
+    for cmd, r in done[lib_jobs:]:
+        checked(cmd, r, f"compiling {cmd[-3]}")
+    if binding and (force or jobs or not os.path.exists(BINDING)):
+        checked(*run(binding[2]), "linking the binding")
         os.replace(BINDING + ".tmp", BINDING)
     return LIB
 
