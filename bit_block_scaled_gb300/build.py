@@ -35,7 +35,8 @@ def nvcc() -> str:
 
 
 def _binding_command():
-    """The binding's object, the command that compiles it and the one that links it; None without what they need."""
+    """The binding's object, the command that compiles it and the one that links it; None without what they need.
+    Its ABI is that of the interpreter and the PyTorch it is compiled against (_made_for)."""
     cxx = shlex.split(os.environ.get("CXX") or shutil.which("g++") or "")
     try:
         import torch
@@ -54,6 +55,12 @@ def _binding_command():
     link = [*cxx, "-shared", "-o", BINDING + ".tmp", obj, LIB, "-Wl,-rpath,$ORIGIN", f"-L{lib}",
             f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     return obj, compile_, link
+
+
+def _made_for(commands):
+    """What the binding is made for; one that was made for something else is made anew."""
+    import torch
+    return "\n".join([str(torch.__version__), str(torch.version.git_version), sys.version, *map(" ".join, commands)])
 
 
 def _stale(obj, deps):
@@ -79,8 +86,15 @@ def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
 
     binding = _binding_command()
     lib_jobs = len(jobs)
-    if binding and (force or _stale(binding[0], [os.path.join(CSRC, "binding.cpp"), headers[-1]])):
-        jobs.append(binding[1])
+    if binding:
+        made_for, made_for_path = _made_for(binding[1:]), binding[0] + ".for"
+        if os.path.exists(made_for_path):
+            with open(made_for_path) as f:
+                same = f.read() == made_for
+        else:
+            same = False
+        if force or not same or _stale(binding[0], [os.path.join(CSRC, "binding.cpp"), headers[-1]]):
+            jobs.append(binding[1])
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -106,6 +120,8 @@ def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
     if binding and (force or jobs or not os.path.exists(BINDING)):
         checked(*run(binding[2]), "linking the binding")
         os.replace(BINDING + ".tmp", BINDING)
+        with open(made_for_path, "w") as f:
+            f.write(made_for)
     return LIB
 
 

@@ -80,3 +80,27 @@ def test_a_binding_that_fails_leaves_the_library(compiler):
     with pytest.raises(RuntimeError):
         B.build()
     assert not os.path.exists(B.LIB)
+
+
+@pytest.mark.parametrize("what", ["__version__", "git_version"])
+def test_another_torch_rebuilds_the_binding(compiler, monkeypatch, what):
+    """Its ABI is that of the PyTorch it was compiled against; the library has nothing to do with it."""
+    torch = pytest.importorskip("torch")
+    B.build()
+    compiler.ran.clear()
+    monkeypatch.setattr(*((torch, "__version__") if what == "__version__" else (torch.version, "git_version")), "another")
+    B.build()
+    assert sources(compiler) == ["binding.cpp"] and len(compiler.ran) == 2
+    compiler.ran.clear()
+    B.build()
+    assert compiler.ran == []
+
+
+def test_a_binding_that_failed_is_tried_again(compiler):
+    pytest.importorskip("torch")
+    compiler.fails = B.BINDING + ".tmp"
+    with pytest.raises(RuntimeError):
+        B.build()
+    compiler.fails = None
+    B.build()
+    assert os.path.exists(B.BINDING)
