@@ -308,3 +308,88 @@ def test_a_cache_past_four_gigabytes():
     ref = torch.einsum("hn,nhd->hd", p, v.double())
     mag = torch.einsum("hn,nhd->hd", p, v.double().abs())
     assert torch.all((out[0].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -7 * mag)
+
+
+def wide(c, columns, page=-5):
+    """The case's table as a program holds it whose contexts may grow to `columns` pages."""
+    t = torch.full((c.B, columns), page, dtype=torch.int32)
+    t[:, :c.table.shape[1]] = c.table
+    return t
+
+
+def is_split(c, **kw):
+    """Checks the case, which has to go through the workspace and the second kernel."""
+    c.check(**kw)
+    assert moe.moe_last_launch_count() == 2
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D,G", [(64, 1), (64, 9), (64, 16), (64, 17), (64, 40), (128, 8), (128, 9), (128, 40), (256, 8),
+                                 (256, 12)])
+def test_partials_of_every_shape(fmt, D, G):
+    """Two column tiles a CTA, several blocks of heads, the widest heads: split over CTAs and joined."""
+    c = Case([4700, 3, 0, 777], H=2, G=G, D=D, fmt=fmt, page=32)
+    is_split(c, sinks=True)
+    is_split(c, window=4500)
+    t = c.table.clone()
+    t[0, 5], t[0, 60:100], t[3, 0] = -1, 1 << 20, c.data.shape[0]
+    is_split(c, table=t, status=5)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("lens,H", [([600, 0, 1, 40, 520], 3), ([130, 129, 0, 17, 90] * 4, 6),
+                                    ([33, 0, 128, 64, 7, 90, 15, 1] * 25, 4), ([1100, 0, 3, 1090] * 3, 40), ([1], 1)])
+def test_tables_wider_than_the_lengths(fmt, lens, H):
+    c = Case(lens, H=H, G=2, D=64, fmt=fmt, page=16)
+    is_split(c, table=wide(c, 4096), sinks=True)
+    if len(lens) < 8:
+        c.check(table=wide(c, 4096), window=100)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_nan_through_the_join(fmt):
+    """In one CTA's share of a sequence that many have; other heads and, with 16-bit caches, other columns are clear."""
+    def kv(k, v):
+        k[4003, 0, 7] = float("nan")
+        v[2009, 1, 5] = float("nan")
+        return k, v
+    c = Case([6000], H=3, G=2, D=64, fmt=fmt, kv=kv)
+    out, lse = c.run(sinks=True)
+    assert moe.moe_last_launch_count() == 2
+    assert torch.isnan(out[0, :2]).all() and torch.isnan(lse[0, :2]).all()
+    assert torch.isnan(out[0, 2:4, 5]).all() and torch.isfinite(lse[0, 2:]).all()
+    if fmt in ("bf16", "fp16"):
+        assert torch.isfinite(out[0, 2:4, 6:]).all()
+    assert torch.isfinite(out[0, 4:]).all()
+
+
+@pytest.mark.parametrize("fmt,D,G", [("bf16", 128, 8), ("nvfp4", 64, 16), ("fp8", 256, 12)])
+def test_split_repeats_are_identical_with_a_used_workspace(fmt, D, G):
+    c = Case([6000, 31, 700], H=2, G=G, D=D, fmt=fmt)
+    want, wl = c.run(sinks=True)
+    assert moe.moe_last_launch_count() == 2
+    for fill in (0xFF, 0x7F, 0x00):
+        ws = torch.full((moe.moe_attn_workspace_size(2 * G, 2, D),), fill, dtype=torch.uint8, device="cuda")
+        moe.moe_clear_status(ws)
+        for _ in range(2):
+            got, gl = c.run(sinks=True, ws=ws)
+            assert torch.equal(got, want) and torch.equal(gl, wl) and c.status == 0
+
+
+def test_split_in_a_graph_with_growing_lengths():
+    c = Case([5200, 90], H=2, G=4, D=64, fmt="fp8", page=64)
+    ws = torch.zeros(moe.moe_attn_workspace_size(8, 2, 64), dtype=torch.uint8, device="cuda")
+    out, lens, table = torch.zeros_like(c.q), torch.zeros_like(c.lens).cuda(), c.table.cuda()
+    moe.moe_attn_decode(c.q, c.cache, table, lens, out, ws)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        moe.moe_attn_decode(c.q, c.cache, table, lens, out, ws)
+    assert moe.moe_last_launch_count() == 2
+    for less in (5000, 17, 0):
+        lens.copy_((c.lens - less).clamp(min=0))
+        graph.replay()
+        torch.cuda.synchronize()
+        want, _ = c.run(lens=lens.cpu())
+        assert torch.equal(out, want)
