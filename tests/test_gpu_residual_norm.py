@@ -213,3 +213,27 @@ def test_many_rows_in_place_off_the_grid():
     g = torch.sigmoid(rnd(T, 1, seed=3)).to(torch.bfloat16)
     moe.moe_residual_norm(z, r, g, spec("rms", H, 10)[0], 1.0, r, spec("rms", H, 20)[0], z)
     assert torch.equal(r, want_h) and torch.equal(z, want_y)
+
+
+@pytest.mark.parametrize("H", [1000, 2048, 2880, 4096, 4104, 8192])
+def test_many_rows_on_the_grid(H):
+    """More than two rows an SM: every size of the walking kernel, with and without gates and biases."""
+    T = 700
+    run(T, H, gate=row)
+    run(T, H, "bf16", "fp32", full, "layer", "layer")
+    run(T, H, "fp16", "fp16", None, "rms", "layer", wtype="fp16", alpha=0.3)
+    run(T, H, "fp16", "fp32", col, "layer", "rms")
+    run(T, H, "fp32", "fp32", None, None, "rms", offset=1.0)
+    run(T, H, "fp32", "fp32", full, "layer", None, alpha=-1.5)
+    run(T, H, gate=row, has_res=False, write_h=False)
+
+
+@pytest.mark.parametrize("H", [2880, 2881, 4104])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_only_the_pre_norm_of_many_rows(H, kind):
+    r = rnd(700, H, seed=5)
+    y = torch.empty(700, H, dtype=torch.bfloat16, device="cuda")
+    n, s = spec(kind, H, 3)
+    moe.moe_residual_norm(None, r, None, None, 1.0, None, n, y)
+    ref = S.norm(f64(r), **s)[0]
+    assert np.all(np.abs(f64(y) - ref) <= half(y) * np.abs(ref) + 64 * 2.0 ** -24 * (1 + half(y)) * terms(f64(r), s))
