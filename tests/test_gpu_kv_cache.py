@@ -180,3 +180,104 @@ def test_a_cache_past_four_gigabytes():
     assert torch.equal(data[-1, -1, -1].cpu(), data[-1, -1, -1].cpu())
     rec = data[-1, H - 1, page // 16 - 1].cpu().numpy()
     assert np.array_equal(stored(rec, 15, 0, "bf16", D)[0], k[1, H - 1].view(torch.int16).cpu().numpy().view(np.uint16))
+
+
+def bytes_of(slots, heads, fmt, D, page, shape):
+    """Which bytes of a cache of that shape belong to the slots."""
+    own = np.zeros(shape, dtype=bool)
+    R, at = KV.row_bytes(fmt, D), KV.place(fmt, D)
+    for slot in slots:
+        i = slot % 16
+        for part in (0, 1):
+            where = [part * 16 * R + at[i]]
+            if fmt == "nvfp4":
+                where.append(32 * R + part * D + np.arange(D // 16) * 16 + i)
+            if fmt in ("fp8", "nvfp4"):
+                where.append(np.array([shape[3] - 32 + 16 * part + i]))
+            own[slot // page, :, slot % page // 16, np.concatenate(where)] = True
+    return own
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp16", "fp8", "nvfp4"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("T,H,page", [(1, 1, 16), (23, 3, 48), (700, 8, 64)])
+def test_other_slots_keep_their_bytes(fmt, D, T, H, page):
+    """A write changes no byte but those of its slots; neighbours in the same record, line and 16-byte piece among them."""
+    k, v = tokens(T, H, D, "bf16", 1), tokens(T, H, D, "bf16", 2)
+    pages = T // page + 3
+    slots = torch.randperm(pages * page, generator=torch.Generator().manual_seed(5))[:T].to(torch.int32)
+    own = bytes_of(slots.tolist(), H, fmt, D, page, (pages, H, page // 16, KV.record_bytes(fmt, D)))
+    for fill in (0xA5, 0x5A):
+        data, c = new_cache(fmt, D, H, pages, page, fill=fill)
+        moe.moe_kv_write(k, v, slots.cuda(), c, ws_status())
+        assert (data.cpu().numpy()[~own] == fill).all()
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_values_of_32_bits(fmt, D):
+    """Genuine fp32 inputs, of many sizes, byte by byte."""
+    T, H, page = 40, 2, 32
+    g = torch.Generator().manual_seed(11)
+    k, v = (torch.randn(T, H, D, generator=g) * torch.exp(8 * torch.randn(T, H, 1, generator=g)) for _ in range(2))
+    v *= torch.exp(3 * torch.randn(T, H, D, generator=g))
+    data, c = new_cache(fmt, D, H, T // page + 1, page)
+    slots = torch.arange(T, dtype=torch.int32)
+    moe.moe_kv_write(k.cuda(), v.cuda(), slots.cuda(), c, ws_status())
+    check_written(data, slots, k, v, fmt, page)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
+@pytest.mark.parametrize("step", [-1, 0, 1])
+def test_values_of_32_bits_next_to_ties(fmt, step):
+    """Values halfway between two codes (and block maxima halfway between two block scales), and one fp32 step to
+    either side, where a quotient that is rounded first could land on the tie."""
+    D, e4m3 = 64, KV._E4M3
+    ties = (e4m3[1:] + e4m3[:-1]) / 2
+
+    def beside(x):
+        x = np.asarray(x, dtype=np.float32)
+        return x if step == 0 else np.nextafter(x, np.float32(step * np.inf))
+    rows = []
+    if fmt == "fp8":
+        for at in range(0, len(ties), 32):
+            r = np.zeros(D, np.float32)
+            t = ties[at:at + 32]
+            r[:len(t)] = beside(t)
+            r[32:32 + len(t)] = -beside(t)
+            r[63] = 448.0 if t.max() < 400 else r[63]
+            rows.append(r)
+    else:
+        mid = (KV._E2M1[1:] + KV._E2M1[:-1]) / 2
+        for s in e4m3[1:]:
+            r = np.zeros(D, np.float32)
+            r[0], r[1:8], r[8:15] = 6 * s, beside(mid * s), -beside(mid * s)   # codes' ties under a scale of s
+            r[48] = 2688.0                                                      # row scale 1
+            rows.append(r)
+        for t in ties[:-1]:
+            r = np.zeros(D, np.float32)
+            r[0], r[1:8] = beside(6 * t), 6 * t * np.linspace(0.1, 0.9, 7)      # the block scale's ties
+            r[48] = 2688.0
+            rows.append(r)
+    x = torch.from_numpy(np.stack(rows))[:, None]
+    T = x.shape[0]
+    data, c = new_cache(fmt, D, 1, T // 16 + 1, 16)
+    slots = torch.arange(T, dtype=torch.int32)
+    moe.moe_kv_write(x.cuda(), -x.cuda(), slots.cuda(), c, ws_status())
+    check_written(data, slots, x, -x, fmt, 16)
+
+
+def test_a_write_past_four_gigabytes_leaves_the_rest():
+    D, H, page, pages = 128, 8, 128, 20000
+    data, c = new_cache("bf16", D, H, pages, page)
+    slots = [0, pages * page - 1, pages * page // 2 + 7, 17]
+    k, v = tokens(4, H, D, "bf16", 1), tokens(4, H, D, "bf16", 2)
+    moe.moe_kv_write(k, v, torch.tensor(slots, dtype=torch.int32, device="cuda"), c, ws_status())
+    written = sorted({s // page for s in slots})
+    own = bytes_of([written.index(s // page) * page + s % page for s in slots], H, "bf16", D, page,
+                   (len(written),) + tuple(data.shape[1:]))
+    assert (data[written].cpu().numpy()[~own] == 0).all()
+    check_written(data[written], torch.tensor([written.index(s // page) * page + s % page for s in slots]), k, v, "bf16",
+                  page)
+    for lo, hi in zip([-1] + written, written + [pages]):
+        assert not data[lo + 1:hi].any()
