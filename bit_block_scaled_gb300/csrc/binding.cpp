@@ -10,6 +10,7 @@
 #include <initializer_list>
 
 #include <c10/core/DeviceGuard.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -79,13 +80,14 @@ T *struct_of(PyObject *o) {
   return p;
 }
 
-// The one device that all are on, which is current for the rest of the call: the library launches there.
+// The one device that all are on, which is current for the rest of the call: the library launches there. Where there
+// is but one, it is (asking and setting take 0.15 us, as long as the rest of a call).
 struct Together {
-  c10::DeviceGuard guard;
-  Together(const Arg &t, std::initializer_list<const Arg *> others) : guard(same(t, others)) {}
-  static c10::Device same(const Arg &t, std::initializer_list<const Arg *> others) {
-    for (const Arg *o : others) need(!*o || o->t->device() == t.t->device());
-    return t.t->device();
+  c10::OptionalDeviceGuard guard;
+  Together(const Arg &t, std::initializer_list<const Arg *> others) {
+    const c10::Device d = t.t->device();
+    for (const Arg *o : others) need(!*o || o->t->device() == d);
+    if (!d.is_cuda() || c10::cuda::device_count() > 1) guard.reset_device(d);
   }
 };
 
