@@ -670,13 +670,10 @@ __global__ void __launch_bounds__(kWarps * 32, PL <= 8 ? 7 : 5) group_route_kern
     if (a.score == MOE_SCORE_SOFTMAX) {
       if (has) w = a.renorm ? exp_rel(lv, mx) : exp_rel(lv, m) / sum;
     } else if (has) {
-      // far below 0 every sigmoid is exp(l), which only its ratios keep in range
-      if (a.renorm && mx < -30.f) {
-        w = exp_rel(lv, mx);
-      } else {
-        const float x = expf(-fabsf(lv));
-        w = lv >= 0.f ? 1.0f / (1.0f + x) : x / (1.0f + x);
-      }
+      // renormalised ones are taken relative to exp(the largest logit) where that is below 0, or those far under it
+      // would be subnormal, or all 0, before they are divided by their sum
+      const float x = expf(-fabsf(lv));
+      w = (lv >= 0.f ? 1.0f : exp_rel(lv, a.renorm ? fminf(mx, 0.f) : 0.f)) / (1.0f + x);
     }
     if (a.renorm) {
       float total = w;

@@ -216,3 +216,16 @@ def test_sums_that_lose_what_pairs_of_floats_hold():
     open_ = np.abs(gap) <= 8 * 2.0 ** -53 * (1 + size)
     wrong = (ids[:, 0] // 2 != (gap < 0)) & ~open_
     assert open_.mean() < 0.5 and not wrong.any(), (int(wrong.sum()), int(open_.sum()))
+
+
+@pytest.mark.parametrize("top", [5.0, 0.0, -5.0, -20.0, -29.0, -31.0, -60.0])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_sigmoids_far_below_the_largest_chosen(top, renorm):
+    """Ratios are kept where a sigmoid by itself is subnormal (logits below -87) and the largest is not: renormalised
+    weights have the error of any other, down to fp32's normal range."""
+    g = torch.Generator().manual_seed(21)
+    l = top - 83 * torch.rand(400, 8, generator=g)
+    l[:, 3] = top
+    l[::2, 5] = -95.0 - torch.rand(200, generator=g)
+    check(l.cuda(), None, 8, score="sigmoid", renormalize=renorm)
+    check(l.cuda(), bias_of(8, std=100.0), 4, score="sigmoid", renormalize=renorm, n_group=4, topk_group=3)
