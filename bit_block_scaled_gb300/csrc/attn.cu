@@ -151,14 +151,6 @@ __device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t *h) {
       : "r"(w));
 }
 
-// One contiguous piece of global memory into shared memory; 16-byte aligned
-// on both sides, bytes a multiple of 16 (records are multiples of 32).
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
-}
-
 // Tokens of sequence b that are read: [first, len), in records [lo, lo + n), n >= 1.
 struct Span {
   int len, first, lo, n;
