@@ -19,8 +19,8 @@
 // softmax over infinities, more than 32 candidates -- goes through select_exact,
 // 16 us for a row, with its loops rolled up because its instructions come from
 // memory each time. 8192 random rows of 256 experts in 8 groups with a bias:
-// some 200 with close choices and one in two calls with close groups; 16 us for
-// sigmoids, 20 for softmax (37 with its sum in 64 bits).
+// some 200 with close choices and one in two calls with close groups; 16.5 us for
+// sigmoids, 21 for softmax (37 with its sum in 64 bits).
 #include <type_traits>
 
 #include "common.cuh"
@@ -204,7 +204,8 @@ __device__ __forceinline__ Pair quotient(Pair n, Pair d) {
 // is 1e-12, which six squarings make 6e-11 of the exponential.
 __device__ __noinline__ Pair pair_exp(Pair x) {
   const float n = rintf(x.hi * 1.44269504f);
-  // r = x - n ln 2, ln 2 as 0.693145751953125 (16 bits, so that n times it is exact) + 1.42860682030941723e-6
+  // r = x - n ln 2, a two-part reduction after Cody and Waite: ln 2 as 0.693145751953125 (16 bits, so that n times it
+  // is exact) + 1.42860682030941723e-6
   Pair r = two_sum(fmaf(n, -0.693145751953125f, x.hi), n * -1.42860682030941723e-6f);
   r.hi *= 0.015625f;
   r.lo = (r.lo + x.lo) * 0.015625f;

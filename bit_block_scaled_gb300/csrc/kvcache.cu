@@ -7,9 +7,11 @@
 //
 // Row scales are powers of two: x / r is exact, so an FP8 code is one rounding
 // of x / r, and an NVFP4 code one rounding of the quotient x / r / s by the
-// E4M3 scale. Quotients of a 16-bit x that lie on a tie of E2M1 are exact in
-// fp32 and others cannot round onto one (x and the tie times s both have at
-// most 11 significant bits), so the codes are those of real arithmetic.
+// E4M3 scale. Quotients that lie on a tie of E2M1 are exact in fp32 and others
+// cannot round onto one: x differs from the tie times s, of at most 7 significant
+// bits, by a step of fp32 at least, and s < 2 in the units of its leading bit, so
+// that the quotient differs from the tie by more than half a step. The same holds
+// for m / 6 and the ties of E4M3. So the codes are those of real arithmetic.
 #include "common.cuh"
 #include "kernels.h"
 #include "kvcache.cuh"

@@ -9,7 +9,8 @@
 //
 // 8192 x 2880, bf16, RMS before and after with a gate a row: 33.5 us, 83% of the
 // copy bandwidth. What counted were instructions: 33 an element with a CTA a row
-// that looks up the weights' type (96 us, 44 at the best split), 9 needed.
+// that looks up the weights' type (96 us, 44 at the best split), 9 needed. In fp32
+// with a gate of every element and layer norms, 8192 x 2880: 90 us, 77%.
 #include "common.cuh"
 #include "device.cuh"
 #include "kernels.h"

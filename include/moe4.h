@@ -473,8 +473,9 @@ moe_status_t moe_kv_write(const void *k, const void *v, int type,
                           void *ws, moe_stream_t stream);
 
 /* Reads tokens back: k_out, v_out [n][kv_heads][D] of `type`, strides as in
- * moe_kv_write. A negative slot gives zeros, one past the cache gives zeros
- * and latches MOE_ERR_BAD_INDEX. Either output may be NULL. */
+ * moe_kv_write; rows that share elements are refused. A negative slot gives
+ * zeros, one past the cache gives zeros and latches MOE_ERR_BAD_INDEX. Either
+ * output may be NULL. */
 moe_status_t moe_kv_read(const moe_kv_cache_t *cache, const int32_t *slots, int n,
                          void *k_out, void *v_out, int type, int64_t k_stride_t,
                          int64_t k_stride_h, int64_t v_stride_t, int64_t v_stride_h,
@@ -492,7 +493,8 @@ moe_status_t moe_attn_workspace_size(int q_heads, int kv_heads, int head_dim,
  *   sinks (fp32 [q_heads]) is given, one more logit sinks[h] without a value,
  *   of the logits scale * q[b][h] . k_i.
  * q and out are bf16 or fp16 (q_type) [B][q_heads][D] with strides (multiples
- * of 8); a BF16 or FP16 cache takes a query of its own type. lse (fp32
+ * of 8; rows of out that share elements are refused, and it must not overlap
+ * q); a BF16 or FP16 cache takes a query of its own type. lse (fp32
  * [B][q_heads], or NULL) receives the natural log of the sum of exponentials,
  * the sink's included. A sequence of length 0 gives zeros, and lse = sinks[h]
  * or -inf. A length past the table or negative is taken as the table's
