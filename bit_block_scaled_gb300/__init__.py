@@ -9,4 +9,5 @@ from ._lib import (ACT, FMT, LAYOUT, ROUTE, STATUS, Act, MoeError, QWeight, act,
                    moe_import_modelopt_global_scale, moe_wait_selftest,
                    GROUP_SCORE, KV_FMT, NORM, SCORE, STATUS_BYTES, KvCache, Norm, Router, kv_cache,
                    moe_attn_decode, moe_attn_workspace_size, moe_kv_read, moe_kv_record_bytes, moe_kv_write,
-                   moe_residual_norm, moe_route_grouped, norm, router)
+                   moe_residual_norm, moe_route_grouped, norm, router,
+                   Fp4, fp4, moe_fp4_dequantize, moe_fp4_linear, moe_fp4_pack_scales, moe_fp4_quantize, moe_fp4_scale_bytes)

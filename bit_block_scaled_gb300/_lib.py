@@ -13,7 +13,7 @@ LIB_PATH = os.path.join(HERE, "libmoe4.so")
 MOE_OK = 0
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_CUDA",
           4: "MOE_ERR_TIMEOUT", 5: "MOE_ERR_BAD_INDEX", 6: "MOE_ERR_WORKSPACE",
-          7: "MOE_ERR_SCALE_RANGE"}
+          7: "MOE_ERR_SCALE_RANGE", 8: "MOE_ERR_CAPACITY"}
 FMT = {"nvfp4": 0, "mxfp4": 1, "int4": 2}
 ACT = {"swigluoai": 0, "relu2": 1}
 ROUTE = {"topk_softmax": 0, "sigmoid_bias": 1}
@@ -31,7 +31,8 @@ EXPORTS = ("moe_padded_rows", "moe_workspace_size", "moe_route_topk", "moe_align
            "moe_status_string", "moe_last_launch_count", "moe_forward_static", "moe_forward_profile",
            "moe_import_gptq_int4", "moe_import_modelopt_global_scale", "moe_route_grouped",
            "moe_residual_norm", "moe_kv_record_bytes", "moe_kv_write", "moe_kv_read",
-           "moe_attn_workspace_size", "moe_attn_decode")
+           "moe_attn_workspace_size", "moe_attn_decode", "moe_fp4_scale_bytes", "moe_fp4_quantize", "moe_fp4_dequantize",
+           "moe_fp4_pack_scales", "moe_fp4_linear")
 
 
 class MoeError(RuntimeError):
@@ -66,6 +67,12 @@ class KvCache(ctypes.Structure):
     _fields_ = [("fmt", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("data", ctypes.c_void_p),
                 ("place", ctypes.c_int32)]  # behind moe_kv_cache_t, for the binding's check: where the data is (_place)
+
+
+class Fp4(ctypes.Structure):
+    _fields_ = [("fmt", ctypes.c_int32), ("rows", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("row_scale_stride", ctypes.c_int32), ("q", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("row_scale", ctypes.c_void_p), ("place", ctypes.c_int32)]  # behind moe_fp4_t: where it is (_place)
 
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
@@ -106,6 +113,11 @@ _SIGS = {
     "moe_attn_workspace_size": (_i32, [_i32, _i32, _i32, ctypes.POINTER(_sz)]),
     "moe_attn_decode": (_i32, [_vp, _i32, _i64, _i64, ctypes.POINTER(KvCache), _vp, _i64, _i32, _vp, _i32, _i32,
                                ctypes.c_float, _i32, _vp, _vp, _i64, _i64, _vp, _vp, _sz, _vp]),
+    "moe_fp4_scale_bytes": (_i64, [_i32, _i32, _i32]),
+    "moe_fp4_quantize": (_i32, [_vp, _i32, _i64, ctypes.POINTER(Fp4), _vp]),
+    "moe_fp4_dequantize": (_i32, [ctypes.POINTER(Fp4), _vp, _i32, _i64, _vp]),
+    "moe_fp4_pack_scales": (_i32, [_vp, _i32, _i32, _i32, _vp, _vp]),
+    "moe_fp4_linear": (_i32, [ctypes.POINTER(Fp4), ctypes.POINTER(Fp4), _vp, _vp, _i32, _i64, _vp, _vp]),
 }
 
 _lib = None
@@ -442,3 +454,61 @@ def moe_attn_decode(q, cache, block_table, seq_lens, out, ws, scale=None, window
     code = (_fast or _setup()).attn_decode(q, cache, block_table, seq_lens, out, ws, scale, window, sinks, lse, stream)
     if code:
         raise MoeError(code, "moe_attn_decode")
+
+
+# ------------------------------------------------------------------------------------ dense projections in 4 bits
+def _fp4_format(fmt):
+    return FMT[fmt] if isinstance(fmt, str) else int(fmt)
+
+
+def moe_fp4_scale_bytes(fmt, rows, K):
+    return int(load().moe_fp4_scale_bytes(_fp4_format(fmt), rows, K))
+
+
+def fp4(q, scales, fmt, row_scale=None) -> Fp4:
+    """A 4-bit matrix: q uint8 [rows, K / 2], scales uint8 [moe_fp4_scale_bytes(fmt, rows, K)] (tiled), row_scale fp32
+    [rows], or of one value for all rows, or None; the caller keeps the tensors alive while the struct is in use."""
+    import torch
+    code = _fp4_format(fmt)
+    if q.dim() != 2 or q.dtype != torch.uint8 or not q.is_contiguous():
+        _fail("fp4")
+    rows, K = int(q.shape[0]), int(q.shape[1]) * 2
+    if (scales.dtype != torch.uint8 or not scales.is_contiguous() or scales.device != q.device or
+            scales.numel() != moe_fp4_scale_bytes(code, rows, K) or (rows and not scales.numel())):
+        _fail("fp4")
+    stride = 0
+    if row_scale is not None:
+        if (row_scale.dtype != torch.float32 or not row_scale.is_contiguous() or row_scale.device != q.device or
+                row_scale.numel() not in (1, rows)):
+            _fail("fp4")
+        stride = int(row_scale.numel() == rows)
+    return Fp4(code, rows, K, stride, q.data_ptr(), scales.data_ptr(), None if row_scale is None else row_scale.data_ptr(),
+               _place(q))
+
+
+def moe_fp4_quantize(x, out, stream=None):
+    """x [rows, K] bf16, fp16 or fp32 (rows may be apart) into the tensors of out, from fp4()."""
+    code = (_fast or _setup()).fp4_quantize(x, out, stream)
+    if code:
+        raise MoeError(code, "moe_fp4_quantize")
+
+
+def moe_fp4_dequantize(f, out, stream=None):
+    """The values of f, from fp4(), into out [rows, K] bf16, fp16 or fp32."""
+    code = (_fast or _setup()).fp4_dequantize(f, out, stream)
+    if code:
+        raise MoeError(code, "moe_fp4_dequantize")
+
+
+def moe_fp4_pack_scales(plain, fmt, K, scales, stream=None):
+    """A checkpoint's block scales (bytes [rows, K / 16] or [rows, K / 32]) into scales, tiled as fp4() takes them."""
+    code = (_fast or _setup()).fp4_pack_scales(plain, _fp4_format(fmt), K, scales, stream)
+    if code:
+        raise MoeError(code, "moe_fp4_pack_scales")
+
+
+def moe_fp4_linear(x, w, bias, out, ws, stream=None):
+    """out [T, N] = x w^T + bias; x [T, K] and w [N, K] from fp4(), bias [N] of out's type or None."""
+    code = (_fast or _setup()).fp4_linear(x, w, bias, out, ws, stream)
+    if code:
+        raise MoeError(code, "moe_fp4_linear")

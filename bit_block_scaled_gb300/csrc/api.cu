@@ -399,6 +399,7 @@ const char *moe_status_string(int status) {
     case MOE_ERR_BAD_INDEX: return "MOE_ERR_BAD_INDEX";
     case MOE_ERR_WORKSPACE: return "MOE_ERR_WORKSPACE";
     case MOE_ERR_SCALE_RANGE: return "MOE_ERR_SCALE_RANGE";
+    case MOE_ERR_CAPACITY: return "MOE_ERR_CAPACITY";
     default: return "MOE_ERR_UNKNOWN";
   }
 }

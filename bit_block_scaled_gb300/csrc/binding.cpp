@@ -274,8 +274,71 @@ PyObject *attn_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
+// moe_fp4_t with where its memory is
+struct PlacedFp4 {
+  moe_fp4_t m;
+  int32_t place;
+};
+
+// x, out, stream
+PyObject *fp4_quantize(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return status(n, 3, [&]() -> int {
+    const Arg x(a[0]);
+    const PlacedFp4 *f = struct_of<PlacedFp4>(a[1]);
+    need(x && f && x.dim() == 2 && x.size(0) == f->m.rows && x.size(1) == f->m.K && (x.stride(1) == 1 || x.size(1) <= 1));
+    const Together on(x, {});
+    beside(f->place, x);
+    return moe_fp4_quantize(x.ptr(), type_code(x.type()), x.size(0) > 1 ? x.stride(0) : f->m.K, &f->m, stream_of(a[2], x));
+  });
+}
+
+// f, out, stream
+PyObject *fp4_dequantize(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return status(n, 3, [&]() -> int {
+    const PlacedFp4 *f = struct_of<PlacedFp4>(a[0]);
+    const Arg o(a[1]);
+    need(o && f && o.dim() == 2 && o.size(0) == f->m.rows && o.size(1) == f->m.K && (o.stride(1) == 1 || o.size(1) <= 1));
+    const Together on(o, {});
+    beside(f->place, o);
+    return moe_fp4_dequantize(&f->m, o.ptr(), type_code(o.type()), o.size(0) > 1 ? o.stride(0) : f->m.K, stream_of(a[2], o));
+  });
+}
+
+// plain, fmt, K, scales, stream
+PyObject *fp4_pack_scales(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return status(n, 5, [&]() -> int {
+    const Arg plain(a[0]), out(a[3]);
+    need(plain && out && plain.dim() == 2);
+    const int fmt = int_of(a[1]), K = int_of(a[2]);
+    const Together on(plain, {&out});
+    const int64_t rows = plain.size(0);
+    need(rows <= INT32_MAX && plain.size(1) == K / (fmt == MOE_FMT_NVFP4 ? 16 : 32) && plain.t->element_size() == 1 &&
+         plain.t->is_contiguous());
+    return moe_fp4_pack_scales(static_cast<uint8_t *>(plain.ptr()), fmt, (int)rows, K,
+                               static_cast<uint8_t *>(out.flat(at::kByte, moe_fp4_scale_bytes(fmt, (int)rows, K))),
+                               stream_of(a[4], plain));
+  });
+}
+
+// x, w, bias, out, ws, stream
+PyObject *fp4_linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return status(n, 6, [&]() -> int {
+    const PlacedFp4 *x = struct_of<PlacedFp4>(a[0]), *w = struct_of<PlacedFp4>(a[1]);
+    const Arg bias(a[2]), o(a[3]), ws(a[4]);
+    need(x && w && o && o.dim() == 2 && o.size(0) == x->m.rows && o.size(1) == w->m.rows && (o.stride(1) == 1 || o.size(1) <= 1));
+    workspace(ws);
+    const Together on(o, {&bias, &ws});
+    beside(x->place, o);
+    beside(w->place, o);
+    const int64_t N = w->m.rows;
+    return moe_fp4_linear(&x->m, &w->m, bias.flat(o.type(), N), o.ptr(), type_code(o.type()),
+                          o.size(0) > 1 ? o.stride(0) : (N + 7) / 8 * 8, ws.ptr(), stream_of(a[5], o));
+  });
+}
+
 #define FAST(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(route_grouped), FAST(residual_norm), FAST(kv_write), FAST(kv_read), FAST(attn_decode),
+                         FAST(fp4_quantize), FAST(fp4_dequantize), FAST(fp4_pack_scales), FAST(fp4_linear),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

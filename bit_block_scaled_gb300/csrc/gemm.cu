@@ -47,15 +47,11 @@
 //    memory.
 //  * GPTQ INT4: bf16_rne((q - z) * s), the exact product rounded once, built
 //    from bf16-pair FMAs (the fp16 scale split into two bf16 parts).
-#include <cudaTypedefs.h>
-
-#include <atomic>
-#include <mutex>
-
 #include "common.cuh"
 #include "device.cuh"
 #include "dequant.cuh"
 #include "kernels.h"
+#include "tmap.cuh"
 
 namespace moe4 {
 
@@ -791,20 +787,6 @@ __global__ void __launch_bounds__(cta_threads(KPB), 1) grouped_gemm_kernel(const
 
 // --------------------------------------------------------------------- host
 namespace {
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  });
-  return fn;
-}
 
 constexpr uint32_t kMaxSmem = 227 * 1024;  // dynamic shared memory a CTA may opt into
 

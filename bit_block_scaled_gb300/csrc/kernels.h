@@ -100,6 +100,15 @@ moe_status_t launch_attn_decode(const void *q, int q_type, int64_t qsb, int64_t 
                                 int heads, float scale, int window, const float *sinks, void *out, int64_t osb,
                                 int64_t osh, float *lse, void *ws, cudaStream_t stream, int *launches);
 
+moe_status_t launch_fp4_quantize(const void *x, int type, int64_t ld, const moe_fp4_t &out, cudaStream_t stream,
+                                 int *launches);
+moe_status_t launch_fp4_dequantize(const moe_fp4_t &f, void *out, int type, int64_t ld, cudaStream_t stream,
+                                   int *launches);
+moe_status_t launch_fp4_pack_scales(const uint8_t *plain, int fmt, int rows, int K, uint8_t *out, cudaStream_t stream,
+                                    int *launches);
+moe_status_t launch_fp4_linear(const moe_fp4_t &x, const moe_fp4_t &w, const void *bias, void *out, int type, int64_t ldo,
+                               unsigned int *status, cudaStream_t stream, int *launches);
+
 moe_status_t launch_unpermute(const uint16_t *y, const int32_t *row_pos, int T, int k, int H, int P_max,
                               uint16_t *out, unsigned int *status, cudaStream_t stream, int *launches);
 

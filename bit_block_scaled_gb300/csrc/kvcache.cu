@@ -14,14 +14,13 @@
 // for m / 6 and the ties of E4M3. So the codes are those of real arithmetic.
 #include "common.cuh"
 #include "kernels.h"
-#include "kvcache.cuh"
+#include "kvput.cuh"
 #include "types.cuh"
 
 namespace moe4 {
 
 namespace {
 
-constexpr unsigned kAll = 0xffffffffu;
 constexpr int kThreads = 128;
 
 struct KvArgs {
@@ -34,132 +33,6 @@ struct KvArgs {
   uint32_t rows;  // T * heads
   int type, heads, D, log_n, page, pages;
 };
-
-// 2^e for e in -127..127, exactly (2^-127 is a subnormal).
-__device__ __forceinline__ float pow2(int e) { return __uint_as_float(e == -127 ? 0x00400000u : (uint32_t)(e + 127) << 23); }
-
-// Least e in -127..127 with amax * 2^-e <= top, 2^x > top >= 2^(x - 1); amax
-// below fp32's normal range gives -127, as 0 does.
-__device__ __forceinline__ int row_exponent(float amax, float top, int x) {
-  const uint32_t a = __float_as_uint(amax);
-  const int over = (a & 0x7fffffu) > (__float_as_uint(top) & 0x7fffffu) ? 1 : 0;
-  return max((int)(a >> 23) - 126 - x + over, -127);
-}
-
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
-      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
-      : "=r"(r)
-      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
-  return r;
-}
-
-__device__ __forceinline__ float2 e4m3x2_f32(uint32_t b) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)b));
-  return __half22float2(*reinterpret_cast<const __half2 *>(&h));
-}
-
-__device__ __forceinline__ void e2m1x8_f32(uint32_t w, float (&v)[8]) {
-  uint32_t h[4];
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(w));
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
-  }
-}
-
-// Largest magnitude of a lane's 8 values, as the bits of that type: they order
-// as the magnitudes do, with infinities and NaN above all numbers.
-template <int TYPE>
-__device__ __forceinline__ uint32_t abs_max(const Raw8 &r) {
-  const uint32_t a[4] = {r.a.x, r.a.y, r.a.z, r.a.w}, b[4] = {r.b.x, r.b.y, r.b.z, r.b.w};
-  if (TYPE == MOE_FP32) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = max(m, max(a[i] & 0x7fffffffu, b[i] & 0x7fffffffu));
-    return m;
-  }
-  const uint32_t m = __vmaxu2(__vmaxu2(a[0] & 0x7fff7fffu, a[1] & 0x7fff7fffu),
-                              __vmaxu2(a[2] & 0x7fff7fffu, a[3] & 0x7fff7fffu));
-  return max(m & 0xffffu, m >> 16);
-}
-template <int TYPE>
-__device__ __forceinline__ float from_bits(uint32_t b) {
-  if (TYPE == MOE_FP32) return __uint_as_float(b);
-  if (TYPE == MOE_BF16) return __uint_as_float(b << 16);
-  return __half2float(__ushort_as_half((unsigned short)b));
-}
-
-// Quantises a lane's 8 values of a row and stores its codes (and the scales
-// that fall to this lane). rec: the record; i: token in it; part: 0 keys, 1
-// values; j: lane of the row; n: lanes of the row.
-template <int FMT, int TYPE>
-__device__ __forceinline__ void put8(uint8_t *rec, int i, int part, int j, int n, int D, const Raw8 &raw, bool live) {
-  const int row = kv_row(FMT, D);
-  uint8_t *codes = rec + part * 16 * row;
-  float x[8];
-  if (FMT == MOE_KV_BF16 || FMT == MOE_KV_FP16) {
-    constexpr int kTo = FMT == MOE_KV_BF16 ? MOE_BF16 : MOE_FP16;
-    Raw8 r = raw;
-    if (TYPE != kTo) {
-      raw8_to_f32(raw, TYPE, x);
-      r = f32_to_raw8(x, kTo);
-    }
-    if (live) *reinterpret_cast<uint4 *>(codes + kv_place(row, i, 16 * j)) = r.a;
-    return;
-  }
-  const uint32_t own = abs_max<TYPE>(raw);
-  uint32_t top = own;
-  for (int o = 1; o < n; o <<= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
-  constexpr uint32_t kInf = TYPE == MOE_FP32 ? 0x7f800000u : TYPE == MOE_BF16 ? 0x7f80u : 0x7c00u;
-  const bool bad = top >= kInf;
-  const int e = FMT == MOE_KV_FP8 ? row_exponent(from_bits<TYPE>(top), 448.f, 9) : row_exponent(from_bits<TYPE>(top), 2688.f, 12);
-  const float up = pow2(-e);  // e is at most 119 for finite values; a bad row's codes are not used
-  raw8_to_f32(raw, TYPE, x);
-#pragma unroll
-  for (int q = 0; q < 8; ++q) x[q] *= up;
-  if (FMT == MOE_KV_FP8) {
-    uint2 c;
-    c.x = e4m3x2(x[0], x[1]) | (e4m3x2(x[2], x[3]) << 16);
-    c.y = e4m3x2(x[4], x[5]) | (e4m3x2(x[6], x[7]) << 16);
-    if (bad) c = make_uint2(0, 0);
-    if (live) *reinterpret_cast<uint2 *>(codes + kv_place(row, i, 8 * j)) = c;
-  } else {
-    // two lanes hold a block of 16
-    const float m = from_bits<TYPE>(max(own, __shfl_xor_sync(kAll, own, 1))) * up;
-    const uint32_t sb = bad ? 0u : e4m3x2(m / 6.0f, 0.f) & 0xFFu;
-    const float s = e4m3x2_f32(sb).x;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) x[q] = s > 0.f ? x[q] / s : 0.f;
-    const uint32_t c = e2m1x8(x);
-    if (live) {
-      *reinterpret_cast<uint32_t *>(codes + kv_place(row, i, 4 * j)) = c;
-      if ((j & 1) == 0) rec[kv_scales_at(FMT, D) + part * D + (j >> 1) * 16 + i] = (uint8_t)sb;
-    }
-  }
-  if (live && j == 0) rec[kv_exps_at(FMT, D) + part * 16 + i] = (uint8_t)(bad ? 255 : e + 127);
-}
 
 // A lane's 8 values of a row as they are stored.
 template <int FMT>

@@ -65,7 +65,8 @@ typedef enum {
   MOE_ERR_TIMEOUT = 4,     /* device: a bounded wait inside a kernel ran out */
   MOE_ERR_BAD_INDEX = 5,   /* device: an expert id or row index out of range */
   MOE_ERR_WORKSPACE = 6,   /* ws_bytes smaller than moe_workspace_size      */
-  MOE_ERR_SCALE_RANGE = 7  /* device: an MXFP4 exponent above 2^1 (e8m0>128) */
+  MOE_ERR_SCALE_RANGE = 7, /* device: an MXFP4 exponent above 2^1 (e8m0>128) */
+  MOE_ERR_CAPACITY = 8     /* device: too few free pages, table columns or rows */
 } moe_status_t;
 
 /* Weight formats [MARLIN "Minimal repro"; GPTQ "1. Quantize"; EP]. */
@@ -513,6 +514,59 @@ moe_status_t moe_attn_decode(const void *q, int q_type, int64_t q_stride_b,
                              const float *sinks, void *out, int64_t out_stride_b,
                              int64_t out_stride_h, float *lse, void *ws,
                              size_t ws_bytes, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Dense projections in 4 bits: rows of values quantised to NVFP4 or MXFP4, and
+ * the product of two such operands, out = x w^T, on the block-scaled tensor
+ * cores. They follow the conventions of the calls around the layer.
+ * ------------------------------------------------------------------------- */
+
+/* A matrix [rows][K] in 4 bits. value = E2M1 code * block scale * row scale.
+ *   MOE_FMT_NVFP4: E4M3 block scale for 16 values, row scales fp32;
+ *   MOE_FMT_MXFP4: E8M0 block scale (2^(byte - 127), 255 = NaN) for 32 values,
+ *                  no row scales.
+ * q as in moe_qweight_t. scales in tiles of 128 rows by 4 blocks, 512 bytes
+ * each, all tiles of the first 128 rows first: the byte of (row, block) is at
+ *   ((row / 128) * ceil(blocks / 4) + block / 4) * 512 + (row % 32) * 16 +
+ *   (row % 128 / 32) * 4 + block % 4
+ * Scales of blocks past K / 16 (K / 32) in a row's last tile must be 0; those of
+ * rows past the last do not matter. */
+typedef struct {
+  int32_t fmt;              /* MOE_FMT_NVFP4 or MOE_FMT_MXFP4                        */
+  int32_t rows, K;          /* K a multiple of 32, at most 2^20; rows < 2^24         */
+  int32_t row_scale_stride; /* 1: a scale for each row, 0: row_scale[0] for all      */
+  uint8_t *q;               /* [rows][K / 2]                                         */
+  uint8_t *scales;          /* moe_fp4_scale_bytes(fmt, rows, K) bytes               */
+  float *row_scale;         /* NVFP4 only: fp32, or NULL = 1 (4-byte aligned)        */
+} moe_fp4_t;
+
+/* Bytes of the tiled scales; 0 for a format or sizes that are not built. Host only. */
+int64_t moe_fp4_scale_bytes(int fmt, int rows, int K);
+
+/* Quantises x [out->rows][K] (of `type`, rows x_stride apart, a multiple of 8)
+ * into q, scales and row_scale (NVFP4: required, with stride 1) of `out`. NVFP4:
+ * row scale r the least power of two (exponent -127..127) with amax / r <= 6 *
+ * 448, block scales E4M3(amax16 / r / 6), codes E2M1(x / r / s), 0 where s is 0.
+ * MXFP4: block scale s the least power of two with amax32 / s <= 6, codes
+ * E2M1(x / s). Roundings are to nearest, ties to even, of the exact quotients. A
+ * NaN or an infinity makes its row (NVFP4: row scale NaN) or its block (MXFP4:
+ * scale 255) NaN, with zero codes. K <= 32768. */
+moe_status_t moe_fp4_quantize(const void *x, int type, int64_t x_stride, const moe_fp4_t *out, moe_stream_t stream);
+
+/* The values of f as `type`, rows out_stride (a multiple of 8, at least K) apart. */
+moe_status_t moe_fp4_dequantize(const moe_fp4_t *f, void *out, int type, int64_t out_stride, moe_stream_t stream);
+
+/* Tiles the block scales of a checkpoint, [rows][K / 16] or [rows][K / 32] bytes
+ * (any alignment), into `scales`. For load time. */
+moe_status_t moe_fp4_pack_scales(const uint8_t *plain, int fmt, int rows, int K, uint8_t *scales, moe_stream_t stream);
+
+/* out[t][n] = sum_k x[t][k] w[n][k] + bias[n], fp32 sums, rounded once to `type`
+ * (as bias [N], or NULL, is): x [T][K], w [N][K] of one format and K, out [T][N]
+ * with rows ldo >= N apart. One token (T = 1) and any N are fine; ldo a multiple
+ * of 8 (4 in fp32) is fastest. Out must not overlap the operands. ws: >= MOE_STATUS_BYTES (status word).
+ * Deterministic: repeated calls give bit-identical outputs. */
+moe_status_t moe_fp4_linear(const moe_fp4_t *x, const moe_fp4_t *w, const void *bias, void *out, int type, int64_t ldo,
+                            void *ws, moe_stream_t stream);
 
 #ifdef __cplusplus
 }
