@@ -35,7 +35,8 @@ struct LinArgs {
   void *out;
   unsigned int *status;
   int64_t ldo;
-  int T, N, K, xr_stride, wr_stride, type, split, stages, tiles_t, tiles_n, bulk_out;
+  int T, N, K, xr_stride, wr_stride, type, split, stages, tiles_t, tiles_n;
+  int bulk_n;  // columns of out that are stored by TMA
 };
 
 // 512-byte tiles of scales a stage and block of 128 rows, K values a tile.
@@ -342,6 +343,254 @@ moe_status_t launch_narrow(LinArgs &a, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+// --------------------------------------------------------------------- wide
+constexpr int kWideN = 192, kWideStages = 5, kVecs = 2;
+
+template <int FMT>
+struct Wide {
+  static constexpr int kA = 128 * 128, kB = kWideN / 2 * 128;  // this CTA's half of the pair's rows
+  static constexpr int kStage = kA + kB + 3 * Sf<FMT>::kBytes;
+  static constexpr int kStageAt = (kStage + 1023) / 1024 * 1024;
+  static constexpr int kStaging = 4 * 2 * 4096;  // two pieces of 32 rows x 128 bytes a warp
+  static constexpr int kSmem = 1024 + kWideStages * kStageAt + kStaging + 2 * kVecs * kWideN * 4;
+  static constexpr int kSfA = 2 * kWideN, kSfB = kSfA + Sf<FMT>::kTiles * 4;  // columns behind the accumulators
+};
+
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(x), "r"(y)
+               : "memory");
+}
+// Arrives on the barrier at this address in both CTAs of the pair once the MMAs issued so far are done.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_remote(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Tiles in groups of 8 along the tokens, so that the CTAs that run at once share rows and columns in L2.
+__device__ __forceinline__ void wide_tile(const LinArgs &p, int i, int &t0, int &n0) {
+  const int group = i / (8 * p.tiles_n), first = group * 8, in = i - group * 8 * p.tiles_n;
+  const int rows = min(8, p.tiles_t - first);
+  t0 = (first + in % rows) * 256;
+  n0 = in / rows * kWideN;
+}
+
+template <int FMT, int TYPE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant__ LinArgs p) {
+  using S = Wide<FMT>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  __shared__ __align__(8) uint64_t bars[2 * kWideStages + 4];
+  __shared__ uint32_t tmem_at;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const uint32_t bar0 = smem_u32(bars), ring = smem_u32(base);
+  auto full = [&](int s) { return bar0 + 8u * s; };  // of the first CTA: both CTAs' copies
+  auto empty = [&](int s) { return bar0 + 8u * (kWideStages + s); };
+  auto accfull = [&](int s) { return bar0 + 8u * (2 * kWideStages + s); };
+  auto accempty = [&](int s) { return bar0 + 8u * (2 * kWideStages + 2 + s); };  // of the first CTA
+  uint8_t *staging = base + kWideStages * S::kStageAt;
+  float *vecs = reinterpret_cast<float *>(staging + S::kStaging);  // [buffer][row scales, biases][kWideN]
+
+  if (tid == 0) {
+    for (int s = 0; s < kWideStages; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1);
+    for (int s = 0; s < 2; ++s) mbar_init(accfull(s), 1), mbar_init(accempty(s), 8);
+    fence_mbar_init();
+    prefetch_tmap(&p.tm_w);
+    prefetch_tmap(&p.tm_ws);
+    prefetch_tmap(&p.tm_x);
+    prefetch_tmap(&p.tm_xs);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_at)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = tmem_at;
+  pdl_trigger();
+  pdl_wait();
+
+  const int total = p.tiles_t * p.tiles_n, all = (p.K + kStageK - 1) / kStageK;
+  bool ok = true;
+  if (warp == 0) {
+    Ring r;
+    bool lapped = false;
+    for (int i = pair; i < total && ok; i += pairs) {
+      int t0, n0;
+      wide_tile(p, i, t0, n0);
+      for (int s = 0; s < all; ++s) {
+        if (lapped && !mbar_wait(empty(r.slot), r.phase ^ 1)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          const uint32_t a = ring + r.slot * S::kStageAt, b = a + S::kA, sa = b + S::kB, sb = sa + Sf<FMT>::kBytes;
+          const uint32_t bar = at_rank(full(r.slot), 0);
+          if (rank == 0) mbar_arrive_expect_tx(full(r.slot), 2 * S::kStage);
+          tma_load_pair(a, &p.tm_x, bar, s * 128, t0 + rank * 128);
+          tma_load_pair(b, &p.tm_w, bar, s * 128, n0 + rank * (kWideN / 2));
+          tma_load_pair(sa, &p.tm_xs, bar, s * (Sf<FMT>::kBytes / 8), t0 / 128 + rank);
+          tma_load_pair(sb, &p.tm_ws, bar, s * (Sf<FMT>::kBytes / 8), n0 / 128);
+          tma_load_pair(sb + Sf<FMT>::kBytes, &p.tm_ws, bar, s * (Sf<FMT>::kBytes / 8), n0 / 128 + 1);
+        }
+        __syncwarp();
+        r.advance(kWideStages);
+        lapped |= r.phase;
+      }
+    }
+    // where a wait ran out: the copies in flight land before the memory is given back
+    if (!ok && rank == 0)
+      for (int s = 0; s < kWideStages; ++s) mbar_wait(full(s), s < r.slot ? r.phase : r.phase ^ 1);
+  } else if (warp == 1) {
+    if (rank == 0) {
+      Ring r;
+      int n = 0;
+      for (int i = pair; i < total && ok; i += pairs, ++n) {
+        int t0, n0;
+        wide_tile(p, i, t0, n0);
+        const int acc = n & 1;
+        if (n >= 2) ok = mbar_wait(accempty(acc), ((n >> 1) - 1) & 1);
+        tc_fence_after();
+        for (int s = 0; s < all && ok; ++s) {
+          ok = mbar_wait(full(r.slot), r.phase);
+          if (ok && lane == 0) {
+            tc_fence_after();
+            const uint32_t a = ring + r.slot * S::kStageAt, b = a + S::kA, sa = b + S::kB, sb = sa + Sf<FMT>::kBytes;
+            stage_mmas<FMT, 2, 2>(tmem + acc * kWideN, 256, kWideN, a, b, sa, sb, tmem + S::kSfA, tmem + S::kSfB,
+                                  (n0 & 127) >> 5, (min(p.K - s * kStageK, kStageK) + 63) / 64, s == 0);
+            commit_pair(empty(r.slot));
+            if (s + 1 == all) commit_pair(accfull(acc));
+          }
+          __syncwarp();
+          r.advance(kWideStages);
+        }
+      }
+    }
+  } else {
+    const int q = warp & 3, e = tid - 64;
+    constexpr int kBytes = TYPE == MOE_FP32 ? 4 : 2, kCols = 128 / kBytes;  // a piece's columns
+    const uint32_t stage = smem_u32(staging) + (warp - 2) * 8192;
+    int n = 0, piece = 0;
+    for (int i = pair; i < total && ok; i += pairs, ++n) {
+      int t0, n0;
+      wide_tile(p, i, t0, n0);
+      const int acc = n & 1, t = t0 + rank * 128 + q * 32 + lane;
+      float *scales = vecs + acc * kVecs * kWideN, *biases = scales + kWideN;
+      for (int j = e; j < kWideN; j += kEpiThreads) {
+        const bool in = n0 + j < p.N;
+        scales[j] = in ? row_scale(p.wr, p.wr_stride, n0 + j) : 0.f;
+        biases[j] = in && p.bias ? load_as_f32(p.bias, n0 + j, TYPE) : 0.f;
+      }
+      const float xr = t < p.T ? row_scale(p.xr, p.xr_stride, t) : 0.f;
+      asm volatile("bar.sync 1, %0;" ::"r"(kEpiThreads) : "memory");
+      ok = mbar_wait(accfull(acc), (n >> 1) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t from = tmem + ((uint32_t)(q * 32) << 16) + acc * kWideN;
+      for (int c = 0; c < kWideN; c += kCols) {
+        const bool bulk = n0 + c < p.bulk_n;
+        if (bulk) {
+          // the piece before the last has left its half of the staging memory
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          __syncwarp();
+        }
+        const uint32_t to = stage + (piece & 1) * 4096 + lane * 128;
+#pragma unroll
+        for (int h = 0; h < kCols; h += 16) {
+          uint32_t v[16];
+          tmem_ld16(from + c + h, v);
+          tmem_ld_wait();
+          if (c + h + 16 == kWideN) {  // the accumulator is read
+            tc_fence_before();
+            if (lane == 0) arrive_remote(at_rank(accempty(acc), 0));
+          }
+          float f[16];
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            const float4 sc = *reinterpret_cast<const float4 *>(scales + c + h + j);
+            const float4 bi = *reinterpret_cast<const float4 *>(biases + c + h + j);
+            f[j] = fmaf(__uint_as_float(v[j]) * xr, sc.x, bi.x);
+            f[j + 1] = fmaf(__uint_as_float(v[j + 1]) * xr, sc.y, bi.y);
+            f[j + 2] = fmaf(__uint_as_float(v[j + 2]) * xr, sc.z, bi.z);
+            f[j + 3] = fmaf(__uint_as_float(v[j + 3]) * xr, sc.w, bi.w);
+          }
+          if (bulk) {
+            // 16-byte pieces in the order of the 128-byte swizzle
+#pragma unroll
+            for (int j = 0; j < 16; j += 8) {
+              const float (&g)[8] = *reinterpret_cast<const float (*)[8]>(f + j);
+              const Raw8 raw = f32_to_raw8(g, TYPE);
+              const int at = (h + j) * kBytes / 16;
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + ((at ^ (lane & 7)) << 4)), "r"(raw.a.x),
+                           "r"(raw.a.y), "r"(raw.a.z), "r"(raw.a.w)
+                           : "memory");
+              if (TYPE == MOE_FP32)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (((at + 1) ^ (lane & 7)) << 4)),
+                             "r"(raw.b.x), "r"(raw.b.y), "r"(raw.b.z), "r"(raw.b.w)
+                             : "memory");
+            }
+          }
+          if (n0 + c + h + 16 > p.bulk_n && t < p.T) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const int at = n0 + c + h + j;
+              if (at >= p.bulk_n && at < p.N) store_from_f32(p.out, t * p.ldo + at, TYPE, f[j]);
+            }
+          }
+        }
+        if (bulk) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (t < p.T) tma_store_2d(&p.tm_out, stage + (piece & 1) * 4096, n0 + c, t);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+          ++piece;
+        }
+      }
+    }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
+  }
+  if (!ok && lane == 0) raise_status(p.status, MOE_ERR_TIMEOUT);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+template <int FMT, int TYPE>
+moe_status_t launch_wide(const LinArgs &a, cudaStream_t stream) {
+  auto kern = wide_kernel<FMT, TYPE>;
+  static PerDevice configured;
+  const int set = configured.get([&] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Wide<FMT>::kSmem) == cudaSuccess ? 1 : 0;
+  });
+  if (set < 1) return MOE_ERR_CUDA;
+  const int64_t tiles = (int64_t)a.tiles_t * a.tiles_n, pairs = sm_count() / 2;
+  const dim3 grid((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
+  return launch_pdl(kern, grid, dim3(kThreads), Wide<FMT>::kSmem, stream, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
 // Codes: [rows][K / 2] bytes, boxes of 128 bytes of `box` rows.
 bool map_codes(CUtensorMap *m, const uint8_t *q, int rows, int K, int box) {
   const cuuint64_t dims[2] = {(cuuint64_t)(K / 2), (cuuint64_t)rows}, strides[1] = {(cuuint64_t)(K / 2)};
@@ -375,16 +624,42 @@ moe_status_t launch_fp4_linear(const moe_fp4_t &x, const moe_fp4_t &w, const voi
   a.N = w.rows;
   a.K = x.K;
   a.type = type;
-  const int tn = a.T <= 16 ? 16 : a.T <= 32 ? 32 : a.T <= 64 ? 64 : 128;
+  // TODO rule
+  const bool wide = a.T >= 512;
+  const int tn = wide ? 256 : a.T <= 16 ? 16 : a.T <= 32 ? 32 : a.T <= 64 ? 64 : 128;
+  const int wn = wide ? kWideN : 128;
   a.tiles_t = (a.T + tn - 1) / tn;
-  a.tiles_n = (a.N + 127) / 128;
+  a.tiles_n = (a.N + wn - 1) / wn;
+  if (!map_codes(&a.tm_x, x.q, a.T, a.K, wide ? 128 : tn) || !map_codes(&a.tm_w, w.q, a.N, a.K, wide ? kWideN / 2 : 128) ||
+      !map_scales(&a.tm_xs, x.scales, x.fmt, a.T, a.K) || !map_scales(&a.tm_ws, w.scales, w.fmt, a.N, a.K))
+    return MOE_ERR_CUDA;
+  if (wide) {
+    const int bytes = dtype_bytes(type);
+    // Rows on the 16-byte grid go out by TMA, as far as a row is a multiple of 16 bytes (a store that is cut off at the
+    // tensor's edge was seen to write up to the next such multiple); the rest goes value by value.
+    a.bulk_n = ldo * bytes % 16 == 0 ? a.N / (16 / bytes) * (16 / bytes) : 0;
+    if (a.bulk_n) {
+      const cuuint64_t dims[2] = {(cuuint64_t)a.bulk_n, (cuuint64_t)a.T}, strides[1] = {(cuuint64_t)ldo * bytes};
+      const cuuint32_t box[2] = {(cuuint32_t)(128 / bytes), 32};
+      const CUtensorMapDataType t = type == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                    : type == MOE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+      if (!encode_tiled(&a.tm_out, t, 2, out, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return MOE_ERR_CUDA;
+    }
+    if (launches) ++*launches;
+#define MOE4_WIDE(F)                                                       \
+  if (x.fmt == F) {                                                        \
+    if (type == MOE_BF16) return launch_wide<F, MOE_BF16>(a, stream);      \
+    if (type == MOE_FP16) return launch_wide<F, MOE_FP16>(a, stream);      \
+    return launch_wide<F, MOE_FP32>(a, stream);                            \
+  }
+    MOE4_WIDE(MOE_FMT_NVFP4)
+    MOE4_WIDE(MOE_FMT_MXFP4)
+#undef MOE4_WIDE
+  }
   const int64_t tiles = (int64_t)a.tiles_t * a.tiles_n;
   const int all = (a.K + kStageK - 1) / kStageK;
   a.split = 1;
   while (a.split < kMaxSplit && a.split < all && tiles * (a.split + 1) <= sm_count()) ++a.split;
-  if (!map_codes(&a.tm_x, x.q, a.T, a.K, tn) || !map_codes(&a.tm_w, w.q, a.N, a.K, 128) ||
-      !map_scales(&a.tm_xs, x.scales, x.fmt, a.T, a.K) || !map_scales(&a.tm_ws, w.scales, w.fmt, a.N, a.K))
-    return MOE_ERR_CUDA;
   if (launches) ++*launches;
 #define MOE4_NARROW(F)                                         \
   if (x.fmt == F) {                                            \

@@ -173,3 +173,17 @@ def test_linear(fmt, T, N, K):
 def test_linear_types(fmt, dtype, bias):
     check_linear(5, 200, 576, fmt, dtype, bias, ldo=203)
     check_linear(150, 72, 2880, fmt, dtype, bias, gscale=0.37 if fmt == "nvfp4" else None)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T,N,K", [(512, 192, 256), (513, 200, 96), (600, 1, 32), (1000, 1000, 544), (1111, 5120, 2880),
+                                   (4096, 3000, 1600), (700, 8200, 4096)])
+def test_linear_many_tokens(fmt, T, N, K):
+    check_linear(T, N, K, fmt, "bf16", True, seed=T)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("N,ldo", [(384, 384), (333, 333), (333, 400), (40, 41)])
+def test_linear_many_tokens_types(fmt, dtype, N, ldo):
+    check_linear(900, N, 608, fmt, dtype, True, ldo=ldo, gscale=0.0037 if fmt == "nvfp4" else None)
