@@ -90,26 +90,33 @@ __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint
 #undef MOE4_MMA
 }
 
-// The MMAs of one stage, issued by one thread: `steps` of 64 values of K. sfa
-// and sfb: tensor memory of the stage's scales, 4 and 4 * BLOCKS columns a tile.
+// The MMAs of one stage, issued by one thread: `steps` of 64 values of K. a, b, sa, sb: descriptors of the stage's
+// codes and scales; sfa and sfb: tensor memory of its scales, 4 and 4 * BLOCKS columns a tile.
 template <int FMT, int CG, int BLOCKS>
-__device__ __forceinline__ void stage_mmas(uint32_t d, int M, int N, uint32_t a, uint32_t b, uint32_t sa, uint32_t sb,
+__device__ __forceinline__ void stage_mmas(uint32_t d, int M, int N, uint64_t a, uint64_t b, uint64_t sa, uint64_t sb,
                                            uint32_t sfa, uint32_t sfb, uint32_t sfb_at, int steps, bool first) {
   constexpr int kSteps = FMT == MOE_FMT_NVFP4 ? 1 : 2;  // MMAs a tile of scales
-#pragma unroll
-  for (int t = 0; t < Sf<FMT>::kTiles; ++t) {
-    if (t * kSteps >= steps) break;
-    copy_scales<CG>(sfa + 4 * t, scale_desc(sa + t * kFp4Tile));
+  auto scales = [&](int t) {
+    copy_scales<CG>(sfa + 4 * t, sa + t * (kFp4Tile >> 4));
 #pragma unroll
     for (int j = 0; j < BLOCKS; ++j)
-      copy_scales<CG>(sfb + 4 * (BLOCKS * t + j), scale_desc(sb + j * Sf<FMT>::kBytes + t * kFp4Tile));
-  }
-#pragma unroll
-  for (int k = 0; k < kStageK / 64; ++k) {
-    if (k >= steps) break;
+      copy_scales<CG>(sfb + 4 * (BLOCKS * t + j), sb + (j * Sf<FMT>::kBytes + t * kFp4Tile) / 16);
+  };
+  auto multiply = [&](int k) {
     const int t = k / kSteps, id = (k % kSteps) * 2;
-    mma_fp4<FMT, CG>(d, smem_desc_sw128(a + 32 * k), smem_desc_sw128(b + 32 * k), idesc_fp4<FMT>(M, N, id), sfa + 4 * t,
-                     sfb + 4 * BLOCKS * t + sfb_at, !(first && k == 0));
+    mma_fp4<FMT, CG>(d, a + 2 * k, b + 2 * k, idesc_fp4<FMT>(M, N, id), sfa + 4 * t, sfb + 4 * BLOCKS * t + sfb_at,
+                     !(first && k == 0));
+  };
+  if (steps == kStageK / 64) {
+#pragma unroll
+    for (int t = 0; t < Sf<FMT>::kTiles; ++t) scales(t);
+#pragma unroll
+    for (int k = 0; k < kStageK / 64; ++k) multiply(k);
+  } else {
+#pragma unroll 1
+    for (int t = 0; t * kSteps < steps; ++t) scales(t);
+#pragma unroll 1
+    for (int k = 0; k < steps; ++k) multiply(k);
   }
 }
 
@@ -131,6 +138,13 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 __device__ __forceinline__ float row_scale(const float *r, int stride, int i) { return r ? r[(int64_t)i * stride] : 1.f; }
+
+// The whole warp waits, and agrees on the outcome. One lane is then elected to issue (elect.sync, not a comparison of
+// the lane: only then the compiler knows that one thread runs, and issues each tcgen05 instruction without a loop over
+// lanes; 4096 x 6144 x 8192 184 -> 89 us).
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
 
 // A ring slot and its parity.
 struct Ring {
@@ -198,11 +212,11 @@ __global__ void __launch_bounds__(kThreads) narrow_kernel(const __grid_constant_
   if (warp == 0) {
     Ring r;
     for (int s = s_begin; s < s_end; ++s) {
-      if (s - s_begin >= p.stages && !mbar_wait(empty(r.slot), r.phase ^ 1)) {
+      if (s - s_begin >= p.stages && !warp_wait(empty(r.slot), r.phase ^ 1)) {
         ok = false;
         break;
       }
-      if (lane == 0) {
+      if (elect_one()) {
         const uint32_t a = ring + r.slot * S::kStage, b = a + S::kA, sa = b + S::kB, sb = sa + Sf<FMT>::kBytes;
         mbar_arrive_expect_tx(full(r.slot), S::kStage);
         tma_load_2d(a, &p.tm_w, full(r.slot), s * 128, n0);
@@ -220,13 +234,13 @@ __global__ void __launch_bounds__(kThreads) narrow_kernel(const __grid_constant_
   } else if (warp == 1) {
     Ring r;
     for (int s = s_begin; s < s_end && ok; ++s) {
-      ok = mbar_wait(full(r.slot), r.phase);
-      if (ok && lane == 0) {
+      ok = warp_wait(full(r.slot), r.phase);
+      if (ok && elect_one()) {
         tc_fence_after();
         const uint32_t a = ring + r.slot * S::kStage, b = a + S::kA, sa = b + S::kB, sb = sa + Sf<FMT>::kBytes;
         const uint32_t sfa = tmem + TN + (s & 1) * S::kSfCols, sfb = sfa + Sf<FMT>::kTiles * 4;
-        stage_mmas<FMT, 1, S::kBlocks>(tmem, 128, TN, a, b, sa, sb, sfa, sfb, 0, (min(p.K - s * kStageK, kStageK) + 63) / 64,
-                                       s == s_begin);
+        stage_mmas<FMT, 1, S::kBlocks>(tmem, 128, TN, smem_desc_sw128(a), smem_desc_sw128(b), scale_desc(sa), scale_desc(sb),
+                                       sfa, sfb, 0, (min(p.K - s * kStageK, kStageK) + 63) / 64, s == s_begin);
         umma_commit(empty(r.slot));
         if (s + 1 == s_end) umma_commit(done);
       }
@@ -243,7 +257,7 @@ __global__ void __launch_bounds__(kThreads) narrow_kernel(const __grid_constant_
       scale = row_scale(p.wr, p.wr_stride, n);
       bias = p.bias ? load_as_f32(p.bias, n, p.type) : 0.f;
     }
-    ok = mbar_wait(done, 0);
+    ok = warp_wait(done, 0);
     tc_fence_after();
   }
   if (!ok && lane == 0) {
@@ -344,18 +358,29 @@ moe_status_t launch_narrow(LinArgs &a, cudaStream_t stream) {
 }
 
 // --------------------------------------------------------------------- wide
-constexpr int kWideN = 192, kWideStages = 5, kVecs = 2;
+constexpr int kWideN = 192, kWideStages = 5, kVecs = 2, kWideEpi = 8, kWideThreads = 64 + 32 * kWideEpi;
 
 template <int FMT>
 struct Wide {
   static constexpr int kA = 128 * 128, kB = kWideN / 2 * 128;  // this CTA's half of the pair's rows
   static constexpr int kStage = kA + kB + 3 * Sf<FMT>::kBytes;
   static constexpr int kStageAt = (kStage + 1023) / 1024 * 1024;
-  static constexpr int kStaging = 4 * 2 * 4096;  // two pieces of 32 rows x 128 bytes a warp
+  static constexpr int kStaging = 8 * 4096;  // a warp's pieces of 32 rows x 32 columns: two of 16 bits, one of 32
   static constexpr int kSmem = 1024 + kWideStages * kStageAt + kStaging + 2 * kVecs * kWideN * 4;
   static constexpr int kSfA = 2 * kWideN, kSfB = kSfA + Sf<FMT>::kTiles * 4;  // columns behind the accumulators
 };
 
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+        "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y) {
   asm volatile(
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
@@ -389,7 +414,7 @@ __device__ __forceinline__ void wide_tile(const LinArgs &p, int i, int &t0, int 
 }
 
 template <int FMT, int TYPE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wide_kernel(const __grid_constant__ LinArgs p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1) wide_kernel(const __grid_constant__ LinArgs p) {
   using S = Wide<FMT>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -407,7 +432,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wide_ke
 
   if (tid == 0) {
     for (int s = 0; s < kWideStages; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1);
-    for (int s = 0; s < 2; ++s) mbar_init(accfull(s), 1), mbar_init(accempty(s), 8);
+    for (int s = 0; s < 2; ++s) mbar_init(accfull(s), 1), mbar_init(accempty(s), 2 * kWideEpi);
     fence_mbar_init();
     prefetch_tmap(&p.tm_w);
     prefetch_tmap(&p.tm_ws);
@@ -435,11 +460,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wide_ke
       int t0, n0;
       wide_tile(p, i, t0, n0);
       for (int s = 0; s < all; ++s) {
-        if (lapped && !mbar_wait(empty(r.slot), r.phase ^ 1)) {
+        if (lapped && !warp_wait(empty(r.slot), r.phase ^ 1)) {
           ok = false;
           break;
         }
-        if (lane == 0) {
+        if (elect_one()) {
           const uint32_t a = ring + r.slot * S::kStageAt, b = a + S::kA, sa = b + S::kB, sb = sa + Sf<FMT>::kBytes;
           const uint32_t bar = at_rank(full(r.slot), 0);
           if (rank == 0) mbar_arrive_expect_tx(full(r.slot), 2 * S::kStage);
@@ -458,9 +483,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wide_ke
     if (!ok && rank == 0)
       for (int s = 0; s < kWideStages; ++s) mbar_wait(full(s), s < r.slot ? r.phase : r.phase ^ 1);
   } else if (warp == 1) {
-    if (rank == 0) {
+    if (rank == 0 && elect_one()) {
       Ring r;
       int n = 0;
+      const uint64_t a0 = smem_desc_sw128(ring), b0 = smem_desc_sw128(ring + S::kA), sa0 = scale_desc(ring + S::kA + S::kB),
+                     sb0 = scale_desc(ring + S::kA + S::kB + Sf<FMT>::kBytes);
       for (int i = pair; i < total && ok; i += pairs, ++n) {
         int t0, n0;
         wide_tile(p, i, t0, n0);
@@ -469,87 +496,93 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wide_ke
         tc_fence_after();
         for (int s = 0; s < all && ok; ++s) {
           ok = mbar_wait(full(r.slot), r.phase);
-          if (ok && lane == 0) {
+          if (ok) {
             tc_fence_after();
-            const uint32_t a = ring + r.slot * S::kStageAt, b = a + S::kA, sa = b + S::kB, sb = sa + Sf<FMT>::kBytes;
-            stage_mmas<FMT, 2, 2>(tmem + acc * kWideN, 256, kWideN, a, b, sa, sb, tmem + S::kSfA, tmem + S::kSfB,
-                                  (n0 & 127) >> 5, (min(p.K - s * kStageK, kStageK) + 63) / 64, s == 0);
+            const uint32_t at = r.slot * (S::kStageAt >> 4);
+            stage_mmas<FMT, 2, 2>(tmem + acc * kWideN, 256, kWideN, a0 + at, b0 + at, sa0 + at, sb0 + at, tmem + S::kSfA,
+                                  tmem + S::kSfB, (n0 & 127) >> 5, (min(p.K - s * kStageK, kStageK) + 63) / 64, s == 0);
             commit_pair(empty(r.slot));
             if (s + 1 == all) commit_pair(accfull(acc));
           }
-          __syncwarp();
           r.advance(kWideStages);
         }
       }
     }
+    ok = __all_sync(0xffffffffu, ok);
   } else {
-    const int q = warp & 3, e = tid - 64;
-    constexpr int kBytes = TYPE == MOE_FP32 ? 4 : 2, kCols = 128 / kBytes;  // a piece's columns
-    const uint32_t stage = smem_u32(staging) + (warp - 2) * 8192;
+    // warps 2..9: 32 rows of tensor memory and one half of the columns each, in pieces of 32 columns
+    constexpr int kBytes = TYPE == MOE_FP32 ? 4 : 2, kPiece = 32 * 32 * kBytes, kBufs = S::kStaging / (kWideEpi * kPiece);
+    const int q = warp & 3, e = tid - 64, half = (warp - 2) >> 2;
+    const uint32_t stage = smem_u32(staging) + (warp - 2) * (kBufs * kPiece);
     int n = 0, piece = 0;
-    for (int i = pair; i < total && ok; i += pairs, ++n) {
+    for (int i = pair; i < total; i += pairs, ++n) {
       int t0, n0;
       wide_tile(p, i, t0, n0);
-      const int acc = n & 1, t = t0 + rank * 128 + q * 32 + lane;
+      const int acc = n & 1, t = t0 + rank * 128 + q * 32 + lane, c0 = half * (kWideN / 2);
       float *scales = vecs + acc * kVecs * kWideN, *biases = scales + kWideN;
-      for (int j = e; j < kWideN; j += kEpiThreads) {
-        const bool in = n0 + j < p.N;
-        scales[j] = in ? row_scale(p.wr, p.wr_stride, n0 + j) : 0.f;
-        biases[j] = in && p.bias ? load_as_f32(p.bias, n0 + j, TYPE) : 0.f;
+      if (e < kWideN) {
+        const bool in = n0 + e < p.N;
+        scales[e] = in ? row_scale(p.wr, p.wr_stride, n0 + e) : 0.f;
+        biases[e] = in && p.bias ? load_as_f32(p.bias, n0 + e, TYPE) : 0.f;
       }
       const float xr = t < p.T ? row_scale(p.xr, p.xr_stride, t) : 0.f;
-      asm volatile("bar.sync 1, %0;" ::"r"(kEpiThreads) : "memory");
-      ok = mbar_wait(accfull(acc), (n >> 1) & 1);
+      asm volatile("bar.sync 1, %0;" ::"r"(kWideEpi * 32) : "memory");
+      ok = warp_wait(accfull(acc), (n >> 1) & 1);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t from = tmem + ((uint32_t)(q * 32) << 16) + acc * kWideN;
-      for (int c = 0; c < kWideN; c += kCols) {
-        const bool bulk = n0 + c < p.bulk_n;
-        if (bulk) {
-          // the piece before the last has left its half of the staging memory
-          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      const uint32_t from = tmem + ((uint32_t)(q * 32) << 16) + acc * kWideN + c0;
+      uint32_t v[2][32];
+      tmem_ld32(from, v[0]);
+#pragma unroll
+      for (int pc = 0; pc < 3; ++pc) {
+        const int c = c0 + 32 * pc, col = n0 + c;
+        tmem_ld_wait();
+        if (pc < 2) {
+          tmem_ld32(from + 32 * (pc + 1), v[(pc + 1) & 1]);
+        } else {  // the accumulator is read
+          tc_fence_before();
+          if (lane == 0) arrive_remote(at_rank(accempty(acc), 0));
+        }
+        const bool bulk = col < p.bulk_n;
+        const uint32_t buf = stage + piece % kBufs * kPiece;
+        if (bulk) {  // the piece that was there has been read
+          if (lane == 0) {
+            if (kBufs == 2)
+              asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            else
+              asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          }
           __syncwarp();
         }
-        const uint32_t to = stage + (piece & 1) * 4096 + lane * 128;
 #pragma unroll
-        for (int h = 0; h < kCols; h += 16) {
-          uint32_t v[16];
-          tmem_ld16(from + c + h, v);
-          tmem_ld_wait();
-          if (c + h + 16 == kWideN) {  // the accumulator is read
-            tc_fence_before();
-            if (lane == 0) arrive_remote(at_rank(accempty(acc), 0));
-          }
-          float f[16];
+        for (int h = 0; h < 32; h += 8) {
+          float f[8];
 #pragma unroll
-          for (int j = 0; j < 16; j += 4) {
+          for (int j = 0; j < 8; j += 4) {
             const float4 sc = *reinterpret_cast<const float4 *>(scales + c + h + j);
             const float4 bi = *reinterpret_cast<const float4 *>(biases + c + h + j);
-            f[j] = fmaf(__uint_as_float(v[j]) * xr, sc.x, bi.x);
-            f[j + 1] = fmaf(__uint_as_float(v[j + 1]) * xr, sc.y, bi.y);
-            f[j + 2] = fmaf(__uint_as_float(v[j + 2]) * xr, sc.z, bi.z);
-            f[j + 3] = fmaf(__uint_as_float(v[j + 3]) * xr, sc.w, bi.w);
+            f[j] = fmaf(__uint_as_float(v[pc & 1][h + j]) * xr, sc.x, bi.x);
+            f[j + 1] = fmaf(__uint_as_float(v[pc & 1][h + j + 1]) * xr, sc.y, bi.y);
+            f[j + 2] = fmaf(__uint_as_float(v[pc & 1][h + j + 2]) * xr, sc.z, bi.z);
+            f[j + 3] = fmaf(__uint_as_float(v[pc & 1][h + j + 3]) * xr, sc.w, bi.w);
           }
           if (bulk) {
-            // 16-byte pieces in the order of the 128-byte swizzle
-#pragma unroll
-            for (int j = 0; j < 16; j += 8) {
-              const float (&g)[8] = *reinterpret_cast<const float (*)[8]>(f + j);
-              const Raw8 raw = f32_to_raw8(g, TYPE);
-              const int at = (h + j) * kBytes / 16;
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + ((at ^ (lane & 7)) << 4)), "r"(raw.a.x),
-                           "r"(raw.a.y), "r"(raw.a.z), "r"(raw.a.w)
+            // rows of 64 or 128 bytes, 16-byte pieces in the order of that swizzle
+            const Raw8 raw = f32_to_raw8(f, TYPE);
+            const int at = h * kBytes / 16, x = kBytes == 2 ? (lane >> 1) & 3 : lane & 7;
+            const uint32_t to = buf + lane * (32 * kBytes);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + ((at ^ x) << 4)), "r"(raw.a.x), "r"(raw.a.y),
+                         "r"(raw.a.z), "r"(raw.a.w)
+                         : "memory");
+            if (TYPE == MOE_FP32)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (((at + 1) ^ x) << 4)), "r"(raw.b.x),
+                           "r"(raw.b.y), "r"(raw.b.z), "r"(raw.b.w)
                            : "memory");
-              if (TYPE == MOE_FP32)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (((at + 1) ^ (lane & 7)) << 4)),
-                             "r"(raw.b.x), "r"(raw.b.y), "r"(raw.b.z), "r"(raw.b.w)
-                             : "memory");
-            }
           }
-          if (n0 + c + h + 16 > p.bulk_n && t < p.T) {
+          if (col + h + 8 > p.bulk_n && t < p.T) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int at = n0 + c + h + j;
+            for (int j = 0; j < 8; ++j) {
+              const int at = col + h + j;
               if (at >= p.bulk_n && at < p.N) store_from_f32(p.out, t * p.ldo + at, TYPE, f[j]);
             }
           }
@@ -558,7 +591,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) wide_ke
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (t < p.T) tma_store_2d(&p.tm_out, stage + (piece & 1) * 4096, n0 + c, t);
+            if (t < p.T) tma_store_2d(&p.tm_out, buf, col, t);
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
           ++piece;
@@ -588,7 +621,7 @@ moe_status_t launch_wide(const LinArgs &a, cudaStream_t stream) {
   if (set < 1) return MOE_ERR_CUDA;
   const int64_t tiles = (int64_t)a.tiles_t * a.tiles_n, pairs = sm_count() / 2;
   const dim3 grid((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
-  return launch_pdl(kern, grid, dim3(kThreads), Wide<FMT>::kSmem, stream, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return launch_pdl(kern, grid, dim3(kWideThreads), Wide<FMT>::kSmem, stream, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 // Codes: [rows][K / 2] bytes, boxes of 128 bytes of `box` rows.
@@ -640,10 +673,11 @@ moe_status_t launch_fp4_linear(const moe_fp4_t &x, const moe_fp4_t &w, const voi
     a.bulk_n = ldo * bytes % 16 == 0 ? a.N / (16 / bytes) * (16 / bytes) : 0;
     if (a.bulk_n) {
       const cuuint64_t dims[2] = {(cuuint64_t)a.bulk_n, (cuuint64_t)a.T}, strides[1] = {(cuuint64_t)ldo * bytes};
-      const cuuint32_t box[2] = {(cuuint32_t)(128 / bytes), 32};
+      const cuuint32_t box[2] = {32, 32};
       const CUtensorMapDataType t = type == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                     : type == MOE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
-      if (!encode_tiled(&a.tm_out, t, 2, out, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return MOE_ERR_CUDA;
+      const CUtensorMapSwizzle swizzle = bytes == 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+      if (!encode_tiled(&a.tm_out, t, 2, out, dims, strides, box, swizzle)) return MOE_ERR_CUDA;
     }
     if (launches) ++*launches;
 #define MOE4_WIDE(F)                                                       \
