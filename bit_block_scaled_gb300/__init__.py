@@ -10,4 +10,6 @@ from ._lib import (ACT, FMT, LAYOUT, ROUTE, STATUS, Act, MoeError, QWeight, act,
                    GROUP_SCORE, KV_FMT, NORM, SCORE, STATUS_BYTES, KvCache, Norm, Router, kv_cache,
                    moe_attn_decode, moe_attn_workspace_size, moe_kv_read, moe_kv_record_bytes, moe_kv_write,
                    moe_residual_norm, moe_route_grouped, norm, router,
-                   Fp4, fp4, moe_fp4_dequantize, moe_fp4_linear, moe_fp4_pack_scales, moe_fp4_quantize, moe_fp4_scale_bytes)
+                   Fp4, fp4, moe_fp4_dequantize, moe_fp4_linear, moe_fp4_pack_scales, moe_fp4_quantize, moe_fp4_scale_bytes,
+                   ROPE_LAYOUT, ROPE_SCALING, Rope, RopeConfig, moe_batch_plan, moe_rope, moe_rope_kv_write, moe_rope_table,
+                   moe_rope_turns, rope)

@@ -21,6 +21,8 @@ LAYOUT = {"interleaved": 0, "concat": 1}
 SCORE = {"softmax": 0, "sigmoid": 1}
 GROUP_SCORE = {"max": 0, "top2": 1}
 NORM = {"rms": 0, "layer": 1}
+ROPE_LAYOUT = {"half": 0, "interleaved": 1}
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "llama3": 4}
 KV_FMT = {"bf16": 0, "fp16": 1, "fp8": 2, "nvfp4": 3}
 STATUS_BYTES = 256
 
@@ -32,7 +34,8 @@ EXPORTS = ("moe_padded_rows", "moe_workspace_size", "moe_route_topk", "moe_align
            "moe_import_gptq_int4", "moe_import_modelopt_global_scale", "moe_route_grouped",
            "moe_residual_norm", "moe_kv_record_bytes", "moe_kv_write", "moe_kv_read",
            "moe_attn_workspace_size", "moe_attn_decode", "moe_fp4_scale_bytes", "moe_fp4_quantize", "moe_fp4_dequantize",
-           "moe_fp4_pack_scales", "moe_fp4_linear")
+           "moe_fp4_pack_scales", "moe_fp4_linear", "moe_batch_plan", "moe_rope_table", "moe_rope_turns", "moe_rope",
+           "moe_rope_kv_write")
 
 
 class MoeError(RuntimeError):
@@ -67,6 +70,17 @@ class KvCache(ctypes.Structure):
     _fields_ = [("fmt", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("data", ctypes.c_void_p),
                 ("place", ctypes.c_int32)]  # behind moe_kv_cache_t, for the binding's check: where the data is (_place)
+
+
+class RopeConfig(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("scaling", ctypes.c_int32), ("original_len", ctypes.c_int32),
+                ("truncate", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double), ("amplitude", ctypes.c_double)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("amplitude", ctypes.c_float),
+                ("turns", ctypes.c_void_p), ("place", ctypes.c_int32)]  # behind moe_rope_t: where the table is (_place)
 
 
 class Fp4(ctypes.Structure):
@@ -113,6 +127,14 @@ _SIGS = {
     "moe_attn_workspace_size": (_i32, [_i32, _i32, _i32, ctypes.POINTER(_sz)]),
     "moe_attn_decode": (_i32, [_vp, _i32, _i64, _i64, ctypes.POINTER(KvCache), _vp, _i64, _i32, _vp, _i32, _i32,
                                ctypes.c_float, _i32, _vp, _vp, _i64, _i64, _vp, _vp, _sz, _vp]),
+    "moe_batch_plan": (_i32, [_vp, _vp, _i32, _i32, _i32, _vp, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp,
+                              _vp]),
+    "moe_rope_table": (_i32, [ctypes.POINTER(RopeConfig), _vp, _vp]),
+    "moe_rope_turns": (_i32, [_vp, _i32, _vp]),
+    "moe_rope": (_i32, [ctypes.POINTER(Rope), _vp, _i32, _i32, _vp, _i64, _i64, _i32, _vp, _i64, _i64, _vp, _i64, _i64, _i32,
+                        _vp, _i64, _i64, _i32, _vp]),
+    "moe_rope_kv_write": (_i32, [ctypes.POINTER(Rope), _vp, _vp, _i64, _i64, _i32, _vp, _i64, _i64, _vp, _i64, _i64, _vp,
+                                 _i64, _i64, _i32, _vp, _i32, ctypes.POINTER(KvCache), _vp, _vp]),
     "moe_fp4_scale_bytes": (_i64, [_i32, _i32, _i32]),
     "moe_fp4_quantize": (_i32, [_vp, _i32, _i64, ctypes.POINTER(Fp4), _vp]),
     "moe_fp4_dequantize": (_i32, [ctypes.POINTER(Fp4), _vp, _i32, _i64, _vp]),
@@ -454,6 +476,75 @@ def moe_attn_decode(q, cache, block_table, seq_lens, out, ws, scale=None, window
     code = (_fast or _setup()).attn_decode(q, cache, block_table, seq_lens, out, ws, scale, window, sinks, lse, stream)
     if code:
         raise MoeError(code, "moe_attn_decode")
+
+
+# ------------------------------------------------------------------------- before the attention: plan, rotary positions
+def moe_batch_plan(new_lens, seq_lens, block_table, free_pages, free_count, page_size, slots, seq_lens_out, free_count_out,
+                   ws, positions=None, seq_ids=None, offsets=None, stream=None):
+    """Pages, slots and positions of a batch's new tokens. new_lens, seq_lens int32 [B] (below 0: the sequence ends),
+    block_table int32 [B, pages], free_pages int32 [pages of the cache], free_count int32 [1]; out: slots, positions,
+    seq_ids int32 [T], seq_lens_out [B] and free_count_out [1] (may be the inputs), offsets [B + 1]. See the header."""
+    code = (_fast or _setup()).batch_plan(new_lens, seq_lens, block_table, free_pages, free_count, page_size, slots,
+                                          seq_lens_out, free_count_out, ws, positions, seq_ids, offsets, stream)
+    if code:
+        raise MoeError(code, "moe_batch_plan")
+
+
+def moe_rope_table(rot_dim, base=10000.0, scaling="none", factor=1.0, original_len=4096, truncate=True, low=1.0, high=None,
+                   amplitude=0.0):
+    """(frequencies as uint64 fractions of a turn, numpy [rot_dim / 2]; amplitude). high None: 32 for YaRN, else 4."""
+    import numpy as np
+    code = ROPE_SCALING[scaling] if isinstance(scaling, str) else int(scaling)
+    if high is None:
+        high = 32.0 if code == ROPE_SCALING["yarn"] else 4.0
+    turns, amp = np.zeros(max(int(rot_dim) // 2, 1), dtype=np.uint64), ctypes.c_float(0.0)
+    cfg = RopeConfig(int(rot_dim), code, int(original_len), int(bool(truncate)), float(base), float(factor), float(low),
+                     float(high), float(amplitude))
+    if rot_dim > 256:
+        _fail("moe_rope_table")
+    _check(load().moe_rope_table(ctypes.byref(cfg), _host_ptr(turns), ctypes.addressof(amp)), "moe_rope_table")
+    return turns, float(amp.value)
+
+
+def moe_rope_turns(frequencies):
+    """Frequencies in radians a position (numpy float64) as uint64 fractions of a turn."""
+    import numpy as np
+    f = np.ascontiguousarray(frequencies, dtype=np.float64).reshape(-1)
+    turns = np.zeros(f.size, dtype=np.uint64)
+    _check(load().moe_rope_turns(_host_ptr(f), f.size, _host_ptr(turns)), "moe_rope_turns")
+    return turns
+
+
+def rope(rot_dim, layout="half", base=10000.0, scaling="none", factor=1.0, original_len=4096, truncate=True, low=1.0,
+         high=None, amplitude=0.0, frequencies=None, device="cuda") -> Rope:
+    """Rotary positions with their table on a device. frequencies: rot_dim / 2 of the caller's, in radians a position, in
+    place of base and scaling. The struct keeps its table."""
+    import numpy as np
+    import torch
+    if frequencies is not None:
+        turns, amp = moe_rope_turns(frequencies), float(amplitude) or 1.0
+        if turns.size * 2 != rot_dim:
+            _fail("rope")
+    else:
+        turns, amp = moe_rope_table(rot_dim, base, scaling, factor, original_len, truncate, low, high, amplitude)
+    table = torch.from_numpy(turns.view(np.int64)).to(device)
+    r = Rope(int(rot_dim), ROPE_LAYOUT[layout] if isinstance(layout, str) else int(layout), amp, table.data_ptr(), _place(table))
+    r.table = table
+    return r
+
+
+def moe_rope(rope, positions, q, q_out, k=None, k_out=None, stream=None):
+    """q_out, k_out: q, k [T, heads, head_dim] rotated by positions (int32 [T]); an output may be its input."""
+    code = (_fast or _setup()).rope(rope, positions, q, q_out, k, k_out, stream)
+    if code:
+        raise MoeError(code, "moe_rope")
+
+
+def moe_rope_kv_write(rope, positions, q, q_out, k, v, slots, cache, ws, stream=None):
+    """moe_rope of q into q_out (both may be None) and moe_kv_write of the rotated k and of v, in one launch."""
+    code = (_fast or _setup()).rope_kv_write(rope, positions, q, q_out, k, v, slots, cache, ws, stream)
+    if code:
+        raise MoeError(code, "moe_rope_kv_write")
 
 
 # ------------------------------------------------------------------------------------ dense projections in 4 bits

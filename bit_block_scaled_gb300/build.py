@@ -21,7 +21,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe4.so")
 BINDING = os.path.join(HERE, "_binding.so")
 SOURCES = ["api.cu", "route.cu", "align.cu", "gemm.cu", "unpermute.cu", "static_ws.cu", "convert.cu",
-           "block_api.cu", "group_route.cu", "norm.cu", "kvcache.cu", "attn.cu", "fp4_api.cu", "fp4.cu", "linear.cu"]
+           "block_api.cu", "group_route.cu", "norm.cu", "kvcache.cu", "attn.cu", "fp4_api.cu", "fp4.cu", "linear.cu",
+           "rope_api.cu", "plan.cu", "rope.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xptxas", "-warn-spills"]

@@ -274,6 +274,85 @@ PyObject *attn_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
+// new_lens, seq_lens, block_table, free_pages, free_count, page_size, slots, seq_lens_out, free_count_out, ws, positions,
+// seq_ids, offsets, stream
+PyObject *batch_plan(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return status(n, 14, [&]() -> int {
+    const Arg grow(a[0]), lens(a[1]), table(a[2]), pages(a[3]), count(a[4]), slots(a[6]), lens_out(a[7]), count_out(a[8]),
+        ws(a[9]), positions(a[10]), seqs(a[11]), offsets(a[12]);
+    need(grow && lens && table && pages && count && slots && lens_out && count_out);
+    workspace(ws);
+    const Together on(lens, {&grow, &table, &pages, &count, &slots, &lens_out, &count_out, &ws, &positions, &seqs, &offsets});
+    const int64_t B = lens.t->numel(), T = slots.t->numel(), free = pages.t->numel();
+    need(table.dim() == 2 && table.type() == at::kInt && table.size(0) == B);
+    const int64_t cols = table.size(1);
+    need(B <= INT32_MAX && T <= INT32_MAX && free <= INT32_MAX && cols <= INT32_MAX && (table.stride(1) == 1 || cols <= 1));
+    auto ints = [](const Arg &x, int64_t size) { return static_cast<int32_t *>(x.flat(at::kInt, size)); };
+    return moe_batch_plan(ints(grow, B), ints(lens, B), (int)B, int_of(a[5]), (int)free, static_cast<int32_t *>(table.ptr()),
+                          B > 1 ? table.stride(0) : cols, (int)cols, ints(pages, free), ints(count, 1), ints(lens_out, B),
+                          ints(count_out, 1), ints(offsets, B + 1), (int)T, ints(slots, T), ints(positions, T), ints(seqs, T),
+                          ws.ptr(), stream_of(a[13], lens));
+  });
+}
+
+// moe_rope_t with where its table is
+struct PlacedRope {
+  moe_rope_t rope;
+  int32_t place;
+};
+
+// rope, positions, q, q_out, k, k_out, stream
+PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return status(n, 7, [&]() -> int {
+    const PlacedRope *r = struct_of<PlacedRope>(a[0]);
+    const Arg pos(a[1]), q(a[2]), qo(a[3]), k(a[4]), ko(a[5]);
+    need(r && pos && q && qo && (bool)k == (bool)ko && q.dim() == 3 && qo.type() == q.type());
+    const Together on(q, {&pos, &qo, &k, &ko});
+    beside(r->place, q);
+    const int64_t T = q.size(0), heads = q.size(1), D = q.size(2);
+    need(T <= INT32_MAX && heads <= INT32_MAX && D <= INT32_MAX);
+    const Rows3 qs(q, T, heads, D), os(qo, T, heads, D);
+    int64_t kheads = 0, s[4] = {0, 0, 0, 0};
+    if (k) {
+      need(k.dim() == 3 && k.type() == q.type() && ko.type() == q.type() && k.size(1) <= INT32_MAX);
+      kheads = k.size(1);
+      const Rows3 ks(k, T, kheads, D), kos(ko, T, kheads, D);
+      s[0] = ks.t, s[1] = ks.h, s[2] = kos.t, s[3] = kos.h;
+    }
+    return moe_rope(&r->rope, static_cast<int32_t *>(pos.flat(at::kInt, T)), (int)T, (int)D, q.ptr(), qs.t, qs.h, (int)heads,
+                    qo.ptr(), os.t, os.h, k.ptr(), s[0], s[1], (int)kheads, ko.ptr(), s[2], s[3], type_code(q.type()),
+                    stream_of(a[6], q));
+  });
+}
+
+// rope, positions, q, q_out, k, v, slots, cache, ws, stream
+PyObject *rope_kv_write(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return status(n, 10, [&]() -> int {
+    const PlacedRope *r = struct_of<PlacedRope>(a[0]);
+    const Arg pos(a[1]), q(a[2]), qo(a[3]), k(a[4]), v(a[5]), slots(a[6]), ws(a[8]);
+    const PlacedCache *pc = struct_of<PlacedCache>(a[7]);
+    need(r && pos && (bool)q == (bool)qo && k && v && slots && pc && k.type() == v.type());
+    workspace(ws);
+    const Together on(k, {&pos, &q, &qo, &v, &slots, &ws});
+    beside(pc->place, k);
+    beside(r->place, k);
+    const moe_kv_cache_t *c = &pc->cache;
+    const int64_t T = slots.t->numel(), D = c->head_dim;
+    need(T <= INT32_MAX);
+    const Rows3 ks(k, T, c->kv_heads, D), vs(v, T, c->kv_heads, D);
+    int64_t heads = 0, s[4] = {0, 0, 0, 0};
+    if (q) {
+      need(q.dim() == 3 && q.type() == k.type() && qo.type() == k.type() && q.size(1) <= INT32_MAX);
+      heads = q.size(1);
+      const Rows3 qs(q, T, heads, D), os(qo, T, heads, D);
+      s[0] = qs.t, s[1] = qs.h, s[2] = os.t, s[3] = os.h;
+    }
+    return moe_rope_kv_write(&r->rope, static_cast<int32_t *>(pos.flat(at::kInt, T)), q.ptr(), s[0], s[1], (int)heads, qo.ptr(),
+                             s[2], s[3], k.ptr(), ks.t, ks.h, v.ptr(), vs.t, vs.h, type_code(k.type()),
+                             static_cast<int32_t *>(slots.flat(at::kInt, T)), (int)T, c, ws.ptr(), stream_of(a[9], k));
+  });
+}
+
 // moe_fp4_t with where its memory is
 struct PlacedFp4 {
   moe_fp4_t m;
@@ -339,6 +418,7 @@ PyObject *fp4_linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
 #define FAST(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(route_grouped), FAST(residual_norm), FAST(kv_write), FAST(kv_read), FAST(attn_decode),
                          FAST(fp4_quantize), FAST(fp4_dequantize), FAST(fp4_pack_scales), FAST(fp4_linear),
+                         FAST(batch_plan), FAST(rope), FAST(rope_kv_write),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

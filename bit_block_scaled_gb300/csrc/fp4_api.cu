@@ -1,5 +1,6 @@
 // The C ABI of the dense projections in 4 bits: argument checks, all before
 // anything is launched.
+#include "checks.h"
 #include "common.cuh"
 #include "fp4.cuh"
 #include "kernels.h"
@@ -8,9 +9,6 @@
 using namespace moe4;
 
 namespace {
-
-inline bool aligned16(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-inline bool aligned4(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 bool valid_sizes(int fmt, int rows, int K) {
   return (fmt == MOE_FMT_NVFP4 || fmt == MOE_FMT_MXFP4) && rows >= 0 && rows < 1 << 24 && K >= 32 && K % 32 == 0 && K <= 1 << 20;
@@ -77,7 +75,7 @@ moe_status_t moe_fp4_linear(const moe_fp4_t *x, const moe_fp4_t *w, const void *
   if (x->fmt != w->fmt || x->K != w->K || !valid_dtype(type) || !aligned16(ws)) return MOE_ERR_INVALID_ARG;
   if (x->rows == 0 || w->rows == 0) return MOE_OK;
   if (!aligned16(out) || (bias && !aligned16(bias)) || ldo < 0 || (x->rows > 1 && ldo < w->rows)) return MOE_ERR_INVALID_ARG;
-  return launch_fp4_linear(*x, *w, bias, out, type, ldo, static_cast<unsigned int *>(ws), (cudaStream_t)stream, n);
+  return launch_fp4_linear(*x, *w, bias, out, type, ldo, status_of(ws), (cudaStream_t)stream, n);
 }
 
 }  // extern "C"

@@ -109,6 +109,22 @@ moe_status_t launch_fp4_pack_scales(const uint8_t *plain, int fmt, int rows, int
 moe_status_t launch_fp4_linear(const moe_fp4_t &x, const moe_fp4_t &w, const void *bias, void *out, int type, int64_t ldo,
                                unsigned int *status, cudaStream_t stream, int *launches);
 
+moe_status_t launch_batch_plan(const int32_t *new_lens, const int32_t *seq_lens, int B, int page, int num_pages,
+                               int32_t *table, int64_t ts, int max_pages, int32_t *free_pages, const int32_t *free_count,
+                               int32_t *lens_out, int32_t *count_out, int32_t *offsets, int T, int32_t *slots,
+                               int32_t *positions, int32_t *seq_ids, unsigned int *status, cudaStream_t stream,
+                               int *launches);
+
+// k_heads 0: q alone.
+moe_status_t launch_rope(const moe_rope_t &r, const int32_t *positions, int T, int D, const void *q, int64_t qst, int64_t qsh,
+                         int q_heads, void *qo, int64_t qost, int64_t qosh, const void *k, int64_t kst, int64_t ksh,
+                         int k_heads, void *ko, int64_t kost, int64_t kosh, int type, cudaStream_t stream, int *launches);
+// q NULL: keys and values alone.
+moe_status_t launch_rope_kv_write(const moe_rope_t &r, const int32_t *positions, int T, const void *q, int64_t qst,
+                                  int64_t qsh, int q_heads, void *qo, int64_t qost, int64_t qosh, const void *k, int64_t kst,
+                                  int64_t ksh, const void *v, int64_t vst, int64_t vsh, int type, const int32_t *slots,
+                                  const moe_kv_cache_t &c, unsigned int *status, cudaStream_t stream, int *launches);
+
 moe_status_t launch_unpermute(const uint16_t *y, const int32_t *row_pos, int T, int k, int H, int P_max,
                               uint16_t *out, unsigned int *status, cudaStream_t stream, int *launches);
 

@@ -516,6 +516,112 @@ moe_status_t moe_attn_decode(const void *q, int q_type, int64_t q_stride_b,
                              size_t ws_bytes, moe_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Before the attention of a step: which pages and slots its tokens get, and the
+ * rotation of queries and keys by their positions, alone or with the cache write.
+ * ------------------------------------------------------------------------- */
+
+/* The plan of a batch of B sequences, on the device and in one launch, so that it
+ * can be captured with the step that it is for. Sequence b has seq_lens[b] cached
+ * tokens in the pages that its row of block_table names (moe_attn_decode), and
+ * new_lens[b] tokens more to come; new_lens[b] < 0 ends it. free_pages [num_pages]
+ * is a stack of free pages with free_count[0] of them at its beginning.
+ *  1. An ended sequence's pages, ceil(seq_lens[b] / page_size) of them, are put
+ *     onto the stack in the order of b and of the pages; its length becomes 0. Its
+ *     row of block_table stays as it is.
+ *  2. Sequence b (new_lens[b] > 0) needs ceil((seq_lens[b] + new_lens[b]) /
+ *     page_size) - ceil(seq_lens[b] / page_size) pages. It is served if its row
+ *     has columns for them, they and those that the ones before it need are on the
+ *     stack (or it needs none), and its last token is among the T rows; all of it
+ *     or nothing. From the first that the stack does not cover on, only sequences that
+ *     need no page are served.
+ *  3. Pages come off the top of the stack in the order of b, into the columns
+ *     behind those in use.
+ * Out: seq_lens_out [B] (old plus new, 0 for an ended one, else unchanged) and
+ * free_count_out [1], which may be seq_lens and free_count; offsets [B + 1] (or
+ * NULL): where each sequence's rows begin, the sum of max(new_lens, 0) before it
+ * (served or not, at most 2^31 - 1). For row t < T, token i of sequence b: slots[t] (for moe_kv_write),
+ * positions[t] = seq_lens[b] + i, seq_ids[t] = b (either may be NULL); rows of a
+ * sequence that is not served have slot -1 and position 0, rows past the last token
+ * slot -1, position 0, sequence -1.
+ * Latched in ws: MOE_ERR_CAPACITY for a sequence that is not served; MOE_ERR_BAD_INDEX
+ * for a length below 0 or past the row (that sequence is left as it is), a
+ * free_count outside 0..num_pages (taken as the nearest), more pages than the stack
+ * holds (the rest is dropped), and a page number outside 0..num_pages - 1, whose tokens
+ * get slot -1 and which a row gets as -1.
+ * B <= 4096, T <= 2^28, page_size and num_pages as in moe_kv_cache_t, (max_pages + 1)
+ * * page_size < 2^31. Outputs other than these two must not overlap inputs. */
+moe_status_t moe_batch_plan(const int32_t *new_lens, const int32_t *seq_lens, int B, int page_size, int num_pages,
+                            int32_t *block_table, int64_t table_stride, int max_pages, int32_t *free_pages,
+                            const int32_t *free_count, int32_t *seq_lens_out, int32_t *free_count_out, int32_t *offsets,
+                            int T, int32_t *slots, int32_t *positions, int32_t *seq_ids, void *ws, moe_stream_t stream);
+
+/* Pairs of a head's first rot_dim columns: (i, i + rot_dim / 2), or (2i, 2i + 1). */
+typedef enum { MOE_ROPE_HALF = 0, MOE_ROPE_INTERLEAVED = 1 } moe_rope_layout_t;
+
+/* Frequencies f_i = base^(-2i / rot_dim), i < rot_dim / 2, and how they are
+ * stretched for contexts longer than the model was trained on:
+ *   LINEAR  f / factor
+ *   NTK     base * factor^(rot_dim / (rot_dim - 2)) for base
+ *   YARN    f / factor (1 - g) + f g with g = 1 - clamp((i - lo) / (hi - lo), 0, 1),
+ *           lo = rot_dim ln(original_len / (2 pi high)) / (2 ln base), hi the same
+ *           of low (high and low: turns over the original length, 32 and 1), both
+ *           rounded outwards if truncate, lo >= 0, hi <= rot_dim - 1; amplitude
+ *           0.1 ln(factor) + 1 for factors above 1
+ *   LLAMA3  the same blend with g = clamp((original_len f / (2 pi) - low) / (high -
+ *           low), 0, 1) (low 1, high 4); amplitude 1 */
+typedef enum {
+  MOE_ROPE_PLAIN = 0, MOE_ROPE_LINEAR = 1, MOE_ROPE_NTK = 2, MOE_ROPE_YARN = 3, MOE_ROPE_LLAMA3 = 4
+} moe_rope_scaling_t;
+
+typedef struct {
+  int32_t rot_dim;      /* even, 2..256                              */
+  int32_t scaling;      /* moe_rope_scaling_t                        */
+  int32_t original_len; /* YARN, LLAMA3                              */
+  int32_t truncate;     /* YARN                                      */
+  double base;          /* above 1                                   */
+  double factor;        /* above 0; PLAIN: ignored                   */
+  double low, high;     /* YARN, LLAMA3: 0 < low < high              */
+  double amplitude;     /* of cosine and sine; 0: the scaling's own  */
+} moe_rope_config_t;
+
+/* The frequencies as 64-bit fractions of a turn a position (f / (2 pi) 2^64
+ * modulo 2^64), turns [rot_dim / 2], and the amplitude. Host only. */
+moe_status_t moe_rope_table(const moe_rope_config_t *config, uint64_t *turns, float *amplitude);
+
+/* The same of n frequencies of the caller's, in radians a position. Host only. */
+moe_status_t moe_rope_turns(const double *frequencies, int n, uint64_t *turns);
+
+typedef struct {
+  int32_t rot_dim, layout; /* moe_rope_layout_t                                */
+  float amplitude;
+  const uint64_t *turns; /* device, [rot_dim / 2], 8-byte aligned              */
+} moe_rope_t;
+
+/* Rotates q [T][q_heads][head_dim] into q_out and k [T][k_heads][head_dim] into
+ * k_out (k_heads 0: q alone), all of `type`: a pair (a, b) of token t becomes
+ * amplitude * (a cos - b sin, b cos + a sin) of the angle positions[t] f_i. The angle
+ * is exact to 2^-34 turns at any position; negative positions rotate back. Columns
+ * from rot_dim on are copied. fp32 inside, rounded once. An output may be its own
+ * input (same strides); otherwise they must not overlap, and rows of an output that
+ * share elements are refused. Element strides over tokens and heads; any head_dim up to 256 and any strides;
+ * rot_dim and head_dim multiples of 16 with strides that are multiples of 8 and
+ * 16-byte aligned tensors are fastest. At most 4096 heads each. */
+moe_status_t moe_rope(const moe_rope_t *rope, const int32_t *positions, int T, int head_dim, const void *q, int64_t q_stride_t,
+                      int64_t q_stride_h, int q_heads, void *q_out, int64_t q_out_stride_t, int64_t q_out_stride_h,
+                      const void *k, int64_t k_stride_t, int64_t k_stride_h, int k_heads, void *k_out, int64_t k_out_stride_t,
+                      int64_t k_out_stride_h, int type, moe_stream_t stream);
+
+/* moe_rope of q (NULL: none) and moe_kv_write of the rotated keys and the values in
+ * one launch. The rotated keys are quantised as they are, in fp32, without being rounded
+ * to `type` first. Arguments as in these two calls; strides are multiples of 8,
+ * q_out may be q, and must not overlap k or v. Tokens with a slot below 0 have their query rotated. */
+moe_status_t moe_rope_kv_write(const moe_rope_t *rope, const int32_t *positions, const void *q, int64_t q_stride_t,
+                               int64_t q_stride_h, int q_heads, void *q_out, int64_t q_out_stride_t, int64_t q_out_stride_h,
+                               const void *k, int64_t k_stride_t, int64_t k_stride_h, const void *v, int64_t v_stride_t,
+                               int64_t v_stride_h, int type, const int32_t *slots, int T, const moe_kv_cache_t *cache,
+                               void *ws, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Dense projections in 4 bits: rows of values quantised to NVFP4 or MXFP4, and
  * the product of two such operands, out = x w^T, on the block-scaled tensor
  * cores. They follow the conventions of the calls around the layer.
