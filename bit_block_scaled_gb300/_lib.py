@@ -558,7 +558,7 @@ def moe_fp4_scale_bytes(fmt, rows, K):
 
 def fp4(q, scales, fmt, row_scale=None) -> Fp4:
     """A 4-bit matrix: q uint8 [rows, K / 2], scales uint8 [moe_fp4_scale_bytes(fmt, rows, K)] (tiled), row_scale fp32
-    [rows], or of one value for all rows, or None; the caller keeps the tensors alive while the struct is in use."""
+    [rows], or of one value for all rows, or None. The struct keeps its tensors."""
     import torch
     code = _fp4_format(fmt)
     if q.dim() != 2 or q.dtype != torch.uint8 or not q.is_contiguous():
@@ -573,8 +573,10 @@ def fp4(q, scales, fmt, row_scale=None) -> Fp4:
                 row_scale.numel() not in (1, rows)):
             _fail("fp4")
         stride = int(row_scale.numel() == rows)
-    return Fp4(code, rows, K, stride, q.data_ptr(), scales.data_ptr(), None if row_scale is None else row_scale.data_ptr(),
-               _place(q))
+    f = Fp4(code, rows, K, stride, q.data_ptr(), scales.data_ptr(), None if row_scale is None else row_scale.data_ptr(),
+            _place(q))
+    f.tensors = (q, scales, row_scale)
+    return f
 
 
 def moe_fp4_quantize(x, out, stream=None):

@@ -7,11 +7,18 @@
 // Two kernels:
 //  * narrow (few tokens): the weights are the 128 rows of the MMA, the tokens
 //    its columns. K is split over a cluster of CTAs whose partial sums are
-//    joined through distributed shared memory in the order of K.
-//  * wide (many tokens): pairs of CTAs (cta_group::2) share 256 tokens x 192
+//    joined through distributed shared memory in the order of K. Bound by
+//    latency for one token (4.0 us at 5120 x 2880), then by what an SM can take
+//    in, 64 bytes a cycle (333 x 2880 x 4096 7.4 us).
+//  * wide (many tokens): pairs of CTAs (cta_group::2) share 256 tokens x 256
 //    weight rows, persistent, two accumulators so that one tile is written
-//    while the next is summed.
+//    while the next is summed. A stage of 256 values of K is 38 KB an SM, 600
+//    cycles at 64 bytes, and its MMAs take 512 (16384 products a cycle): bound by
+//    the way into the SMs. 256 columns instead of 192, whose two accumulators
+//    need no sharing of columns, take 19% fewer bytes a product (16384 x 8192 x
+//    8192 347 -> 313 us, 7.0 PFLOP/s, 0.92 of four times the measured bf16 rate).
 #include <cudaTypedefs.h>
+#include <math.h>
 #include <string.h>
 
 #include "device.cuh"
@@ -35,8 +42,8 @@ struct LinArgs {
   void *out;
   unsigned int *status;
   int64_t ldo;
-  int T, N, K, xr_stride, wr_stride, type, split, stages, tiles_t, tiles_n;
-  int bulk_n;  // columns of out that are stored by TMA
+  int T, N, K, xr_stride, wr_stride, type, split, stages, parts_at, tiles_t, tiles_n;
+  int bulk_n;  // columns of out that bulk copies write
 };
 
 // 512-byte tiles of scales a stage and block of 128 rows, K values a tile.
@@ -91,10 +98,11 @@ __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint
 }
 
 // The MMAs of one stage, issued by one thread: `steps` of 64 values of K. a, b, sa, sb: descriptors of the stage's
-// codes and scales; sfa and sfb: tensor memory of its scales, 4 and 4 * BLOCKS columns a tile.
+// codes and scales; sfa and sfb: tensor memory of its scales, 4 and 4 * BLOCKS columns a tile;
+// sfb_shift: columns of 32 rows by which the tile begins within its first 128 rows of scales.
 template <int FMT, int CG, int BLOCKS>
 __device__ __forceinline__ void stage_mmas(uint32_t d, int M, int N, uint64_t a, uint64_t b, uint64_t sa, uint64_t sb,
-                                           uint32_t sfa, uint32_t sfb, uint32_t sfb_at, int steps, bool first) {
+                                           uint32_t sfa, uint32_t sfb, int steps, bool first, uint32_t sfb_shift = 0) {
   constexpr int kSteps = FMT == MOE_FMT_NVFP4 ? 1 : 2;  // MMAs a tile of scales
   auto scales = [&](int t) {
     copy_scales<CG>(sfa + 4 * t, sa + t * (kFp4Tile >> 4));
@@ -104,7 +112,7 @@ __device__ __forceinline__ void stage_mmas(uint32_t d, int M, int N, uint64_t a,
   };
   auto multiply = [&](int k) {
     const int t = k / kSteps, id = (k % kSteps) * 2;
-    mma_fp4<FMT, CG>(d, a + 2 * k, b + 2 * k, idesc_fp4<FMT>(M, N, id), sfa + 4 * t, sfb + 4 * BLOCKS * t + sfb_at,
+    mma_fp4<FMT, CG>(d, a + 2 * k, b + 2 * k, idesc_fp4<FMT>(M, N, id), sfa + 4 * t, sfb + 4 * BLOCKS * t + sfb_shift,
                      !(first && k == 0));
   };
   if (steps == kStageK / 64) {
@@ -124,14 +132,6 @@ __device__ __forceinline__ uint32_t at_rank(uint32_t addr, int rank) {
   uint32_t r;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
-}
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -161,9 +161,8 @@ template <int FMT, int TN>
 struct Narrow {
   static constexpr int kA = 128 * 128, kB = TN * 128, kBlocks = (TN + 127) / 128;
   static constexpr int kStage = kA + kB + Sf<FMT>::kBytes * (1 + kBlocks);
-  static constexpr int kJoin = TN * 128 * 4;  // partial sums, over the ring when it is drained
   static constexpr int kSfCols = Sf<FMT>::kTiles * 4 * (1 + kBlocks);
-  static constexpr int kUsed = TN + 2 * kSfCols;
+  static constexpr int kUsed = TN + kSfCols;
   static constexpr int kCols = kUsed <= 32 ? 32 : kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
 };
 
@@ -172,15 +171,14 @@ __global__ void __launch_bounds__(kThreads) narrow_kernel(const __grid_constant_
   using S = Narrow<FMT, TN>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 1];
+  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2];
   __shared__ uint32_t tmem_at;
-  __shared__ int failed;
-  __shared__ float xr_s[TN];
+  __shared__ float xr_s[TN + 8];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t bar0 = smem_u32(bars), ring = smem_u32(base);
   auto full = [&](int s) { return bar0 + 8u * s; };
   auto empty = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
-  const uint32_t done = bar0 + 8u * 2 * kMaxStages;
+  const uint32_t done = bar0 + 8u * 2 * kMaxStages, joined = done + 8;
   // cluster rank = part of K; tiles of weight rows, then of tokens
   const int rank = blockIdx.x % p.split, tile = blockIdx.x / p.split;
   const int n0 = tile % p.tiles_n * 128, t0 = tile / p.tiles_n * TN;
@@ -190,7 +188,7 @@ __global__ void __launch_bounds__(kThreads) narrow_kernel(const __grid_constant_
   if (tid == 0) {
     for (int s = 0; s < p.stages; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1);
     mbar_init(done, 1);
-    failed = 0;
+    mbar_init(joined, 1);
     fence_mbar_init();
     prefetch_tmap(&p.tm_w);
     prefetch_tmap(&p.tm_ws);
@@ -203,6 +201,7 @@ __global__ void __launch_bounds__(kThreads) narrow_kernel(const __grid_constant_
   }
   tc_fence_before();
   __syncthreads();
+  if (p.split > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   tc_fence_after();
   const uint32_t tmem = tmem_at;
   pdl_trigger();
@@ -210,13 +209,13 @@ __global__ void __launch_bounds__(kThreads) narrow_kernel(const __grid_constant_
 
   bool ok = true;
   if (warp == 0) {
-    Ring r;
-    for (int s = s_begin; s < s_end; ++s) {
-      if (s - s_begin >= p.stages && !warp_wait(empty(r.slot), r.phase ^ 1)) {
-        ok = false;
-        break;
-      }
-      if (elect_one()) {
+    if (elect_one()) {
+      Ring r;
+      for (int s = s_begin; s < s_end; ++s) {
+        if (s - s_begin >= p.stages && !mbar_wait(empty(r.slot), r.phase ^ 1)) {
+          ok = false;
+          break;
+        }
         const uint32_t a = ring + r.slot * S::kStage, b = a + S::kA, sa = b + S::kB, sb = sa + Sf<FMT>::kBytes;
         mbar_arrive_expect_tx(full(r.slot), S::kStage);
         tma_load_2d(a, &p.tm_w, full(r.slot), s * 128, n0);
@@ -224,99 +223,166 @@ __global__ void __launch_bounds__(kThreads) narrow_kernel(const __grid_constant_
         tma_load_2d(sa, &p.tm_ws, full(r.slot), s * (Sf<FMT>::kBytes / 8), n0 / 128);
         for (int j = 0; j < S::kBlocks; ++j)
           tma_load_2d(sb + j * Sf<FMT>::kBytes, &p.tm_xs, full(r.slot), s * (Sf<FMT>::kBytes / 8), t0 / 128 + j);
+        r.advance(p.stages);
       }
-      __syncwarp();
-      r.advance(p.stages);
+      // where a wait ran out: the copies in flight land before this CTA's memory is given back
+      if (!ok)
+        for (int s = 0; s < p.stages; ++s) mbar_wait(full(s), s < r.slot ? r.phase : r.phase ^ 1);
     }
-    // where a wait ran out: the copies in flight land before this CTA's memory is given back
-    if (!ok)
-      for (int s = 0; s < p.stages; ++s) mbar_wait(full(s), s < r.slot ? r.phase : r.phase ^ 1);
+    ok = __all_sync(0xffffffffu, ok);
   } else if (warp == 1) {
-    Ring r;
-    for (int s = s_begin; s < s_end && ok; ++s) {
-      ok = warp_wait(full(r.slot), r.phase);
-      if (ok && elect_one()) {
-        tc_fence_after();
-        const uint32_t a = ring + r.slot * S::kStage, b = a + S::kA, sa = b + S::kB, sb = sa + Sf<FMT>::kBytes;
-        const uint32_t sfa = tmem + TN + (s & 1) * S::kSfCols, sfb = sfa + Sf<FMT>::kTiles * 4;
-        stage_mmas<FMT, 1, S::kBlocks>(tmem, 128, TN, smem_desc_sw128(a), smem_desc_sw128(b), scale_desc(sa), scale_desc(sb),
-                                       sfa, sfb, 0, (min(p.K - s * kStageK, kStageK) + 63) / 64, s == s_begin);
-        umma_commit(empty(r.slot));
-        if (s + 1 == s_end) umma_commit(done);
+    if (elect_one()) {
+      Ring r;
+      const uint64_t a0 = smem_desc_sw128(ring), b0 = smem_desc_sw128(ring + S::kA), sa0 = scale_desc(ring + S::kA + S::kB),
+                     sb0 = scale_desc(ring + S::kA + S::kB + Sf<FMT>::kBytes);
+      for (int s = s_begin; s < s_end && ok; ++s) {
+        ok = mbar_wait(full(r.slot), r.phase);
+        if (ok) {
+          tc_fence_after();
+          const uint32_t at = r.slot * (S::kStage >> 4);
+          stage_mmas<FMT, 1, S::kBlocks>(tmem, 128, TN, a0 + at, b0 + at, sa0 + at, sb0 + at, tmem + TN,
+                                         tmem + TN + Sf<FMT>::kTiles * 4, (min(p.K - s * kStageK, kStageK) + 63) / 64,
+                                         s == s_begin, (t0 & 127) >> 5);
+          umma_commit(empty(r.slot));
+          if (s + 1 == s_end) umma_commit(done);
+        }
+        r.advance(p.stages);
       }
-      __syncwarp();
-      r.advance(p.stages);
     }
+    ok = __all_sync(0xffffffffu, ok);
   }
-  const int q = warp & 3, n = n0 + q * 32 + lane;  // the writing warps' rows of tensor memory
+  const int live = min(TN, p.T - t0);  // tokens of this tile
+  // the writing warps' rows of tensor memory are 32 weight rows
+  const int q = warp & 3, row = q * 32 + lane, n = n0 + row, e = tid - 64;
   float scale = 0.f, bias = 0.f;
   if (warp >= 2) {
-    const int e = tid - 64;
-    for (int i = e; i < TN; i += kEpiThreads) xr_s[i] = t0 + i < p.T ? row_scale(p.xr, p.xr_stride, t0 + i) : 0.f;
+    for (int i = e; i < live; i += kEpiThreads) xr_s[i] = row_scale(p.xr, p.xr_stride, t0 + i);
     if (n < p.N) {
       scale = row_scale(p.wr, p.wr_stride, n);
       bias = p.bias ? load_as_f32(p.bias, n, p.type) : 0.f;
     }
+    asm volatile("bar.sync 1, %0;" ::"r"(kEpiThreads) : "memory");  // xr_s
     ok = warp_wait(done, 0);
     tc_fence_after();
   }
-  if (!ok && lane == 0) {
-    raise_status(p.status, MOE_ERR_TIMEOUT);
-    failed = 1;
-  }
-  __syncthreads();
-  if (p.split == 1) {
-    if (warp >= 2 && !failed) {
-      for (int c = 0; c < TN && t0 + c < p.T; c += 16) {
-        uint32_t v[16];
-        tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + c, v);
-        tmem_ld_wait();
+  // The ring is empty once `done` is: it becomes this CTA's sums [TN][128] (where K is split), then the outputs [TN][128]
+  // as they are written, a token's 128 a bulk copy.
+  const uint32_t from = tmem + ((uint32_t)(q * 32) << 16);
+  const int bytes = dtype_bytes(p.type);
+  float *sums = reinterpret_cast<float *>(base);
+  uint8_t *tile_s = base + (p.split > 1 ? TN * 512 : 0);
+  int first = 0, count = live;  // the tokens that this CTA writes
+  // n sums of the tokens from c on into the outputs from i on; what lies past the tile's tokens is not copied out
+  auto put = [&](int i, int c, auto &v) {
+    constexpr int n_put = sizeof(v) / 4;
+    float f[n_put];
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (t0 + c + i < p.T && n < p.N)
-            store_from_f32(p.out, (t0 + c + i) * p.ldo + n, p.type, fmaf(__uint_as_float(v[i]) * xr_s[c + i], scale, bias));
+    for (int j = 0; j < n_put; ++j) f[j] = fmaf(v[j] * xr_s[c + j], scale, bias);
+    if (n < p.bulk_n) {
+      if (p.type == MOE_FP32) {
+#pragma unroll
+        for (int j = 0; j < n_put; ++j) reinterpret_cast<float *>(tile_s)[(i + j) * 128 + row] = f[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < n_put; ++j)
+          reinterpret_cast<uint16_t *>(tile_s)[(i + j) * 128 + row] =
+              p.type == MOE_BF16 ? float_to_bf16_bits(f[j]) : __half_as_ushort(__float2half_rn(f[j]));
       }
+    } else if (n < p.N) {
+      for (int j = 0; j < n_put; ++j)
+        if (i + j < count) store_from_f32(p.out, (t0 + c + j) * p.ldo + n, p.type, f[j]);
     }
-  } else {
-    float *join = reinterpret_cast<float *>(base);  // [TN][128]
-    if (warp >= 2) {
-      for (int c = 0; c < TN; c += 16) {
-        uint32_t v[16];
-        tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + c, v);
-        tmem_ld_wait();
+  };
+  if (p.split > 1) {
+    // rank d sums and writes the tokens from d * share on; the others' parts of them come to [rank][share][128] behind the ring
+    const int share = (live + p.split - 1) / p.split;
+    first = min(rank * share, live);
+    count = min(share, live - first);
+    float *parts = reinterpret_cast<float *>(base + p.parts_at);
+    // sums of up to 8 tokens from `i` on of those that this CTA writes, in the order of K
+    auto join = [&](auto part) {
+      for (int i = 0; i < count; i += 8) {
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int k = 0; k < p.split; ++k) {
+          const float *from_k = part(k) + i * 128 + row;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) join[(c + i) * 128 + q * 32 + lane] = __uint_as_float(v[i]);
-      }
-    }
-    cluster_sync();
-    if (!failed) {
-      // 4 weight rows of a token a thread, the tokens of this rank; sums in the order of K
-      const int c_begin = TN * rank / p.split, c_end = TN * (rank + 1) / p.split;
-      for (int i = c_begin * 32 + tid; i < c_end * 32; i += kThreads) {
-        const int c = i >> 5, m = (i & 31) * 4, t = t0 + c;
-        if (t >= p.T) break;
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        const uint32_t from = ring + (c * 128 + m) * 4;
-        float4 part[kMaxSplit];
-#pragma unroll
-        for (int k = 0; k < kMaxSplit; ++k)
-          if (k < p.split) part[k] = ld_cluster4(at_rank(from, k));
-#pragma unroll
-        for (int k = 0; k < kMaxSplit; ++k)
-          if (k < p.split) sum.x += part[k].x, sum.y += part[k].y, sum.z += part[k].z, sum.w += part[k].w;
-        const float v[4] = {sum.x, sum.y, sum.z, sum.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int nn = n0 + m + j;
-          if (nn < p.N) {
-            const float b = p.bias ? load_as_f32(p.bias, nn, p.type) : 0.f;
-            store_from_f32(p.out, t * p.ldo + nn, p.type, fmaf(v[j] * xr_s[c], row_scale(p.wr, p.wr_stride, nn), b));
-          }
+          for (int j = 0; j < 8; ++j) v[j] += from_k[j * 128];
         }
+        put(i, first + i, v);
+      }
+    };
+    if (TN == 16) {
+      // few values: each lane stores its own where they belong (one token of 5120 x 2880 3.4 us; by bulk copies 4.1)
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // all ranks run
+      if (warp >= 2) {
+        const uint32_t to = smem_u32(parts + rank * share * 128 + row);
+        uint32_t v[16];
+        tmem_ld16(from, v);
+        tmem_ld_wait();
+        int d = 0, i = 0;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (j < live) {
+            asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(at_rank(to + i * 512, d)), "r"(v[j]) : "memory");
+            if (++i == share) i = 0, ++d;
+          }
+      }
+      __syncwarp();
+      cluster_sync();
+      if (warp >= 2) join([&](int k) { return parts + k * share * 128; });
+    } else {
+      if (warp >= 2) {
+        for (int c = 0; c < live; c += 16) {
+          uint32_t v[16];
+          tmem_ld16(from + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) sums[(c + j) * 128 + row] = __uint_as_float(v[j]);
+        }
+        fence_proxy_async_smem();
+      }
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // all ranks' barriers are there
+      if (warp >= 2) {
+        asm volatile("bar.sync 1, %0;" ::"r"(kEpiThreads) : "memory");
+        if (e < p.split && e != rank) {
+          const int c0 = min(e * share, live), size = (min(c0 + share, live) - c0) * 512;
+          if (size)
+            asm volatile(
+                "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                    at_rank(smem_u32(parts + rank * share * 128), e)),
+                "r"(smem_u32(sums + c0 * 128)), "r"(size), "r"(at_rank(joined, e))
+                : "memory");
+        }
+        if (e == 0) mbar_arrive_expect_tx(joined, (p.split - 1) * count * 512);
+        ok &= warp_wait(joined, 0);
+        join([&](int k) { return k == rank ? sums + first * 128 : parts + k * share * 128; });
       }
     }
-    cluster_sync();  // the others may still be reading here
+  } else if (warp >= 2) {
+    for (int c = 0; c < live; c += 16) {
+      uint32_t u[16];
+      float v[16];
+      tmem_ld16(from + c, u);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(u[i]);
+      put(c, c, v);
+    }
   }
+  if (warp >= 2 && n0 < p.bulk_n) {
+    fence_proxy_async_smem();
+    asm volatile("bar.sync 1, %0;" ::"r"(kEpiThreads) : "memory");
+    const int size = min(128, p.bulk_n - n0) * bytes;
+    uint8_t *to = static_cast<uint8_t *>(p.out) + ((t0 + first) * p.ldo + n0) * bytes;
+    for (int i = e; i < count; i += kEpiThreads)
+      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to + i * p.ldo * bytes),
+                   "r"(smem_u32(tile_s + i * 128 * bytes)), "r"(size)
+                   : "memory");
+    asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+  }
+  __syncwarp();
+  if (p.split > 1 && TN > 16) cluster_sync();  // what was sent has arrived
+  if (!ok && lane == 0) raise_status(p.status, MOE_ERR_TIMEOUT);
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -336,11 +402,15 @@ moe_status_t launch_narrow(LinArgs &a, cudaStream_t stream) {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem) == cudaSuccess ? 1 : 0;
   });
   if (set < 1) return MOE_ERR_CUDA;
-  const int all = (a.K + kStageK - 1) / kStageK;
-  const int own = (all + a.split - 1) / a.split;
-  a.stages = own < 4 ? own : 4;
-  uint32_t smem = a.stages * S::kStage;
-  if (a.split > 1 && smem < S::kJoin) smem = S::kJoin;
+  const int all = (a.K + kStageK - 1) / kStageK, own = (all + a.split - 1) / a.split;
+  const int parts = a.split > 1 ? (a.split * ((TN + a.split - 1) / a.split) + 8) * 512 : 0;  // and 8 that are read in vain
+  // sums and outputs, over the ring, and 8 tokens that are written in vain
+  const int tail = (TN + 8) * 128 * dtype_bytes(a.type) + (a.split > 1 ? TN * 512 : 0);
+  a.stages = (int)(kMaxSmem - 1024 - parts) / S::kStage;
+  if (a.stages > own) a.stages = own;
+  if (a.stages > kMaxStages) a.stages = kMaxStages;
+  a.parts_at = a.stages * S::kStage > tail ? a.stages * S::kStage : tail;
+  const uint32_t smem = a.parts_at + parts;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.tiles_t * a.tiles_n * a.split));
   cfg.blockDim = dim3(kThreads);
@@ -358,16 +428,18 @@ moe_status_t launch_narrow(LinArgs &a, cudaStream_t stream) {
 }
 
 // --------------------------------------------------------------------- wide
-constexpr int kWideN = 192, kWideStages = 5, kVecs = 2, kWideEpi = 8, kWideThreads = 64 + 32 * kWideEpi;
+constexpr int kWideN = 256, kWideStages = 5, kWideEpi = 8, kWideThreads = 64 + 32 * kWideEpi;
+// The accumulators of two tiles and 48 columns of scales share 512 columns: the second begins 48 before the first ends. A
+// tile's MMAs begin when the writing warps have read what it has in common with the tile before, which they do first.
+constexpr int kAcc1 = 208, kWideSf = 464;
 
 template <int FMT>
 struct Wide {
   static constexpr int kA = 128 * 128, kB = kWideN / 2 * 128;  // this CTA's half of the pair's rows
   static constexpr int kStage = kA + kB + 3 * Sf<FMT>::kBytes;
-  static constexpr int kStageAt = (kStage + 1023) / 1024 * 1024;
-  static constexpr int kStaging = 8 * 4096;  // a warp's pieces of 32 rows x 32 columns: two of 16 bits, one of 32
-  static constexpr int kSmem = 1024 + kWideStages * kStageAt + kStaging + 2 * kVecs * kWideN * 4;
-  static constexpr int kSfA = 2 * kWideN, kSfB = kSfA + Sf<FMT>::kTiles * 4;  // columns behind the accumulators
+  static constexpr int kStaging = kWideEpi * 4096;  // 32 rows x 128 bytes a warp
+  static constexpr int kSmem = 1024 + kWideStages * kStage + kStaging + 2 * kWideN * 4;
+  static_assert(kStage % 1024 == 0 && kWideSf + 12 * Sf<FMT>::kTiles <= 512, "alignment of the swizzle, tensor memory");
 };
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
@@ -388,10 +460,13 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap *m
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
       : "memory");
 }
+// The outputs leave L2 first: the operands are read again (8192 x 5120 x 2880 53.7 -> 52.2 us).
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t src, int x, int y) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+  uint64_t policy;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group.L2::cache_hint [%0, {%2, %3}], [%1], %4;" ::"l"(
                    reinterpret_cast<uint64_t>(map)),
-               "r"(src), "r"(x), "r"(y)
+               "r"(src), "r"(x), "r"(y), "l"(policy)
                : "memory");
 }
 // Arrives on the barrier at this address in both CTAs of the pair once the MMAs issued so far are done.
@@ -418,7 +493,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1) wid
   using S = Wide<FMT>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  __shared__ __align__(8) uint64_t bars[2 * kWideStages + 4];
+  __shared__ __align__(8) uint64_t bars[2 * kWideStages + 3];
   __shared__ uint32_t tmem_at;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -426,13 +501,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1) wid
   auto full = [&](int s) { return bar0 + 8u * s; };  // of the first CTA: both CTAs' copies
   auto empty = [&](int s) { return bar0 + 8u * (kWideStages + s); };
   auto accfull = [&](int s) { return bar0 + 8u * (2 * kWideStages + s); };
-  auto accempty = [&](int s) { return bar0 + 8u * (2 * kWideStages + 2 + s); };  // of the first CTA
-  uint8_t *staging = base + kWideStages * S::kStageAt;
-  float *vecs = reinterpret_cast<float *>(staging + S::kStaging);  // [buffer][row scales, biases][kWideN]
+  const uint32_t shared_read = bar0 + 8u * (2 * kWideStages + 2);  // of the first CTA: once a tile, by both CTAs' writing warps
+  uint8_t *staging = base + kWideStages * S::kStage;
+  float *scales = reinterpret_cast<float *>(staging + S::kStaging), *biases = scales + kWideN;  // of the tile's columns
 
   if (tid == 0) {
     for (int s = 0; s < kWideStages; ++s) mbar_init(full(s), 1), mbar_init(empty(s), 1);
-    for (int s = 0; s < 2; ++s) mbar_init(accfull(s), 1), mbar_init(accempty(s), 2 * kWideEpi);
+    for (int s = 0; s < 2; ++s) mbar_init(accfull(s), 1);
+    mbar_init(shared_read, 2 * kWideEpi);
     fence_mbar_init();
     prefetch_tmap(&p.tm_w);
     prefetch_tmap(&p.tm_ws);
@@ -465,7 +541,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1) wid
           break;
         }
         if (elect_one()) {
-          const uint32_t a = ring + r.slot * S::kStageAt, b = a + S::kA, sa = b + S::kB, sb = sa + Sf<FMT>::kBytes;
+          const uint32_t a = ring + r.slot * S::kStage, b = a + S::kA, sa = b + S::kB, sb = sa + Sf<FMT>::kBytes;
           const uint32_t bar = at_rank(full(r.slot), 0);
           if (rank == 0) mbar_arrive_expect_tx(full(r.slot), 2 * S::kStage);
           tma_load_pair(a, &p.tm_x, bar, s * 128, t0 + rank * 128);
@@ -492,15 +568,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1) wid
         int t0, n0;
         wide_tile(p, i, t0, n0);
         const int acc = n & 1;
-        if (n >= 2) ok = mbar_wait(accempty(acc), ((n >> 1) - 1) & 1);
+        if (n >= 1) ok = mbar_wait(shared_read, (n - 1) & 1);
         tc_fence_after();
         for (int s = 0; s < all && ok; ++s) {
           ok = mbar_wait(full(r.slot), r.phase);
           if (ok) {
             tc_fence_after();
-            const uint32_t at = r.slot * (S::kStageAt >> 4);
-            stage_mmas<FMT, 2, 2>(tmem + acc * kWideN, 256, kWideN, a0 + at, b0 + at, sa0 + at, sb0 + at, tmem + S::kSfA,
-                                  tmem + S::kSfB, (n0 & 127) >> 5, (min(p.K - s * kStageK, kStageK) + 63) / 64, s == 0);
+            const uint32_t at = r.slot * (S::kStage >> 4);
+            stage_mmas<FMT, 2, 2>(tmem + acc * kAcc1, 256, kWideN, a0 + at, b0 + at, sa0 + at, sb0 + at, tmem + kWideSf,
+                                  tmem + kWideSf + 4 * Sf<FMT>::kTiles, (min(p.K - s * kStageK, kStageK) + 63) / 64, s == 0);
             commit_pair(empty(r.slot));
             if (s + 1 == all) commit_pair(accfull(acc));
           }
@@ -511,90 +587,98 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1) wid
     ok = __all_sync(0xffffffffu, ok);
   } else {
     // warps 2..9: 32 rows of tensor memory and one half of the columns each, in pieces of 32 columns
-    constexpr int kBytes = TYPE == MOE_FP32 ? 4 : 2, kPiece = 32 * 32 * kBytes, kBufs = S::kStaging / (kWideEpi * kPiece);
+    constexpr int kBytes = TYPE == MOE_FP32 ? 4 : 2, kCols = 128 / kBytes;  // columns of the staging memory
     const int q = warp & 3, e = tid - 64, half = (warp - 2) >> 2;
-    const uint32_t stage = smem_u32(staging) + (warp - 2) * (kBufs * kPiece);
-    int n = 0, piece = 0;
+    uint8_t *stage = staging + (warp - 2) * 4096;
+    int n = 0;
     for (int i = pair; i < total; i += pairs, ++n) {
       int t0, n0;
       wide_tile(p, i, t0, n0);
-      const int acc = n & 1, t = t0 + rank * 128 + q * 32 + lane, c0 = half * (kWideN / 2);
-      float *scales = vecs + acc * kVecs * kWideN, *biases = scales + kWideN;
-      if (e < kWideN) {
-        const bool in = n0 + e < p.N;
-        scales[e] = in ? row_scale(p.wr, p.wr_stride, n0 + e) : 0.f;
-        biases[e] = in && p.bias ? load_as_f32(p.bias, n0 + e, TYPE) : 0.f;
-      }
+      const int acc = n & 1, t = t0 + rank * 128 + q * 32 + lane;
+      static_assert(kWideEpi * 32 == kWideN, "a thread a column");
+      const bool in = n0 + e < p.N;
+      const float wr = in ? row_scale(p.wr, p.wr_stride, n0 + e) : 0.f, bi = in && p.bias ? load_as_f32(p.bias, n0 + e, TYPE) : 0.f;
+      if (n) asm volatile("bar.sync 1, %0;" ::"r"(kWideEpi * 32) : "memory");  // the tile before has used them
+      scales[e] = wr;
+      biases[e] = bi;
       const float xr = t < p.T ? row_scale(p.xr, p.xr_stride, t) : 0.f;
       asm volatile("bar.sync 1, %0;" ::"r"(kWideEpi * 32) : "memory");
       ok = warp_wait(accfull(acc), (n >> 1) & 1);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t from = tmem + ((uint32_t)(q * 32) << 16) + acc * kWideN + c0;
-      uint32_t v[2][32];
-      tmem_ld32(from, v[0]);
-#pragma unroll
-      for (int pc = 0; pc < 3; ++pc) {
-        const int c = c0 + 32 * pc, col = n0 + c;
+      // the columns that the next tile has, too, are the first's last 48 and the second's first: the last two pieces of
+      // the upper half, the first two of the lower
+      const uint32_t from = tmem + ((uint32_t)(q * 32) << 16) + acc * kAcc1 + half * 128;
+      const int turn = acc == 0 && half == 1 ? 2 : 0;
+#pragma unroll 1
+      for (int g = 0; g < 2; ++g) {  // two pieces at a time; the code is kept small, it is not in the instruction cache at first
+        const int pc = (2 * g + turn) & 3;
+        uint32_t v[2][32];
+        tmem_ld32(from + 32 * pc, v[0]);
+        tmem_ld32(from + 32 * pc + 32, v[1]);
         tmem_ld_wait();
-        if (pc < 2) {
-          tmem_ld32(from + 32 * (pc + 1), v[(pc + 1) & 1]);
-        } else {  // the accumulator is read
+        if (g == 0) {
           tc_fence_before();
-          if (lane == 0) arrive_remote(at_rank(accempty(acc), 0));
-        }
-        const bool bulk = col < p.bulk_n;
-        const uint32_t buf = stage + piece % kBufs * kPiece;
-        if (bulk) {  // the piece that was there has been read
-          if (lane == 0) {
-            if (kBufs == 2)
-              asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-            else
-              asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-          }
-          __syncwarp();
+          if (lane == 0) arrive_remote(at_rank(shared_read, 0));
         }
 #pragma unroll
-        for (int h = 0; h < 32; h += 8) {
-          float f[8];
+        for (int w = 0; w < 2; ++w) {
+          const int c = half * 128 + 32 * (pc + w);
+          float f[4][8];
 #pragma unroll
-          for (int j = 0; j < 8; j += 4) {
-            const float4 sc = *reinterpret_cast<const float4 *>(scales + c + h + j);
-            const float4 bi = *reinterpret_cast<const float4 *>(biases + c + h + j);
-            f[j] = fmaf(__uint_as_float(v[pc & 1][h + j]) * xr, sc.x, bi.x);
-            f[j + 1] = fmaf(__uint_as_float(v[pc & 1][h + j + 1]) * xr, sc.y, bi.y);
-            f[j + 2] = fmaf(__uint_as_float(v[pc & 1][h + j + 2]) * xr, sc.z, bi.z);
-            f[j + 3] = fmaf(__uint_as_float(v[pc & 1][h + j + 3]) * xr, sc.w, bi.w);
+          for (int j = 0; j < 32; j += 4) {
+            const float4 sc = *reinterpret_cast<const float4 *>(scales + c + j);
+            const float4 bs = *reinterpret_cast<const float4 *>(biases + c + j);
+            const uint32_t *u = &v[w][j];
+            float *x = &f[j >> 3][j & 7];
+            x[0] = fmaf(__uint_as_float(u[0]) * xr, sc.x, bs.x);
+            x[1] = fmaf(__uint_as_float(u[1]) * xr, sc.y, bs.y);
+            x[2] = fmaf(__uint_as_float(u[2]) * xr, sc.z, bs.z);
+            x[3] = fmaf(__uint_as_float(u[3]) * xr, sc.w, bs.w);
           }
-          if (bulk) {
-            // rows of 64 or 128 bytes, 16-byte pieces in the order of that swizzle
-            const Raw8 raw = f32_to_raw8(f, TYPE);
-            const int at = h * kBytes / 16, x = kBytes == 2 ? (lane >> 1) & 3 : lane & 7;
-            const uint32_t to = buf + lane * (32 * kBytes);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + ((at ^ x) << 4)), "r"(raw.a.x), "r"(raw.a.y),
-                         "r"(raw.a.z), "r"(raw.a.w)
-                         : "memory");
-            if (TYPE == MOE_FP32)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (((at + 1) ^ x) << 4)), "r"(raw.b.x),
-                           "r"(raw.b.y), "r"(raw.b.z), "r"(raw.b.w)
-                           : "memory");
+          // rows of 128 bytes in the staging memory, 16-byte pieces in the order of that swizzle: 64 columns of 16 bits (both
+          // pieces), 32 of fp32
+          constexpr bool kWhole = TYPE == MOE_FP32;
+          const int x = lane & 7, at0 = kWhole ? 0 : 4 * w;
+          uint8_t *to = stage + lane * 128;
+          if (kWhole || w == 0) {
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // what was there has been read
+            __syncwarp();
           }
-          if (col + h + 8 > p.bulk_n && t < p.T) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int at = col + h + j;
-              if (at >= p.bulk_n && at < p.N) store_from_f32(p.out, t * p.ldo + at, TYPE, f[j]);
+          for (int j = 0; j < 4; ++j) {
+            const Raw8 raw = f32_to_raw8(f[j], TYPE);
+            if (kWhole) {
+              *reinterpret_cast<uint4 *>(to + (((2 * j) ^ x) << 4)) = raw.a;
+              *reinterpret_cast<uint4 *>(to + (((2 * j + 1) ^ x) << 4)) = raw.b;
+            } else {
+              *reinterpret_cast<uint4 *>(to + (((at0 + j) ^ x) << 4)) = raw.a;
             }
           }
-        }
-        if (bulk) {
+          if (!kWhole && w == 0) continue;
+          const int col = n0 + (kWhole ? c : c - 32);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (t < p.T) tma_store_2d(&p.tm_out, buf, col, t);
+            if (col < p.bulk_n && t < p.T) tma_store_2d(&p.tm_out, smem_u32(stage), col, t);
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
-          ++piece;
+          if (col + kCols > p.bulk_n) {  // columns that no bulk copy writes: a row at a time
+            const int rows = min(32, p.T - (t - lane));
+#pragma unroll 1
+            for (int o = lane; o < kCols; o += 32)
+              if (col + o >= p.bulk_n && col + o < p.N)
+#pragma unroll 1
+                for (int r = 0; r < rows; ++r) {
+                  const uint8_t *from_s = stage + r * 128 + ((o * kBytes) ^ ((r & 7) << 4));
+                  uint8_t *out = static_cast<uint8_t *>(p.out) + ((t - lane + r) * p.ldo + col + o) * kBytes;
+                  if (TYPE == MOE_FP32)
+                    *reinterpret_cast<uint32_t *>(out) = *reinterpret_cast<const uint32_t *>(from_s);
+                  else
+                    *reinterpret_cast<uint16_t *>(out) = *reinterpret_cast<const uint16_t *>(from_s);
+                }
+            __syncwarp();
+          }
         }
       }
     }
@@ -639,6 +723,45 @@ bool map_scales(CUtensorMap *m, const uint8_t *s, int fmt, int rows, int K) {
   return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_INT64, 2, s, dims, strides, b, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+struct Shape {
+  int tn, split;  // tokens a tile (256: the wide kernel), CTAs that share a tile's K
+};
+
+// The shape of least estimated time, in us beyond what every launch takes. A stage of 256 values of K takes as long as
+// its bytes take into an SM (64 a cycle: 0.18 to 0.30 us for 16 to 128 tokens, 0.31 for the pairs' 256). CTAs that fit
+// the SMs' shared memory together share that; another round of them takes 3 us more. Clusters are laid into groups of
+// about 19 SMs. Joining parts of K takes 0.4 us for 16 tokens, 0.9 and 0.03 a token that a CTA sums for more; the wide
+// kernel's last tile is written in 1 us more. Measured, in us, the chosen first: 1 x 5120 x 2880 16 tokens in 4 parts 4.0,
+// whole 5.2; 8 x 8192 x 8192 16 in 2 7.3, whole 10.2; 64 x 5120 x 2880 64 whole 6.5, in 4 11.6; 333 x 2880 x 4096 64
+// whole 7.4, 128 7.7, wide 8.9; 1024 x 4096 x 4096 wide 9.8, 128 16.7.
+Shape choose(int T, int N, int K) {
+  const int stages = (K + kStageK - 1) / kStageK, sms = sm_count();
+  const int64_t wide_tiles = (int64_t)((T + 255) / 256) * ((N + kWideN - 1) / kWideN), pairs = sms / 2;
+  Shape best = {256, 1};
+  float least = ((wide_tiles + pairs - 1) / pairs) * stages * 0.31f + 1.0f;
+  if (T <= 64) least = INFINITY;  // half of a pair's first tile at most
+  constexpr int kTn[4] = {16, 32, 64, 128};
+  constexpr float kStageUs[4] = {0.18f, 0.20f, 0.235f, 0.30f};
+  for (int i = 0; i < 4; ++i) {
+    const int tn = kTn[i];
+    if (tn < 64 && T > tn) continue;  // a tile's scales begin on an even column of 32 tokens, or the MMA faults
+    const int64_t tiles = (int64_t)((T + tn - 1) / tn) * ((N + 127) / 128);
+    for (int split = 1; split <= kMaxSplit && split <= stages; ++split) {
+      const int own = (stages + split - 1) / split, stage_bytes = 16384 + tn * 128 + 4096;
+      int bytes = own * stage_bytes + (split > 1 ? (tn + 8) * 512 : 0);
+      if (bytes > (int)kMaxSmem) bytes = kMaxSmem;
+      const int together = (int)kMaxSmem / (bytes + 2048) > 1 ? (int)kMaxSmem / (bytes + 2048) : 1;
+      const int64_t ctas = tiles * split, held = (split == 1 ? sms : sms / 19 * (19 / split) * split) * together;
+      const int share = ((tn < T ? tn : T) + split - 1) / split;
+      const float join = split == 1 ? 0.f : tn == 16 ? 0.4f : 0.9f + 0.03f * share;
+      const float us = ((ctas + sms - 1) / sms) * own * kStageUs[i] + ((ctas + held - 1) / held - 1) * 3.0f + join + 0.005f * tn;
+      if (us < least) least = us, best = {tn, split};
+    }
+    if (tn >= T) break;
+  }
+  return best;
+}
+
 }  // namespace
 
 moe_status_t launch_fp4_linear(const moe_fp4_t &x, const moe_fp4_t &w, const void *bias, void *out, int type, int64_t ldo,
@@ -657,27 +780,27 @@ moe_status_t launch_fp4_linear(const moe_fp4_t &x, const moe_fp4_t &w, const voi
   a.N = w.rows;
   a.K = x.K;
   a.type = type;
-  // TODO rule
-  const bool wide = a.T >= 512;
-  const int tn = wide ? 256 : a.T <= 16 ? 16 : a.T <= 32 ? 32 : a.T <= 64 ? 64 : 128;
+  const Shape shape = choose(a.T, a.N, a.K);
+  const int tn = shape.tn;
+  if (tn < 64 && a.T > tn) return MOE_ERR_UNSUPPORTED;
+  const bool wide = tn == 256;
   const int wn = wide ? kWideN : 128;
   a.tiles_t = (a.T + tn - 1) / tn;
   a.tiles_n = (a.N + wn - 1) / wn;
   if (!map_codes(&a.tm_x, x.q, a.T, a.K, wide ? 128 : tn) || !map_codes(&a.tm_w, w.q, a.N, a.K, wide ? kWideN / 2 : 128) ||
       !map_scales(&a.tm_xs, x.scales, x.fmt, a.T, a.K) || !map_scales(&a.tm_ws, w.scales, w.fmt, a.N, a.K))
     return MOE_ERR_CUDA;
+  const int bytes = dtype_bytes(type);
+  // Rows on the 16-byte grid go out by bulk copies, as far as a row is a multiple of 16 bytes (a tensor store that is cut
+  // off at the tensor's edge was seen to write up to the next such multiple); the rest goes value by value.
+  a.bulk_n = ldo * bytes % 16 == 0 ? a.N / (16 / bytes) * (16 / bytes) : 0;
   if (wide) {
-    const int bytes = dtype_bytes(type);
-    // Rows on the 16-byte grid go out by TMA, as far as a row is a multiple of 16 bytes (a store that is cut off at the
-    // tensor's edge was seen to write up to the next such multiple); the rest goes value by value.
-    a.bulk_n = ldo * bytes % 16 == 0 ? a.N / (16 / bytes) * (16 / bytes) : 0;
     if (a.bulk_n) {
       const cuuint64_t dims[2] = {(cuuint64_t)a.bulk_n, (cuuint64_t)a.T}, strides[1] = {(cuuint64_t)ldo * bytes};
-      const cuuint32_t box[2] = {32, 32};
+      const cuuint32_t box[2] = {(cuuint32_t)(128 / bytes), 32};
       const CUtensorMapDataType t = type == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                     : type == MOE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
-      const CUtensorMapSwizzle swizzle = bytes == 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
-      if (!encode_tiled(&a.tm_out, t, 2, out, dims, strides, box, swizzle)) return MOE_ERR_CUDA;
+      if (!encode_tiled(&a.tm_out, t, 2, out, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B)) return MOE_ERR_CUDA;
     }
     if (launches) ++*launches;
 #define MOE4_WIDE(F)                                                       \
@@ -690,10 +813,7 @@ moe_status_t launch_fp4_linear(const moe_fp4_t &x, const moe_fp4_t &w, const voi
     MOE4_WIDE(MOE_FMT_MXFP4)
 #undef MOE4_WIDE
   }
-  const int64_t tiles = (int64_t)a.tiles_t * a.tiles_n;
-  const int all = (a.K + kStageK - 1) / kStageK;
-  a.split = 1;
-  while (a.split < kMaxSplit && a.split < all && tiles * (a.split + 1) <= sm_count()) ++a.split;
+  a.split = shape.split;
   if (launches) ++*launches;
 #define MOE4_NARROW(F)                                         \
   if (x.fmt == F) {                                            \
