@@ -24,6 +24,14 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxPairs = 128;  // of a head: at most 256 columns
 
+// Division of small numbers: x * d < 2^32 for every x that is divided.
+struct Divisor {
+  uint32_t d, m;
+  Divisor() = default;
+  explicit Divisor(uint32_t by) : d(by), m(by > 1 ? (uint32_t)((((uint64_t)1 << 32) - 1) / by + 1) : 0) {}
+  __device__ __forceinline__ int div(int x) const { return m ? (int)__umulhi((uint32_t)x, m) : x; }
+};
+
 // Tensors whose heads are rotated, [T][heads][D].
 struct RopeTensor {
   const void *in;
@@ -38,24 +46,40 @@ struct RopeArgs {
   const int32_t *positions;
   float amplitude;
   int T, D, rot, tokens, head_blocks, heads_each;  // a CTA's tokens and heads
+  Divisor by_pairs, by_items, by_heads;  // pairs of a head; threads that share one; heads_each
 };
 
 __device__ __forceinline__ float2 sine_of(unsigned long long turns, int position, float amplitude) {
   const uint32_t f = (uint32_t)((turns * (unsigned long long)(long long)position) >> 32);  // of 2^-32 turns
   const uint32_t quarter = (f + 0x20000000u) >> 30;
-  const int rest = (int)(f - (quarter << 30));  // -2^29 .. 2^29
-  float s, c;
-  sincospif((float)rest * 0x1p-31f, &s, &c);  // half turns
+  const float x = (float)(int)(f - (quarter << 30)) * 0x1p-31f, z = x * x;  // half turns, at most a quarter
+  // Taylor's series of sin(pi x) and cos(pi x): the first terms left out are 2e-9 and 5e-10; pi in two parts
+  float s = fmaf(z, 8.2145887e-2f, -5.9926453e-1f), c = fmaf(z, -2.5806891e-2f, 2.3533063e-1f);
+  s = fmaf(z, s, 2.5501640f);
+  s = fmaf(z, s, -5.1677128f);
+  s = fmaf(x, 3.1415927f, x * fmaf(z, s, -8.7422777e-8f));
+  c = fmaf(z, c, -1.3352628f);
+  c = fmaf(z, c, 4.0587121f);
+  c = fmaf(z, c, -4.9348022f);
+  c = fmaf(z, c, 1.0f);
   const float cc = (quarter & 1) ? -s : c, ss = (quarter & 1) ? c : s;
   return (quarter & 2) ? make_float2(-cc * amplitude, -ss * amplitude) : make_float2(cc * amplitude, ss * amplitude);
 }
 
-// Cosines and sines of the CTA's tokens: [tokens][pairs].
+// Cosines and sines of the CTA's tokens: [tokens][pairs]. Where lanes take 8 pairs or 4 each, they are in the order in
+// which neighbouring lanes read neighbouring 16 bytes, without bank conflicts: two pairs of each 8, then the next two.
+__device__ __forceinline__ int sine_at(int p, int rot) {
+  return rot % 16 == 0 ? ((p >> 1) & 3) * (rot / 8) + (p >> 3) * 2 + (p & 1) : p;
+}
+// Pairs 2 m and 2 m + 1 of the 8 pairs number i.
+__device__ __forceinline__ float4 two_sines(const float2 *cs, int i, int m, int rot) {
+  return *reinterpret_cast<const float4 *>(cs + m * (rot / 8) + 2 * i);
+}
 __device__ __forceinline__ void make_sines(float2 *sines, const RopeArgs &a, int t0, int tokens) {
   const int pairs = a.rot / 2;
   for (int i = threadIdx.x; i < tokens * pairs; i += blockDim.x) {
-    const int t = i / pairs, p = i - t * pairs;
-    if (t0 + t < a.T) sines[i] = sine_of(a.turns[p], a.positions[t0 + t], a.amplitude);
+    const int t = a.by_pairs.div(i), p = i - t * pairs;
+    if (t0 + t < a.T) sines[t * pairs + sine_at(p, a.rot)] = sine_of(a.turns[p], a.positions[t0 + t], a.amplitude);
   }
 }
 
@@ -63,81 +87,116 @@ __device__ __forceinline__ void make_sines(float2 *sines, const RopeArgs &a, int
 __device__ __forceinline__ float rotated_a(float a, float b, float2 w) { return fmaf(a, w.x, -__fmul_rn(b, w.y)); }
 __device__ __forceinline__ float rotated_b(float a, float b, float2 w) { return fmaf(b, w.x, __fmul_rn(a, w.y)); }
 
-// 8 pairs: a, b are their first and second halves.
-__device__ __forceinline__ void rotate8(float (&a)[8], float (&b)[8], const float2 *cs) {
+// 8 pairs, number i: a, b are their first and second halves.
+__device__ __forceinline__ void rotate8(float (&a)[8], float (&b)[8], const float2 *cs, int i, int rot) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 w = cs[i];
-    const float x = a[i], y = b[i];
-    a[i] = rotated_a(x, y, w);
-    b[i] = rotated_b(x, y, w);
+  for (int m = 0; m < 4; ++m) {
+    const float4 w = two_sines(cs, i, m, rot);
+    const float x = a[2 * m], y = b[2 * m], u = a[2 * m + 1], v = b[2 * m + 1];
+    a[2 * m] = rotated_a(x, y, make_float2(w.x, w.y));
+    b[2 * m] = rotated_b(x, y, make_float2(w.x, w.y));
+    a[2 * m + 1] = rotated_a(u, v, make_float2(w.z, w.w));
+    b[2 * m + 1] = rotated_b(u, v, make_float2(w.z, w.w));
   }
 }
-// 8 values that hold 4 pairs side by side.
-__device__ __forceinline__ void rotate4(float (&v)[8], const float2 *cs) {
+// 8 values that hold 4 pairs side by side, half `part` of the 8 pairs number i.
+__device__ __forceinline__ void rotate4(float (&v)[8], const float2 *cs, int i, int part, int rot) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 w = cs[i];
-    const float x = v[2 * i], y = v[2 * i + 1];
-    v[2 * i] = rotated_a(x, y, w);
-    v[2 * i + 1] = rotated_b(x, y, w);
+  for (int m = 0; m < 2; ++m) {
+    const float4 w = two_sines(cs, i, 2 * part + m, rot);
+    const float x = v[4 * m], y = v[4 * m + 1], z = v[4 * m + 2], u = v[4 * m + 3];
+    v[4 * m] = rotated_a(x, y, make_float2(w.x, w.y));
+    v[4 * m + 1] = rotated_b(x, y, make_float2(w.x, w.y));
+    v[4 * m + 2] = rotated_a(z, u, make_float2(w.z, w.w));
+    v[4 * m + 3] = rotated_b(z, u, make_float2(w.z, w.w));
   }
 }
 
-// Where the pairs fall on 16-byte pieces (rot a multiple of 16): a thread takes 16 columns of a head, 8 pairs or 16
-// that are not rotated.
-template <int TYPE, bool HALF>
-__device__ __forceinline__ void rotate_piece(const RopeTensor &x, const float2 *cs, int64_t t, int h, int i, int rot) {
-  const int c0 = i < rot / 16 ? (HALF ? 8 * i : 16 * i) : 16 * i, c1 = i < rot / 16 && HALF ? rot / 2 + 8 * i : c0 + 8;
-  const int64_t in = t * x.its + h * x.ith, out = t * x.ots + h * x.oth;
-  Raw8 ra = load_raw8(x.in, in + c0, TYPE), rb = load_raw8(x.in, in + c1, TYPE);
-  if (i < rot / 16) {
-    float a[8], b[8];
-    raw8_to_f32(ra, TYPE, a);
-    raw8_to_f32(rb, TYPE, b);
-    if (HALF) {
-      rotate8(a, b, cs + 8 * i);
-    } else {
-      rotate4(a, cs + 8 * i);
-      rotate4(b, cs + 8 * i + 4);
-    }
-    ra = f32_to_raw8(a, TYPE);
-    rb = f32_to_raw8(b, TYPE);
-  }
-  store_raw8(x.out, out + c0, TYPE, ra);
-  store_raw8(x.out, out + c1, TYPE, rb);
-}
-
-// Any rot: a thread takes a pair, or one column that is not rotated.
-template <int TYPE, bool HALF>
-__device__ __forceinline__ void rotate_pair(const RopeTensor &x, const float2 *cs, int64_t t, int h, int i, int rot) {
-  const int64_t in = t * x.its + h * x.ith, out = t * x.ots + h * x.oth;
-  if (i >= rot / 2) {
-    const int c = i + rot / 2;
-    store_from_f32(x.out, out + c, TYPE, load_as_f32(x.in, in + c, TYPE));
-    return;
-  }
-  const int c0 = HALF ? i : 2 * i, c1 = HALF ? i + rot / 2 : 2 * i + 1;
-  const float a = load_as_f32(x.in, in + c0, TYPE), b = load_as_f32(x.in, in + c1, TYPE);
-  const float2 w = cs[i];
-  store_from_f32(x.out, out + c0, TYPE, rotated_a(a, b, w));
-  store_from_f32(x.out, out + c1, TYPE, rotated_b(a, b, w));
-}
-
-// The heads [h0, h1) of tokens [t0, t0 + a.tokens), those of x[1] behind those of x[0].
+// A thread's share of a head. Where the pairs fall on 16-byte pieces (rot a multiple of 16) it is 16 columns, 8 pairs or
+// 16 that are not rotated; else a pair, or one column that is not rotated.
 template <int TYPE, bool HALF, bool PIECES>
-__device__ __forceinline__ void rotate_block(const RopeArgs &a, const float2 *sines, int t0, int h0, int h1) {
+struct Item {
+  Raw8 a, b;
+  float x, y;
+  __device__ __forceinline__ void load(const RopeTensor &s, int64_t t, int h, int i, int rot) {
+    const int64_t in = t * s.its + h * s.ith;
+    if (PIECES) {
+      const bool turned = i < rot / 16;
+      const int c0 = turned && HALF ? 8 * i : 16 * i, c1 = turned && HALF ? rot / 2 + 8 * i : c0 + 8;
+      a = load_raw8(s.in, in + c0, TYPE);
+      b = load_raw8(s.in, in + c1, TYPE);
+    } else if (i < rot / 2) {
+      x = load_as_f32(s.in, in + (HALF ? i : 2 * i), TYPE);
+      y = load_as_f32(s.in, in + (HALF ? i + rot / 2 : 2 * i + 1), TYPE);
+    } else {
+      x = load_as_f32(s.in, in + i + rot / 2, TYPE);
+    }
+  }
+  __device__ __forceinline__ void store(const RopeTensor &s, int64_t t, int h, int i, int rot, const float2 *cs) {
+    const int64_t out = t * s.ots + h * s.oth;
+    if (PIECES) {
+      const bool turned = i < rot / 16;
+      const int c0 = turned && HALF ? 8 * i : 16 * i, c1 = turned && HALF ? rot / 2 + 8 * i : c0 + 8;
+      if (turned) {
+        float u[8], v[8];
+        raw8_to_f32(a, TYPE, u);
+        raw8_to_f32(b, TYPE, v);
+        if (HALF) {
+          rotate8(u, v, cs, i, rot);
+        } else {
+          rotate4(u, cs, i, 0, rot);
+          rotate4(v, cs, i, 1, rot);
+        }
+        a = f32_to_raw8(u, TYPE);
+        b = f32_to_raw8(v, TYPE);
+      }
+      store_raw8(s.out, out + c0, TYPE, a);
+      store_raw8(s.out, out + c1, TYPE, b);
+    } else if (i < rot / 2) {
+      const float2 w = cs[sine_at(i, rot)];
+      store_from_f32(s.out, out + (HALF ? i : 2 * i), TYPE, rotated_a(x, y, w));
+      store_from_f32(s.out, out + (HALF ? i + rot / 2 : 2 * i + 1), TYPE, rotated_b(x, y, w));
+    } else {
+      store_from_f32(s.out, out + i + rot / 2, TYPE, x);
+    }
+  }
+};
+
+// The heads [h0, h1) of tokens [t0, t0 + a.tokens), those of x[1] behind those of x[0]. A thread keeps its place in a head
+// and walks the heads, two at a time; the first two are asked for before the sines are made.
+template <int TYPE, bool HALF, bool PIECES>
+__device__ __forceinline__ void rotate_block(const RopeArgs &a, float2 *sines, int t0, int h0, int h1) {
+  constexpr int U = 2;
   const int items = PIECES ? a.D / 16 : a.D - a.rot / 2, heads = h1 - h0;
-  const int per_token = items * heads, n = min(a.tokens, a.T - t0) * per_token;
-  for (int at = threadIdx.x; at < n; at += kThreads) {
-    const int t = at / per_token, r = at - t * per_token, hh = r / items, i = r - hh * items, h = h0 + hh;
-    const bool second = h >= a.x[0].heads;
-    const RopeTensor &x = a.x[second];
-    const float2 *cs = sines + t * (a.rot / 2);
-    if (PIECES)
-      rotate_piece<TYPE, HALF>(x, cs, t0 + t, second ? h - a.x[0].heads : h, i, a.rot);
-    else
-      rotate_pair<TYPE, HALF>(x, cs, t0 + t, second ? h - a.x[0].heads : h, i, a.rot);
+  const int first = a.by_items.div(threadIdx.x), i = threadIdx.x - first * items, step = a.by_items.div(kThreads);
+  const int tokens = min(a.tokens, a.T - t0);
+  const bool whole = heads == a.heads_each;  // the last heads may be fewer
+  const int rows = (int)threadIdx.x < step * items ? tokens * heads : 0;
+  Item<TYPE, HALF, PIECES> it[U];
+  bool made = false;
+  for (int r0 = first; r0 < rows || !made; r0 += U * step) {
+    int t[U], h[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * step;
+      t[u] = whole ? a.by_heads.div(r) : r / heads;
+      h[u] = h0 + r - t[u] * heads;
+      if (r < rows) {
+        const bool second = h[u] >= a.x[0].heads;
+        it[u].load(a.x[second], t0 + t[u], second ? h[u] - a.x[0].heads : h[u], i, a.rot);
+      }
+    }
+    if (!made) {
+      make_sines(sines, a, t0, tokens);
+      __syncthreads();
+      made = true;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (r0 + u * step < rows) {
+        const bool second = h[u] >= a.x[0].heads;
+        it[u].store(a.x[second], t0 + t[u], second ? h[u] - a.x[0].heads : h[u], i, a.rot, sines + t[u] * (a.rot / 2));
+      }
   }
 }
 
@@ -145,12 +204,11 @@ constexpr int kMaxTokens = 16;
 
 template <int TYPE, bool HALF, bool PIECES>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
-  __shared__ float2 sines[kMaxTokens * kMaxPairs];
+  __shared__ __align__(16) float2 sines[kMaxTokens * kMaxPairs];
   pdl_wait();
   pdl_trigger();
-  const int t0 = blockIdx.x / a.head_blocks * a.tokens, h0 = blockIdx.x % a.head_blocks * a.heads_each;
-  make_sines(sines, a, t0, a.tokens);
-  __syncthreads();
+  const int block = a.head_blocks == 1 ? blockIdx.x : blockIdx.x / a.head_blocks;
+  const int t0 = block * a.tokens, h0 = (blockIdx.x - block * a.head_blocks) * a.heads_each;
   rotate_block<TYPE, HALF, PIECES>(a, sines, t0, h0, min(h0 + a.heads_each, a.x[0].heads + a.x[1].heads));
 }
 
@@ -163,15 +221,33 @@ struct WriteArgs {
   unsigned int *status;
   int64_t kst, ksh, vst, vsh;
   uint32_t rows;  // T * kv heads
-  int kv_heads, log_n, page, pages, q_ctas;
+  int kv_heads, log_n, page, pages, rows_each;
+  uint32_t kv_share;  // 0: there are no queries
 };
+
+// The other 8 values of a lane's pairs where they are half a rotation away.
+template <int TYPE>
+__device__ __forceinline__ Raw8 load_partners(const void *k, int64_t row, int c0, int rot) {
+  const int half = rot / 2;
+  if (rot % 16 == 0) return load_raw8(k, row + (c0 >= rot ? c0 : c0 < half ? c0 + half : c0 - half), TYPE);
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int c = c0 + i;
+    y[i] = c < rot ? load_as_f32(k, row + (c < half ? c + half : c - half), TYPE) : 0.f;
+  }
+  return f32_to_raw8(y, TYPE);  // exact
+}
 
 // A lane's 8 columns of a key, rotated.
 template <int TYPE, bool HALF>
-__device__ __forceinline__ void rotate_key(float (&x)[8], const void *k, int64_t row, int j, int rot, const float2 *cs) {
-  const int c0 = 8 * j;
+__device__ __forceinline__ void rotate_key(float (&x)[8], const Raw8 &partners, int c0, int rot, const float2 *cs) {
   if (c0 >= rot) return;
   if (!HALF) {
+    if (rot % 16 == 0) {
+      rotate4(x, cs, c0 / 16, (c0 >> 3) & 1, rot);
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (c0 + 2 * i < rot) {
@@ -183,15 +259,19 @@ __device__ __forceinline__ void rotate_key(float (&x)[8], const void *k, int64_t
     return;
   }
   const int half = rot / 2;
-  float y[8];  // the other ones of the pairs
+  float y[8];
+  raw8_to_f32(partners, TYPE, y);
   if (rot % 16 == 0) {
-    raw8_to_f32(load_raw8(k, row + (c0 < half ? c0 + half : c0 - half), TYPE), TYPE, y);
-  } else {
+    // rotated_a(x, y) or rotated_b(y, x), which differ in a sign
+    const uint32_t sign = c0 < half ? 0x80000000u : 0u;
+    auto signed_sine = [&](float s) { return __uint_as_float(__float_as_uint(s) ^ sign); };
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = c0 + i;
-      y[i] = c < rot ? load_as_f32(k, row + (c < half ? c + half : c - half), TYPE) : 0.f;
+    for (int m = 0; m < 4; ++m) {
+      const float4 w = two_sines(cs, (c0 < half ? c0 : c0 - half) / 8, m, rot);
+      x[2 * m] = fmaf(x[2 * m], w.x, __fmul_rn(y[2 * m], signed_sine(w.y)));
+      x[2 * m + 1] = fmaf(x[2 * m + 1], w.z, __fmul_rn(y[2 * m + 1], signed_sine(w.w)));
     }
+    return;
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -203,67 +283,84 @@ __device__ __forceinline__ void rotate_key(float (&x)[8], const void *k, int64_t
   }
 }
 
-// R rows (token, kv head) a lane; 1 << log_n lanes a row.
-constexpr int kRows = 2;
-static_assert(kThreads / 8 * kRows * 32 <= kMaxTokens * kMaxPairs, "sines of the keys' rows");
-
+// CTAs that rotate queries and CTAs that write a row (token, kv head) of keys and values for each 1 << log_n lanes,
+// dealt out evenly: the former wait for memory where the latter have instructions to issue.
 template <int FMT, int TYPE, bool HALF, bool PIECES>
 __global__ void __launch_bounds__(kThreads) rope_write_kernel(const WriteArgs a) {
-  __shared__ float2 sines[kMaxTokens * kMaxPairs];  // the keys' rows: 64, 32 or 16 tokens of 32, 64 or 128 pairs at most
+  __shared__ __align__(16) float2 sines[kMaxTokens * kMaxPairs];
   pdl_wait();
   pdl_trigger();
-  if ((int)blockIdx.x < a.q_ctas) {
-    const int t0 = blockIdx.x / a.q.head_blocks * a.q.tokens, h0 = blockIdx.x % a.q.head_blocks * a.q.heads_each;
-    make_sines(sines, a.q, t0, a.q.tokens);
-    __syncthreads();
+  // CTAs of rows before this one: kv_share is their number of all, of 2^32 and rounded up, so that the last makes them up
+  const uint32_t before = a.kv_share ? __umulhi(blockIdx.x, a.kv_share) : blockIdx.x;
+  if (a.kv_share && before == __umulhi(blockIdx.x + 1, a.kv_share)) {
+    const int at = blockIdx.x - before, block = a.q.head_blocks == 1 ? at : at / a.q.head_blocks;
+    const int t0 = block * a.q.tokens, h0 = (at - block * a.q.head_blocks) * a.q.heads_each;
     rotate_block<TYPE, HALF, PIECES>(a.q, sines, t0, h0, min(h0 + a.q.heads_each, a.q.x[0].heads));
     return;
   }
+  // a lane 8 columns of a.rows_each rows, the next one's asked for while one is quantised
   const int n = 1 << a.log_n, j = threadIdx.x & (n - 1), D = a.q.D;
-  const uint32_t per = kThreads >> a.log_n, first = (blockIdx.x - a.q_ctas) * (per * kRows);
-  const uint32_t last = min(first + per * kRows, a.rows) - 1;
-  const int t0 = first / a.kv_heads;
-  // tokens of these rows: at most their number
-  make_sines(sines, a.q, t0, (int)(last / a.kv_heads) - t0 + 1);
+  const uint32_t per = kThreads >> a.log_n, first = before * (per * a.rows_each);
+  const int t0 = first / a.kv_heads, t1 = (min(first + per * a.rows_each, a.rows) - 1) / a.kv_heads;
+  uint32_t r = first + (threadIdx.x >> a.log_n);
+  int t = r / (uint32_t)a.kv_heads, head = r - t * a.kv_heads;
+  const int t_step = per / (uint32_t)a.kv_heads, head_step = per - t_step * a.kv_heads;
+  Raw8 k, partners, v;
+  int slot;
+  auto load = [&]() {
+    if (r >= a.rows) t = t0, head = 0;  // reads what is there, and writes nothing
+    slot = a.slots[t];
+    const int64_t krow = (int64_t)t * a.kst + (int64_t)head * a.ksh;
+    k = load_raw8(a.k, krow + 8 * j, TYPE);
+    if (HALF) partners = load_partners<TYPE>(a.k, krow, 8 * j, a.q.rot);
+    v = load_raw8(a.v, (int64_t)t * a.vst + (int64_t)head * a.vsh + 8 * j, TYPE);
+  };
+  load();
+  make_sines(sines, a.q, t0, t1 - t0 + 1);
   __syncthreads();
-#pragma unroll
-  for (int x = 0; x < kRows; ++x) {
-    const uint32_t r = first + x * per + (threadIdx.x >> a.log_n);
+  const uint32_t page16 = (uint32_t)a.page >> 4;
+  for (int x = 0; x < a.rows_each; ++x) {
     const bool live = r < a.rows;
-    const int t = live ? r / (uint32_t)a.kv_heads : t0, head = live ? r - t * a.kv_heads : 0;
-    int slot = a.slots[t];
     if (slot >= a.pages * a.page) {
       if (live && j == 0) raise_status(a.status, MOE_ERR_BAD_INDEX);
       slot = -1;
     }
-    const int64_t krow = (int64_t)t * a.kst + (int64_t)head * a.ksh;
-    const Raw8 k = load_raw8(a.k, krow + 8 * j, TYPE);
-    const Raw8 v = load_raw8(a.v, (int64_t)t * a.vst + (int64_t)head * a.vsh + 8 * j, TYPE);
     const bool held = live && slot >= 0;
+    const int token = slot & 15;
     uint8_t *rec = nullptr;
     if (held) {
-      const uint32_t block = (uint32_t)slot >> 4, page16 = (uint32_t)a.page >> 4, page = block / page16;
+      const uint32_t block = (uint32_t)slot >> 4, page = block / page16;
       rec = a.data + (((int64_t)page * a.kv_heads + head) * page16 + (block - page * page16)) * kv_record(FMT, D);
     }
     float f[8];
     raw8_to_f32(k, TYPE, f);
-    rotate_key<TYPE, HALF>(f, a.k, krow, j, a.q.rot, sines + (t - t0) * (a.q.rot / 2));
-    put8<FMT, MOE_FP32>(rec, slot & 15, 0, j, n, D, f32_to_raw8(f, MOE_FP32), held);
-    put8<FMT, TYPE>(rec, slot & 15, 1, j, n, D, v, held);
+    rotate_key<TYPE, HALF>(f, partners, 8 * j, a.q.rot, sines + (t - t0) * (a.q.rot / 2));
+    const Raw8 own = v;
+    if (x + 1 < a.rows_each) {
+      r += per;
+      t += t_step;
+      head += head_step;
+      if (head >= a.kv_heads) head -= a.kv_heads, ++t;
+      load();
+    }
+    put8<FMT, MOE_FP32>(rec, token, 0, j, n, D, f32_to_raw8(f, MOE_FP32), held);
+    put8<FMT, TYPE>(rec, token, 1, j, n, D, own, held);
   }
 }
 
-// How many tokens and heads a CTA takes: about four pieces a thread, all heads of its tokens where there are tokens
+// How many tokens and heads a CTA takes: about four items a thread, all heads of its tokens where there are tokens
 // enough for two CTAs an SM, else heads apart.
 void share(RopeArgs &a, int heads, bool pieces) {
-  const int items = pieces ? a.D / 16 : a.D - a.rot / 2, want = 4 * kThreads;
+  const int items = pieces ? a.D / 16 : a.D - a.rot / 2;
   a.tokens = 1;
-  while (a.tokens < kMaxTokens && 2 * a.tokens * heads * items <= want && a.T / (2 * a.tokens) >= 304) a.tokens *= 2;
+  while (a.tokens < kMaxTokens && 2 * a.tokens * heads * items <= 4 * kThreads && a.T / (2 * a.tokens) >= 304) a.tokens *= 2;
   a.head_blocks = 1;
-  while (a.head_blocks < heads && a.tokens * (heads / a.head_blocks) * items > kThreads && (int64_t)a.T * a.head_blocks < 304)
-    ++a.head_blocks;
+  while (a.head_blocks < heads && (heads / a.head_blocks) * items > kThreads && (int64_t)a.T * a.head_blocks < 304) ++a.head_blocks;
   a.heads_each = (heads + a.head_blocks - 1) / a.head_blocks;
   a.head_blocks = (heads + a.heads_each - 1) / a.heads_each;
+  a.by_pairs = Divisor(a.rot / 2);
+  a.by_items = Divisor(items);
+  a.by_heads = Divisor(a.heads_each);
 }
 
 }  // namespace
@@ -311,14 +408,20 @@ moe_status_t launch_rope_kv_write(const moe_rope_t &r, const int32_t *positions,
   a.page = c.page_size;
   a.pages = c.num_pages;
   int64_t q_ctas = 0;
+  share(a.q, q ? q_heads : 1, a.q.rot % 16 == 0);
   if (q) {
-    share(a.q, q_heads, a.q.rot % 16 == 0);
     q_ctas = (int64_t)((T + a.q.tokens - 1) / a.q.tokens) * a.q.head_blocks;
   }
-  const uint32_t step = (kThreads >> a.log_n) * kRows;
-  const int64_t ctas = q_ctas + a.rows / step + (a.rows % step != 0);
+  // one row a lane until there are CTAs enough for every SM four times over, then four, as far as the sines of their
+  // tokens fit
+  const uint32_t per = kThreads >> a.log_n;
+  static_assert(kThreads / 8 * 32 <= kMaxTokens * kMaxPairs, "sines of one row a lane: 32, 16 or 8 tokens of 32, 64 or 128 pairs");
+  a.rows_each = 1;
+  if (a.rows > 4 * per * 608 && ((4 * per - 1) / c.kv_heads + 2) * (r.rot_dim / 2) <= kMaxTokens * kMaxPairs) a.rows_each = 4;
+  const uint32_t step = per * a.rows_each;
+  const int64_t kv_ctas = a.rows / step + (a.rows % step != 0), ctas = q_ctas + kv_ctas;
   if (ctas >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
-  a.q_ctas = (int)q_ctas;
+  if (q_ctas) a.kv_share = (uint32_t)((((uint64_t)kv_ctas << 32) + ctas - 1) / ctas);
   using Kernel = void (*)(WriteArgs);
 #define MOE4_W(F, T) {{rope_write_kernel<F, T, true, false>, rope_write_kernel<F, T, true, true>}, {rope_write_kernel<F, T, false, false>, rope_write_kernel<F, T, false, true>}}
 #define MOE4_W_TYPES(F) {MOE4_W(F, MOE_BF16), MOE4_W(F, MOE_FP16), MOE4_W(F, MOE_FP32)}
