@@ -5,10 +5,12 @@
 // = E4M3(amax16 / r / 6); codes E2M1(x / r / s). MXFP4: s = 2^e, the least with
 // amax32 / s <= 6; codes E2M1(x / s). Scaling by powers of two is exact. An fp32
 // value's x / r / s is a true quotient (kvcache.cu says why its rounding moves it
-// over no tie of E2M1). A 16-bit one is multiplied by 1 / s, rounded up, and cut
-// to 16 significant bits: x and a tie times s (4 + 3 bits) are equal or differ by
-// 2^-12 of them, the product is at most 2^-22 too large, so that a product on a
-// tie is cut to the tie and no other reaches it from either side.
+// over no tie of E2M1). A 16-bit one is multiplied by 1 / s rounded up, and the
+// product cut off: x and a tie times s (4 + 3 bits) are equal or differ by 2^-12 of
+// them, the product before the cut is too large by 2^-23 at most, so that no product
+// reaches a tie from below, and one on a tie is cut to the tie itself for each of
+// the 8 significands of s and 7 ties, as amax16 / r / 6 is for the ties of E4M3
+// (tests/test_fp4_rounding.py tries them all).
 //
 // Bound by memory: 2 bytes of a value are read, 9/16 or 17/32 written. A lane
 // holds 16 consecutive values (an NVFP4 block, half an MXFP4 one), a row stays
@@ -31,6 +33,19 @@ struct QuantArgs {
   float *row_scale;
   int T, K, units, tiles_k, W;  // units of 16 values; W warps a row
 };
+
+// x f for pairs of values, cut off towards zero.
+__device__ __forceinline__ void scale8_rz(float (&x)[8], float f) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2)
+    asm("{\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%0, %1};\n\t"
+        "mov.b64 b, {%2, %2};\n\t"
+        "mul.rz.f32x2 a, a, b;\n\t"
+        "mov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(x[i]), "+f"(x[i + 1])
+        : "f"(f));
+}
 
 template <int TYPE>
 __device__ __forceinline__ uint32_t half_max(const Raw8 (&r)[2]) { return max(abs_max<TYPE>(r[0]), abs_max<TYPE>(r[1])); }
@@ -56,7 +71,7 @@ __global__ void __launch_bounds__(kWarps * 32) fp4_quantize_kernel(const QuantAr
       raw[p][0].a = raw[p][0].b = raw[p][1].a = raw[p][1].b = make_uint4(0, 0, 0, 0);
     }
   }
-  float up = 1.f;
+  float up = 1.f, pre = 1.f;  // the row's factor 1 / r, and what of it is applied ahead so that up / s stays finite
   bool bad = false;
   if (FMT == MOE_FMT_NVFP4) {
 #pragma unroll
@@ -69,7 +84,9 @@ __global__ void __launch_bounds__(kWarps * 32) fp4_quantize_kernel(const QuantAr
     }
     bad = top >= inf_bits<TYPE>();
     const int e = row_exponent(from_bits<TYPE>(top), 2688.f, 12);
-    up = pow2(-e);  // e is at most 116 for finite values; a bad row's codes are not used
+    // e is at most 116 for finite values (a bad row's codes are not used)
+    if (TYPE != MOE_FP32 && e < -110) pre = 0x1p64f;
+    up = pow2(pre > 1.f ? -e - 64 : -e);
     if (live && wr == 0 && lane == 0) a.row_scale[row] = bad ? __int_as_float(0x7fc00000) : pow2(e);
   }
   if (!live) return;
@@ -83,14 +100,27 @@ __global__ void __launch_bounds__(kWarps * 32) fp4_quantize_kernel(const QuantAr
     uint32_t sb;
     bool none = bad;
     if (FMT == MOE_FMT_NVFP4) {
-      sb = bad ? 0u : e4m3x2(from_bits<TYPE>(half_max<TYPE>(raw[p])) * up / 6.0f, 0.f) & 0xFFu;
-      const float s = e4m3x2_f32(sb).x, inv = s > 0.f ? __frcp_ru(s) : 0.f;
+      const float top16 = from_bits<TYPE>(half_max<TYPE>(raw[p]));
+      if (TYPE == MOE_FP32) {
+        sb = e4m3x2(top16 * up / 6.0f, 0.f) & 0xFFu;
+      } else {
+        constexpr float kSixth = 0.16666667163372039794921875f;  // rounded up
+        sb = e4m3x2(__fmul_rz(top16 * pre, kSixth * up), 0.f) & 0xFFu;
+      }
+      if (bad) sb = 0;
+      const float s = e4m3x2_f32(sb).x;
       none = !(s > 0.f);
+      if (TYPE == MOE_FP32) {
 #pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        float &v = x[q >> 3][q & 7];
-        v *= up;
-        v = TYPE == MOE_FP32 ? (s > 0.f ? v / s : 0.f) : __uint_as_float(__float_as_uint(v * inv) & 0xFFFFFF00u);
+        for (int q = 0; q < 16; ++q) x[q >> 3][q & 7] = none ? 0.f : x[q >> 3][q & 7] * up / s;
+      } else {
+        if (pre > 1.f) {
+#pragma unroll
+          for (int q = 0; q < 16; ++q) x[q >> 3][q & 7] *= pre;
+        }
+        const float f = none ? 0.f : __frcp_ru(s) * up;
+        scale8_rz(x[0], f);
+        scale8_rz(x[1], f);
       }
     } else {
       const uint32_t own = half_max<TYPE>(raw[p]), m = max(own, __shfl_xor_sync(kAll, own, 1));
