@@ -127,8 +127,8 @@ _SIGS = {
     "moe_attn_workspace_size": (_i32, [_i32, _i32, _i32, ctypes.POINTER(_sz)]),
     "moe_attn_decode": (_i32, [_vp, _i32, _i64, _i64, ctypes.POINTER(KvCache), _vp, _i64, _i32, _vp, _i32, _i32,
                                ctypes.c_float, _i32, _vp, _vp, _i64, _i64, _vp, _vp, _sz, _vp]),
-    "moe_batch_plan": (_i32, [_vp, _vp, _i32, _i32, _i32, _vp, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp,
-                              _vp]),
+    "moe_batch_plan": (_i32, [_vp, _vp, _i32, _i32, _i32, _vp, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp,
+                              _vp, _vp]),
     "moe_rope_table": (_i32, [ctypes.POINTER(RopeConfig), _vp, _vp]),
     "moe_rope_turns": (_i32, [_vp, _i32, _vp]),
     "moe_rope": (_i32, [ctypes.POINTER(Rope), _vp, _i32, _i32, _vp, _i64, _i64, _i32, _vp, _i64, _i64, _vp, _i64, _i64, _i32,
@@ -480,12 +480,12 @@ def moe_attn_decode(q, cache, block_table, seq_lens, out, ws, scale=None, window
 
 # ------------------------------------------------------------------------- before the attention: plan, rotary positions
 def moe_batch_plan(new_lens, seq_lens, block_table, free_pages, free_count, page_size, slots, seq_lens_out, free_count_out,
-                   ws, positions=None, seq_ids=None, offsets=None, stream=None):
-    """Pages, slots and positions of a batch's new tokens. new_lens, seq_lens int32 [B] (below 0: the sequence ends),
+                   ws, positions=None, seq_ids=None, offsets=None, rows_each=0, stream=None):
+    """Pages, slots and positions of a batch's new tokens, in packed rows or in rows_each for a sequence. new_lens, seq_lens int32 [B] (below 0: the sequence ends),
     block_table int32 [B, pages], free_pages int32 [pages of the cache], free_count int32 [1]; out: slots, positions,
     seq_ids int32 [T], seq_lens_out [B] and free_count_out [1] (may be the inputs), offsets [B + 1]. See the header."""
     code = (_fast or _setup()).batch_plan(new_lens, seq_lens, block_table, free_pages, free_count, page_size, slots,
-                                          seq_lens_out, free_count_out, ws, positions, seq_ids, offsets, stream)
+                                          seq_lens_out, free_count_out, ws, positions, seq_ids, offsets, rows_each, stream)
     if code:
         raise MoeError(code, "moe_batch_plan")
 

@@ -275,9 +275,9 @@ PyObject *attn_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
 }
 
 // new_lens, seq_lens, block_table, free_pages, free_count, page_size, slots, seq_lens_out, free_count_out, ws, positions,
-// seq_ids, offsets, stream
+// seq_ids, offsets, rows_each, stream
 PyObject *batch_plan(PyObject *, PyObject *const *a, Py_ssize_t n) {
-  return status(n, 14, [&]() -> int {
+  return status(n, 15, [&]() -> int {
     const Arg grow(a[0]), lens(a[1]), table(a[2]), pages(a[3]), count(a[4]), slots(a[6]), lens_out(a[7]), count_out(a[8]),
         ws(a[9]), positions(a[10]), seqs(a[11]), offsets(a[12]);
     need(grow && lens && table && pages && count && slots && lens_out && count_out);
@@ -290,8 +290,8 @@ PyObject *batch_plan(PyObject *, PyObject *const *a, Py_ssize_t n) {
     auto ints = [](const Arg &x, int64_t size) { return static_cast<int32_t *>(x.flat(at::kInt, size)); };
     return moe_batch_plan(ints(grow, B), ints(lens, B), (int)B, int_of(a[5]), (int)free, static_cast<int32_t *>(table.ptr()),
                           B > 1 ? table.stride(0) : cols, (int)cols, ints(pages, free), ints(count, 1), ints(lens_out, B),
-                          ints(count_out, 1), ints(offsets, B + 1), (int)T, ints(slots, T), ints(positions, T), ints(seqs, T),
-                          ws.ptr(), stream_of(a[13], lens));
+                          ints(count_out, 1), ints(offsets, B + 1), (int)T, int_of(a[13]), ints(slots, T), ints(positions, T),
+                          ints(seqs, T), ws.ptr(), stream_of(a[14], lens));
   });
 }
 

@@ -111,7 +111,7 @@ moe_status_t launch_fp4_linear(const moe_fp4_t &x, const moe_fp4_t &w, const voi
 
 moe_status_t launch_batch_plan(const int32_t *new_lens, const int32_t *seq_lens, int B, int page, int num_pages,
                                int32_t *table, int64_t ts, int max_pages, int32_t *free_pages, const int32_t *free_count,
-                               int32_t *lens_out, int32_t *count_out, int32_t *offsets, int T, int32_t *slots,
+                               int32_t *lens_out, int32_t *count_out, int32_t *offsets, int T, int rows_each, int32_t *slots,
                                int32_t *positions, int32_t *seq_ids, unsigned int *status, cudaStream_t stream,
                                int *launches);
 

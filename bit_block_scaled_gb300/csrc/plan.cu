@@ -28,7 +28,7 @@ constexpr unsigned kAll = 0xffffffffu;
 struct Divisor {
   uint32_t m;
   int shift;
-  explicit Divisor(uint32_t d) {
+  explicit Divisor(uint32_t d) {  // d > 1
     int l = 1;
     while (((uint32_t)1 << l) < d) ++l;
     m = (uint32_t)((((uint64_t)1 << (31 + l)) + d - 1) / d);
@@ -42,8 +42,8 @@ struct PlanArgs {
   int32_t *table, *free_pages, *lens_out, *count_out, *offsets, *slots, *positions, *seq_ids;
   unsigned int *status;
   int64_t ts;
-  int B, T, page, num_pages, max_pages, log_b, wide;  // 2^log_b > B; rows' outputs are 16-byte aligned
-  Divisor by_page;
+  int B, T, rows_each, page, num_pages, max_pages, log_b, wide;  // 2^log_b > B; rows' outputs are 16-byte aligned
+  Divisor by_page, by_rows;
 };
 
 // What a sequence adds to the sums: tokens, pages needed, pages given back. Sums stay at 2^31 - 1 once they are there.
@@ -143,8 +143,31 @@ __device__ __forceinline__ void put_rows(const PlanArgs &a, const int *ends, con
   }
 }
 
+// Sequence b's rows are those from b * rows_each on.
+__device__ __forceinline__ void put_fixed_rows(const PlanArgs &a, const int *tokens, const int *before, const int *lens, int top,
+                                               int thread, int step) {
+  for (int t = thread; t < a.T; t += step) {
+    int b = a.rows_each > 1 ? a.by_rows.div(t) : t, pos = 0, slot = -1;
+    const int i = t - b * a.rows_each;
+    if (b >= a.B || i >= tokens[b]) {
+      b = -1;
+    } else if (lens[b] >= 0) {
+      pos = lens[b] + i;
+      const int pg = a.by_page.div(pos), held = a.by_page.div(lens[b] + a.page - 1);
+      const int p = pg < held ? a.table[b * a.ts + pg] : a.free_pages[top - 1 - (before[b] + pg - held)];
+      if (p < 0 || p >= a.num_pages)
+        raise_status(a.status, MOE_ERR_BAD_INDEX);
+      else
+        slot = p * a.page + (pos - pg * a.page);
+    }
+    a.slots[t] = slot;
+    if (a.positions) a.positions[t] = pos;
+    if (a.seq_ids) a.seq_ids[t] = b;
+  }
+}
+
 __global__ void __launch_bounds__(kMaxThreads) plan_kernel(const PlanArgs a) {
-  // per sequence: end of its tokens, pages before its own on the stack's way down, length (-1: not served)
+  // per sequence: end of its tokens (their number where rows are fixed), pages before its own on the stack's way down, length (-1: not served)
   extern __shared__ int shared[];
   int *ends = shared, *before = ends + a.B, *lens = before + a.B;
   __shared__ Sums warp_sums[kWarps];
@@ -186,7 +209,9 @@ __global__ void __launch_bounds__(kMaxThreads) plan_kernel(const PlanArgs a) {
       if (ok) {
         valid |= 1u << i;
         const int held = pages_of(L[i]);
-        if (n[i] > 0 && n[i] <= cap - L[i]) {
+        // where rows are fixed, a sequence that has too few of them asks for nothing
+        const bool rows = !a.rows_each || (n[i] <= a.rows_each && (int64_t)(tid * each + i) * a.rows_each + n[i] <= a.T);
+        if (n[i] > 0 && n[i] <= cap - L[i] && rows) {
           fits |= 1u << i;
           mine[i].need = pages_of(L[i] + n[i]) - held;
         }
@@ -220,17 +245,19 @@ __global__ void __launch_bounds__(kMaxThreads) plan_kernel(const PlanArgs a) {
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     if (i >= each) break;
-    const int b = tid * each + i, end = add31(at.tokens, mine[i].tokens), taken = add31(at.need, mine[i].need);
+    const int b = tid * each + i, taken = add31(at.need, mine[i].need);
+    const int64_t start = a.rows_each ? (int64_t)b * a.rows_each : at.tokens;  // of its rows
+    const int end = (int)min(start + mine[i].tokens, (int64_t)INT32_MAX);
     if (b < a.B) {
       const bool served = (fits >> i & 1) && (mine[i].need == 0 || taken <= top) && end <= a.T;
-      ends[b] = end;
+      ends[b] = a.rows_each ? mine[i].tokens : end;
       before[b] = at.need;
       lens[b] = served ? L[i] : -1;
       if (served && mine[i].need) atomicMax(&given, taken);
       if (first) {
         if (n[i] > 0 && (valid >> i & 1) && !served) raise_status(a.status, MOE_ERR_CAPACITY);
         a.lens_out[b] = served ? L[i] + n[i] : n[i] < 0 && (valid >> i & 1) ? 0 : L[i];
-        if (a.offsets) a.offsets[b + 1] = end;
+        if (a.offsets) a.offsets[b + 1] = a.rows_each ? (int)min(start + a.rows_each, (int64_t)INT32_MAX) : end;
       }
     }
     // a warp the pages of one lane's sequence after the other's
@@ -261,7 +288,9 @@ __global__ void __launch_bounds__(kMaxThreads) plan_kernel(const PlanArgs a) {
     *a.count_out = top - given;
     if (a.offsets) a.offsets[0] = 0;
   }
-  if (a.T <= step)
+  if (a.rows_each)
+    put_fixed_rows(a, ends, before, lens, top, rank * threads + tid, step);
+  else if (a.T <= step)
     put_rows<1>(a, ends, before, lens, top, rank * threads + tid, step);
   else
     put_rows<4>(a, ends, before, lens, top, rank * threads + tid, step);
@@ -271,14 +300,15 @@ __global__ void __launch_bounds__(kMaxThreads) plan_kernel(const PlanArgs a) {
 
 moe_status_t launch_batch_plan(const int32_t *new_lens, const int32_t *seq_lens, int B, int page, int num_pages,
                                int32_t *table, int64_t ts, int max_pages, int32_t *free_pages, const int32_t *free_count,
-                               int32_t *lens_out, int32_t *count_out, int32_t *offsets, int T, int32_t *slots,
+                               int32_t *lens_out, int32_t *count_out, int32_t *offsets, int T, int rows_each, int32_t *slots,
                                int32_t *positions, int32_t *seq_ids, unsigned int *status, cudaStream_t stream,
                                int *launches) {
   int log_b = 1;
   while (1 << log_b <= B) ++log_b;
   const int wide = aligned16(slots) && (!positions || aligned16(positions)) && (!seq_ids || aligned16(seq_ids));
   const PlanArgs a = {new_lens, seq_lens, free_count, table, free_pages, lens_out, count_out, offsets, slots,
-                      positions, seq_ids, status, ts, B, T, page, num_pages, max_pages, log_b, wide, Divisor(page)};
+                      positions, seq_ids, status, ts, B, T, rows_each, page, num_pages, max_pages, log_b, wide, Divisor(page),
+                      Divisor(rows_each > 1 ? rows_each : 2)};
   static PerDevice configured;
   const int set = configured.get([] {
     return cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 12 * kMaxB) == cudaSuccess &&

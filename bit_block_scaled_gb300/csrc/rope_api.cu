@@ -40,10 +40,11 @@ extern "C" {
 moe_status_t moe_batch_plan(const int32_t *new_lens, const int32_t *seq_lens, int B, int page_size, int num_pages,
                             int32_t *block_table, int64_t table_stride, int max_pages, int32_t *free_pages,
                             const int32_t *free_count, int32_t *seq_lens_out, int32_t *free_count_out, int32_t *offsets,
-                            int T, int32_t *slots, int32_t *positions, int32_t *seq_ids, void *ws, moe_stream_t stream) {
+                            int T, int rows_each, int32_t *slots, int32_t *positions, int32_t *seq_ids, void *ws,
+                            moe_stream_t stream) {
   int *n = launch_counter();
   *n = 0;
-  if (B < 0 || T < 0 || T > 1 << 28 || !aligned16(ws)) return MOE_ERR_INVALID_ARG;
+  if (B < 0 || T < 0 || T > 1 << 28 || rows_each < 0 || rows_each > 1 << 28 || !aligned16(ws)) return MOE_ERR_INVALID_ARG;
   if (page_size < 16 || page_size % 16 || page_size > 4096) return MOE_ERR_INVALID_ARG;
   if (num_pages < 1 || (int64_t)num_pages * page_size >= (int64_t)1 << 31) return MOE_ERR_INVALID_ARG;
   if (max_pages < 0 || ((int64_t)max_pages + 1) * page_size >= (int64_t)1 << 31) return MOE_ERR_INVALID_ARG;
@@ -56,7 +57,7 @@ moe_status_t moe_batch_plan(const int32_t *new_lens, const int32_t *seq_lens, in
   if ((offsets && !aligned4(offsets)) || (positions && !aligned4(positions)) || (seq_ids && !aligned4(seq_ids)))
     return MOE_ERR_INVALID_ARG;
   return launch_batch_plan(new_lens, seq_lens, B, page_size, num_pages, block_table, table_stride, max_pages, free_pages,
-                           free_count, seq_lens_out, free_count_out, offsets, T, slots, positions, seq_ids, status_of(ws),
+                           free_count, seq_lens_out, free_count_out, offsets, T, rows_each, slots, positions, seq_ids, status_of(ws),
                            (cudaStream_t)stream, n);
 }
 

@@ -538,11 +538,14 @@ moe_status_t moe_attn_decode(const void *q, int q_type, int64_t q_stride_b,
  *     behind those in use.
  * Out: seq_lens_out [B] (old plus new, 0 for an ended one, else unchanged) and
  * free_count_out [1], which may be seq_lens and free_count; offsets [B + 1] (or
- * NULL): where each sequence's rows begin, the sum of max(new_lens, 0) before it
- * (served or not, at most 2^31 - 1). For row t < T, token i of sequence b: slots[t] (for moe_kv_write),
- * positions[t] = seq_lens[b] + i, seq_ids[t] = b (either may be NULL); rows of a
- * sequence that is not served have slot -1 and position 0, rows past the last token
- * slot -1, position 0, sequence -1.
+ * NULL): where each sequence's rows begin. With rows_each 0 the T rows are packed,
+ * the tokens of one sequence behind those of the one before, served or not; else
+ * sequence b has the rows from b * rows_each on, its tokens first (1 for one token
+ * a sequence, where idle or ended ones keep their row; one with more tokens than rows
+ * is not served and asks for no page). Offsets stay at 2^31 - 1 once they are there. For row t < T,
+ * token i of sequence b: slots[t] (for moe_kv_write), positions[t] = seq_lens[b] +
+ * i, seq_ids[t] = b (either may be NULL); rows of a sequence that is not served have
+ * slot -1 and position 0, rows without a token slot -1, position 0, sequence -1.
  * Latched in ws: MOE_ERR_CAPACITY for a sequence that is not served; MOE_ERR_BAD_INDEX
  * for a length below 0 or past the row (that sequence is left as it is), a
  * free_count outside 0..num_pages (taken as the nearest), more pages than the stack
@@ -553,7 +556,8 @@ moe_status_t moe_attn_decode(const void *q, int q_type, int64_t q_stride_b,
 moe_status_t moe_batch_plan(const int32_t *new_lens, const int32_t *seq_lens, int B, int page_size, int num_pages,
                             int32_t *block_table, int64_t table_stride, int max_pages, int32_t *free_pages,
                             const int32_t *free_count, int32_t *seq_lens_out, int32_t *free_count_out, int32_t *offsets,
-                            int T, int32_t *slots, int32_t *positions, int32_t *seq_ids, void *ws, moe_stream_t stream);
+                            int T, int rows_each, int32_t *slots, int32_t *positions, int32_t *seq_ids, void *ws,
+                            moe_stream_t stream);
 
 /* Pairs of a head's first rot_dim columns: (i, i + rot_dim / 2), or (2i, 2i + 1). */
 typedef enum { MOE_ROPE_HALF = 0, MOE_ROPE_INTERLEAVED = 1 } moe_rope_layout_t;

@@ -9,7 +9,7 @@ import numpy as np
 CAPACITY, BAD_INDEX = 1, 2
 
 
-def batch_plan(new, lens, table, free, count, page, T):
+def batch_plan(new, lens, table, free, count, page, T, rows_each=0):
     """All as lists or arrays -> dict of slots, positions, seq_ids, offsets, lens, count, table, free, and the errors (a
     sum of CAPACITY and BAD_INDEX)."""
     new, lens = [int(x) for x in new], [int(x) for x in lens]
@@ -36,9 +36,12 @@ def batch_plan(new, lens, table, free, count, page, T):
     offsets, top, asked, left, row = [0], count, 0, count, 0
     for b in range(B):
         n = max(new[b], 0)
-        seqs[min(row, T):min(row + n, T)] = b
+        if rows_each:
+            row = b * rows_each
+        shown = min(n, rows_each) if rows_each else n  # tokens that have rows of their own
+        seqs[min(row, T):min(row + shown, T)] = b
         if n > 0 and valid[b]:
-            if lens[b] + n <= cols * page:
+            if lens[b] + n <= cols * page and (not rows_each or (n <= rows_each and row + n <= T)):
                 held = -(-lens[b] // page)
                 need = -(-(lens[b] + n) // page) - held
                 asked += need
@@ -63,7 +66,7 @@ def batch_plan(new, lens, table, free, count, page, T):
                     errors.add(CAPACITY)
             else:
                 errors.add(CAPACITY)
-        row += n
+        row += rows_each or n
         offsets.append(min(row, 2 ** 31 - 1))
     return dict(slots=slots, positions=positions, seq_ids=seqs, offsets=np.array(offsets), lens=np.array(out_lens, dtype=np.int64),
                 count=left, table=table, free=free, errors=sum(errors))

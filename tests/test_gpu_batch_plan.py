@@ -24,7 +24,7 @@ def status_bits(ws):
     return (P.CAPACITY if word & (1 << 7) else 0) + (P.BAD_INDEX if word & (1 << 4) else 0), word & ~((1 << 7) | (1 << 4))
 
 
-def run(new, lens, table, free, count, page, T, in_place=False, bare=False):
+def run(new, lens, table, free, count, page, T, in_place=False, bare=False, rows_each=0):
     B = len(lens)
     n, l, f, c = dev(new), dev(lens), dev(free), dev([count])
     t = dev(np.asarray(table).reshape(B, np.asarray(table).size // B))
@@ -36,7 +36,7 @@ def run(new, lens, table, free, count, page, T, in_place=False, bare=False):
     lo, co = (l, c) if in_place else (torch.full_like(l, 77), torch.full_like(c, 77))
     ws = ws_status()
     extra = {} if bare else dict(positions=pos, seq_ids=seqs, offsets=offs)
-    moe.moe_batch_plan(n, l, t, f, c, page, slots, lo, co, ws, **extra)
+    moe.moe_batch_plan(n, l, t, f, c, page, slots, lo, co, ws, rows_each=rows_each, **extra)
     errors, other = status_bits(ws)
     assert other == 0 and (wide[:, t.shape[1]:] == 99).all()
     out = dict(slots=slots, lens=lo, count=co, table=t, free=f)
@@ -47,7 +47,8 @@ def run(new, lens, table, free, count, page, T, in_place=False, bare=False):
 
 def check(new, lens, table, free, count, page, T, **kw):
     got = run(new, lens, table, free, count, page, T, **kw)
-    ref = P.batch_plan(new, lens, np.asarray(table).reshape(len(lens), np.asarray(table).size // len(lens)), free, count, page, T)
+    ref = P.batch_plan(new, lens, np.asarray(table).reshape(len(lens), np.asarray(table).size // len(lens)), free, count, page, T,
+                       kw.get("rows_each", 0))
     for k, v in got.items():
         np.testing.assert_array_equal(v.reshape(-1) if k == "count" else v, ref[k], err_msg=k)
     return ref
@@ -92,6 +93,16 @@ def test_shortages(seed):
     s = state(B, cols, page, seed, 100, 0.1 * (seed % 3), 0.1, spare=[0, 1, 50, 200, 400, 90][seed])
     ref = check(*s, page, [20000, 3000, 20000, 5000, 100, 1][seed])
     assert ref["errors"] == P.CAPACITY
+
+
+@pytest.mark.parametrize("B,cols,page,most,rows_each,T", [
+    (1, 3, 16, 1, 1, 1), (64, 20, 16, 1, 1, 64), (700, 12, 48, 1, 1, 700), (90, 20, 16, 4, 4, 360), (90, 20, 16, 6, 4, 350),
+    (1025, 9, 16, 3, 3, 3075), (4096, 5, 16, 7, 7, 28672), (3, 40, 32, 500, 600, 1700), (5, 9, 16, 1, 1 << 28, 9)])
+def test_fixed_rows(B, cols, page, most, rows_each, T):
+    """Sequence b keeps its rows, whatever the others do."""
+    s = state(B, cols, page, B + most, most, 0.2, 0.2)
+    check(*s, page, T, rows_each=rows_each)
+    check(*state(B, cols, page, B, most, 0.1, 0.1, spare=B // 8), page, T, rows_each=rows_each, in_place=True)
 
 
 def test_in_place_and_without_the_rest():

@@ -187,3 +187,79 @@ def test_linear_many_tokens(fmt, T, N, K):
 @pytest.mark.parametrize("N,ldo", [(384, 384), (333, 333), (333, 400), (40, 41)])
 def test_linear_many_tokens_types(fmt, dtype, N, ldo):
     check_linear(900, N, 608, fmt, dtype, True, ldo=ldo, gscale=0.0037 if fmt == "nvfp4" else None)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T", [3, 40, 150, 600])
+def test_linear_rows_that_hold_no_numbers(fmt, T):
+    """A NaN or an infinity makes its token's outputs NaN and no other's; rows of zeros and of extremes are as they are."""
+    x = rows(T, 320, torch.bfloat16, T)
+    x[1, 5] = float("inf")
+    x[T - 1, 319] = float("nan")
+    x[0] = 0
+    if T > 3:
+        x[2] = 1e30
+        x[3] = 1e-38
+    out = check_linear(T, 200, 320, fmt, "bf16", True, x=x)
+    assert torch.isnan(out[1]).all() and torch.isnan(out[T - 1]).all() and torch.isnan(out).any(dim=1).sum() == 2
+
+
+def test_linear_weights_without_numbers():
+    """An MXFP4 block of exponent 255 makes its output column NaN, and no other."""
+    x, w = rows(20, 128, torch.bfloat16), rows(130, 128, torch.bfloat16, 1)
+    w[129, 70] = float("nan")
+    (_, xm), (_, wm) = operand(20, 128, "mxfp4"), operand(130, 128, "mxfp4")
+    moe.moe_fp4_quantize(x, xm)
+    moe.moe_fp4_quantize(w, wm)
+    out = torch.zeros(20, 130, device="cuda")
+    moe.moe_fp4_linear(xm, wm, None, out, ws_status())
+    assert torch.isnan(out[:, 129]).all() and not torch.isnan(out[:, :129]).any()
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 640, 2880), (24, 640, 2880), (100, 640, 8192), (333, 2880, 1024), (2000, 1500, 2880)])
+def test_linear_repeats_itself_and_is_captured(T, N, K):
+    """Bit for bit, on another stream and in a graph whose inputs change."""
+    x, w = rows(T, K, torch.bfloat16), rows(N, K, torch.bfloat16, 1)
+    (bx, xm), (_, wm) = operand(T, K, "nvfp4"), operand(N, K, "nvfp4")
+    moe.moe_fp4_quantize(w, wm)
+    moe.moe_fp4_quantize(x, xm)
+    ws = ws_status()
+    a, b = torch.zeros(T, N, device="cuda"), torch.zeros(T, N, device="cuda")
+    moe.moe_fp4_linear(xm, wm, None, a, ws)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        moe.moe_fp4_linear(xm, wm, None, b, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
+    g, y = torch.cuda.CUDAGraph(), x.clone()
+    with torch.cuda.graph(g, stream=s):
+        moe.moe_fp4_quantize(y, xm)
+        moe.moe_fp4_linear(xm, wm, None, b, ws)
+    b.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
+    y.copy_(x.flip(0))
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(b, a.flip(0)) and moe.moe_read_status(ws) == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_a_part_of_the_rows(fmt):
+    """Operands over the first rows of larger buffers, as a padded batch has: what lies behind stays, in the output too."""
+    T, N, K, most = 70, 130, 96, 300
+    q = torch.full((most, K // 2), 0xFF, dtype=torch.uint8, device="cuda")
+    s = torch.full((moe.moe_fp4_scale_bytes(fmt, most, K),), 0xFF, dtype=torch.uint8, device="cuda")  # NaN to both formats
+    r = torch.full((most,), float("nan"), device="cuda") if fmt == "nvfp4" else None
+    xm = moe.fp4(q[:T], s[:moe.moe_fp4_scale_bytes(fmt, T, K)], fmt, None if r is None else r[:T])
+    x, w = rows(T, K, torch.bfloat16), rows(N, K, torch.bfloat16, 1)
+    (wq, wsc, wr), wm = operand(N, K, fmt)
+    moe.moe_fp4_quantize(x, xm)
+    moe.moe_fp4_quantize(w, wm)
+    out = torch.full((most, N), 5.0, dtype=torch.bfloat16, device="cuda")
+    moe.moe_fp4_linear(xm, wm, None, out[:T], ws_status())
+    assert (out[T:] == 5).all() and (q[T:] == 0xFF).all()
+    ref, mag = F.linear(F.values(*F.quantise_rows(f64(x), fmt), fmt), F.values(*F.quantise_rows(f64(w), fmt), fmt))
+    assert (np.abs(f64(out[:T]) - ref) <= 2.0 ** -8 * np.abs(ref) + 6 * 2.0 ** -22 * mag).all()

@@ -39,6 +39,14 @@ def test_all_or_nothing():
     assert list(p["lens"]) == [0, 1, 16] and p["errors"] & P.CAPACITY
 
 
+def test_fixed_rows():
+    p = P.batch_plan([1, 0, 3, -1, 1], [15, 4, 0, 16, 16], np.array([[0], [1], [-1], [2], [3]]), [4, -1, -1, -1, -1], 1, 16, 10, 2)
+    # the third has more tokens than rows, the last no column for its next page
+    assert list(p["lens"]) == [16, 4, 0, 0, 16] and p["errors"] == P.CAPACITY and p["count"] == 2
+    assert list(p["slots"]) == [15] + [-1] * 9 and list(p["offsets"]) == [0, 2, 4, 6, 8, 10]
+    assert list(p["seq_ids"]) == [0, -1, -1, -1, 2, 2, -1, -1, 4, -1] and p["positions"][0] == 15
+
+
 def test_rotations():
     x = np.random.default_rng(0).standard_normal((3, 2, 8))
     f, amp = R.frequencies(6)
