@@ -12,9 +12,10 @@
 // the 8 significands of s and 7 ties, as amax16 / r / 6 is for the ties of E4M3
 // (tests/test_fp4_rounding.py tries them all).
 //
-// Bound by memory: 2 bytes of a value are read, 9/16 or 17/32 written. A lane
-// holds 16 consecutive values (an NVFP4 block, half an MXFP4 one), a row stays
-// in the registers of 1 to 8 warps, so it is read once.
+// Bound by memory: 2 bytes of a value are read, 9/16 or 17/32 written (16384 x
+// 8192 into MXFP4 at 99% of the copy bandwidth, into NVFP4, which waits for a row's
+// largest value first, at 83%). A lane holds 16 consecutive values (an NVFP4 block,
+// half an MXFP4 one), a row stays in the registers of 1 to 8 warps, so it is read once.
 #include "fp4.cuh"
 #include "kernels.h"
 #include "quant.cuh"
@@ -196,20 +197,22 @@ __global__ void __launch_bounds__(256) fp4_pack_scales_kernel(const uint8_t *pla
 moe_status_t launch_fp4_quantize(const void *x, int type, int64_t ld, const moe_fp4_t &f, cudaStream_t stream,
                                  int *launches) {
   QuantArgs a = {x, ld, f.q, f.scales, f.row_scale, f.rows, f.K, f.K / 16, fp4_tiles_k(f.fmt, f.K), 1};
-  // Few rows: as many warps a row as there are loads for, so that a lane waits for one load; many rows: one warp a
-  // row while 8 loads a lane hold it (4 in fp32, whose values take twice the registers).
-  const int most = type == MOE_FP32 ? 4 : 8;
+  // Few rows: as many warps a row as there are loads for, so that a lane waits for one load. Many rows: one warp a row while
+  // 4 loads a lane hold it (2 in fp32, whose values take twice the registers): with 8, registers leave room for half the
+  // warps (16384 x 8192 into NVFP4 67 us against 61, into MXFP4 58 against 51), with 2, rows wait for more warps (69, 53).
+  const int most = type == MOE_FP32 ? 2 : 4;
   auto units_of = [&](int w) { return (a.units + 32 * w - 1) / (32 * w); };
   if (a.T <= 4 * 152)
     while (a.W < kWarps && units_of(a.W) > 1) a.W *= 2;
   else
     while (a.W < kWarps && units_of(a.W) > most) a.W *= 2;
-  const int need = units_of(a.W), p = need <= 1 ? 0 : need <= 2 ? 1 : need <= 4 ? 2 : 3;
+  const int need = units_of(a.W), p = need <= 4 ? need - 1 : 4;
   if (need > 8) return MOE_ERR_UNSUPPORTED;
   using Kernel = void (*)(QuantArgs);
-#define MOE4_Q(F, T) {fp4_quantize_kernel<F, T, 1>, fp4_quantize_kernel<F, T, 2>, fp4_quantize_kernel<F, T, 4>, fp4_quantize_kernel<F, T, 8>}
+#define MOE4_Q(F, T) {fp4_quantize_kernel<F, T, 1>, fp4_quantize_kernel<F, T, 2>, fp4_quantize_kernel<F, T, 3>, \
+                      fp4_quantize_kernel<F, T, 4>, fp4_quantize_kernel<F, T, 8>}
 #define MOE4_Q_TYPES(F) {MOE4_Q(F, MOE_BF16), MOE4_Q(F, MOE_FP16), MOE4_Q(F, MOE_FP32)}
-  static const Kernel kernels[2][3][4] = {MOE4_Q_TYPES(MOE_FMT_NVFP4), MOE4_Q_TYPES(MOE_FMT_MXFP4)};
+  static const Kernel kernels[2][3][5] = {MOE4_Q_TYPES(MOE_FMT_NVFP4), MOE4_Q_TYPES(MOE_FMT_MXFP4)};
 #undef MOE4_Q_TYPES
 #undef MOE4_Q
   const int per = kWarps / a.W;
