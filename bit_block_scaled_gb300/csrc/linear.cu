@@ -204,8 +204,8 @@ __global__ void __launch_bounds__(kThreads) narrow_kernel(const __grid_constant_
   if (p.split > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   tc_fence_after();
   const uint32_t tmem = tmem_at;
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();
 
   bool ok = true;
   if (warp == 0) {
@@ -524,8 +524,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1) wid
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = tmem_at;
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();
 
   const int total = p.tiles_t * p.tiles_n, all = (p.K + kStageK - 1) / kStageK;
   bool ok = true;
@@ -751,7 +751,7 @@ Shape choose(int T, int N, int K) {
       int bytes = own * stage_bytes + (split > 1 ? (tn + 8) * 512 : 0);
       if (bytes > (int)kMaxSmem) bytes = kMaxSmem;
       const int together = (int)kMaxSmem / (bytes + 2048) > 1 ? (int)kMaxSmem / (bytes + 2048) : 1;
-      const int64_t ctas = tiles * split, held = (split == 1 ? sms : sms / 19 * (19 / split) * split) * together;
+      const int64_t ctas = tiles * split, held = (split == 1 || sms < 19 ? sms : sms / 19 * (19 / split) * split) * together;
       const int share = ((tn < T ? tn : T) + split - 1) / split;
       const float join = split == 1 ? 0.f : tn == 16 ? 0.4f : 0.9f + 0.03f * share;
       const float us = ((ctas + sms - 1) / sms) * own * kStageUs[i] + ((ctas + held - 1) / held - 1) * 3.0f + join + 0.005f * tn;
@@ -787,6 +787,7 @@ moe_status_t launch_fp4_linear(const moe_fp4_t &x, const moe_fp4_t &w, const voi
   const int wn = wide ? kWideN : 128;
   a.tiles_t = (a.T + tn - 1) / tn;
   a.tiles_n = (a.N + wn - 1) / wn;
+  if ((int64_t)a.tiles_t * a.tiles_n * shape.split >= (int64_t)1 << 30) return MOE_ERR_UNSUPPORTED;
   if (!map_codes(&a.tm_x, x.q, a.T, a.K, wide ? 128 : tn) || !map_codes(&a.tm_w, w.q, a.N, a.K, wide ? kWideN / 2 : 128) ||
       !map_scales(&a.tm_xs, x.scales, x.fmt, a.T, a.K) || !map_scales(&a.tm_ws, w.scales, w.fmt, a.N, a.K))
     return MOE_ERR_CUDA;

@@ -172,8 +172,8 @@ __global__ void __launch_bounds__(kMaxThreads) plan_kernel(const PlanArgs a) {
   int *ends = shared, *before = ends + a.B, *lens = before + a.B;
   __shared__ Sums warp_sums[kWarps];
   __shared__ int given;  // pages: the served that need some come before all others that do
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();
   uint32_t ranks, rank;
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));

@@ -632,7 +632,7 @@ moe_status_t moe_rope_kv_write(const moe_rope_t *rope, const int32_t *positions,
  * ------------------------------------------------------------------------- */
 
 /* A matrix [rows][K] in 4 bits. value = E2M1 code * block scale * row scale.
- *   MOE_FMT_NVFP4: E4M3 block scale for 16 values, row scales fp32;
+ *   MOE_FMT_NVFP4: E4M3 block scale (not negative) for 16 values, row scales fp32;
  *   MOE_FMT_MXFP4: E8M0 block scale (2^(byte - 127), 255 = NaN) for 32 values,
  *                  no row scales.
  * q as in moe_qweight_t. scales in tiles of 128 rows by 4 blocks, 512 bytes
