@@ -8,7 +8,7 @@
 //  * narrow (few tokens): the weights are the 128 rows of the MMA, the tokens
 //    its columns. K is split over a cluster of CTAs whose partial sums are
 //    joined through distributed shared memory in the order of K. Bound by
-//    latency for one token (4.0 us at 5120 x 2880), then by what an SM can take
+//    latency for one token (3.8 us at 5120 x 2880), then by what an SM can take
 //    in, 64 bytes a cycle (333 x 2880 x 4096 7.4 us).
 //  * wide (many tokens): pairs of CTAs (cta_group::2) share 256 tokens x 256
 //    weight rows, persistent, two accumulators so that one tile is written
