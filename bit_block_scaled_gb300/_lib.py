@@ -22,7 +22,8 @@ SCORE = {"softmax": 0, "sigmoid": 1}
 GROUP_SCORE = {"max": 0, "top2": 1}
 NORM = {"rms": 0, "layer": 1}
 ROPE_LAYOUT = {"half": 0, "interleaved": 1}
-ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "llama3": 4}
+#: "llama3" is what checkpoints' configurations call the scaling by wavelength
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "wavelength": 4, "llama3": 4}
 KV_FMT = {"bf16": 0, "fp16": 1, "fp8": 2, "nvfp4": 3}
 STATUS_BYTES = 256
 

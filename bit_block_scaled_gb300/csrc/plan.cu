@@ -4,9 +4,10 @@
 // Every CTA of one cluster reads all B sequences and sums their tokens and pages
 // (a scan, up to 4 sequences a thread, in 32 bits that saturate); the work that
 // the sums lay out is then shared by the cluster: token rows and fresh pages by
-// number, each found by a binary search of the sums in shared memory. All inputs are read before the cluster's first barrier and nothing that
-// was read is written before it, so that outputs may be the inputs; the pages of
-// ended sequences are on the stack before the second, after which pages are taken.
+// number, each found by a binary search of the sums in shared memory. All inputs are read before the first barrier and nothing that was read
+// is written before it, so that outputs may be the inputs; the pages of ended
+// sequences are on the stack before the second, after which pages are taken. The
+// barriers are the cluster's only where there is something to keep apart.
 //
 // Bound by latency: 16 bytes a sequence and 12 a token. One launch, three rounds
 // of memory (lengths, pages, rows): 64 sequences of one token each 2.5 us, 500
@@ -180,8 +181,9 @@ __global__ void __launch_bounds__(kMaxThreads) plan_kernel(const PlanArgs a) {
   const int tid = threadIdx.x, threads = blockDim.x, warp = tid >> 5, lane = tid & 31;
   const bool first = rank == 0;
   const int cap = a.max_pages * a.page;
-  auto everyone = [&] {
-    if (ranks > 1)
+  // the cluster where what follows may write what others have yet to read, or read what they write; else the CTA
+  auto everyone = [&](bool all_ranks) {
+    if (ranks > 1 && all_ranks)
       cluster_sync();
     else
       __syncthreads();
@@ -239,7 +241,7 @@ __global__ void __launch_bounds__(kMaxThreads) plan_kernel(const PlanArgs a) {
   const int room = a.num_pages - count;
   if (all.back > room && first && tid == 0) raise_status(a.status, MOE_ERR_BAD_INDEX);
   const int top = count + min(all.back, room);
-  everyone();  // all has been read
+  everyone(a.lens_out == a.seq_lens || a.count_out == a.free_count);  // all has been read
 
   // who is served, and the ended sequences' pages onto the stack
 #pragma unroll
@@ -271,19 +273,24 @@ __global__ void __launch_bounds__(kMaxThreads) plan_kernel(const PlanArgs a) {
     }
     at = add(at, mine[i]);
   }
-  everyone();  // the sums are there, and the stack is whole
+  everyone(all.back > 0);  // the sums are there, and the stack is whole
 
   const int step = ranks * threads;
   auto fresh = [&](int j) {  // page number j of those that are given, -1 for one that is none
     const int p = a.free_pages[top - 1 - j];
     return p >= 0 && p < a.num_pages ? p : -1;
   };
-  for (int j = rank * threads + tid; j < given; j += step) {
-    const int b = upper(before, a.B, a.log_b, j) - 1;  // the last that no more than j pages lie before: it needs some
-    const int p = fresh(j);
+  // pages into the table: the first of a thread is on its way while its rows are made
+  auto put_page = [&](int j, int b, int p) {
     a.table[b * a.ts + pages_of(lens[b]) + (j - before[b])] = p;
     if (p < 0) raise_status(a.status, MOE_ERR_BAD_INDEX);
-  }
+  };
+  // the last that no more than j pages lie before: it needs some
+  auto owner = [&](int j) { return upper(before, a.B, a.log_b, j) - 1; };
+  const int j0 = rank * threads + tid;
+  int b0 = 0, p0 = 0;
+  if (j0 < given) b0 = owner(j0), p0 = fresh(j0);
+  for (int j = j0 + step; j < given; j += step) put_page(j, owner(j), fresh(j));
   if (first && tid == 0) {
     *a.count_out = top - given;
     if (a.offsets) a.offsets[0] = 0;
@@ -294,6 +301,7 @@ __global__ void __launch_bounds__(kMaxThreads) plan_kernel(const PlanArgs a) {
     put_rows<1>(a, ends, before, lens, top, rank * threads + tid, step);
   else
     put_rows<4>(a, ends, before, lens, top, rank * threads + tid, step);
+  if (j0 < given) put_page(j0, b0, p0);
 }
 
 }  // namespace

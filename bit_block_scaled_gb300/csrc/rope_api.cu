@@ -73,8 +73,8 @@ moe_status_t moe_rope_table(const moe_rope_config_t *c, uint64_t *turns, float *
   if (!c || !turns || !amplitude) return MOE_ERR_INVALID_ARG;
   const int R = c->rot_dim;
   if (R < 2 || R % 2 || R > 256 || !(c->base > 1.0) || !isfinite(c->base)) return MOE_ERR_INVALID_ARG;
-  if (c->scaling < MOE_ROPE_PLAIN || c->scaling > MOE_ROPE_LLAMA3) return MOE_ERR_INVALID_ARG;
-  const bool scaled = c->scaling != MOE_ROPE_PLAIN, bands = c->scaling == MOE_ROPE_YARN || c->scaling == MOE_ROPE_LLAMA3;
+  if (c->scaling < MOE_ROPE_PLAIN || c->scaling > MOE_ROPE_WAVELENGTH) return MOE_ERR_INVALID_ARG;
+  const bool scaled = c->scaling != MOE_ROPE_PLAIN, bands = c->scaling == MOE_ROPE_YARN || c->scaling == MOE_ROPE_WAVELENGTH;
   if (scaled && (!(c->factor > 0.0) || !isfinite(c->factor))) return MOE_ERR_INVALID_ARG;
   if (bands && (c->original_len < 1 || !(c->high > c->low) || !(c->low > 0.0) || !isfinite(c->high))) return MOE_ERR_INVALID_ARG;
   if (c->scaling == MOE_ROPE_NTK && R == 2) return MOE_ERR_INVALID_ARG;
@@ -96,7 +96,7 @@ moe_status_t moe_rope_table(const moe_rope_config_t *c, uint64_t *turns, float *
     double keep = 1.0;  // the share that is not stretched
     if (c->scaling == MOE_ROPE_LINEAR) keep = 0.0;
     if (c->scaling == MOE_ROPE_YARN) keep = 1.0 - fmin(fmax((i - lo) / fmax(hi - lo, 0.001), 0.0), 1.0);
-    if (c->scaling == MOE_ROPE_LLAMA3) keep = fmin(fmax((L * f / kTwoPi - c->low) / (c->high - c->low), 0.0), 1.0);
+    if (c->scaling == MOE_ROPE_WAVELENGTH) keep = fmin(fmax((L * f / kTwoPi - c->low) / (c->high - c->low), 0.0), 1.0);
     if (keep < 1.0) f = f / c->factor * (1.0 - keep) + f * keep;
     turns[i] = turns_of(f);
   }

@@ -571,20 +571,20 @@ typedef enum { MOE_ROPE_HALF = 0, MOE_ROPE_INTERLEAVED = 1 } moe_rope_layout_t;
  *           of low (high and low: turns over the original length, 32 and 1), both
  *           rounded outwards if truncate, lo >= 0, hi <= rot_dim - 1; amplitude
  *           0.1 ln(factor) + 1 for factors above 1
- *   LLAMA3  the same blend with g = clamp((original_len f / (2 pi) - low) / (high -
+ *   WAVELENGTH  the same blend with g = clamp((original_len f / (2 pi) - low) / (high -
  *           low), 0, 1) (low 1, high 4); amplitude 1 */
 typedef enum {
-  MOE_ROPE_PLAIN = 0, MOE_ROPE_LINEAR = 1, MOE_ROPE_NTK = 2, MOE_ROPE_YARN = 3, MOE_ROPE_LLAMA3 = 4
+  MOE_ROPE_PLAIN = 0, MOE_ROPE_LINEAR = 1, MOE_ROPE_NTK = 2, MOE_ROPE_YARN = 3, MOE_ROPE_WAVELENGTH = 4
 } moe_rope_scaling_t;
 
 typedef struct {
   int32_t rot_dim;      /* even, 2..256                              */
   int32_t scaling;      /* moe_rope_scaling_t                        */
-  int32_t original_len; /* YARN, LLAMA3                              */
+  int32_t original_len; /* YARN, WAVELENGTH                          */
   int32_t truncate;     /* YARN                                      */
   double base;          /* above 1                                   */
   double factor;        /* above 0; PLAIN: ignored                   */
-  double low, high;     /* YARN, LLAMA3: 0 < low < high              */
+  double low, high;     /* YARN, WAVELENGTH: 0 < low < high          */
   double amplitude;     /* of cosine and sine; 0: the scaling's own  */
 } moe_rope_config_t;
 
