@@ -602,8 +602,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1) wid
       scales[e] = wr;
       biases[e] = bi;
       const float xr = t < p.T ? row_scale(p.xr, p.xr_stride, t) : 0.f;
-      asm volatile("bar.sync 1, %0;" ::"r"(kWideEpi * 32) : "memory");
-      ok = warp_wait(accfull(acc), (n >> 1) & 1);
+      ok = bar_and(1, kWideEpi * 32, mbar_wait(accfull(acc), (n >> 1) & 1));  // all go on, or none; scales and biases are there
       if (!ok) break;
       tc_fence_after();
       // the columns that the next tile has, too, are the first's last 48 and the second's first: the last two pieces of
@@ -729,11 +728,12 @@ struct Shape {
 
 // The shape of least estimated time, in us beyond what every launch takes. A stage of 256 values of K takes as long as
 // its bytes take into an SM (64 a cycle: 0.18 to 0.30 us for 16 to 128 tokens, 0.31 for the pairs' 256). CTAs that fit
-// the SMs' shared memory together share that; another round of them takes 3 us more. Clusters are laid into groups of
-// about 19 SMs. Joining parts of K takes 0.4 us for 16 tokens, 0.9 and 0.03 a token that a CTA sums for more; the wide
-// kernel's last tile is written in 1 us more. Measured, in us, the chosen first: 1 x 5120 x 2880 16 tokens in 4 parts 4.0,
-// whole 5.2; 8 x 8192 x 8192 16 in 2 7.3, whole 10.2; 64 x 5120 x 2880 64 whole 6.5, in 4 11.6; 333 x 2880 x 4096 64
-// whole 7.4, 128 7.7, wide 8.9; 1024 x 4096 x 4096 wide 9.8, 128 16.7.
+// the SMs' shared memory together share that, for 0.5 us more; another round of them takes 3. Clusters are laid into
+// groups of about 19 SMs. Joining parts of K takes 0.4 us for 16 tokens, for more 1 (128 tokens: 1.6) and 0.03 a token that a
+// CTA sums; the wide kernel's last tile is written in 1 us more. Measured, in us, the chosen first: 1 x 5120 x 2880 16
+// tokens in 3 parts 3.7, whole 5.2; 8 x 8192 x 8192 16 in 2 7.3, whole 10.1; 64 x 5120 x 2880 64 in 3 6.5, whole 6.4, in 4
+// 11.6; 100 x 2688 x 4096 64 in 3 6.4, whole 7.1, 128 in 6 7.3; 333 x 2880 x 4096 64 whole 7.4, 128 7.7, wide 8.9; 1024 x
+// 4096 x 4096 wide 9.8, 128 16.6.
 Shape choose(int T, int N, int K) {
   const int stages = (K + kStageK - 1) / kStageK, sms = sm_count();
   const int64_t wide_tiles = (int64_t)((T + 255) / 256) * ((N + kWideN - 1) / kWideN), pairs = sms / 2;
@@ -753,8 +753,9 @@ Shape choose(int T, int N, int K) {
       const int together = (int)kMaxSmem / (bytes + 2048) > 1 ? (int)kMaxSmem / (bytes + 2048) : 1;
       const int64_t ctas = tiles * split, held = (split == 1 || sms < 19 ? sms : sms / 19 * (19 / split) * split) * together;
       const int share = ((tn < T ? tn : T) + split - 1) / split;
-      const float join = split == 1 ? 0.f : tn == 16 ? 0.4f : 0.9f + 0.03f * share;
-      const float us = ((ctas + sms - 1) / sms) * own * kStageUs[i] + ((ctas + held - 1) / held - 1) * 3.0f + join + 0.005f * tn;
+      const float join = split == 1 ? 0.f : tn == 16 ? 0.4f : (tn == 128 ? 1.6f : 1.0f) + 0.03f * share;
+      const float us = ((ctas + sms - 1) / sms) * own * kStageUs[i] + ((ctas + held - 1) / held - 1) * 3.0f +
+                       (ctas > sms ? 0.5f : 0.f) + join + 0.005f * tn;
       if (us < least) least = us, best = {tn, split};
     }
     if (tn >= T) break;
