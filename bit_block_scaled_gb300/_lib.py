@@ -80,7 +80,7 @@ class RopeConfig(ctypes.Structure):
 
 
 class Rope(ctypes.Structure):
-    _fields_ = [("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("amplitude", ctypes.c_float),
+    _fields_ = [("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("amplitude", ctypes.c_double),
                 ("turns", ctypes.c_void_p), ("place", ctypes.c_int32)]  # behind moe_rope_t: where the table is (_place)
 
 
@@ -498,7 +498,7 @@ def moe_rope_table(rot_dim, base=10000.0, scaling="none", factor=1.0, original_l
     code = ROPE_SCALING[scaling] if isinstance(scaling, str) else int(scaling)
     if high is None:
         high = 32.0 if code == ROPE_SCALING["yarn"] else 4.0
-    turns, amp = np.zeros(max(int(rot_dim) // 2, 1), dtype=np.uint64), ctypes.c_float(0.0)
+    turns, amp = np.zeros(max(int(rot_dim) // 2, 1), dtype=np.uint64), ctypes.c_double(0.0)
     cfg = RopeConfig(int(rot_dim), code, int(original_len), int(bool(truncate)), float(base), float(factor), float(low),
                      float(high), float(amplitude))
     if rot_dim > 256:

@@ -45,26 +45,35 @@ struct RopeArgs {
   RopeTensor x[2];
   const unsigned long long *turns;
   const int32_t *positions;
-  float amplitude;
+  float2 amplitude;  // its nearest float and the rest
   int T, D, rot, tokens, head_blocks, heads_each;  // a CTA's tokens and heads
   Divisor by_pairs, by_items, by_heads;  // pairs of a head; threads that share one; heads_each
 };
 
-__device__ __forceinline__ float2 sine_of(unsigned long long turns, int position, float amplitude) {
+// Cosine and sine of position * frequency, times the amplitude (in two parts). Their root mean square errors are 1.9e-8 and
+// 1.2e-8 of the amplitude, a correct rounding's are 1.4e-8 and 1e-8: what is lost here is lost by every key, and more of
+// them fall on the other side of a border between two codes.
+__device__ __forceinline__ float2 sine_of(unsigned long long turns, int position, float2 amplitude) {
   const uint32_t f = (uint32_t)((turns * (unsigned long long)(long long)position) >> 32);  // of 2^-32 turns
   const uint32_t quarter = (f + 0x20000000u) >> 30;
-  const float x = (float)(int)(f - (quarter << 30)) * 0x1p-31f, z = x * x;  // half turns, at most a quarter
-  // Taylor's series of sin(pi x) and cos(pi x): the first terms left out are 2e-9 and 5e-10; pi in two parts
+  const int rest = (int)(f - (quarter << 30));  // at most 2^29: 24 bits of it, and the other 6 as a small angle
+  const float x = (float)(rest & ~63) * 0x1p-31f, dx = (float)(rest & 63) * (3.1415927f * 0x1p-31f);  // half turns; radians
+  const float z = x * x, dz = fmaf(x, x, -z);
+  // Taylor's series of sin(pi x) and of cos(pi x) - 1: the first terms left out are 2e-9 and 5e-10; pi in two parts
   float s = fmaf(z, 8.2145887e-2f, -5.9926453e-1f), c = fmaf(z, -2.5806891e-2f, 2.3533063e-1f);
   s = fmaf(z, s, 2.5501640f);
   s = fmaf(z, s, -5.1677128f);
-  s = fmaf(x, 3.1415927f, x * fmaf(z, s, -8.7422777e-8f));
   c = fmaf(z, c, -1.3352628f);
   c = fmaf(z, c, 4.0587121f);
   c = fmaf(z, c, -4.9348022f);
-  c = fmaf(z, c, 1.0f);
-  const float cc = (quarter & 1) ? -s : c, ss = (quarter & 1) ? c : s;
-  return (quarter & 2) ? make_float2(-cc * amplitude, -ss * amplitude) : make_float2(cc * amplitude, ss * amplitude);
+  const float sh = x * 3.1415927f;
+  c = fmaf(z, c, dz * c);
+  const float sl = fmaf(x, fmaf(z, s, -8.7422777e-8f), fmaf(x, 3.1415927f, -sh)) + fmaf(c, dx, dx);
+  c = fmaf(-sh, dx, c);
+  const float cosine = amplitude.x + fmaf(amplitude.x, c, amplitude.y);
+  const float sine = fmaf(amplitude.x, sh, fmaf(amplitude.x, sl, amplitude.y * sh));
+  const float cc = (quarter & 1) ? -sine : cosine, ss = (quarter & 1) ? cosine : sine;
+  return (quarter & 2) ? make_float2(-cc, -ss) : make_float2(cc, ss);
 }
 
 // Cosines and sines of the CTA's tokens: [tokens][pairs]. Where lanes take 8 pairs or 4 each, they are in the order in
@@ -113,136 +122,23 @@ __device__ __forceinline__ void rotate4(float (&v)[8], const float2 *cs, int i, 
   }
 }
 
-// A thread's share of a head. Where the pairs fall on 16-byte pieces (rot a multiple of 16) it is 16 columns, 8 pairs or
-// 16 that are not rotated; else a pair, or one column that is not rotated.
-template <int TYPE, bool HALF, bool PIECES>
-struct Item {
-  Raw8 a, b;
-  float x, y;
-  __device__ __forceinline__ void load(const RopeTensor &s, int64_t t, int h, int i, int rot) {
-    const int64_t in = t * s.its + h * s.ith;
-    if (PIECES) {
-      const bool turned = i < rot / 16;
-      const int c0 = turned && HALF ? 8 * i : 16 * i, c1 = turned && HALF ? rot / 2 + 8 * i : c0 + 8;
-      a = load_raw8(s.in, in + c0, TYPE);
-      b = load_raw8(s.in, in + c1, TYPE);
-    } else if (i < rot / 2) {
-      x = load_as_f32(s.in, in + (HALF ? i : 2 * i), TYPE);
-      y = load_as_f32(s.in, in + (HALF ? i + rot / 2 : 2 * i + 1), TYPE);
-    } else {
-      x = load_as_f32(s.in, in + i + rot / 2, TYPE);
-    }
-  }
-  __device__ __forceinline__ void store(const RopeTensor &s, int64_t t, int h, int i, int rot, const float2 *cs) {
-    const int64_t out = t * s.ots + h * s.oth;
-    if (PIECES) {
-      const bool turned = i < rot / 16;
-      const int c0 = turned && HALF ? 8 * i : 16 * i, c1 = turned && HALF ? rot / 2 + 8 * i : c0 + 8;
-      if (turned) {
-        float u[8], v[8];
-        raw8_to_f32(a, TYPE, u);
-        raw8_to_f32(b, TYPE, v);
-        if (HALF) {
-          rotate8(u, v, cs, i, rot);
-        } else {
-          rotate4(u, cs, i, 0, rot);
-          rotate4(v, cs, i, 1, rot);
-        }
-        a = f32_to_raw8(u, TYPE);
-        b = f32_to_raw8(v, TYPE);
-      }
-      store_raw8(s.out, out + c0, TYPE, a);
-      store_raw8(s.out, out + c1, TYPE, b);
-    } else if (i < rot / 2) {
-      const float2 w = cs[sine_at(i, rot)];
-      store_from_f32(s.out, out + (HALF ? i : 2 * i), TYPE, rotated_a(x, y, w));
-      store_from_f32(s.out, out + (HALF ? i + rot / 2 : 2 * i + 1), TYPE, rotated_b(x, y, w));
-    } else {
-      store_from_f32(s.out, out + i + rot / 2, TYPE, x);
-    }
-  }
-};
-
-// The heads [h0, h1) of tokens [t0, t0 + a.tokens), those of x[1] behind those of x[0]. A thread keeps its place in a head
-// and walks the heads, two at a time; the first two are asked for before the sines are made.
-template <int TYPE, bool HALF, bool PIECES>
-__device__ __forceinline__ void rotate_block(const RopeArgs &a, float2 *sines, int t0, int h0, int h1) {
-  constexpr int U = 2;
-  const int items = PIECES ? a.D / 16 : a.D - a.rot / 2, heads = h1 - h0;
-  const int first = a.by_items.div(threadIdx.x), i = threadIdx.x - first * items, step = a.by_items.div(kThreads);
-  const int tokens = min(a.tokens, a.T - t0);
-  const bool whole = heads == a.heads_each;  // the last heads may be fewer
-  const int rows = (int)threadIdx.x < step * items ? tokens * heads : 0;
-  Item<TYPE, HALF, PIECES> it[U];
-  bool made = false;
-  for (int r0 = first; r0 < rows || !made; r0 += U * step) {
-    int t[U], h[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = r0 + u * step;
-      t[u] = whole ? a.by_heads.div(r) : r / heads;
-      h[u] = h0 + r - t[u] * heads;
-      if (r < rows) {
-        const bool second = h[u] >= a.x[0].heads;
-        it[u].load(a.x[second], t0 + t[u], second ? h[u] - a.x[0].heads : h[u], i, a.rot);
-      }
-    }
-    if (!made) {
-      make_sines(sines, a, t0, tokens);
-      __syncthreads();
-      made = true;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (r0 + u * step < rows) {
-        const bool second = h[u] >= a.x[0].heads;
-        it[u].store(a.x[second], t0 + t[u], second ? h[u] - a.x[0].heads : h[u], i, a.rot, sines + t[u] * (a.rot / 2));
-      }
-  }
-}
-
-constexpr int kMaxTokens = 16;
-
-template <int TYPE, bool HALF, bool PIECES>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
-  __shared__ __align__(16) float2 sines[kMaxTokens * kMaxPairs];
-  pdl_wait();
-  pdl_trigger();
-  const int block = a.head_blocks == 1 ? blockIdx.x : blockIdx.x / a.head_blocks;
-  const int t0 = block * a.tokens, h0 = (blockIdx.x - block * a.head_blocks) * a.heads_each;
-  rotate_block<TYPE, HALF, PIECES>(a, sines, t0, h0, min(h0 + a.heads_each, a.x[0].heads + a.x[1].heads));
-}
-
-// ------------------------------------------------------- with the cache write
-struct WriteArgs {
-  RopeArgs q;
-  uint8_t *data;
-  const void *k, *v;
-  const int32_t *slots;
-  unsigned int *status;
-  int64_t kst, ksh, vst, vsh;
-  uint32_t rows;  // T * kv heads
-  int kv_heads, log_n, page, pages, rows_each;
-  uint32_t kv_ctas;
-};
-
 // The other 8 values of a lane's pairs where they are half a rotation away.
 template <int TYPE>
-__device__ __forceinline__ Raw8 load_partners(const void *k, int64_t row, int c0, int rot) {
+__device__ __forceinline__ Raw8 load_partners(const void *x, int64_t row, int c0, int rot) {
   const int half = rot / 2;
-  if (rot % 16 == 0) return load_raw8(k, row + (c0 >= rot ? c0 : c0 < half ? c0 + half : c0 - half), TYPE);
+  if (rot % 16 == 0) return load_raw8(x, row + (c0 >= rot ? c0 : c0 < half ? c0 + half : c0 - half), TYPE);
   float y[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int c = c0 + i;
-    y[i] = c < rot ? load_as_f32(k, row + (c < half ? c + half : c - half), TYPE) : 0.f;
+    y[i] = c < rot ? load_as_f32(x, row + (c < half ? c + half : c - half), TYPE) : 0.f;
   }
   return f32_to_raw8(y, TYPE);  // exact
 }
 
-// A lane's 8 columns of a key, rotated.
+// A lane's 8 columns of a head, rotated.
 template <int TYPE, bool HALF>
-__device__ __forceinline__ void rotate_key(float (&x)[8], const Raw8 &partners, int c0, int rot, const float2 *cs) {
+__device__ __forceinline__ void rotate_columns(float (&x)[8], const Raw8 &partners, int c0, int rot, const float2 *cs) {
   if (c0 >= rot) return;
   if (!HALF) {
     if (rot % 16 == 0) {
@@ -284,11 +180,146 @@ __device__ __forceinline__ void rotate_key(float (&x)[8], const Raw8 &partners, 
   }
 }
 
+// A thread's share of a head. kPieces: 16 columns, 8 pairs or 16 columns that are not rotated, where the pairs fall on
+// 16-byte pieces (rot a multiple of 16). kColumns: 8 columns, and the other ones of their pairs read value by value; a
+// power of two of lanes of one warp have a head. kPairs, for heads off the 16-byte grid: a pair, or one column that is
+// not rotated. 8192 tokens with 40 heads of 128, rot 100: 92 us by columns in halves and 40 interleaved, 113 and 108 by
+// pairs; rot 96 by pieces 27.7.
+enum { kPairs = 0, kPieces = 1, kColumns = 2 };
+
+template <int TYPE, bool HALF, int MODE>
+struct Item {
+  Raw8 a, b;
+  float x, y;
+  __device__ __forceinline__ void load(const RopeTensor &s, int64_t t, int h, int i, int D, int rot) {
+    const int64_t in = t * s.its + h * s.ith;
+    if (MODE == kPieces) {
+      const bool turned = i < rot / 16;
+      const int c0 = turned && HALF ? 8 * i : 16 * i, c1 = turned && HALF ? rot / 2 + 8 * i : c0 + 8;
+      a = load_raw8(s.in, in + c0, TYPE);
+      b = load_raw8(s.in, in + c1, TYPE);
+    } else if (MODE == kColumns) {
+      if (8 * i < D) {
+        a = load_raw8(s.in, in + 8 * i, TYPE);
+        if (HALF && 8 * i < rot) b = load_partners<TYPE>(s.in, in, 8 * i, rot);
+      }
+    } else if (i < rot / 2) {
+      x = load_as_f32(s.in, in + (HALF ? i : 2 * i), TYPE);
+      y = load_as_f32(s.in, in + (HALF ? i + rot / 2 : 2 * i + 1), TYPE);
+    } else {
+      x = load_as_f32(s.in, in + i + rot / 2, TYPE);
+    }
+  }
+  __device__ __forceinline__ void store(const RopeTensor &s, int64_t t, int h, int i, int D, int rot, const float2 *cs) {
+    const int64_t out = t * s.ots + h * s.oth;
+    if (MODE == kPieces) {
+      const bool turned = i < rot / 16;
+      const int c0 = turned && HALF ? 8 * i : 16 * i, c1 = turned && HALF ? rot / 2 + 8 * i : c0 + 8;
+      if (turned) {
+        float u[8], v[8];
+        raw8_to_f32(a, TYPE, u);
+        raw8_to_f32(b, TYPE, v);
+        if (HALF) {
+          rotate8(u, v, cs, i, rot);
+        } else {
+          rotate4(u, cs, i, 0, rot);
+          rotate4(v, cs, i, 1, rot);
+        }
+        a = f32_to_raw8(u, TYPE);
+        b = f32_to_raw8(v, TYPE);
+      }
+      store_raw8(s.out, out + c0, TYPE, a);
+      store_raw8(s.out, out + c1, TYPE, b);
+    } else if (MODE == kColumns) {
+      if (8 * i < D) {
+        float u[8];
+        raw8_to_f32(a, TYPE, u);
+        rotate_columns<TYPE, HALF>(u, b, 8 * i, rot, cs);
+        store_raw8(s.out, out + 8 * i, TYPE, f32_to_raw8(u, TYPE));
+      }
+    } else if (i < rot / 2) {
+      const float2 w = cs[sine_at(i, rot)];
+      store_from_f32(s.out, out + (HALF ? i : 2 * i), TYPE, rotated_a(x, y, w));
+      store_from_f32(s.out, out + (HALF ? i + rot / 2 : 2 * i + 1), TYPE, rotated_b(x, y, w));
+    } else {
+      store_from_f32(s.out, out + i + rot / 2, TYPE, x);
+    }
+  }
+};
+
+// The heads [h0, h1) of tokens [t0, t0 + a.tokens), those of x[1] behind those of x[0]. A thread keeps its place in a head
+// and walks the heads, two at a time; the first two are asked for before the sines are made.
+template <int TYPE, bool HALF, int MODE>
+__device__ __forceinline__ void rotate_block(const RopeArgs &a, float2 *sines, int t0, int h0, int h1) {
+  constexpr int U = 2;
+  const int items = a.by_items.d, heads = h1 - h0;
+  const int first = a.by_items.div(threadIdx.x), i = threadIdx.x - first * items, step = a.by_items.div(kThreads);
+  const int tokens = min(a.tokens, a.T - t0);
+  const bool whole = heads == a.heads_each;  // the last heads may be fewer
+  const int rows = (int)threadIdx.x < step * items ? tokens * heads : 0;
+  Item<TYPE, HALF, MODE> it[U];
+  bool made = false;
+  for (int r0 = first; r0 < rows || !made; r0 += U * step) {
+    int t[U], h[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * step;
+      t[u] = whole ? a.by_heads.div(r) : r / heads;
+      h[u] = h0 + r - t[u] * heads;
+      if (r < rows) {
+        const bool second = h[u] >= a.x[0].heads;
+        it[u].load(a.x[second], t0 + t[u], second ? h[u] - a.x[0].heads : h[u], i, a.D, a.rot);
+      }
+    }
+    if (!made) {
+      make_sines(sines, a, t0, tokens);
+      __syncthreads();
+      made = true;
+    }
+    if (MODE == kColumns) {
+      // the lanes of a head have read each other's columns before any is written where it was
+      const unsigned lanes = items == 32 ? 0xffffffffu : ((1u << items) - 1) << (threadIdx.x & 31 & ~(items - 1));
+      __syncwarp(lanes);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (r0 + u * step < rows) {
+        const bool second = h[u] >= a.x[0].heads;
+        it[u].store(a.x[second], t0 + t[u], second ? h[u] - a.x[0].heads : h[u], i, a.D, a.rot, sines + t[u] * (a.rot / 2));
+      }
+  }
+}
+
+constexpr int kMaxTokens = 16;
+
+template <int TYPE, bool HALF, int MODE>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
+  __shared__ __align__(16) float2 sines[kMaxTokens * kMaxPairs];
+  pdl_wait();
+  pdl_trigger();
+  const int block = a.head_blocks == 1 ? blockIdx.x : blockIdx.x / a.head_blocks;
+  const int t0 = block * a.tokens, h0 = (blockIdx.x - block * a.head_blocks) * a.heads_each;
+  rotate_block<TYPE, HALF, MODE>(a, sines, t0, h0, min(h0 + a.heads_each, a.x[0].heads + a.x[1].heads));
+}
+
+// ------------------------------------------------------- with the cache write
+struct WriteArgs {
+  RopeArgs q;
+  uint8_t *data;
+  const void *k, *v;
+  const int32_t *slots;
+  unsigned int *status;
+  int64_t kst, ksh, vst, vsh;
+  uint32_t rows;  // T * kv heads
+  int kv_heads, log_n, page, pages, rows_each;
+  uint32_t kv_ctas;
+};
+
 // First the CTAs that write a row (token, kv head) of keys and values for each 1 << log_n lanes, then those that rotate
 // queries (dealing them out in turn made no difference). Bound by instructions next to memory: 12345 tokens, 32 heads on 8
 // of 128, into FP8 take 52 us, 80% of the copy bandwidth, 42 M instructions at 65% of the issue slots; the queries alone
 // take 32 (93%), the cache write without a rotation 17.
-template <int FMT, int TYPE, bool HALF, bool PIECES>
+template <int FMT, int TYPE, bool HALF, int MODE>
 __global__ void __launch_bounds__(kThreads) rope_write_kernel(const WriteArgs a) {
   __shared__ __align__(16) float2 sines[kMaxTokens * kMaxPairs];
   pdl_wait();
@@ -296,7 +327,7 @@ __global__ void __launch_bounds__(kThreads) rope_write_kernel(const WriteArgs a)
   if (blockIdx.x >= a.kv_ctas) {
     const int at = blockIdx.x - a.kv_ctas, block = a.q.head_blocks == 1 ? at : at / a.q.head_blocks;
     const int t0 = block * a.q.tokens, h0 = (at - block * a.q.head_blocks) * a.q.heads_each;
-    rotate_block<TYPE, HALF, PIECES>(a.q, sines, t0, h0, min(h0 + a.q.heads_each, a.q.x[0].heads));
+    rotate_block<TYPE, HALF, MODE>(a.q, sines, t0, h0, min(h0 + a.q.heads_each, a.q.x[0].heads));
     return;
   }
   // a lane 8 columns of a.rows_each rows, the next one's asked for while one is quantised
@@ -335,7 +366,7 @@ __global__ void __launch_bounds__(kThreads) rope_write_kernel(const WriteArgs a)
     }
     float f[8];
     raw8_to_f32(k, TYPE, f);
-    rotate_key<TYPE, HALF>(f, partners, 8 * j, a.q.rot, sines + (t - t0) * (a.q.rot / 2));
+    rotate_columns<TYPE, HALF>(f, partners, 8 * j, a.q.rot, sines + (t - t0) * (a.q.rot / 2));
     const Raw8 own = v;
     if (x + 1 < a.rows_each) {
       r += per;
@@ -349,10 +380,17 @@ __global__ void __launch_bounds__(kThreads) rope_write_kernel(const WriteArgs a)
   }
 }
 
+float2 split(double v) {
+  const float hi = (float)v;
+  return make_float2(hi, (float)(v - hi));
+}
+
 // How many tokens and heads a CTA takes: about four items a thread, all heads of its tokens where there are tokens
 // enough for two CTAs an SM, else heads apart.
-void share(RopeArgs &a, int heads, bool pieces) {
-  const int items = pieces ? a.D / 16 : a.D - a.rot / 2;
+void share(RopeArgs &a, int heads, int mode) {
+  int items = mode == kPieces ? a.D / 16 : a.D - a.rot / 2;
+  if (mode == kColumns)
+    for (items = 1; 8 * items < a.D;) items *= 2;
   a.tokens = 1;
   while (a.tokens < kMaxTokens && 2 * a.tokens * heads * items <= 4 * kThreads && a.T / (2 * a.tokens) >= 304) a.tokens *= 2;
   a.head_blocks = 1;
@@ -370,20 +408,21 @@ moe_status_t launch_rope(const moe_rope_t &r, const int32_t *positions, int T, i
                          int q_heads, void *qo, int64_t qost, int64_t qosh, const void *k, int64_t kst, int64_t ksh,
                          int k_heads, void *ko, int64_t kost, int64_t kosh, int type, cudaStream_t stream, int *launches) {
   RopeArgs a = {{{q, qo, qst, qsh, qost, qosh, q_heads}, {k, ko, kst, ksh, kost, kosh, k_heads}},
-                reinterpret_cast<const unsigned long long *>(r.turns), positions, r.amplitude, T, D, r.rot_dim, 1, 1, 1};
-  // pairs on 16-byte pieces, or one by one
-  bool pieces = a.rot % 16 == 0 && D % 16 == 0;
+                reinterpret_cast<const unsigned long long *>(r.turns), positions, split(r.amplitude), T, D, r.rot_dim, 1, 1, 1};
+  bool grid = D % 8 == 0;  // heads begin and end on 16 bytes
   for (const RopeTensor &x : a.x)
-    if (x.heads)
-      pieces &= strides8(x.its, x.ith) && strides8(x.ots, x.oth) && aligned16(x.in) && aligned16(x.out);
-  share(a, q_heads + k_heads, pieces);
+    if (x.heads) grid &= strides8(x.its, x.ith) && strides8(x.ots, x.oth) && aligned16(x.in) && aligned16(x.out);
+  const int mode = !grid ? kPairs : a.rot % 16 == 0 && D % 16 == 0 ? kPieces : kColumns;
+  share(a, q_heads + k_heads, mode);
   using Kernel = void (*)(RopeArgs);
-#define MOE4_R(T) {{rope_kernel<T, true, false>, rope_kernel<T, true, true>}, {rope_kernel<T, false, false>, rope_kernel<T, false, true>}}
-  static const Kernel kernels[3][2][2] = {MOE4_R(MOE_BF16), MOE4_R(MOE_FP16), MOE4_R(MOE_FP32)};
+#define MOE4_M(T, H) {rope_kernel<T, H, kPairs>, rope_kernel<T, H, kPieces>, rope_kernel<T, H, kColumns>}
+#define MOE4_R(T) {MOE4_M(T, true), MOE4_M(T, false)}
+  static const Kernel kernels[3][2][3] = {MOE4_R(MOE_BF16), MOE4_R(MOE_FP16), MOE4_R(MOE_FP32)};
 #undef MOE4_R
+#undef MOE4_M
   const int64_t ctas = (int64_t)((T + a.tokens - 1) / a.tokens) * a.head_blocks;
   if (ctas >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
-  const cudaError_t err = launch_pdl(kernels[type][r.layout == MOE_ROPE_INTERLEAVED][pieces],
+  const cudaError_t err = launch_pdl(kernels[type][r.layout == MOE_ROPE_INTERLEAVED][mode],
                                      dim3((unsigned)ctas), dim3(kThreads), 0, stream, a);
   if (launches) ++*launches;
   return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
@@ -396,7 +435,7 @@ moe_status_t launch_rope_kv_write(const moe_rope_t &r, const int32_t *positions,
   if ((int64_t)T * c.kv_heads >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
   WriteArgs a = {};
   a.q = {{{q, qo, qst, qsh, qost, qosh, q ? q_heads : 0}, {}}, reinterpret_cast<const unsigned long long *>(r.turns), positions,
-         r.amplitude, T, c.head_dim, r.rot_dim, 1, 1, 1};
+         split(r.amplitude), T, c.head_dim, r.rot_dim, 1, 1, 1};
   a.data = static_cast<uint8_t *>(c.data);
   a.k = k;
   a.v = v;
@@ -409,10 +448,9 @@ moe_status_t launch_rope_kv_write(const moe_rope_t &r, const int32_t *positions,
   a.page = c.page_size;
   a.pages = c.num_pages;
   int64_t q_ctas = 0;
-  share(a.q, q ? q_heads : 1, a.q.rot % 16 == 0);
-  if (q) {
-    q_ctas = (int64_t)((T + a.q.tokens - 1) / a.q.tokens) * a.q.head_blocks;
-  }
+  const int mode = a.q.rot % 16 == 0 ? kPieces : kColumns;
+  share(a.q, q ? q_heads : 1, mode);
+  if (q) q_ctas = (int64_t)((T + a.q.tokens - 1) / a.q.tokens) * a.q.head_blocks;
   // one row a lane until there are CTAs enough for every SM four times over, then four, as far as the sines of their
   // tokens fit
   const uint32_t per = kThreads >> a.log_n;
@@ -424,13 +462,15 @@ moe_status_t launch_rope_kv_write(const moe_rope_t &r, const int32_t *positions,
   const int64_t ctas = q_ctas + a.kv_ctas;
   if (ctas >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
   using Kernel = void (*)(WriteArgs);
-#define MOE4_W(F, T) {{rope_write_kernel<F, T, true, false>, rope_write_kernel<F, T, true, true>}, {rope_write_kernel<F, T, false, false>, rope_write_kernel<F, T, false, true>}}
+#define MOE4_M(F, T, H) {rope_write_kernel<F, T, H, kPieces>, rope_write_kernel<F, T, H, kColumns>}
+#define MOE4_W(F, T) {MOE4_M(F, T, true), MOE4_M(F, T, false)}
 #define MOE4_W_TYPES(F) {MOE4_W(F, MOE_BF16), MOE4_W(F, MOE_FP16), MOE4_W(F, MOE_FP32)}
   static const Kernel kernels[4][3][2][2] = {MOE4_W_TYPES(MOE_KV_BF16), MOE4_W_TYPES(MOE_KV_FP16), MOE4_W_TYPES(MOE_KV_FP8),
                                              MOE4_W_TYPES(MOE_KV_NVFP4)};
 #undef MOE4_W_TYPES
 #undef MOE4_W
-  const cudaError_t err = launch_pdl(kernels[c.fmt][type][r.layout == MOE_ROPE_INTERLEAVED][a.q.rot % 16 == 0],
+#undef MOE4_M
+  const cudaError_t err = launch_pdl(kernels[c.fmt][type][r.layout == MOE_ROPE_INTERLEAVED][mode == kColumns],
                                      dim3((unsigned)ctas), dim3(kThreads), 0, stream, a);
   if (launches) ++*launches;
   return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;

@@ -21,7 +21,7 @@ uint64_t turns_of(double f) {
 bool valid_rope(const moe_rope_t *r, int D) {
   if (!r || r->rot_dim < 2 || r->rot_dim % 2 || r->rot_dim > D) return false;
   if (r->layout != MOE_ROPE_HALF && r->layout != MOE_ROPE_INTERLEAVED) return false;
-  return r->amplitude == r->amplitude && r->turns && (reinterpret_cast<uintptr_t>(r->turns) & 7u) == 0;
+  return isfinite((float)r->amplitude) && r->turns && (reinterpret_cast<uintptr_t>(r->turns) & 7u) == 0;
 }
 
 bool fits(const void *p, int type) { return p && reinterpret_cast<uintptr_t>(p) % dtype_bytes(type) == 0; }
@@ -69,7 +69,7 @@ moe_status_t moe_rope_turns(const double *frequencies, int n, uint64_t *turns) {
   return MOE_OK;
 }
 
-moe_status_t moe_rope_table(const moe_rope_config_t *c, uint64_t *turns, float *amplitude) {
+moe_status_t moe_rope_table(const moe_rope_config_t *c, uint64_t *turns, double *amplitude) {
   if (!c || !turns || !amplitude) return MOE_ERR_INVALID_ARG;
   const int R = c->rot_dim;
   if (R < 2 || R % 2 || R > 256 || !(c->base > 1.0) || !isfinite(c->base)) return MOE_ERR_INVALID_ARG;
@@ -100,7 +100,7 @@ moe_status_t moe_rope_table(const moe_rope_config_t *c, uint64_t *turns, float *
     if (keep < 1.0) f = f / c->factor * (1.0 - keep) + f * keep;
     turns[i] = turns_of(f);
   }
-  *amplitude = (float)(c->amplitude > 0.0 ? c->amplitude : a);
+  *amplitude = c->amplitude > 0.0 ? c->amplitude : a;
   return MOE_OK;
 }
 

@@ -590,14 +590,14 @@ typedef struct {
 
 /* The frequencies as 64-bit fractions of a turn a position (f / (2 pi) 2^64
  * modulo 2^64), turns [rot_dim / 2], and the amplitude. Host only. */
-moe_status_t moe_rope_table(const moe_rope_config_t *config, uint64_t *turns, float *amplitude);
+moe_status_t moe_rope_table(const moe_rope_config_t *config, uint64_t *turns, double *amplitude);
 
 /* The same of n frequencies of the caller's, in radians a position. Host only. */
 moe_status_t moe_rope_turns(const double *frequencies, int n, uint64_t *turns);
 
 typedef struct {
   int32_t rot_dim, layout; /* moe_rope_layout_t                                */
-  float amplitude;
+  double amplitude;
   const uint64_t *turns; /* device, [rot_dim / 2], 8-byte aligned              */
 } moe_rope_t;
 

@@ -65,8 +65,8 @@ def test_rope_kernels_by_alignment(lib):
     for kw in (dict(), dict(q=P + 2), dict(stride=516), dict(rot=40), dict(rot=48)):
         assert rope(lib, 10, 8, **kw) == 0
         names.append(lib.launches()[0][0])
-    aligned, pairs = names[0], names[1]
-    assert aligned != pairs and names[2:] == [pairs, pairs, aligned]
+    pieces, pairs, columns = names[0], names[1], names[3]
+    assert len({pieces, pairs, columns}) == 3 and names[2] == pairs and names[4] == pieces
 
 
 def test_rope_write_grid(lib):

@@ -105,6 +105,7 @@ x4 = torch.zeros(4, 3, 64, dtype=bf16)
     dict(D=512, rot=64), dict(rot=66), dict(edit=lambda r: setattr(r, "rot_dim", 3)), dict(edit=lambda r: setattr(r, "rot_dim", 0)),
     dict(edit=lambda r: setattr(r, "layout", 2)), dict(edit=lambda r: setattr(r, "turns", 0)),
     dict(edit=lambda r: setattr(r, "turns", r.turns + 4)), dict(edit=lambda r: setattr(r, "amplitude", float("nan"))),
+    dict(edit=lambda r: setattr(r, "amplitude", 1e300)),
     dict(edit=lambda r: setattr(r, "place", 1)), dict(pos=ints(3)), dict(pos=torch.zeros(4, dtype=torch.int64)),
     dict(q=torch.zeros(4, 3, 64, dtype=torch.float64)), dict(q=x4, qo=torch.zeros(4, 3, 64)), dict(q=x4, qo=x4[:, :2]),
     dict(k=x4), dict(ko=x4), dict(k=x4, ko=torch.zeros(4, 2, 64, dtype=bf16)), dict(k=torch.zeros(4, 2, 64), ko=torch.zeros(4, 2, 64)),

@@ -49,7 +49,8 @@ def close(got, x, ref, dtype, rot):
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("T,hq,hk,D,rot", [(1, 64, 8, 64, 64), (3, 1, 1, 128, 128), (17, 5, 3, 128, 64), (300, 8, 8, 256, 256),
                                           (700, 40, 8, 64, 32), (5, 7, 2, 80, 80), (9, 3, 1, 48, 16), (33, 4, 2, 64, 20),
-                                          (6, 2, 3, 50, 6), (2, 3, 1, 3, 2), (40, 2, 1, 256, 254), (1, 33, 0, 128, 96)])
+                                          (6, 2, 3, 50, 6), (2, 3, 1, 3, 2), (40, 2, 1, 256, 254), (1, 33, 0, 128, 96), (7, 3, 2, 72, 64),
+                                          (31, 5, 1, 72, 70), (700, 6, 2, 128, 102), (4, 9, 9, 8, 4), (400, 3, 2, 248, 30)])
 def test_rope(layout, dtype, T, hq, hk, D, rot):
     t = TYPES[dtype]
     r = moe.rope(rot, layout, 10000.0)
@@ -88,10 +89,10 @@ def test_frequencies_of_the_callers():
 
 
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
-@pytest.mark.parametrize("rot", [64, 40, 16])
-def test_in_place_and_strided(layout, rot):
+@pytest.mark.parametrize("D,rot", [(64, 64), (64, 40), (64, 16), (256, 250), (128, 34), (72, 54), (50, 50)])
+def test_in_place_and_strided(layout, D, rot):
     """Parts of a projection's output, rotated where they lie; what is beside them stays."""
-    T, hq, hk, D = 130, 6, 2, 64
+    T, hq, hk = 700, 6, 2
     r, pos = moe.rope(rot, layout), positions(T)
     qkv = make(T, hq + 2 * hk, D, torch.bfloat16)
     before = qkv.clone()
