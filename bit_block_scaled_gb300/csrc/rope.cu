@@ -76,20 +76,21 @@ __device__ __forceinline__ float2 sine_of(unsigned long long turns, int position
   return (quarter & 2) ? make_float2(-cc, -ss) : make_float2(cc, ss);
 }
 
-// Cosines and sines of the CTA's tokens: [tokens][pairs]. Where lanes take 8 pairs or 4 each, they are in the order in
-// which neighbouring lanes read neighbouring 16 bytes, without bank conflicts: two pairs of each 8, then the next two.
+// Cosines and sines of the CTA's tokens: [tokens][pairs rounded up to 8], in the order in which lanes with 8 pairs or 4 each
+// read neighbouring 16 bytes, without bank conflicts: two pairs of each 8, then the next two.
+__host__ __device__ __forceinline__ int sine_places(int rot) { return (rot + 15) / 16 * 8; }
 __device__ __forceinline__ int sine_at(int p, int rot) {
-  return rot % 16 == 0 ? ((p >> 1) & 3) * (rot / 8) + (p >> 3) * 2 + (p & 1) : p;
+  return ((p >> 1) & 3) * (sine_places(rot) / 4) + (p >> 3) * 2 + (p & 1);
 }
 // Pairs 2 m and 2 m + 1 of the 8 pairs number i.
 __device__ __forceinline__ float4 two_sines(const float2 *cs, int i, int m, int rot) {
-  return *reinterpret_cast<const float4 *>(cs + m * (rot / 8) + 2 * i);
+  return *reinterpret_cast<const float4 *>(cs + m * (sine_places(rot) / 4) + 2 * i);
 }
 __device__ __forceinline__ void make_sines(float2 *sines, const RopeArgs &a, int t0, int tokens) {
   const int pairs = a.rot / 2;
   for (int i = threadIdx.x; i < tokens * pairs; i += blockDim.x) {
     const int t = a.by_pairs.div(i), p = i - t * pairs;
-    if (t0 + t < a.T) sines[t * pairs + sine_at(p, a.rot)] = sine_of(a.turns[p], a.positions[t0 + t], a.amplitude);
+    if (t0 + t < a.T) sines[t * sine_places(a.rot) + sine_at(p, a.rot)] = sine_of(a.turns[p], a.positions[t0 + t], a.amplitude);
   }
 }
 
@@ -122,18 +123,50 @@ __device__ __forceinline__ void rotate4(float (&v)[8], const float2 *cs, int i, 
   }
 }
 
+// Columns [p, p + 8) of a row that lies on the 16-byte grid, from the two pieces around them; those outside [0, D) are not
+// read. Their values are moved by words, and 16-bit ones by half a word.
+template <int TYPE>
+__device__ __forceinline__ Raw8 load_window(const void *x, int64_t row, int p, int D) {
+  constexpr int W = TYPE == MOE_FP32 ? 8 : 4;  // words of 8 values
+  const int m = p & 7, c = p - m;
+  Raw8 lo = {}, hi = {};
+  if (c >= 0) lo = load_raw8(x, row + c, TYPE);
+  if (m && c + 8 < D) hi = load_raw8(x, row + c + 8, TYPE);
+  uint32_t w[16] = {lo.a.x, lo.a.y, lo.a.z, lo.a.w, lo.b.x, lo.b.y, lo.b.z, lo.b.w};
+  const uint32_t v[8] = {hi.a.x, hi.a.y, hi.a.z, hi.a.w, hi.b.x, hi.b.y, hi.b.z, hi.b.w};
+#pragma unroll
+  for (int i = 0; i < W; ++i) w[W + i] = v[i];
+#pragma unroll
+  for (int s = W / 2; s >= 1; s /= 2) {
+    const bool move = (TYPE == MOE_FP32 ? m : m >> 1) & s;
+#pragma unroll
+    for (int i = 0; i + s < 2 * W; ++i) w[i] = move ? w[i + s] : w[i];
+  }
+  if (TYPE != MOE_FP32) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16 * (m & 1));
+  }
+  Raw8 r;
+  r.a = make_uint4(w[0], w[1], w[2], w[3]);
+  r.b = TYPE == MOE_FP32 ? make_uint4(w[4], w[5], w[6], w[7]) : make_uint4(0, 0, 0, 0);
+  return r;
+}
+
 // The other 8 values of a lane's pairs where they are half a rotation away.
 template <int TYPE>
-__device__ __forceinline__ Raw8 load_partners(const void *x, int64_t row, int c0, int rot) {
+__device__ __forceinline__ Raw8 load_partners(const void *x, int64_t row, int c0, int rot, int D) {
   const int half = rot / 2;
   if (rot % 16 == 0) return load_raw8(x, row + (c0 >= rot ? c0 : c0 < half ? c0 + half : c0 - half), TYPE);
-  float y[8];
+  if (c0 >= rot) return Raw8{};
+  const Raw8 r = load_window<TYPE>(x, row, c0 < half ? c0 + half : c0 - half, D);
+  if (c0 >= half || c0 + 8 <= half) return r;
+  // the first halves end within these columns: the others' partners are the first of the row
+  float u[8], v[8];
+  raw8_to_f32(r, TYPE, u);
+  raw8_to_f32(load_window<TYPE>(x, row, c0 - half, D), TYPE, v);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int c = c0 + i;
-    y[i] = c < rot ? load_as_f32(x, row + (c < half ? c + half : c - half), TYPE) : 0.f;
-  }
-  return f32_to_raw8(y, TYPE);  // exact
+  for (int i = 0; i < 8; ++i) u[i] = c0 + i < half ? u[i] : v[i];
+  return f32_to_raw8(u, TYPE);  // exact
 }
 
 // A lane's 8 columns of a head, rotated.
@@ -141,18 +174,12 @@ template <int TYPE, bool HALF>
 __device__ __forceinline__ void rotate_columns(float (&x)[8], const Raw8 &partners, int c0, int rot, const float2 *cs) {
   if (c0 >= rot) return;
   if (!HALF) {
-    if (rot % 16 == 0) {
-      rotate4(x, cs, c0 / 16, (c0 >> 3) & 1, rot);
-      return;
-    }
+    float v[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (c0 + 2 * i < rot) {
-        const float2 w = cs[c0 / 2 + i];
-        const float a = x[2 * i], b = x[2 * i + 1];
-        x[2 * i] = rotated_a(a, b, w);
-        x[2 * i + 1] = rotated_b(a, b, w);
-      }
+    for (int i = 0; i < 8; ++i) v[i] = x[i];
+    rotate4(v, cs, c0 / 16, (c0 >> 3) & 1, rot);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = c0 + i < rot ? v[i] : x[i];
     return;
   }
   const int half = rot / 2;
@@ -173,18 +200,18 @@ __device__ __forceinline__ void rotate_columns(float (&x)[8], const Raw8 &partne
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int c = c0 + i;
-    if (c < rot) {
-      const float2 w = cs[c < half ? c : c - half];
-      x[i] = c < half ? rotated_a(x[i], y[i], w) : rotated_b(y[i], x[i], w);
-    }
+    const float2 w = cs[sine_at(c >= rot ? 0 : c < half ? c : c - half, rot)];
+    const float sine = __uint_as_float(__float_as_uint(w.y) ^ (c < half ? 0x80000000u : 0u));
+    const float turned = fmaf(x[i], w.x, __fmul_rn(y[i], sine));  // as above, without a branch
+    x[i] = c < rot ? turned : x[i];
   }
 }
 
 // A thread's share of a head. kPieces: 16 columns, 8 pairs or 16 columns that are not rotated, where the pairs fall on
-// 16-byte pieces (rot a multiple of 16). kColumns: 8 columns, and the other ones of their pairs read value by value; a
-// power of two of lanes of one warp have a head. kPairs, for heads off the 16-byte grid: a pair, or one column that is
-// not rotated. 8192 tokens with 40 heads of 128, rot 100: 92 us by columns in halves and 40 interleaved, 113 and 108 by
-// pairs; rot 96 by pieces 27.7.
+// 16-byte pieces (rot a multiple of 16). kColumns: 8 columns, and in halves the other ones of their pairs moved into place;
+// a power of two of lanes of one warp have a head. kPairs, for heads off the 16-byte grid: a pair, or one column that is
+// not rotated. 8192 tokens with 40 heads of 128, rot 96 by pieces: 27.7 us; rot 100 by columns 34 interleaved and 77 in
+// halves (62 M instructions: moving costs more than reading; value by value 92), by pairs 107 and 117.
 enum { kPairs = 0, kPieces = 1, kColumns = 2 };
 
 template <int TYPE, bool HALF, int MODE>
@@ -201,7 +228,7 @@ struct Item {
     } else if (MODE == kColumns) {
       if (8 * i < D) {
         a = load_raw8(s.in, in + 8 * i, TYPE);
-        if (HALF && 8 * i < rot) b = load_partners<TYPE>(s.in, in, 8 * i, rot);
+        if (HALF && 8 * i < rot) b = load_partners<TYPE>(s.in, in, 8 * i, rot, D);
       }
     } else if (i < rot / 2) {
       x = load_as_f32(s.in, in + (HALF ? i : 2 * i), TYPE);
@@ -285,7 +312,7 @@ __device__ __forceinline__ void rotate_block(const RopeArgs &a, float2 *sines, i
     for (int u = 0; u < U; ++u)
       if (r0 + u * step < rows) {
         const bool second = h[u] >= a.x[0].heads;
-        it[u].store(a.x[second], t0 + t[u], second ? h[u] - a.x[0].heads : h[u], i, a.D, a.rot, sines + t[u] * (a.rot / 2));
+        it[u].store(a.x[second], t0 + t[u], second ? h[u] - a.x[0].heads : h[u], i, a.D, a.rot, sines + t[u] * sine_places(a.rot));
       }
   }
 }
@@ -344,7 +371,7 @@ __global__ void __launch_bounds__(kThreads) rope_write_kernel(const WriteArgs a)
     slot = a.slots[t];
     const int64_t krow = (int64_t)t * a.kst + (int64_t)head * a.ksh;
     k = load_raw8(a.k, krow + 8 * j, TYPE);
-    if (HALF) partners = load_partners<TYPE>(a.k, krow, 8 * j, a.q.rot);
+    if (HALF) partners = load_partners<TYPE>(a.k, krow, 8 * j, a.q.rot, a.q.D);
     v = load_raw8(a.v, (int64_t)t * a.vst + (int64_t)head * a.vsh + 8 * j, TYPE);
   };
   load();
@@ -366,7 +393,7 @@ __global__ void __launch_bounds__(kThreads) rope_write_kernel(const WriteArgs a)
     }
     float f[8];
     raw8_to_f32(k, TYPE, f);
-    rotate_columns<TYPE, HALF>(f, partners, 8 * j, a.q.rot, sines + (t - t0) * (a.q.rot / 2));
+    rotate_columns<TYPE, HALF>(f, partners, 8 * j, a.q.rot, sines + (t - t0) * sine_places(a.q.rot));
     const Raw8 own = v;
     if (x + 1 < a.rows_each) {
       r += per;
@@ -456,7 +483,7 @@ moe_status_t launch_rope_kv_write(const moe_rope_t &r, const int32_t *positions,
   const uint32_t per = kThreads >> a.log_n;
   static_assert(kThreads / 8 * 32 <= kMaxTokens * kMaxPairs, "sines of one row a lane: 32, 16 or 8 tokens of 32, 64 or 128 pairs");
   a.rows_each = 1;
-  if (a.rows > 4 * per * 608 && ((4 * per - 1) / c.kv_heads + 2) * (r.rot_dim / 2) <= kMaxTokens * kMaxPairs) a.rows_each = 4;
+  if (a.rows > 4 * per * 608 && ((4 * per - 1) / c.kv_heads + 2) * sine_places(r.rot_dim) <= kMaxTokens * kMaxPairs) a.rows_each = 4;
   const uint32_t step = per * a.rows_each;
   a.kv_ctas = a.rows / step + (a.rows % step != 0);
   const int64_t ctas = q_ctas + a.kv_ctas;
