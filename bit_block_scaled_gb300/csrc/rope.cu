@@ -152,11 +152,12 @@ __device__ __forceinline__ Raw8 load_window(const void *x, int64_t row, int p, i
   return r;
 }
 
-// The other 8 values of a lane's pairs where they are half a rotation away.
-template <int TYPE>
+// The other 8 values of a lane's pairs where they are half a rotation away. PIECES: rot is a multiple of 16, here and below;
+// known to the compiler, because the registers that the other case needs cost this one a third of its rate.
+template <int TYPE, bool PIECES>
 __device__ __forceinline__ Raw8 load_partners(const void *x, int64_t row, int c0, int rot, int D) {
   const int half = rot / 2;
-  if (rot % 16 == 0) return load_raw8(x, row + (c0 >= rot ? c0 : c0 < half ? c0 + half : c0 - half), TYPE);
+  if (PIECES) return load_raw8(x, row + (c0 >= rot ? c0 : c0 < half ? c0 + half : c0 - half), TYPE);
   if (c0 >= rot) return Raw8{};
   const Raw8 r = load_window<TYPE>(x, row, c0 < half ? c0 + half : c0 - half, D);
   if (c0 >= half || c0 + 8 <= half) return r;
@@ -170,7 +171,7 @@ __device__ __forceinline__ Raw8 load_partners(const void *x, int64_t row, int c0
 }
 
 // A lane's 8 columns of a head, rotated.
-template <int TYPE, bool HALF>
+template <int TYPE, bool HALF, bool PIECES>
 __device__ __forceinline__ void rotate_columns(float (&x)[8], const Raw8 &partners, int c0, int rot, const float2 *cs) {
   if (c0 >= rot) return;
   if (!HALF) {
@@ -179,13 +180,13 @@ __device__ __forceinline__ void rotate_columns(float (&x)[8], const Raw8 &partne
     for (int i = 0; i < 8; ++i) v[i] = x[i];
     rotate4(v, cs, c0 / 16, (c0 >> 3) & 1, rot);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = c0 + i < rot ? v[i] : x[i];
+    for (int i = 0; i < 8; ++i) x[i] = PIECES || c0 + i < rot ? v[i] : x[i];
     return;
   }
   const int half = rot / 2;
   float y[8];
   raw8_to_f32(partners, TYPE, y);
-  if (rot % 16 == 0) {
+  if (PIECES) {
     // rotated_a(x, y) or rotated_b(y, x), which differ in a sign
     const uint32_t sign = c0 < half ? 0x80000000u : 0u;
     auto signed_sine = [&](float s) { return __uint_as_float(__float_as_uint(s) ^ sign); };
@@ -228,7 +229,7 @@ struct Item {
     } else if (MODE == kColumns) {
       if (8 * i < D) {
         a = load_raw8(s.in, in + 8 * i, TYPE);
-        if (HALF && 8 * i < rot) b = load_partners<TYPE>(s.in, in, 8 * i, rot, D);
+        if (HALF && 8 * i < rot) b = load_partners<TYPE, false>(s.in, in, 8 * i, rot, D);
       }
     } else if (i < rot / 2) {
       x = load_as_f32(s.in, in + (HALF ? i : 2 * i), TYPE);
@@ -261,7 +262,7 @@ struct Item {
       if (8 * i < D) {
         float u[8];
         raw8_to_f32(a, TYPE, u);
-        rotate_columns<TYPE, HALF>(u, b, 8 * i, rot, cs);
+        rotate_columns<TYPE, HALF, false>(u, b, 8 * i, rot, cs);
         store_raw8(s.out, out + 8 * i, TYPE, f32_to_raw8(u, TYPE));
       }
     } else if (i < rot / 2) {
@@ -371,7 +372,7 @@ __global__ void __launch_bounds__(kThreads) rope_write_kernel(const WriteArgs a)
     slot = a.slots[t];
     const int64_t krow = (int64_t)t * a.kst + (int64_t)head * a.ksh;
     k = load_raw8(a.k, krow + 8 * j, TYPE);
-    if (HALF) partners = load_partners<TYPE>(a.k, krow, 8 * j, a.q.rot, a.q.D);
+    if (HALF) partners = load_partners<TYPE, MODE == kPieces>(a.k, krow, 8 * j, a.q.rot, a.q.D);
     v = load_raw8(a.v, (int64_t)t * a.vst + (int64_t)head * a.vsh + 8 * j, TYPE);
   };
   load();
@@ -393,7 +394,7 @@ __global__ void __launch_bounds__(kThreads) rope_write_kernel(const WriteArgs a)
     }
     float f[8];
     raw8_to_f32(k, TYPE, f);
-    rotate_columns<TYPE, HALF>(f, partners, 8 * j, a.q.rot, sines + (t - t0) * sine_places(a.q.rot));
+    rotate_columns<TYPE, HALF, MODE == kPieces>(f, partners, 8 * j, a.q.rot, sines + (t - t0) * sine_places(a.q.rot));
     const Raw8 own = v;
     if (x + 1 < a.rows_each) {
       r += per;
