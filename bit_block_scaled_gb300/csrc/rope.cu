@@ -211,7 +211,7 @@ __device__ __forceinline__ void rotate_columns(float (&x)[8], const Raw8 &partne
 // A thread's share of a head. kPieces: 16 columns, 8 pairs or 16 columns that are not rotated, where the pairs fall on
 // 16-byte pieces (rot a multiple of 16). kColumns: 8 columns, and in halves the other ones of their pairs moved into place;
 // a power of two of lanes of one warp have a head. kPairs, for heads off the 16-byte grid: a pair, or one column that is
-// not rotated. 8192 tokens with 40 heads of 128, rot 96 by pieces: 27.7 us; rot 100 by columns 34 interleaved and 77 in
+// not rotated. 8192 tokens with 40 heads of 128, rot 96 by pieces: 27.7 us; rot 100 by columns 34 interleaved and 78 in
 // halves (62 M instructions: moving costs more than reading; value by value 92), by pairs 107 and 117.
 enum { kPairs = 0, kPieces = 1, kColumns = 2 };
 
@@ -276,10 +276,11 @@ struct Item {
 };
 
 // The heads [h0, h1) of tokens [t0, t0 + a.tokens), those of x[1] behind those of x[0]. A thread keeps its place in a head
-// and walks the heads, two at a time; the first two are asked for before the sines are made.
+// and walks the heads, two at a time; the first ones are asked for before the sines are made.
 template <int TYPE, bool HALF, int MODE>
 __device__ __forceinline__ void rotate_block(const RopeArgs &a, float2 *sines, int t0, int h0, int h1) {
-  constexpr int U = 2;
+  // moved partners need the second head's registers: 78 us with one at a time, 92 with two
+  constexpr int U = MODE == kColumns && HALF ? 1 : 2;
   const int items = a.by_items.d, heads = h1 - h0;
   const int first = a.by_items.div(threadIdx.x), i = threadIdx.x - first * items, step = a.by_items.div(kThreads);
   const int tokens = min(a.tokens, a.T - t0);
@@ -345,7 +346,7 @@ struct WriteArgs {
 
 // First the CTAs that write a row (token, kv head) of keys and values for each 1 << log_n lanes, then those that rotate
 // queries (dealing them out in turn made no difference). Bound by instructions next to memory: 12345 tokens, 32 heads on 8
-// of 128, into FP8 take 52 us, 80% of the copy bandwidth, 42 M instructions at 65% of the issue slots; the queries alone
+// of 128, into FP8 take 50 us, 84% of the copy bandwidth; the queries alone
 // take 32 (93%), the cache write without a rotation 17.
 template <int FMT, int TYPE, bool HALF, int MODE>
 __global__ void __launch_bounds__(kThreads) rope_write_kernel(const WriteArgs a) {
