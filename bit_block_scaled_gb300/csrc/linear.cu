@@ -18,12 +18,14 @@
 //    need no sharing of columns, take 19% fewer bytes a product (16384 x 8192 x
 //    8192 347 -> 313 us, 7.0 PFLOP/s, 0.92 of four times the measured bf16 rate).
 #include <cudaTypedefs.h>
+#include <float.h>
 #include <math.h>
 #include <string.h>
 
 #include "device.cuh"
 #include "fp4.cuh"
 #include "kernels.h"
+#include "quant.cuh"
 #include "tmap.cuh"
 #include "types.cuh"
 
@@ -139,6 +141,29 @@ __device__ __forceinline__ void cluster_sync() {
 
 __device__ __forceinline__ float row_scale(const float *r, int stride, int i) { return r ? r[(int64_t)i * stride] : 1.f; }
 
+// A sum of NVFP4 products, 0 or from 2^-20 to 2^43 and a multiple of 2^-20, times a token's row scale is a normal number or
+// exact for scales from 2^-60 to 2^61 and for the 2^-127 of a row of zeros: what follows is rounded once.
+__device__ __forceinline__ bool is_near(float r) {
+  const uint32_t bits = __float_as_uint(r) & 0x7fffffffu;
+  return bits - (67u << 23) < 121u << 23 || bits == 0x00400000u;
+}
+// Any other one as a 2^h, a at that range's end (subnormal ones: from 2^-82 on), 2^h for the weight's scale.
+struct Parted {
+  float a, up;
+  __device__ __forceinline__ explicit Parted(float r) {
+    const int e = (int)(__float_as_uint(r) >> 23 & 255u) - 127;  // infinities and NaN stay what they are
+    const int h = is_near(r) ? 0 : e - max(-60, min(e, 60));
+    a = r * pow2(-h);
+    up = pow2(h);
+  }
+};
+// v xr w + bias for any scales. Where w 2^h would pass fp32's range, v a (2^40 at least, or 0) makes an infinity of the
+// largest number, too.
+__device__ __forceinline__ float scaled_far(float v, const Parted &xr, float w, float bias) {
+  const float m = w * xr.up;
+  return fmaf(v * xr.a, fabsf(m) > FLT_MAX && fabsf(w) <= FLT_MAX ? copysignf(FLT_MAX, w) : m, bias);
+}
+
 // The whole warp waits, and agrees on the outcome. One lane is then elected to issue (elect.sync, not a comparison of
 // the lane: only then the compiler knows that one thread runs, and issues each tcgen05 instruction without a loop over
 // lanes; 4096 x 6144 x 8192 184 -> 89 us).
@@ -165,6 +190,22 @@ struct Narrow {
   static constexpr int kUsed = TN + kSfCols;
   static constexpr int kCols = kUsed <= 32 ? 32 : kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
 };
+
+// 8 sums of tokens from c on, whose row scales are any, into the outputs from i on (`put` below takes nearly all tiles).
+// Not inline, so that the code of the others stays together: 64 x 5120 x 2880 6.5 us, with it inline 6.7 to 6.8.
+__device__ __noinline__ void put8_far(const LinArgs &p, uint8_t *tile_s, const float *xr_s, int i, int c, int count, int t0, int n,
+                                      int row, float scale, float bias, float v0, float v1, float v2, float v3, float v4, float v5,
+                                      float v6, float v7) {
+  const float v[8] = {v0, v1, v2, v3, v4, v5, v6, v7};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float f = scaled_far(v[j], Parted(xr_s[c + j]), scale, bias);
+    if (n < p.bulk_n)
+      store_from_f32(tile_s, (i + j) * 128 + row, p.type, f);
+    else if (n < p.N && i + j < count)
+      store_from_f32(p.out, (t0 + c + j) * p.ldo + n, p.type, f);
+  }
+}
 
 template <int FMT, int TN>
 __global__ void __launch_bounds__(kThreads) narrow_kernel(const __grid_constant__ LinArgs p) {
@@ -255,13 +296,17 @@ __global__ void __launch_bounds__(kThreads) narrow_kernel(const __grid_constant_
   // the writing warps' rows of tensor memory are 32 weight rows
   const int q = warp & 3, row = q * 32 + lane, n = n0 + row, e = tid - 64;
   float scale = 0.f, bias = 0.f;
+  bool near = true;  // all of the tile's row scales are
   if (warp >= 2) {
-    for (int i = e; i < live; i += kEpiThreads) xr_s[i] = row_scale(p.xr, p.xr_stride, t0 + i);
+    for (int i = e; i < live; i += kEpiThreads) {
+      xr_s[i] = row_scale(p.xr, p.xr_stride, t0 + i);
+      near &= is_near(xr_s[i]);
+    }
     if (n < p.N) {
       scale = row_scale(p.wr, p.wr_stride, n);
       bias = p.bias ? load_as_f32(p.bias, n, p.type) : 0.f;
     }
-    asm volatile("bar.sync 1, %0;" ::"r"(kEpiThreads) : "memory");  // xr_s
+    near = bar_and(1, kEpiThreads, near);  // xr_s is there
     ok = warp_wait(done, 0);
     tc_fence_after();
   }
@@ -275,6 +320,13 @@ __global__ void __launch_bounds__(kThreads) narrow_kernel(const __grid_constant_
   // n sums of the tokens from c on into the outputs from i on; what lies past the tile's tokens is not copied out
   auto put = [&](int i, int c, auto &v) {
     constexpr int n_put = sizeof(v) / 4;
+    if (FMT == MOE_FMT_NVFP4 && !near) {
+#pragma unroll
+      for (int j = 0; j < n_put; j += 8)
+        put8_far(p, tile_s, xr_s, i + j, c + j, count, t0, n, row, scale, bias, v[j], v[j + 1], v[j + 2], v[j + 3], v[j + 4],
+                 v[j + 5], v[j + 6], v[j + 7]);
+      return;
+    }
     float f[n_put];
 #pragma unroll
     for (int j = 0; j < n_put; ++j) f[j] = fmaf(v[j] * xr_s[c + j], scale, bias);
@@ -601,7 +653,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1) wid
       if (n) asm volatile("bar.sync 1, %0;" ::"r"(kWideEpi * 32) : "memory");  // the tile before has used them
       scales[e] = wr;
       biases[e] = bi;
-      const float xr = t < p.T ? row_scale(p.xr, p.xr_stride, t) : 0.f;
+      const float xr = t < p.T ? row_scale(p.xr, p.xr_stride, t) : 1.f;
+      const bool near = FMT != MOE_FMT_NVFP4 || __all_sync(0xffffffffu, is_near(xr));
       ok = bar_and(1, kWideEpi * 32, mbar_wait(accfull(acc), (n >> 1) & 1));  // all go on, or none; scales and biases are there
       if (!ok) break;
       tc_fence_after();
@@ -624,16 +677,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1) wid
         for (int w = 0; w < 2; ++w) {
           const int c = half * 128 + 32 * (pc + w);
           float f[4][8];
+          if (__builtin_expect(near, 1)) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 sc = *reinterpret_cast<const float4 *>(scales + c + j);
-            const float4 bs = *reinterpret_cast<const float4 *>(biases + c + j);
-            const uint32_t *u = &v[w][j];
-            float *x = &f[j >> 3][j & 7];
-            x[0] = fmaf(__uint_as_float(u[0]) * xr, sc.x, bs.x);
-            x[1] = fmaf(__uint_as_float(u[1]) * xr, sc.y, bs.y);
-            x[2] = fmaf(__uint_as_float(u[2]) * xr, sc.z, bs.z);
-            x[3] = fmaf(__uint_as_float(u[3]) * xr, sc.w, bs.w);
+            for (int j = 0; j < 32; j += 4) {
+              const float4 sc = *reinterpret_cast<const float4 *>(scales + c + j);
+              const float4 bs = *reinterpret_cast<const float4 *>(biases + c + j);
+              const uint32_t *u = &v[w][j];
+              float *x = &f[j >> 3][j & 7];
+              x[0] = fmaf(__uint_as_float(u[0]) * xr, sc.x, bs.x);
+              x[1] = fmaf(__uint_as_float(u[1]) * xr, sc.y, bs.y);
+              x[2] = fmaf(__uint_as_float(u[2]) * xr, sc.z, bs.z);
+              x[3] = fmaf(__uint_as_float(u[3]) * xr, sc.w, bs.w);
+            }
+          } else {
+            const Parted r(xr);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) f[j >> 3][j & 7] = scaled_far(__uint_as_float(v[w][j]), r, scales[c + j], biases[c + j]);
           }
           // rows of 128 bytes in the staging memory, 16-byte pieces in the order of that swizzle: 64 columns of 16 bits (both
           // pieces), 32 of fp32

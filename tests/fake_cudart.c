@@ -3,7 +3,8 @@
  * runtime. It has two devices, of 152 and 100 SMs, and keeps what a launch
  * depends on apart for each: a kernel's limit of dynamic shared memory is 48 KB
  * on a device until it is raised there, and a launch or an occupancy query past
- * it fails, as on a GPU. Launches are recorded. */
+ * it fails, as on a GPU. Launches are recorded. There is no driver, but an
+ * encoder of tensor maps on demand, which takes everything and writes nothing. */
 #include <stddef.h>
 #include <string.h>
 
@@ -25,6 +26,8 @@ void fake_refuse(int n) { refuse = n; } /* the next n settings of an attribute f
 int fake_launches(void) { return n_launches; }
 const launch_t *fake_launch(int i) { return &launches[i]; }
 void fake_clear(void) { n_launches = 0; }
+static int encoder;
+void fake_encoder(int on) { encoder = on; }
 
 /* ---- registration of kernels */
 void **__cudaRegisterFatBinary(void *f) { static void *h; (void)f; return &h; }
@@ -81,9 +84,18 @@ int cudaLaunchKernelExC(const config_t *c, const void *f, void **args) {
   return 0;
 }
 
+static int encode(void) { return 0; }
+int cudaGetDriverEntryPointByVersion(const char *symbol, void **f, unsigned version, unsigned long long flags, int *found) {
+  (void)version; (void)flags;
+  if (!encoder || strcmp(symbol, "cuTensorMapEncodeTiled")) return ERR;
+  *f = (void *)encode;
+  *found = 0;
+  return 0;
+}
+
 /* ---- what the calls under test do not reach */
 #define NEVER(name) int name(void) { return ERR; }
 NEVER(__cudaGetKernel) NEVER(__cudaLaunchKernel) NEVER(__cudaPopCallConfiguration) NEVER(__cudaPushCallConfiguration)
 NEVER(cudaEventCreate) NEVER(cudaEventDestroy) NEVER(cudaEventElapsedTime) NEVER(cudaEventRecord) NEVER(cudaEventSynchronize)
-NEVER(cudaGetDriverEntryPointByVersion) NEVER(cudaGetLastError) NEVER(cudaGetSymbolAddress) NEVER(cudaHostGetDevicePointer)
+NEVER(cudaGetLastError) NEVER(cudaGetSymbolAddress) NEVER(cudaHostGetDevicePointer)
 NEVER(cudaMemcpy) NEVER(cudaMemcpyAsync) NEVER(cudaMemsetAsync) NEVER(cudaStreamSynchronize)

@@ -1,0 +1,51 @@
+"""The sizes with which the GPU tests of the 4-bit product reach a kernel, a tile or a split of K: held to them here, over a
+runtime that launches nothing (fake_cuda.py), so that a changed rule of choice does not leave one of them without a test."""
+import re
+
+import pytest
+
+import bit_block_scaled_gb300 as moe
+from fake_cuda import Library, link
+
+P = 1 << 20  # stands for every pointer; nothing is read
+
+# (kernel, tokens a tile, whether K is split): sizes (T, N, K). "wide" is the kernel of pairs of CTAs.
+PRODUCTS = {
+    ("narrow", 16, False): [(1, 130, 64), (13, 130, 96)],
+    ("narrow", 16, True): [(1, 5120, 2880), (16, 640, 4096)],
+    ("narrow", 32, False): [(20, 333, 544)],
+    ("narrow", 32, True): [(20, 640, 2880)],
+    ("narrow", 64, False): [(900, 333, 608)],
+    ("narrow", 64, True): [(40, 1000, 2880)],
+    ("narrow", 128, False): [(256, 5120, 544), (400, 2880, 1024)],
+    ("narrow", 128, True): [(493, 890, 5984)],
+    ("wide", 256, False): [(3000, 2885, 608), (9000, 333, 608)],
+}
+
+
+@pytest.fixture(scope="module")
+def path(tmp_path_factory):
+    return link(tmp_path_factory.mktemp("fake"))
+
+
+@pytest.fixture
+def lib(path, tmp_path):
+    l = Library(path, tmp_path)
+    l.lib.fake_encoder(1)
+    return l
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("kernel", PRODUCTS)
+def test_products(lib, kernel, fmt):
+    for T, N, K in PRODUCTS[kernel]:
+        for dtype in (0, 1, 2):
+            r = P if fmt == 0 else None
+            x, w = moe.Fp4(fmt, T, K, 1, P, P, r), moe.Fp4(fmt, N, K, 1, P, P, r)
+            assert lib.lib.moe_fp4_linear(x, w, None, P, dtype, N, P, None) == 0
+            (name, _, grid, _, cluster), = lib.launches()
+            if kernel[0] == "wide":
+                assert f"wide_kernelILi{fmt}ELi{dtype}E" in name, (T, N, K, name)
+                continue
+            assert f"narrow_kernelILi{fmt}ELi{kernel[1]}E" in name and (cluster > 1) == kernel[2], (T, N, K, name, cluster)
+            assert grid[0] == -(-T // kernel[1]) * -(-N // 128) * cluster
