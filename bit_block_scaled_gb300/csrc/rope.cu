@@ -3,11 +3,11 @@
 // the rotated keys and the values quantised into the paged cache in the same pass.
 //
 // Angles. A frequency is kept as a fraction of a turn a position, in 64-bit fixed
-// point: position * fraction modulo 2^64 is the fraction of a turn that is left, with
-// an error below |position| 2^-65 turns, whatever the position. Its two highest bits
-// (rounded) are the quarter, the next 30 the angle within it, at most an eighth of a
-// turn from its middle, whose sine and cosine are good to fp32's last bits. Negative
-// positions turn back.
+// point, rounded: position * fraction modulo 2^64 is the fraction of a turn that is
+// left, with an error of at most |position| 2^-65 turns, whatever the position. Its two
+// highest bits (rounded) are the quarter, the next 48 the angle within it, at most an
+// eighth of a turn from its middle, whose sine and cosine are good to fp32's last bits.
+// Negative positions turn back.
 //
 // Bound by memory: every value is read and written once. The sines of a CTA's tokens
 // are made once, in shared memory, and used by all of its heads. 8192 tokens with 40
@@ -54,10 +54,12 @@ struct RopeArgs {
 // 1.2e-8 of the amplitude, a correct rounding's are 1.4e-8 and 1e-8: what is lost here is lost by every key, and more of
 // them fall on the other side of a border between two codes.
 __device__ __forceinline__ float2 sine_of(unsigned long long turns, int position, float2 amplitude) {
-  const uint32_t f = (uint32_t)((turns * (unsigned long long)(long long)position) >> 32);  // of 2^-32 turns
+  const unsigned long long p = turns * (unsigned long long)(long long)position;  // of 2^-64 turns
+  const uint32_t f = (uint32_t)(p >> 32);
   const uint32_t quarter = (f + 0x20000000u) >> 30;
-  const int rest = (int)(f - (quarter << 30));  // at most 2^29: 24 bits of it, and the other 6 as a small angle
-  const float x = (float)(rest & ~63) * 0x1p-31f, dx = (float)(rest & 63) * (3.1415927f * 0x1p-31f);  // half turns; radians
+  const int rest = (int)(f - (quarter << 30));  // at most 2^29: 24 bits of it, and the 24 below them as a small angle
+  const float x = (float)(rest & ~63) * 0x1p-31f;  // half turns
+  const float dx = (float)((uint32_t)(p >> 14) & 0xffffffu) * (3.1415927f * 0x1p-49f);  // radians
   const float z = x * x, dz = fmaf(x, x, -z);
   // Taylor's series of sin(pi x) and of cos(pi x) - 1: the first terms left out are 2e-9 and 5e-10; pi in two parts
   float s = fmaf(z, 8.2145887e-2f, -5.9926453e-1f), c = fmaf(z, -2.5806891e-2f, 2.3533063e-1f);

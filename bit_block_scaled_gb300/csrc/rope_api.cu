@@ -10,12 +10,15 @@ using namespace moe4;
 
 namespace {
 
-constexpr double kTwoPi = 6.283185307179586476925;
+constexpr double kTwoPi = 6.283185307179586476925, kTwoPiRest = 2.4492935982947064e-16;  // 2 pi is their sum
 
-// A frequency in radians a position as a 64-bit fraction of a turn.
+// A frequency in radians a position as a 64-bit fraction of a turn, to the nearest: the quotient by 2 pi in two doubles,
+// whose fractions are exact.
 uint64_t turns_of(double f) {
-  const double t = f / kTwoPi, frac = t - floor(t);
-  return frac >= 1.0 ? 0 : (uint64_t)ldexp(frac, 64);
+  if (f < 0.0) return 0 - turns_of(-f);
+  const double t = f / kTwoPi, low = (fma(-t, kTwoPi, f) - t * kTwoPiRest) / kTwoPi;
+  const double high = ldexp(t - floor(t), 64), rest = floor(high - floor(high) + ldexp(low - nearbyint(low), 64) + 0.5);
+  return (uint64_t)high + (rest < 0.0 ? 0 - (uint64_t)-rest : (uint64_t)rest);
 }
 
 bool valid_rope(const moe_rope_t *r, int D) {

@@ -588,8 +588,9 @@ typedef struct {
   double amplitude;     /* of cosine and sine; 0: the scaling's own  */
 } moe_rope_config_t;
 
-/* The frequencies as 64-bit fractions of a turn a position (f / (2 pi) 2^64
- * modulo 2^64), turns [rot_dim / 2], and the amplitude. Host only. */
+/* The frequencies, computed as doubles, as 64-bit fractions of a turn a position
+ * (f / (2 pi) 2^64 modulo 2^64, to the nearest), turns [rot_dim / 2], and the
+ * amplitude. Host only. */
 moe_status_t moe_rope_table(const moe_rope_config_t *config, uint64_t *turns, double *amplitude);
 
 /* The same of n frequencies of the caller's, in radians a position. Host only. */
@@ -603,10 +604,10 @@ typedef struct {
 
 /* Rotates q [T][q_heads][head_dim] into q_out and k [T][k_heads][head_dim] into
  * k_out (k_heads 0: q alone), all of `type`: a pair (a, b) of token t becomes
- * amplitude * (a cos - b sin, b cos + a sin) of the angle positions[t] f_i. The angle
- * is exact to 2^-34 turns at any position; negative positions rotate back. Columns
- * from rot_dim on are copied. fp32 inside, rounded once. An output may be its own
- * input (same strides); otherwise they must not overlap, and rows of an output that
+ * amplitude * (a cos - b sin, b cos + a sin) of the angle positions[t] f_i. That is
+ * positions[t] turns[i] to 2^-49 turns, so exact to 2^-33 turns at any position for the
+ * doubles f_i; negative positions rotate back. Columns from rot_dim on are copied. fp32
+ * inside, rounded once. An output may be its own input (same strides); otherwise they must not overlap, and rows of an output that
  * share elements are refused. Element strides over tokens and heads; any head_dim up to 256 and any strides;
  * rot_dim and head_dim multiples of 16 with strides that are multiples of 8 and
  * 16-byte aligned tensors are fastest. At most 4096 heads each. */
