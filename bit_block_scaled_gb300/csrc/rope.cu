@@ -451,7 +451,7 @@ moe_status_t launch_rope(const moe_rope_t &r, const int32_t *positions, int T, i
   static const Kernel kernels[3][2][3] = {MOE4_R(MOE_BF16), MOE4_R(MOE_FP16), MOE4_R(MOE_FP32)};
 #undef MOE4_R
 #undef MOE4_M
-  const int64_t ctas = (int64_t)((T + a.tokens - 1) / a.tokens) * a.head_blocks;
+  const int64_t ctas = ((int64_t)T + a.tokens - 1) / a.tokens * a.head_blocks;
   if (ctas >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
   const cudaError_t err = launch_pdl(kernels[type][r.layout == MOE_ROPE_INTERLEAVED][mode],
                                      dim3((unsigned)ctas), dim3(kThreads), 0, stream, a);
@@ -481,7 +481,7 @@ moe_status_t launch_rope_kv_write(const moe_rope_t &r, const int32_t *positions,
   int64_t q_ctas = 0;
   const int mode = a.q.rot % 16 == 0 ? kPieces : kColumns;
   share(a.q, q ? q_heads : 1, mode);
-  if (q) q_ctas = (int64_t)((T + a.q.tokens - 1) / a.q.tokens) * a.q.head_blocks;
+  if (q) q_ctas = ((int64_t)T + a.q.tokens - 1) / a.q.tokens * a.q.head_blocks;
   // one row a lane until there are CTAs enough for every SM four times over, then four, as far as the sines of their
   // tokens fit
   const uint32_t per = kThreads >> a.log_n;

@@ -1,5 +1,6 @@
-"""The sizes with which the GPU tests of the 4-bit product reach a kernel, a tile or a split of K: held to them here, over a
-runtime that launches nothing (fake_cuda.py), so that a changed rule of choice does not leave one of them without a test."""
+"""The sizes with which the GPU tests of the 4-bit product and of rotary positions reach a kernel, a tile, a split of K or
+several rows a lane: held to them here, over a runtime that launches nothing (fake_cuda.py), so that a changed rule of
+choice does not leave one of them without a test. And the grids of the most tokens that the calls take."""
 import re
 
 import pytest
@@ -49,3 +50,23 @@ def test_products(lib, kernel, fmt):
                 continue
             assert f"narrow_kernelILi{fmt}ELi{kernel[1]}E" in name and (cluster > 1) == kernel[2], (T, N, K, name, cluster)
             assert grid[0] == -(-T // kernel[1]) * -(-N // 128) * cluster
+
+
+def write_grid(lib, T, hk, D, q=None, q_heads=0):
+    r, c = moe.Rope(D, 0, 1.0, P), moe.KvCache(2, 1000, 16, hk, D, P)
+    args = [P, hk * D, D, P, hk * D, D, 0, P, T, c, P, None]
+    assert lib.lib.moe_rope_kv_write(r, P, q, q_heads * D, D, q_heads, q, q_heads * D, D, *args) == 0
+    return lib.launches()[0][2][0]
+
+
+def rope_grid(lib, T, hq, hk, D, rot):
+    k = (P, hk * D, D, hk, P + (1 << 29), hk * D, D)
+    assert lib.lib.moe_rope(moe.Rope(rot, 0, 1.0, P), P, T, D, P, hq * D, D, hq, P + (1 << 30), hq * D, D, *k, 0, None) == 0
+    return lib.launches()[0][2][0]
+
+
+@pytest.mark.parametrize("T", [2 ** 31 - 1, 2 ** 31 - 16, 2 ** 31 - 17])
+def test_the_most_tokens(lib, T):
+    """One head of two columns: 16 tokens a CTA, the last of them within 16 of 2^31."""
+    assert rope_grid(lib, T, 1, 0, 2, 2) == -(-T // 16)
+    assert write_grid(lib, T, 1, 64, P, 1) == -(-T // 16) + -(-T // 32)  # queries, and a row of keys a lane
