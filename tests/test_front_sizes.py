@@ -22,6 +22,10 @@ PRODUCTS = {
     ("narrow", 128, True): [(493, 890, 5984)],
     ("wide", 256, False): [(3000, 2885, 608), (9000, 333, 608)],
 }
+# (T, kv heads, head_dim): four rows of keys and values a lane
+WRITES = [(6700, 3, 256), (13001, 3, 128), (16001, 5, 64)]
+# (T, q heads, k heads, head_dim, rot): 16 tokens a CTA
+ROTATIONS = [(10007, 2, 1, 64, 64), (10007, 2, 1, 64, 40), (10007, 1, 1, 80, 64)]
 
 
 @pytest.fixture(scope="module")
@@ -59,10 +63,23 @@ def write_grid(lib, T, hk, D, q=None, q_heads=0):
     return lib.launches()[0][2][0]
 
 
+@pytest.mark.parametrize("T,hk,D", WRITES)
+def test_writes(lib, T, hk, D):
+    per = 256 // (D // 8)
+    assert write_grid(lib, T, hk, D) == -(-T * hk // (4 * per))  # four rows a lane
+    assert T * hk % (4 * per) and hk * 4 % per  # a ragged end, and tokens that end within a lane's walk
+    assert write_grid(lib, 700, hk, D) == -(-700 * hk // per)
+
+
 def rope_grid(lib, T, hq, hk, D, rot):
     k = (P, hk * D, D, hk, P + (1 << 29), hk * D, D)
     assert lib.lib.moe_rope(moe.Rope(rot, 0, 1.0, P), P, T, D, P, hq * D, D, hq, P + (1 << 30), hq * D, D, *k, 0, None) == 0
     return lib.launches()[0][2][0]
+
+
+@pytest.mark.parametrize("T,hq,hk,D,rot", ROTATIONS)
+def test_rotations(lib, T, hq, hk, D, rot):
+    assert rope_grid(lib, T, hq, hk, D, rot) == -(-T // 16)
 
 
 @pytest.mark.parametrize("T", [2 ** 31 - 1, 2 ** 31 - 16, 2 ** 31 - 17])
