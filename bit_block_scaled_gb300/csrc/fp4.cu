@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kWarps * 32) fp4_quantize_kernel(const QuantAr
     }
     bad = top >= inf_bits<TYPE>();
     const int e = row_exponent(from_bits<TYPE>(top), 2688.f, 12);
-    // e is at most 116 for finite values (a bad row's codes are not used)
+    // e is at most 117 for finite values (a bad row's codes are not used), so that up / s, s <= 448, is a normal number
     if (TYPE != MOE_FP32 && e < -110) pre = 0x1p64f;
     up = pow2(pre > 1.f ? -e - 64 : -e);
     if (live && wr == 0 && lane == 0) a.row_scale[row] = bad ? __int_as_float(0x7fc00000) : pow2(e);

@@ -29,7 +29,7 @@ __device__ __forceinline__ void put8(uint8_t *rec, int i, int part, int j, int n
   for (int o = 1; o < n; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
   const bool bad = top >= inf_bits<TYPE>();
   const int e = FMT == MOE_KV_FP8 ? row_exponent(from_bits<TYPE>(top), 448.f, 9) : row_exponent(from_bits<TYPE>(top), 2688.f, 12);
-  const float up = pow2(-e);  // e is at most 119 for finite values; a bad row's codes are not used
+  const float up = pow2(-e);  // e is at most 120 for finite values; a bad row's codes are not used
   raw8_to_f32(raw, TYPE, x);
 #pragma unroll
   for (int q = 0; q < 8; ++q) x[q] *= up;

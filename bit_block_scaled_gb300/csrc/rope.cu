@@ -50,9 +50,10 @@ struct RopeArgs {
   Divisor by_pairs, by_items, by_heads;  // pairs of a head; threads that share one; heads_each
 };
 
-// Cosine and sine of position * frequency, times the amplitude (in two parts). Their root mean square errors are 1.9e-8 and
-// 1.2e-8 of the amplitude, a correct rounding's are 1.4e-8 and 1e-8: what is lost here is lost by every key, and more of
-// them fall on the other side of a border between two codes.
+// Cosine and sine of position * frequency, times the amplitude (in two parts). Root mean square errors, of the larger of the
+// two and of the smaller: 1.94e-8 and 1.15e-8 at amplitude 1 (a correct rounding's 1.72e-8 and 1.13e-8), 2.67e-8 and 1.00e-8 of
+// YaRN's for a factor of 32 (2.49e-8 and 0.98e-8). Of 50.6 million keys in FP8, 64 got another code than real
+// arithmetic's, with correctly rounded ones 62: what is left is the products' rounding.
 __device__ __forceinline__ float2 sine_of(unsigned long long turns, int position, float2 amplitude) {
   const unsigned long long p = turns * (unsigned long long)(long long)position;  // of 2^-64 turns
   const uint32_t f = (uint32_t)(p >> 32);
