@@ -17,6 +17,8 @@
 //    the way into the SMs. 256 columns instead of 192, whose two accumulators
 //    need no sharing of columns, take 19% fewer bytes a product (16384 x 8192 x
 //    8192 347 -> 313 us, 7.0 PFLOP/s, 0.92 of four times the measured bf16 rate).
+//    Rows of outputs off the 16-byte grid are written value by value (8192 x 5120 x
+//    2880 52 us, with rows of 5121 79).
 #include <cudaTypedefs.h>
 #include <float.h>
 #include <math.h>
@@ -192,7 +194,8 @@ struct Narrow {
 };
 
 // 8 sums of tokens from c on, whose row scales are any, into the outputs from i on (`put` below takes nearly all tiles).
-// Not inline, so that the code of the others stays together: 64 x 5120 x 2880 6.5 us, with it inline 6.7 to 6.8.
+// Not inline, so that the code of the others stays together: 64 x 5120 x 2880 6.5 us, with it inline 6.7 to 6.8 (this way
+// itself 9.6).
 __device__ __noinline__ void put8_far(const LinArgs &p, uint8_t *tile_s, const float *xr_s, int i, int c, int count, int t0, int n,
                                       int row, float scale, float bias, float v0, float v1, float v2, float v3, float v4, float v5,
                                       float v6, float v7) {
@@ -364,7 +367,8 @@ __global__ void __launch_bounds__(kThreads) narrow_kernel(const __grid_constant_
       }
     };
     if (TN == 16) {
-      // few values: each lane stores its own where they belong (one token of 5120 x 2880 3.4 us; by bulk copies 4.1)
+      // few values: each lane stores its own where they belong (one token of 5120 x 2880 in 3 parts 3.8 us, by bulk copies
+      // the same, in 4 parts 4.1 against 4.3)
       asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // all ranks run
       if (warp >= 2) {
         const uint32_t to = smem_u32(parts + rank * share * 128 + row);
@@ -790,9 +794,9 @@ struct Shape {
 // the SMs' shared memory together share that, for 0.5 us more; another round of them takes 3. Clusters are laid into
 // groups of about 19 SMs. Joining parts of K takes 0.4 us for 16 tokens, for more 1 (128 tokens: 1.6) and 0.03 a token that a
 // CTA sums; the wide kernel's last tile is written in 1 us more. Measured, in us, the chosen first: 1 x 5120 x 2880 16
-// tokens in 3 parts 3.7, whole 5.2; 8 x 8192 x 8192 16 in 2 7.3, whole 10.1; 64 x 5120 x 2880 64 in 3 6.5, whole 6.4, in 4
-// 11.6; 100 x 2688 x 4096 64 in 3 6.4, whole 7.1, 128 in 6 7.3; 333 x 2880 x 4096 64 whole 7.4, 128 7.7, wide 8.9; 1024 x
-// 4096 x 4096 wide 9.8, 128 16.6.
+// tokens in 3 parts 3.8, whole 5.0; 8 x 8192 x 8192 16 in 2 7.3, whole 10.1; 64 x 5120 x 2880 64 in 3 6.5, whole 6.5, too, in
+// 4 11.1; 100 x 2688 x 4096 64 in 3 6.5, whole 7.5, 128 in 6 7.3; 333 x 2880 x 4096 (MXFP4) 64 whole 7.4, 128 7.7, wide 9.0;
+// 1024 x 4096 x 4096 wide 9.8, 128 16.9.
 Shape choose(int T, int N, int K) {
   const int stages = (K + kStageK - 1) / kStageK, sms = sm_count();
   const int64_t wide_tiles = (int64_t)((T + 255) / 256) * ((N + kWideN - 1) / kWideN), pairs = sms / 2;

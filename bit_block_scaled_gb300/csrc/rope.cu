@@ -11,7 +11,7 @@
 //
 // Bound by memory: every value is read and written once. The sines of a CTA's tokens
 // are made once, in shared memory, and used by all of its heads. 8192 tokens with 40
-// heads of 128 take 26.9 us, 92% of the copy bandwidth, one token 1.6.
+// heads of 128 take 27.5 us, 90% of the copy bandwidth, one token 1.7.
 #include "checks.h"
 #include "common.cuh"
 #include "kernels.h"
@@ -349,8 +349,8 @@ struct WriteArgs {
 
 // First the CTAs that write a row (token, kv head) of keys and values for each 1 << log_n lanes, then those that rotate
 // queries (dealing them out in turn made no difference). Bound by instructions next to memory: 12345 tokens, 32 heads on 8
-// of 128, into FP8 take 50 us, 84% of the copy bandwidth; the queries alone
-// take 32 (93%), the cache write without a rotation 17.
+// of 128, into FP8 take 49 us, 84% of the copy bandwidth; the queries alone
+// take 32 (93%), the cache write without a rotation 16. Into NVFP4 60, the floor 39.5: the write alone is 29, a division a value.
 template <int FMT, int TYPE, bool HALF, int MODE>
 __global__ void __launch_bounds__(kThreads) rope_write_kernel(const WriteArgs a) {
   __shared__ __align__(16) float2 sines[kMaxTokens * kMaxPairs];

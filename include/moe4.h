@@ -552,7 +552,8 @@ moe_status_t moe_attn_decode(const void *q, int q_type, int64_t q_stride_b,
  * holds (the rest is dropped), and a page number outside 0..num_pages - 1, whose tokens
  * get slot -1 and which a row gets as -1.
  * B <= 4096, T <= 2^28, page_size and num_pages as in moe_kv_cache_t, (max_pages + 1)
- * * page_size < 2^31. Outputs other than these two must not overlap inputs. */
+ * * page_size < 2^31. Outputs other than these two must not overlap inputs. With B = 0 and
+ * T = 0 nothing is launched and nothing written, free_count_out and offsets neither. */
 moe_status_t moe_batch_plan(const int32_t *new_lens, const int32_t *seq_lens, int B, int page_size, int num_pages,
                             int32_t *block_table, int64_t table_stride, int max_pages, int32_t *free_pages,
                             const int32_t *free_count, int32_t *seq_lens_out, int32_t *free_count_out, int32_t *offsets,
@@ -659,7 +660,9 @@ int64_t moe_fp4_scale_bytes(int fmt, int rows, int K);
  * row scale r the least power of two (exponent -127..127) with amax / r <= 6 *
  * 448, block scales E4M3(amax16 / r / 6), codes E2M1(x / r / s), 0 where s is 0.
  * MXFP4: block scale s the least power of two with amax32 / s <= 6, codes
- * E2M1(x / s). Roundings are to nearest, ties to even, of the exact quotients. A
+ * E2M1(x / s); nothing saturates. (The OCP specification's example takes the largest
+ * power of two up to amax32, over 4, and saturates: half of s where amax32 is above 6 and
+ * below 8 of it, else the same.) Roundings are to nearest, ties to even, of the exact quotients. A
  * NaN or an infinity makes its row (NVFP4: row scale NaN) or its block (MXFP4:
  * scale 255) NaN, with zero codes. K <= 32768. */
 moe_status_t moe_fp4_quantize(const void *x, int type, int64_t x_stride, const moe_fp4_t *out, moe_stream_t stream);
