@@ -675,8 +675,8 @@ moe_status_t moe_fp4_dequantize(const moe_fp4_t *f, void *out, int type, int64_t
 moe_status_t moe_fp4_pack_scales(const uint8_t *plain, int fmt, int rows, int K, uint8_t *scales, moe_stream_t stream);
 
 /* out[t][n] = sum_k x[t][k] w[n][k] + bias[n], fp32 sums, rounded once to `type`
- * (as bias [N], or NULL, is), whatever the row scales' sizes: an infinity stands for a
- * result past the type's range alone. x [T][K], w [N][K] of one format and K, out [T][N]
+ * (as bias [N], or NULL, is). Finite row scales may have any size: an infinity in NVFP4
+ * stands for a result past the type's range alone. x [T][K], w [N][K] of one format and K, out [T][N]
  * with rows ldo >= N apart. One token (T = 1) and any N are fine; ldo a multiple
  * of 8 (4 in fp32) is fastest. Out must not overlap the operands. ws: >= MOE_STATUS_BYTES (status word).
  * Deterministic: repeated calls give bit-identical outputs. */
